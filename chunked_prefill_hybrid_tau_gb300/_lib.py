@@ -75,6 +75,7 @@ PROTOTYPES = {
     "hb_rope_table": (C.c_int, [vp, i32, i32, C.c_double, vp]),
     "hb_rmsnorm": (C.c_int, [vp, vp, vp, i32, i32, C.c_float, vp]),
     "hb_kv_append": (C.c_int, [vp, i32, vp, vp, vp, i32, C.POINTER(hb_layer_dims), vp, vp, vp, i32, vp]),
+    "hb_kv_append_norm": (C.c_int, [vp, i32, vp, vp, vp, i32, C.POINTER(hb_layer_dims), vp, vp, vp, vp, vp, i32, vp]),
     "hb_attention_workspace_bytes": (C.c_size_t, [C.POINTER(hb_layer_dims), i32, i32, i32]),
     "hb_attention": (C.c_int, [vp, vp, vp, i32, C.POINTER(hb_device_plan), C.POINTER(hb_layer_dims), i32, vp, vp,
                                C.c_size_t, vp]),
@@ -83,6 +84,8 @@ PROTOTYPES = {
     "hb_gemm": (C.c_int, [vp, vp, vp, vp, i32, i32, i32, i32, vp]),
     "hb_gemm_e4m3": (C.c_int, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp]),
     "hb_quantize_e4m3": (C.c_int, [vp, vp, vp, i32, i32, vp]),
+    "hb_quantize_e4m3_block": (C.c_int, [vp, vp, vp, i32, i32, i32, vp]),
+    "hb_gemm_e4m3_block": (C.c_int, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp]),
     "hb_interleave_gate_up": (C.c_int, [vp, vp, vp, i32, i32, vp]),
     "hb_fold_gamma": (C.c_int, [vp, vp, vp, i32, i32, vp]),
     "hb_layer_workspace_bytes": (C.c_size_t, [C.POINTER(hb_layer_dims), i32, i32, i32]),

@@ -307,6 +307,15 @@ def hb_kv_append(qkv, row_pos, slot_mapping, rope, max_pos, dims, q_out, k_cache
                               _stream(stream)), "hb_kv_append")
 
 
+def hb_kv_append_norm(qkv, row_pos, slot_mapping, rope, max_pos, dims, g_q, g_k, q_out, k_cache, v_cache,
+                      stream=None):
+    """hb_kv_append with q and k heads RMS-normed (gains g_q, g_k bf16 [d_head])."""
+    ds = dims_struct(dims)
+    _check(lib().hb_kv_append_norm(_p(qkv), int(qkv.shape[0]), _p(row_pos), _p(slot_mapping), _p(rope), int(max_pos),
+                                   C.byref(ds), _p(g_q), _p(g_k), _p(q_out), _p(k_cache), _p(v_cache),
+                                   int(k_cache.shape[0]), _stream(stream)), "hb_kv_append_norm")
+
+
 def hb_attention_workspace_bytes(dims, max_rows, max_seqs, max_kv_len) -> int:
     ds = dims_struct(dims)
     return int(lib().hb_attention_workspace_bytes(C.byref(ds), int(max_rows), int(max_seqs), int(max_kv_len)))
@@ -343,6 +352,30 @@ def hb_quantize_e4m3(x, q=None, scale=None, stream=None):
     scale = torch.empty(max(rows, 4), dtype=torch.float32, device=x.device) if scale is None else scale
     _check(lib().hb_quantize_e4m3(_p(x), _p(q), _p(scale), rows, cols, _stream(stream)), "hb_quantize_e4m3")
     return q, scale[:rows]
+
+
+def hb_quantize_e4m3_block(x, q=None, scale=None, block_rows=1, stream=None):
+    """E4M3 codes (uint8 [rows][cols]) of a device bf16 matrix x with one fp32
+    scale per 1 x 128 (block_rows=1) or 128 x 128 (block_rows=128) block;
+    returns (q, scale [ceil(rows / block_rows)][ceil(cols / 128)])."""
+    import torch
+    rows, cols = x.shape
+    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device) if q is None else q
+    if scale is None:
+        scale = torch.empty((-(-rows // block_rows) if block_rows > 0 else 0, -(-cols // 128)), dtype=torch.float32,
+                            device=x.device)
+    _check(lib().hb_quantize_e4m3_block(_p(x), _p(q), _p(scale), rows, cols, int(block_rows), _stream(stream)),
+           "hb_quantize_e4m3_block")
+    return q, scale
+
+
+def hb_gemm_e4m3_block(A, s_a, B, s_b, Cout, R=None, epilogue=L.HB_EPI_STORE, stream=None):
+    """Block-scaled E4M3 codes A [M][K], B [N][K] (uint8 tensors) with fp32
+    scales s_a [M][ceil(K / 128)], s_b [ceil(N / 128)][ceil(K / 128)]."""
+    M, K = A.shape
+    N = B.shape[0]
+    _check(lib().hb_gemm_e4m3_block(_p(A), _p(s_a), _p(B), _p(s_b), _p(Cout), _p(R), M, N, K, int(epilogue),
+                                    _stream(stream)), "hb_gemm_e4m3_block")
 
 
 def hb_interleave_gate_up(w_gate, w_up, w_gu, stream=None):

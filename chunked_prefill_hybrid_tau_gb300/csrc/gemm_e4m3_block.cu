@@ -1,0 +1,973 @@
+// Packed-token projections with block-scaled E4M3 operands (kind::f8f6f4):
+//   C = epilogue(P),
+//   P[m][n] = sum_b sa[m][b] sb[n / 128][b] sum_{k in block b} A[m][k] B[n][k]
+// with A [M][K] token codes (one fp32 scale per row and 128 columns of K)
+// and B [N][K] weight codes (one per 128 x 128 block), codes and scales as
+// hb_quantize_e4m3_block writes them.
+//
+// The scales change along K, so the tensor cores cannot carry the sum over
+// the blocks (the hardware's own block scales are powers of two per 32
+// elements; these are any fp32 number per 128).  Each 128-wide K block is one
+// accumulation in tensor memory; epilogue warps read it back and add it,
+// scaled, to fp32 sums in registers:
+//   acc = fma(part, fl(sa sb), acc), block by block in K order.
+// Every kernel here adds the blocks of an output in this one order with
+// these roundings, so a token's result does not depend on which kernel or
+// tile its batch selected.
+#include <cuda_bf16.h>
+
+#include "device.cuh"
+#include "runtime.h"
+
+namespace hb {
+namespace {
+
+using namespace dev;
+
+constexpr int BM = 128;
+constexpr int BK = 128;
+
+struct Params {
+  int M, N, K;
+  int lda;
+  void* C;
+  const void* R;
+  int ldc;       // row stride of C and R (elements)
+  int out_cols;  // valid output columns (N, or N/2 for SWIGLU)
+  const float* sa;
+  const float* sb;
+  int f_blocks;  // SWIGLU: rows of sb that belong to the gate
+  int kblocks;
+  int* status;
+  int rows;      // skinny kernel: weight rows of a tile
+  int stages;    // skinny kernel: ring depth
+};
+
+// silu(g) = g / (1 + e^-g), the arithmetic of the per-row scaled projections.
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, __fadd_rn(1.0f, __expf(-g))); }
+
+__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+// Two fp32 FMAs / products, each rounded as the scalar ones.
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Byte offset of 16-byte chunk c (0..7) of row r in a slab of 128 rows x 128
+// bytes with the 128-byte swizzle (the TMA box layout).
+__device__ __forceinline__ uint32_t slab_off(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+constexpr int kSlabBytes = 128 * 128;
+
+// Row of sb that scales B row n.  SWIGLU: B holds gate and up rows
+// interleaved in blocks of 64, sb the gate's block scales, then the up's.
+template <bool SWIGLU>
+__device__ __forceinline__ int scale_row(const Params& p, int n) {
+  if constexpr (SWIGLU) {
+    const int f = (n >> 7) * 64 + (n & 63);
+    return (f >> 7) + ((n & 64) ? p.f_blocks : 0);
+  }
+  return n >> 7;
+}
+
+// ================================================================ wide tiles
+// 128 x BN output tiles (PAIR: 256 x BN on a cluster of two CTAs with
+// tcgen05 cta_group::2, each CTA holding its 128 rows of A and half of the B
+// rows), persistent, M fastest so that the CTAs sharing a weight tile run
+// together.
+//   warps 0-7 : promotion and epilogue.  Warp w reads TMEM lanes 32 (w % 4)..
+//               (its output rows) and column half w / 4, so a thread holds
+//               BN / 2 fp32 sums of one row and scales a K block with one or
+//               two factors;
+//   warp 8    : TMA producer (128-byte swizzled boxes of one K block);
+//   warp 9    : MMA issuer; one K block per TMEM buffer, NBUF buffers.
+// The sums leave through shared memory staged apart from the ring and TMA
+// stores, so the next tile's loads and MMAs go on meanwhile.
+template <int BN, bool PAIR>
+struct Cfg {
+  static constexpr int A_BYTES = BM * 128;
+  static constexpr int B_BYTES = (PAIR ? BN / 2 : BN) * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int NBUF = 512 / BN;  // TMEM accumulator buffers
+  static constexpr int STAGING = BM * BN * 2;
+  static constexpr int AVAIL = 232448 - 1024 - 512 - STAGING;
+  static constexpr int STAGES = AVAIL / STAGE_BYTES < 8 ? AVAIL / STAGE_BYTES : 8;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 512 + 1024;
+  static constexpr int CH = BN / 64;  // 32-column chunks of a thread
+  static_assert(BN == 128 || BN == 256, "BN");
+  static_assert(STAGE_BYTES % 1024 == 0 && STAGING % 1024 == 0, "alignment");
+  static_assert(STAGES >= 3, "ring depth");
+};
+constexpr int kWideThreads = 320;
+
+template <int BN, int EPI, bool PAIR>
+__device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
+                                          const CUtensorMap& tmR, const Params& p) {
+  using C = Cfg<BN, PAIR>;
+  constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;
+  constexpr int CH = C::CH;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = smem + C::STAGES * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::STAGING);  // PAIR: the even CTA's are used
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* acc_full = empty + C::STAGES;
+  uint64_t* acc_empty = acc_full + C::NBUF;  // PAIR: the even CTA's are used
+  uint64_t* drain = acc_empty + C::NBUF;
+  uint64_t* res_bar = drain + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
+  const int m_tiles = (p.M + BM - 1) / BM;
+  const int um = PAIR ? (m_tiles + 1) / 2 : m_tiles;  // row tiles of a unit
+  const int n_tiles = (p.N + BN - 1) / BN;
+  const int units = um * n_tiles;
+  const int first = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+  const int stride = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+  const int kblocks = p.kblocks;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < C::NBUF; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], PAIR ? 16 : 8);
+    }
+    mbar_init(drain, 1);
+    mbar_init(res_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmC);
+  }
+  if (warp == 9) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    }
+  }
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 8) {
+    // ---------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      const uint64_t wpol = um <= 4 ? policy_evict_first() : policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      uint32_t pending = 0, armed_parity = 0;
+      auto load_a = [&](int s, int kb, int m0) {
+        uint8_t* dst = smem + s * C::STAGE_BYTES;
+        if constexpr (PAIR)
+          tma_load_2d_pair(dst, &tmA, cluster_addr(&full[s], 0), kb * BK, m0);
+        else
+          tma_load_2d(dst, &tmA, &full[s], kb * BK, m0);
+      };
+      auto load_b = [&](int s, int kb, int n0) {
+        uint8_t* dst = smem + s * C::STAGE_BYTES + C::A_BYTES;
+        if constexpr (PAIR)
+          tma_load_2d_pair_hint(dst, &tmB, cluster_addr(&full[s], 0), kb * BK, n0, wpol);
+        else
+          tma_load_2d_hint(dst, &tmB, &full[s], kb * BK, n0, wpol);
+      };
+      auto arm = [&](int s) {
+        if (leader) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * C::STAGE_BYTES);  // both CTAs' boxes
+      };
+      // the weights do not come from the kernel ahead: their first ring fill
+      // is issued before waiting for it
+      int pre = 0;
+      if (first < units) {
+        const int n0 = (first / um) * BN + static_cast<int>(rank) * (BN / 2);
+        pre = kblocks < C::STAGES ? kblocks : C::STAGES;
+        for (int i = 0; i < pre; ++i) {
+          arm(i);
+          load_b(i, i, n0);
+        }
+      }
+      griddep_wait();
+      for (int u = first; u < units && ok; u += stride) {
+        const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
+        const int n0 = (u / um) * BN + static_cast<int>(rank) * (BN / 2);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (u == first && kb < pre) {
+            pending |= 1u << stage;
+            load_a(stage, kb, mt * BM);
+          } else {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            pending |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            arm(stage);
+            load_a(stage, kb, mt * BM);
+            load_b(stage, kb, n0);
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
+      if (!ok) {
+        // let copies already in flight land before the CTA leaves (one CTA:
+        // their own barrier; a pair: the stage is released once consumed)
+        for (int s = 0; s < C::STAGES; ++s)
+          if (pending & (1u << s)) mbar_drain(PAIR ? &empty[s] : &full[s], (armed_parity >> s) & 1u);
+      }
+    }
+    if (lane != 0) griddep_wait();
+  } else if (warp == 9) {
+    // ---------------------------------------------------------- MMA issuer
+    griddep_wait();
+    if (leader && lane == 0) {
+      constexpr uint32_t kIdesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BN);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t par) {
+        if constexpr (PAIR) return mbar_wait_cluster(bar, par, abort_flag, p.status);
+        return mbar_wait(bar, par, abort_flag, p.status);
+      };
+      for (int u = first; u < units && ok; u += stride) {
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!wait(&acc_empty[buf], bphase ^ 1u) || !wait(&full[stage], phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + stage * C::STAGE_BYTES);
+          const uint32_t b_addr = a_addr + C::A_BYTES;
+          const uint32_t d_tmem = tmem_base + buf * BN;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (PAIR)
+              mma_e4m3_pair(d_tmem, smem_desc_sw128(a_addr + k * 32), smem_desc_sw128(b_addr + k * 32), kIdesc, k != 0);
+            else
+              mma_e4m3(d_tmem, smem_desc_sw128(a_addr + k * 32), smem_desc_sw128(b_addr + k * 32), kIdesc, k != 0);
+          }
+          if constexpr (PAIR) {
+            mma_commit_pair(&empty[stage], 3);
+            mma_commit_pair(&acc_full[buf], 3);
+          } else {
+            mma_commit(&empty[stage]);
+            mma_commit(&acc_full[buf]);
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == C::NBUF) {
+            buf = 0;
+            bphase ^= 1u;
+          }
+        }
+      }
+      if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
+      // no MMA may still read shared memory or write tensor memory when the CTAs leave
+      if constexpr (PAIR)
+        mma_commit_pair(drain, 1);
+      else
+        mma_commit(drain);
+      mbar_drain(drain, 0);
+    }
+  } else {
+    // ---------------------------------------------------------- promotion and epilogue
+    griddep_wait();
+    const int quarter = warp & 3, half = warp >> 2;
+    const bool boss = threadIdx.x == 0;
+    const int rloc = quarter * 32 + lane;
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    // first column of chunk c of this half.  SWIGLU, BN 128: 32 gate columns
+    // and the 32 up columns that go with them.
+    auto chunk_col = [&](int c) {
+      if (SWIGLU && BN == 128) return half * 32 + c * 64;
+      return half * (BN / 2) + c * 32;
+    };
+    int buf = 0;
+    uint32_t bphase = 0, rphase = 0;
+    bool ok = true;
+    bool res_pending = false;  // boss: residual copies in flight
+    for (int u = first; u < units; u += stride) {
+      const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
+      const int n0 = (u / um) * BN;
+      const int row = mt * BM + rloc;
+      const bool row_ok = row < p.M;
+      const bool live = mt < m_tiles;  // a pair's odd row tile may lie past M
+      const float* sap = p.sa + static_cast<size_t>(row_ok ? row : 0) * kblocks;
+      // the scale rows of this half's first and second chunk group (columns
+      // past N read the last row: their sums are not stored)
+      auto sb_row = [&](int c) {
+        const int n = n0 + chunk_col(c);
+        return p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n < p.N ? n : p.N - 1)) * kblocks;
+      };
+      const float* sb0 = sb_row(0);
+      const float* sb1 = sb_row(CH / 2);
+      uint64_t acc[CH][16];
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[c][j] = 0;
+      float a_next = row_ok ? __ldg(sap) : 0.f;
+      float b0_next = __ldg(sb0), b1_next = __ldg(sb1);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        const float f0 = __fmul_rn(a_next, b0_next), f1 = __fmul_rn(a_next, b1_next);
+        if (kb + 1 < kblocks) {
+          a_next = row_ok ? __ldg(sap + kb + 1) : 0.f;
+          b0_next = __ldg(sb0 + kb + 1);
+          b1_next = __ldg(sb1 + kb + 1);
+        }
+        if constexpr (EPI == HB_EPI_RESIDUAL) {
+          // the residual tile into the staging slabs, once the previous
+          // tile's stores have left them (by now long done)
+          if (boss && live && ok && kb == (kblocks > 2 ? 2 : 0)) {
+            bulk_wait_group_read<0>();
+            int slabs = (p.N - n0 + 63) / 64;
+            if (slabs > BN / 64) slabs = BN / 64;
+            mbar_arrive_expect_tx(res_bar, slabs * kSlabBytes);
+            for (int s = 0; s < slabs; ++s)
+              tma_load_2d(staging + s * kSlabBytes, &tmR, res_bar, n0 + s * 64, mt * BM);
+            res_pending = true;
+          }
+        }
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], bphase, abort_flag, p.status));
+        if (ok) {
+          tc_fence_after();
+          const uint64_t s0 = pack_f32x2(__float_as_uint(f0), __float_as_uint(f0));
+          const uint64_t s1 = pack_f32x2(__float_as_uint(f1), __float_as_uint(f1));
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(t_lane + buf * BN + chunk_col(c), r);
+            tmem_ld_wait();
+            if (c == CH - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (PAIR)
+                  mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[buf], 0));
+                else
+                  mbar_arrive(&acc_empty[buf]);
+              }
+            }
+            const uint64_t s = c < CH / 2 ? s0 : s1;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c][j] = fma_f32x2(pack_f32x2(r[2 * j], r[2 * j + 1]), s, acc[c][j]);
+          }
+        }
+        if (++buf == C::NBUF) {
+          buf = 0;
+          bphase ^= 1u;
+        }
+      }
+      // ---- the tile's sums are complete
+      if (!live) continue;  // the same for every thread of the CTA
+      if constexpr (EPI == HB_EPI_RESIDUAL) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(res_bar, rphase, abort_flag, p.status));
+        if (ok) {
+          rphase ^= 1u;
+          res_pending = false;
+        }
+      } else {
+        if (boss) bulk_wait_group_read<0>();
+        named_barrier_sync(1, 256);
+      }
+      if constexpr (EPI == HB_EPI_F32) {
+        constexpr int ROUNDS = 2, PER = CH / 2;  // chunks of a half and round; one 32-column slab each
+#pragma unroll
+        for (int rd = 0; rd < ROUNDS; ++rd) {
+          if (rd > 0) {
+            if (boss) bulk_wait_group_read<0>();
+            named_barrier_sync(1, 256);
+          }
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            uint8_t* slab = staging + (half * PER + i) * kSlabBytes;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const uint64_t lo = acc[rd * PER + i][2 * q], hi = acc[rd * PER + i][2 * q + 1];
+              *reinterpret_cast<ulonglong2*>(slab + slab_off(rloc, q)) = make_ulonglong2(lo, hi);
+            }
+          }
+          fence_proxy_async_smem();
+          named_barrier_sync(2, 256);
+          if (boss && ok) {
+            for (int h = 0; h < 2; ++h)
+              for (int i = 0; i < PER; ++i) {
+                const int x = n0 + h * (BN / 2) + (rd * PER + i) * 32;
+                if (x < p.out_cols) tma_store_2d(&tmC, staging + (h * PER + i) * kSlabBytes, x, mt * BM);
+              }
+            bulk_commit_group();
+          }
+        }
+      } else {
+        if constexpr (SWIGLU) {
+          // BN 256: chunks 0, 1 gate and 2, 3 up of one 64-column output
+          // slab per half; BN 128: one chunk of each, half a slab per half
+          constexpr int G = CH / 2;
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            uint8_t* slab = staging + (BN == 256 ? half : 0) * kSlabBytes;
+            const int c0 = (BN == 256 ? i : half) * 4;  // first 16-byte piece
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float g0, g1, u0, u1;
+                unpack_f32x2(acc[i][4 * q + j], g0, g1);
+                unpack_f32x2(acc[G + i][4 * q + j], u0, u1);
+                w[j] = pack_bf16x2(__fmul_rn(silu(g0), u0), __fmul_rn(silu(g1), u1));
+              }
+              *reinterpret_cast<uint4*>(slab + slab_off(rloc, c0 + q)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < CH; ++c) {
+            const int col = half * (BN / 2) + c * 32;
+            uint8_t* slab = staging + (col >> 6) * kSlabBytes;
+            const int c0 = (col & 32) >> 3;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint4* dst = reinterpret_cast<uint4*>(slab + slab_off(rloc, c0 + q));
+              uint32_t w[4];
+              if constexpr (EPI == HB_EPI_RESIDUAL) {
+                const uint4 rv = *dst;
+                const uint32_t rr[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  float v0, v1;
+                  unpack_f32x2(acc[c][4 * q + j], v0, v1);
+                  const float2 f = unpack_bf16x2(rr[j]);
+                  w[j] = pack_bf16x2(__fadd_rn(f.x, v0), __fadd_rn(f.y, v1));
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  float v0, v1;
+                  unpack_f32x2(acc[c][4 * q + j], v0, v1);
+                  w[j] = pack_bf16x2(v0, v1);
+                }
+              }
+              *dst = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        named_barrier_sync(2, 256);
+        if (boss && ok) {
+          constexpr int SLABS = SWIGLU ? BN / 128 : BN / 64;
+          const int x0 = SWIGLU ? n0 / 2 : n0;
+          for (int s = 0; s < SLABS; ++s)
+            if (x0 + s * 64 < p.out_cols) tma_store_2d(&tmC, staging + s * kSlabBytes, x0 + s * 64, mt * BM);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (res_pending) mbar_drain(res_bar, rphase);
+    if (boss) bulk_wait_group<0>();  // the TMA stores have left shared memory and are performed
+    if (PAIR && lane == 0 && *abort_flag) raise_peer_abort(abort_flag, rank);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  if (warp == 9) {
+    tc_fence_after();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, 512);
+    else
+      tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int BN, int EPI>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    block_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR, Params p) {
+  wide_body<BN, EPI, false>(tmA, tmB, tmC, tmR, p);
+}
+
+template <int BN, int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    block_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR, Params p) {
+  wide_body<BN, EPI, true>(tmA, tmB, tmC, tmR, p);
+}
+
+// ================================================================ few tokens
+// M <= NT: the weights are the bound, so the operands change places: a tile
+// is p.rows weight rows (TMEM lanes) x NT tokens (columns), and the rows per
+// tile are chosen so that the tiles fill the SMs.  The MMA always has M =
+// 128: lanes past p.rows multiply whatever follows in shared memory and are
+// not read.
+//   warps 0-3: promotion and epilogue (those with lanes below p.rows; all
+//              four fill the table of token scales);
+//   warp 4   : TMA producer;  warp 5: MMA issuer.
+constexpr int kSkinnyThreads = 192;
+constexpr int kSkinnyBufs = 4;
+constexpr int kTabK = 16;  // K blocks per fill of the token-scale table
+
+template <int NT>
+struct CfgSkinny {
+  static constexpr int TMEM_COLS = NT * kSkinnyBufs < 32 ? 32 : NT * kSkinnyBufs;
+  static constexpr int TAB_BYTES = 2 * kTabK * NT * 4;
+  static constexpr int MAX_STAGES = 32;
+  static constexpr int BAR_BYTES = 1024;
+  static constexpr int XCH_BYTES = 64 * (NT + 1) * 4;  // SWIGLU: up sums for the gate's threads
+  static constexpr int FIXED = 1024 + BM * 128 + TAB_BYTES + BAR_BYTES + XCH_BYTES;
+};
+
+template <int NT, int EPI>
+__global__ void __launch_bounds__(kSkinnyThreads, 1)
+    block_gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                             Params p) {
+  using C = CfgSkinny<NT>;
+  constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int w_bytes = p.rows * 128, stage_bytes = w_bytes + NT * 128;
+  // BM * 128 bytes past the ring: the last stage's MMA reads its unused lanes there
+  float* table = reinterpret_cast<float*>(smem + p.stages * stage_bytes + BM * 128);
+  float* xch = table + 2 * kTabK * NT;
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xch) + ((C::XCH_BYTES + 15) & ~15));
+  uint64_t* empty = full + C::MAX_STAGES;
+  uint64_t* acc_full = empty + C::MAX_STAGES;
+  uint64_t* acc_empty = acc_full + kSkinnyBufs;
+  uint64_t* drain = acc_empty + kSkinnyBufs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int kblocks = p.kblocks;
+  const int R = p.rows, G = R / 2;
+  const int per_block = SWIGLU ? 64 / G : 1;  // SWIGLU tiles of one 128-row gate/up block
+  const int tiles = SWIGLU ? (p.N / 128) * per_block : (p.N + R - 1) / R;
+  const int act_warps = (R + 31) / 32;
+  const int ring = p.stages;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ring; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < kSkinnyBufs; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], act_warps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  if (warp == 4) {
+    // ---------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      const uint64_t wpol = policy_evict_first();  // each weight box is read once
+      auto load_w = [&](int s, int kb, int t) {
+        uint8_t* dst = smem + s * stage_bytes;
+        if constexpr (SWIGLU) {
+          const int n = (t / per_block) * 128 + (t % per_block) * G;
+          tma_load_2d_hint(dst, &tmB, &full[s], kb * BK, n, wpol);
+          tma_load_2d_hint(dst + G * 128, &tmB, &full[s], kb * BK, n + 64, wpol);
+        } else {
+          tma_load_2d_hint(dst, &tmB, &full[s], kb * BK, t * R, wpol);
+        }
+      };
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      uint32_t pending = 0, armed_parity = 0;
+      const int t0 = static_cast<int>(blockIdx.x);
+      int pre = 0;
+      if (t0 < tiles) {
+        pre = kblocks < ring ? kblocks : ring;
+        for (int i = 0; i < pre; ++i) {
+          mbar_arrive_expect_tx(&full[i], stage_bytes);
+          load_w(i, i, t0);
+        }
+      }
+      griddep_wait();
+      for (int t = t0; t < tiles && ok; t += gridDim.x) {
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!(t == t0 && kb < pre)) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            mbar_arrive_expect_tx(&full[stage], stage_bytes);
+            load_w(stage, kb, t);
+          }
+          pending |= 1u << stage;
+          tma_load_2d(smem + stage * stage_bytes + w_bytes, &tmA, &full[stage], kb * BK, 0);
+          if (++stage == ring) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok)
+        for (int s = 0; s < ring; ++s)
+          if (pending & (1u << s)) mbar_drain(&full[s], (armed_parity >> s) & 1u);
+    }
+    if (lane != 0) griddep_wait();
+  } else if (warp == 5) {
+    // ---------------------------------------------------------- MMA issuer
+    griddep_wait();
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = idesc_e4m3_f32(BM, NT);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(&acc_empty[buf], bphase ^ 1u, abort_flag, p.status) ||
+              !mbar_wait(&full[stage], phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w_addr = smem_u32(smem + stage * stage_bytes);
+          const uint32_t x_addr = w_addr + w_bytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_e4m3(tmem_base + buf * NT, smem_desc_sw128(w_addr + k * 32), smem_desc_sw128(x_addr + k * 32), kIdesc,
+                     k != 0);
+          mma_commit(&empty[stage]);
+          mma_commit(&acc_full[buf]);
+          if (++stage == ring) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == kSkinnyBufs) {
+            buf = 0;
+            bphase ^= 1u;
+          }
+        }
+      }
+      mma_commit(drain);
+      mbar_drain(drain, 0);
+    }
+  } else {
+    // ---------------------------------------------------------- promotion and epilogue
+    griddep_wait();
+    const bool active = warp < act_warps;
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    const int e = warp * 32 + lane;  // weight row within the tile
+    constexpr int PER = kTabK * NT / 128;  // table entries a thread fills
+    float pre_s[PER];
+    // token scales of K blocks kb0 .. kb0 + kTabK - 1, entry (i, j): block kb0 + i of token j
+    auto fetch = [&](int kb0) {
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int idx = x * 128 + static_cast<int>(threadIdx.x);
+        const int i = idx % kTabK, j = idx / kTabK;
+        pre_s[x] = kb0 + i < kblocks && j < p.M ? __ldg(p.sa + static_cast<size_t>(j) * kblocks + kb0 + i) : 0.f;
+      }
+    };
+    auto put = [&](int half) {
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int idx = x * 128 + static_cast<int>(threadIdx.x);
+        table[(half * kTabK + idx % kTabK) * NT + idx / kTabK] = pre_s[x];
+      }
+    };
+    int buf = 0;
+    uint32_t bphase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      int n;  // this thread's row of B
+      bool n_ok;
+      if constexpr (SWIGLU) {
+        n = (t / per_block) * 128 + (t % per_block) * G + (e < G ? e : 64 + e - G);
+        n_ok = e < R;
+      } else {
+        n = t * R + e;
+        n_ok = e < R && n < p.N;
+      }
+      const float* sbp = p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n_ok ? n : 0)) * kblocks;
+      uint64_t acc[NT / 2];
+#pragma unroll
+      for (int j = 0; j < NT / 2; ++j) acc[j] = 0;
+      float b_next = __ldg(sbp);
+      fetch(0);
+      named_barrier_sync(1, 128);  // the previous tile's table reads are done
+      put(0);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        const int i = kb % kTabK, half = (kb / kTabK) & 1;
+        if (i == 0) {
+          named_barrier_sync(1, 128);  // this half of the table is filled, the other one is read
+          if (kb + kTabK < kblocks) fetch(kb + kTabK);
+        }
+        if (i == kTabK - 1 && kb + 1 < kblocks) put(half ^ 1);
+        const float b = b_next;
+        if (kb + 1 < kblocks) b_next = __ldg(sbp + kb + 1);
+        if (active) {
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], bphase, abort_flag, p.status));
+          if (ok) {
+            tc_fence_after();
+            const uint64_t bb = pack_f32x2(__float_as_uint(b), __float_as_uint(b));
+            const ulonglong2* srow = reinterpret_cast<const ulonglong2*>(table + (half * kTabK + i) * NT);
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+              uint32_t r[16];
+              tmem_ld_32x32b_x16(t_lane + buf * NT + c * 16, r);
+              tmem_ld_wait();
+              if (c == NT / 16 - 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[buf]);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const ulonglong2 s = srow[c * 4 + j];
+                const int a = c * 8 + 2 * j;
+                acc[a] = fma_f32x2(pack_f32x2(r[4 * j], r[4 * j + 1]), mul_f32x2(s.x, bb), acc[a]);
+                acc[a + 1] = fma_f32x2(pack_f32x2(r[4 * j + 2], r[4 * j + 3]), mul_f32x2(s.y, bb), acc[a + 1]);
+              }
+            }
+          }
+        }
+        if (++buf == kSkinnyBufs) {
+          buf = 0;
+          bphase ^= 1u;
+        }
+      }
+      // ---- the tile's sums are complete: token j of output column n
+      if constexpr (SWIGLU) {
+        if (active && e >= G && e < R) {
+#pragma unroll
+          for (int j = 0; j < NT / 2; ++j) {
+            float u0, u1;
+            unpack_f32x2(acc[j], u0, u1);
+            xch[(e - G) * (NT + 1) + 2 * j] = u0;
+            xch[(e - G) * (NT + 1) + 2 * j + 1] = u1;
+          }
+        }
+        named_barrier_sync(1, 128);
+        if (active && ok && e < G) {
+          const int f = (t / per_block) * 64 + (t % per_block) * G + e;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + f;
+#pragma unroll
+          for (int j = 0; j < NT / 2; ++j) {
+            float g0, g1;
+            unpack_f32x2(acc[j], g0, g1);
+            if (2 * j < p.M)
+              dst[static_cast<size_t>(2 * j) * p.ldc] =
+                  __float2bfloat16_rn(__fmul_rn(silu(g0), xch[e * (NT + 1) + 2 * j]));
+            if (2 * j + 1 < p.M)
+              dst[static_cast<size_t>(2 * j + 1) * p.ldc] =
+                  __float2bfloat16_rn(__fmul_rn(silu(g1), xch[e * (NT + 1) + 2 * j + 1]));
+          }
+        }
+      } else if (active && ok && n_ok) {
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+          float v[2];
+          unpack_f32x2(acc[j], v[0], v[1]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int m = 2 * j + h;
+            if (m >= p.M) continue;
+            const size_t at = static_cast<size_t>(m) * p.ldc + n;
+            if constexpr (EPI == HB_EPI_F32) {
+              static_cast<float*>(p.C)[at] = v[h];
+            } else if constexpr (EPI == HB_EPI_RESIDUAL) {
+              const float r = __bfloat162float(static_cast<const __nv_bfloat16*>(p.R)[at]);
+              static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(__fadd_rn(r, v[h]));
+            } else {
+              static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v[h]);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+template <int BN, int EPI, bool PAIR>
+hb_status launch_wide(const DeviceCtx& ctx, const void* A, const void* B, const Params& p, cudaStream_t stream) {
+  using C = Cfg<BN, PAIR>;
+  CUtensorMap tmA, tmB, tmC, tmR;
+  hb_status st = encode_tmap_2d(&tmA, A, p.K, p.M, p.lda, BK, BM, true, 1);
+  if (st != HB_OK) return st;
+  st = encode_tmap_2d(&tmB, B, p.K, p.N, p.K, BK, PAIR ? BN / 2 : BN, true, 1);
+  if (st != HB_OK) return st;
+  constexpr int ESZ = EPI == HB_EPI_F32 ? 4 : 2;
+  st = encode_tmap_2d(&tmC, p.C, p.out_cols, p.M, static_cast<uint64_t>(p.ldc) * ESZ, 128 / ESZ, BM, true, ESZ);
+  if (st != HB_OK) return st;
+  if (EPI == HB_EPI_RESIDUAL) {
+    st = encode_tmap_2d(&tmR, p.R, p.out_cols, p.M, static_cast<uint64_t>(p.ldc) * 2, 64, BM, true, 2);
+    if (st != HB_OK) return st;
+  } else {
+    tmR = tmC;
+  }
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const int m_tiles = (p.M + BM - 1) / BM, n_tiles = (p.N + BN - 1) / BN;
+  if constexpr (PAIR) {
+    st = smem_limit_once(attr_set, ctx.device, block_gemm_pair_kernel<BN, EPI>, C::SMEM,
+                         "cudaFuncSetAttribute(block gemm pair)");
+    if (st != HB_OK) return st;
+    const int units = (m_tiles + 1) / 2 * n_tiles, pairs = ctx.num_sms / 2;
+    return launch_pdl(block_gemm_pair_kernel<BN, EPI>, 2 * (units < pairs ? units : pairs), kWideThreads, C::SMEM,
+                      stream, "block_gemm_pair_kernel launch", tmA, tmB, tmC, tmR, p);
+  } else {
+    st = smem_limit_once(attr_set, ctx.device, block_gemm_kernel<BN, EPI>, C::SMEM,
+                         "cudaFuncSetAttribute(block gemm)");
+    if (st != HB_OK) return st;
+    const int units = m_tiles * n_tiles;
+    return launch_pdl(block_gemm_kernel<BN, EPI>, units < ctx.num_sms ? units : ctx.num_sms, kWideThreads, C::SMEM,
+                      stream, "block_gemm_kernel launch", tmA, tmB, tmC, tmR, p);
+  }
+}
+
+template <int NT, int EPI>
+hb_status launch_skinny(const DeviceCtx& ctx, const void* A, const void* B, Params p, cudaStream_t stream) {
+  using C = CfgSkinny<NT>;
+  constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;
+  int tiles;
+  if (SWIGLU) {
+    // G gate and G up rows of one 128-row block: the largest G that still
+    // gives every SM a tile
+    int g = 64;
+    while (g > 8 && (p.N / 128) * (64 / g) < ctx.num_sms) g /= 2;
+    p.rows = 2 * g;
+    tiles = p.N / 128 * (64 / g);
+  } else {
+    // as few waves as 128-row tiles allow, their rows spread evenly
+    const int waves = (p.N + 128 * ctx.num_sms - 1) / (128 * ctx.num_sms);
+    const int even = (p.N + waves * ctx.num_sms - 1) / (waves * ctx.num_sms);
+    p.rows = (even + 7) / 8 * 8;
+    tiles = (p.N + p.rows - 1) / p.rows;
+  }
+  const int stage_bytes = (p.rows + NT) * 128;
+  const int avail = 232448 - C::FIXED;
+  p.stages = avail / stage_bytes < C::MAX_STAGES ? avail / stage_bytes : C::MAX_STAGES;
+  const int smem = C::FIXED + p.stages * stage_bytes;
+  CUtensorMap tmA, tmB;
+  hb_status st = encode_tmap_2d(&tmA, A, p.K, p.M, p.lda, BK, NT, true, 1);
+  if (st != HB_OK) return st;
+  st = encode_tmap_2d(&tmB, B, p.K, p.N, p.K, BK, SWIGLU ? p.rows / 2 : p.rows, true, 1);
+  if (st != HB_OK) return st;
+  static std::atomic<bool> attr_set[kMaxDevices];
+  st = smem_limit_once(attr_set, ctx.device, block_gemm_skinny_kernel<NT, EPI>, 232448,
+                       "cudaFuncSetAttribute(block gemm skinny)");
+  if (st != HB_OK) return st;
+  return launch_pdl(block_gemm_skinny_kernel<NT, EPI>, tiles < ctx.num_sms ? tiles : ctx.num_sms, kSkinnyThreads, smem,
+                    stream, "block_gemm_skinny_kernel launch", tmA, tmB, p);
+}
+
+template <int EPI>
+hb_status launch_epi(const DeviceCtx& ctx, const void* A, const void* B, const Params& p, cudaStream_t stream) {
+  if (p.M <= 16) return launch_skinny<16, EPI>(ctx, A, B, p, stream);
+  if (p.M <= 32) return launch_skinny<32, EPI>(ctx, A, B, p, stream);
+  if (p.M <= 64) return launch_skinny<64, EPI>(ctx, A, B, p, stream);
+  if (p.M <= BM) return launch_wide<128, EPI, false>(ctx, A, B, p, stream);
+  const int pm = (p.M + 2 * BM - 1) / (2 * BM), pairs = ctx.num_sms / 2;
+  auto waves = [&](int bn) { return (pm * ((p.N + bn - 1) / bn) + pairs - 1) / pairs; };
+  if (waves(128) * 128 < waves(256) * 256) return launch_wide<128, EPI, true>(ctx, A, B, p, stream);
+  return launch_wide<256, EPI, true>(ctx, A, B, p, stream);
+}
+
+}  // namespace
+
+hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B,
+                                 const float* sb, void* C, int ldc, const void* R, int M, int N, int K, int epi,
+                                 cudaStream_t stream) {
+  Params p = {};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.lda = lda;
+  p.C = C;
+  p.R = R;
+  p.ldc = ldc;
+  p.out_cols = epi == HB_EPI_SWIGLU ? N / 2 : N;
+  p.sa = sa;
+  p.sb = sb;
+  p.f_blocks = (N / 2 + 127) / 128;
+  p.kblocks = (K + BK - 1) / BK;
+  p.status = ctx.status;
+  switch (epi) {
+    case HB_EPI_STORE: return launch_epi<HB_EPI_STORE>(ctx, A, B, p, stream);
+    case HB_EPI_RESIDUAL: return launch_epi<HB_EPI_RESIDUAL>(ctx, A, B, p, stream);
+    case HB_EPI_SWIGLU: return launch_epi<HB_EPI_SWIGLU>(ctx, A, B, p, stream);
+    default: return launch_epi<HB_EPI_F32>(ctx, A, B, p, stream);
+  }
+}
+
+}  // namespace hb
+
+extern "C" hb_status hb_gemm_e4m3_block(const void* A, const float* s_a, const void* B, const float* s_b, void* C,
+                                        const void* R, int32_t M, int32_t N, int32_t K, int32_t epilogue,
+                                        void* stream) {
+  hb::clear_error();
+  HB_REQUIRE(A && s_a && B && s_b && C, "hb_gemm_e4m3_block: null operand");
+  HB_REQUIRE(M >= 1 && N >= 8 && K >= 16, "hb_gemm_e4m3_block: bad shape M=%d N=%d K=%d", M, N, K);
+  HB_REQUIRE(K % 16 == 0 && N % 8 == 0, "hb_gemm_e4m3_block: K %% 16 and N %% 8 required (K=%d N=%d)", K, N);
+  HB_REQUIRE(epilogue >= HB_EPI_STORE && epilogue <= HB_EPI_F32, "hb_gemm_e4m3_block: unknown epilogue %d", epilogue);
+  HB_REQUIRE(epilogue != HB_EPI_SWIGLU || N % 128 == 0, "hb_gemm_e4m3_block: SWIGLU needs N %% 128 == 0");
+  HB_REQUIRE(epilogue != HB_EPI_RESIDUAL || R != nullptr, "hb_gemm_e4m3_block: RESIDUAL needs R");
+  HB_REQUIRE(hb::aligned16(A) && hb::aligned16(B) && hb::aligned16(C) && (R == nullptr || hb::aligned16(R)),
+             "hb_gemm_e4m3_block: operands must be 16-byte aligned");
+  HB_REQUIRE(hb::aligned4(s_a) && hb::aligned4(s_b), "hb_gemm_e4m3_block: scales must be 4-byte aligned");
+  hb::DeviceCtx ctx;
+  hb_status st = hb::device_context(&ctx);
+  if (st != HB_OK) return st;
+  const int ldc = epilogue == HB_EPI_SWIGLU ? N / 2 : N;
+  return hb::gemm_e4m3_block_launch(ctx, A, K, s_a, B, s_b, C, ldc, R, M, N, K, epilogue,
+                                    static_cast<cudaStream_t>(stream));
+}

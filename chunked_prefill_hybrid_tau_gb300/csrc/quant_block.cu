@@ -1,0 +1,184 @@
+// Block-scaled E4M3 quantization of bf16 matrices: the operand preparation
+// of the projections with one scale per 128 columns of a token row and per
+// 128 x 128 block of a weight (gemm_e4m3_block.cu).
+//
+// Per group (1 x 128 or 128 x 128 elements, smaller at the edges):
+//   amax = max |x|,  top = max(amax, 2^-112),
+//   inv = 448 / top,  scale = top / 448  (correctly rounded fp32 divisions),
+//   code = E4M3(fp32(x * inv)), nearest even, saturating;
+// a group of zeros gets scale 0 and zero codes.  The floor 2^-112 keeps inv
+// (2^120.8) and scale (2^-120.8) normal fp32 numbers: without it 448 / amax
+// is infinite for amax below 2^-119.2 and a zero beside such a value becomes
+// 0 * inf = NaN.  A NaN or an infinity makes the codes of its own group NaN
+// where it stands (an infinity: in the whole group) and leaves other groups
+// alone.
+//
+// Both kernels read 2 bytes and write 1 byte an element once, so HBM bounds
+// them.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "device.cuh"
+#include "runtime.h"
+
+namespace hb {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 256;
+constexpr float kAmaxMin = 0x1p-112f;
+constexpr int kMaxRows = 65535 * 128;  // grid limit of the block kernel
+constexpr int kMaxCols = 1 << 24;
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float inv) {
+  const __nv_fp8x2_storage_t v =
+      __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)), __NV_SATFINITE, __NV_E4M3);
+  return static_cast<uint32_t>(v);
+}
+
+__device__ __forceinline__ float amax8(const uint4& v, float m) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack_bf16x2(w[j]);
+    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = unpack_bf16x2(w[j]);
+    b[j] = e4m3x2(f.x, f.y, inv);
+  }
+  return make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+}
+
+struct GroupScale {
+  float inv, scale;
+};
+__device__ __forceinline__ GroupScale group_scale(float amax) {
+  const float top = fmaxf(amax, kAmaxMin);
+  const bool nz = amax > 0.f;
+  return {nz ? __fdiv_rn(448.0f, top) : 0.f, nz ? __fdiv_rn(top, 448.0f) : 0.f};
+}
+
+// Tokens: 16 lanes own one group (16 bytes of bf16 each), so the group's
+// maximum is four shuffles and no group meets another.  A CTA's 16 half
+// warps cover 2^gshift groups of 16 >> gshift rows; each takes U groups,
+// 2^gshift apart, with all loads in flight.
+template <int U>
+__global__ void __launch_bounds__(kThreads)
+    quant_groups_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int rows,
+                        int c8, int kb, int gshift) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const int row = blockIdx.x * (16 >> gshift) + (sub >> gshift);
+  const int g0 = (blockIdx.y * U << gshift) + (sub & ((1 << gshift) - 1));
+  const bool row_ok = row < rows;
+  const size_t base = static_cast<size_t>(row) * c8;
+  uint4 v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = (g0 + (u << gshift)) * 16 + l;
+    v[u] = row_ok && i < c8 ? x[base + i] : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float m = amax8(v[u], 0.f);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const GroupScale gs = group_scale(m);
+    const int g = g0 + (u << gshift);
+    const int i = g * 16 + l;
+    if (row_ok && i < c8) q[base + i] = codes8(v[u], gs.inv);
+    if (row_ok && g < kb && l == 0) scale[static_cast<size_t>(row) * kb + g] = gs.scale;
+  }
+}
+
+// Weights: one CTA per 128 x 128 block, held in registers (8 pieces of 16
+// bytes a thread) between its maximum and its codes.  The launch signals no
+// dependent early: a projection may read its weights before it waits for the
+// kernel ahead of it.
+__global__ void __launch_bounds__(kThreads)
+    quant_blocks_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int rows,
+                        int c8, int kb) {
+  griddep_wait();
+  __shared__ float red[kThreads / 32];
+  const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  const int i = blockIdx.x * 16 + l;
+  const int row0 = blockIdx.y * 128 + r0;
+  uint4 v[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int r = row0 + 16 * u;
+    v[u] = r < rows && i < c8 ? x[static_cast<size_t>(r) * c8 + i] : make_uint4(0, 0, 0, 0);
+  }
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) m = amax8(v[u], m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, red[w]);
+  const GroupScale gs = group_scale(m);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int r = row0 + 16 * u;
+    if (r < rows && i < c8) q[static_cast<size_t>(r) * c8 + i] = codes8(v[u], gs.inv);
+  }
+  if (threadIdx.x == 0) scale[static_cast<size_t>(blockIdx.y) * kb + blockIdx.x] = gs.scale;
+}
+
+}  // namespace
+
+hb_status quant_block_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int cols,
+                             int block_rows, cudaStream_t stream) {
+  (void)ctx;
+  const int c8 = cols / 8, kb = (cols + 127) / 128;
+  auto* xp = static_cast<const uint4*>(x);
+  auto* qp = static_cast<uint2*>(q);
+  if (block_rows == 128)
+    return launch_pdl(quant_blocks_kernel, dim3(kb, (rows + 127) / 128), kThreads, 0, stream,
+                      "quant_blocks_kernel launch", xp, qp, scale, rows, c8, kb);
+  int gshift = 0;
+  while (gshift < 4 && (1 << gshift) < kb) ++gshift;
+  const int rpc = 16 >> gshift;
+  const int passes = (kb + (1 << gshift) - 1) >> gshift;
+  const int gx = (rows + rpc - 1) / rpc;
+#define HB_QG(U_)                                                                                              \
+  return launch_pdl(quant_groups_kernel<U_>, dim3(gx, (passes + U_ - 1) / U_), kThreads, 0, stream,             \
+                    "quant_groups_kernel launch", xp, qp, scale, rows, c8, kb, gshift)
+  if (passes >= 4) HB_QG(4);
+  if (passes >= 2) HB_QG(2);
+  HB_QG(1);
+#undef HB_QG
+}
+
+}  // namespace hb
+
+extern "C" hb_status hb_quantize_e4m3_block(const void* x, void* q, float* scale, int32_t rows, int32_t cols,
+                                            int32_t block_rows, void* stream) {
+  hb::clear_error();
+  HB_REQUIRE(rows == 0 || (x && q && scale), "hb_quantize_e4m3_block: null pointer");
+  HB_REQUIRE(rows >= 0 && cols > 0 && cols % 16 == 0,
+             "hb_quantize_e4m3_block: rows >= 0 and cols %% 16 == 0 required");
+  HB_REQUIRE(block_rows == 1 || block_rows == 128, "hb_quantize_e4m3_block: block_rows must be 1 or 128, not %d",
+             block_rows);
+  HB_REQUIRE(cols <= hb::kMaxCols && rows <= hb::kMaxRows,
+             "hb_quantize_e4m3_block: at most %d rows and %d columns", hb::kMaxRows, hb::kMaxCols);
+  HB_REQUIRE(hb::aligned16(x) && hb::aligned16(q) && hb::aligned4(scale),
+             "hb_quantize_e4m3_block: 16-byte alignment (scale: 4)");
+  if (rows == 0) return HB_OK;
+  hb::DeviceCtx ctx;
+  hb_status st = hb::device_context(&ctx);
+  if (st != HB_OK) return st;
+  return hb::quant_block_launch(ctx, x, q, scale, rows, cols, block_rows, static_cast<cudaStream_t>(stream));
+}

@@ -35,6 +35,7 @@ hb_status encode_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner, uin
                          int elem_bytes = 2);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Raises a kernel's dynamic shared-memory limit once per device.  `done` is
 // that kernel's per-device flag array (kMaxDevices entries, static storage).
@@ -96,6 +97,12 @@ hb_status rmsnorm_launch(const DeviceCtx& ctx, const void* x, const int* rows, c
 hb_status kv_append_launch(const DeviceCtx& ctx, const void* qkv, int T, const int* row_pos, const int* slots,
                            const void* rope, int max_pos, const hb_layer_dims& dims, void* q_out, void* k_cache,
                            void* v_cache, int num_pages, cudaStream_t stream, int* zero = nullptr, int n_zero = 0);
+// kv_append_launch with every q and k head RMS-normed (gains g_q, g_k
+// [d_head] bf16, dims.rms_eps) before the rotation.
+hb_status kv_append_norm_launch(const DeviceCtx& ctx, const void* qkv, int T, const int* row_pos, const int* slots,
+                                const void* rope, int max_pos, const hb_layer_dims& dims, const void* g_q,
+                                const void* g_k, void* q_out, void* k_cache, void* v_cache, int num_pages,
+                                cudaStream_t stream, int* zero = nullptr, int n_zero = 0);
 hb_status gemm_check(const void* A, const void* B, void* C, const void* R, int M, int N, int K, int epi);
 
 // RMSNorm folded into the projections.  Row statistics are 32-column partial
@@ -164,6 +171,17 @@ hb_status gemm_e4m3_check(const void* A, const float* sa, const void* B, const f
 // at `zero` cleared (as row_sumsq_launch).
 hb_status quant_rows_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int cols,
                             float* ss, int* zero, int n_zero, cudaStream_t stream);
+
+// Block-scaled E4M3 quantization of bf16 x [rows][cols]: codes q, scales
+// [ceil(rows / block_rows)][ceil(cols / 128)]; block_rows 1 or 128.
+hb_status quant_block_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int cols,
+                             int block_rows, cudaStream_t stream);
+
+// Block-scaled E4M3 projection (hb_gemm_e4m3_block); A has row stride lda
+// bytes, C and R row stride ldc elements.
+hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B,
+                                 const float* sb, void* C, int ldc, const void* R, int M, int N, int K, int epi,
+                                 cudaStream_t stream);
 
 // A [M][K] with row stride lda, B [N][K], C/R with row stride ldc (elements).
 hb_status gemm_launch(const DeviceCtx& ctx, const void* A, int lda, const void* B, void* C, int ldc, const void* R,

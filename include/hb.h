@@ -253,6 +253,22 @@ hb_status hb_kv_append(const void* qkv, int32_t T, const int32_t* row_pos, const
                        void* k_cache, void* v_cache, int32_t num_pages, void* stream);
 
 /* ------------------------------------------------------------------------
+ * hb_kv_append_norm - hb_kv_append with every query and key head RMS-normed
+ * before the rotation (models that norm q and k per head; the pages name no
+ * such model: an addition beside the plain append).  Per q or k head vector
+ * x of a row:
+ *   y = x / sqrt(mean(x^2) + dims->rms_eps) * g   (g_q or g_k)
+ * then the rotation of y, all in fp32, rounded once to bf16; V is copied.
+ *   g_q, g_k : device bf16 [d_head], shared by the heads; 16-byte aligned
+ * Everything else as hb_kv_append.  A row's results do not depend on the
+ * other rows of the call.
+ * ---------------------------------------------------------------------- */
+hb_status hb_kv_append_norm(const void* qkv, int32_t T, const int32_t* row_pos, const int32_t* slot_mapping,
+                            const void* rope, int32_t max_pos, const hb_layer_dims* dims, const void* g_q,
+                            const void* g_k, void* q_out, void* k_cache, void* v_cache, int32_t num_pages,
+                            void* stream);
+
+/* ------------------------------------------------------------------------
  * hb_attention - varlen paged hybrid attention.  Row r of sequence s at
  * position p attends to keys 0..p of s, read through its block table: a
  * chunk row sees the request's cached prefix plus the causal part of its own
@@ -349,6 +365,46 @@ hb_status hb_quantize_e4m3(const void* x, void* q, float* scale, int32_t rows, i
  * ---------------------------------------------------------------------- */
 hb_status hb_gemm_e4m3(const void* A, const float* s_a, const void* B, const float* s_b, void* C, const void* R,
                        int32_t M, int32_t N, int32_t K, int32_t epilogue, void* stream);
+
+/* ------------------------------------------------------------------------
+ * hb_quantize_e4m3_block - block-scaled FP8 quantization, the operand
+ * preparation of hb_gemm_e4m3_block: one fp32 scale per 128 columns of a row
+ * (block_rows 1: tokens) or per 128 x 128 block (block_rows 128: weights)
+ * instead of one per whole row (hb_quantize_e4m3), so that an outlier costs
+ * its own block the resolution and not the row.  Per block of x [rows][cols]
+ * (device bf16; the last blocks may be smaller):
+ *   amax = max |x|, top = max(amax, 2^-112), inv = 448 / top,
+ *   scale = top / 448 (correctly rounded fp32 divisions),
+ *   q = E4M3(fp32(x * inv)), nearest-even, saturating to +-448;
+ * an all-zero block gets scale 0 and zero codes.  The floor 2^-112 keeps inv
+ * and scale finite and normal.  A NaN or infinity spoils its own block only.
+ * q: device bytes [rows][cols]; scale: device fp32
+ * [ceil(rows / block_rows)][ceil(cols / 128)].  cols % 16 == 0, cols <=
+ * 2^24, rows <= 8388480; x and q 16-byte aligned.  Asynchronous on stream.
+ * ---------------------------------------------------------------------- */
+hb_status hb_quantize_e4m3_block(const void* x, void* q, float* scale, int32_t rows, int32_t cols,
+                                 int32_t block_rows, void* stream);
+
+/* ------------------------------------------------------------------------
+ * hb_gemm_e4m3_block - C = epilogue(P) with block-scaled E4M3 operands:
+ *   P[m][n] = sum_b s_a[m][b] s_b[n / 128][b] sum_{k in block b} A[m][k] B[n][k]
+ * A [M][K] and B [N][K] codes, K in blocks of 128 (the last one may be
+ * smaller); s_a fp32 [M][ceil(K / 128)] (hb_quantize_e4m3_block of the
+ * tokens, block_rows 1), s_b fp32 [ceil(N / 128)][ceil(K / 128)] (of the
+ * weights, block_rows 128).  Each block's products are summed on the tensor
+ * cores (kind::f8f6f4) and added, scaled, in fp32, block by block in K
+ * order, whatever M is: a token's result does not depend on the batch.
+ * The epilogues are hb_gemm's.  SWIGLU: B's rows interleave gate and up in
+ * blocks of 64 (N / 2 rows of each, as hb_interleave_gate_up lays them out),
+ * and s_b holds the block scales of the gate [ceil(N / 256)][ceil(K / 128)]
+ * followed by those of the up matrix, each quantized on its own.
+ * K % 16 == 0, N % 8 == 0 (N % 128 for SWIGLU); A, B, C and R 16-byte
+ * aligned.  B must be complete before the kernel ahead of this call on the
+ * stream starts, unless that kernel is hb_quantize_e4m3_block with
+ * block_rows 128 or not one of this library's.
+ * ---------------------------------------------------------------------- */
+hb_status hb_gemm_e4m3_block(const void* A, const float* s_a, const void* B, const float* s_b, void* C,
+                             const void* R, int32_t M, int32_t N, int32_t K, int32_t epilogue, void* stream);
 
 /* Weight preparation: w_gu[2 Fp][d], Fp = F rounded up to a multiple of 64,
  * from w_gate[F][d] and w_up[F][d] (device bf16): rows interleaved in blocks

@@ -122,6 +122,51 @@ def gemm(qa, sa, qb, sb):
     return acc * np.asarray(sa, np.float64)[:, None] * np.asarray(sb, np.float64)[None, :]
 
 
+# ---------------------------------------------------------------- block scales
+# One fp32 scale per 128 columns of a row (tokens, block_rows 1) or per 128 x
+# 128 block (weights, block_rows 128).  The group maximum that a scale is
+# formed from is at least 2^-112, so that 448 / amax stays finite.
+BLOCK = 128
+AMAX_MIN = np.float32(2.0 ** -112)
+
+
+def _groups(x, block_rows):
+    """x [rows][cols] -> zero-padded [row groups][block_rows][col groups][128]."""
+    rows, cols = x.shape
+    rg, cg = -(-rows // block_rows), -(-cols // BLOCK)
+    full = np.zeros((rg * block_rows, cg * BLOCK), x.dtype)
+    full[:rows, :cols] = x
+    return full.reshape(rg, block_rows, cg, BLOCK)
+
+
+def spread_scales(scale, rows, cols, block_rows):
+    """The scale of each element (float64 [rows][cols])."""
+    s = np.repeat(np.repeat(np.asarray(scale, np.float64), block_rows, axis=0), BLOCK, axis=1)
+    return s[:rows, :cols]
+
+
+def quantize_blocks(x, block_rows):
+    """-> (codes uint8 [rows][cols], scale float32 [row groups][col groups])."""
+    x = np.asarray(x, np.float32)
+    rows, cols = x.shape
+    amax = np.abs(_groups(x, block_rows)).max(axis=(1, 3))
+    top = np.maximum(amax, AMAX_MIN)
+    inv = np.where(amax > 0, np.float32(E4M3_MAX) / top, np.float32(0)).astype(np.float32)
+    scale = np.where(amax > 0, top / np.float32(E4M3_MAX), np.float32(0)).astype(np.float32)
+    each = spread_scales(inv, rows, cols, block_rows).astype(np.float32)
+    return e4m3_encode((x * each).astype(np.float32)), scale
+
+
+def dequantize_blocks(codes, scale, block_rows):
+    rows, cols = codes.shape
+    return e4m3_decode(codes) * spread_scales(scale, rows, cols, block_rows)
+
+
+def gemm_blocks(qa, sa, qb, sb):
+    """C[m][n] = sum_b sa[m][b] sb[n // 128][b] (sum of code products in block b), float64."""
+    return dequantize_blocks(qa, sa, 1) @ dequantize_blocks(qb, sb, BLOCK).T
+
+
 def prepare_weights(w):
     """The prepared bf16 weights (gains folded, rounded once to bf16), then
     per-row codes and scales: dict name -> (codes, scale) for qkv, o, g, u, d."""

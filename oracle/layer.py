@@ -71,6 +71,11 @@ def rope(x, pos, cos, sin, dtype=np.float32):
     return np.concatenate([x1 * c - x2 * s, x2 * c + x1 * s], axis=-1)
 
 
+def head_norm(x, g, eps, dtype=np.float32):
+    """RMS norm of every head vector: x [rows, heads, d_head], gain g [d_head]."""
+    return rmsnorm(x, g, eps, dtype)
+
+
 def silu(x):
     return x / (1 + np.exp(-x))
 
