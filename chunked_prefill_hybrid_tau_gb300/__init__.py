@@ -6,7 +6,7 @@ token budget tau and runs a decoder-layer forward over the packed rows with a
 (include/hb.h, CUDA kernels in csrc/); this package holds its build script
 and a thin ctypes binding whose functions carry the C names.
 """
-from .binding (DevicePlan, HBError, HostPlan, LayerWeights, Scheduler, dims_struct, hb_attention,
+from .binding import (DevicePlan, HBError, HostPlan, LayerWeights, Scheduler, dims_struct, hb_attention,
                       hb_attention_workspace_bytes, hb_check_status, hb_device_info, hb_final_logits, hb_fold_gamma,
                       hb_gemm, hb_gemm_e4m3, hb_gemm_e4m3_block, hb_interleave_gate_up, hb_kernel_launches,
                       hb_kv_append, hb_kv_append_norm, hb_layer_forward, hb_layer_kernel_count,
