@@ -46,29 +46,6 @@ struct Params {
 // silu(g) = g / (1 + e^-g), the arithmetic of the per-row scaled projections.
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, __fadd_rn(1.0f, __expf(-g))); }
 
-__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-// Two fp32 FMAs / products, each rounded as the scalar ones.
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Byte offset of 16-byte chunk c (0..7) of row r in a slab of 128 rows x 128
 // bytes with the 128-byte swizzle (the TMA box layout).
 __device__ __forceinline__ uint32_t slab_off(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
@@ -98,6 +75,7 @@ __device__ __forceinline__ int scale_row(const Params& p, int n) {
 //   warp 9    : MMA issuer; one K block per TMEM buffer, NBUF buffers.
 // The sums leave through shared memory staged apart from the ring and TMA
 // stores, so the next tile's loads and MMAs go on meanwhile.
+constexpr int kTabK = 8;  // K blocks per fill of the scale table
 template <int BN, bool PAIR>
 struct Cfg {
   static constexpr int A_BYTES = BM * 128;
@@ -105,15 +83,20 @@ struct Cfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int NBUF = 512 / BN;  // TMEM accumulator buffers
   static constexpr int STAGING = BM * BN * 2;
-  static constexpr int AVAIL = 232448 - 1024 - 512 - STAGING;
+  static constexpr int TABLE = kTabK * (BM + 4) * 4;  // one buffer: scales of the rows, then of up to 4 weight blocks
+  static constexpr int AVAIL = 232448 - 1024 - 512 - STAGING - 2 * TABLE;
   static constexpr int STAGES = AVAIL / STAGE_BYTES < 8 ? AVAIL / STAGE_BYTES : 8;
-  static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 512 + 1024;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 2 * TABLE + 512 + 1024;
   static constexpr int CH = BN / 64;  // 32-column chunks of a thread
   static_assert(BN == 128 || BN == 256, "BN");
-  static_assert(STAGE_BYTES % 1024 == 0 && STAGING % 1024 == 0, "alignment");
+  static_assert(STAGE_BYTES % 1024 == 0 && STAGING % 1024 == 0 && TABLE % 16 == 0, "alignment");
   static_assert(STAGES >= 3, "ring depth");
 };
-constexpr int kWideThreads = 320;
+// Three warpgroups of 168 registers a thread at launch; the promotion warps
+// take 216 (their sums are 128), the third warpgroup keeps 72:
+// 256 * 216 + 128 * 72 = 384 * 168.
+constexpr int kWideThreads = 384;
+constexpr int kPromoteRegs = 216, kIssueRegs = 72;
 
 template <int BN, int EPI, bool PAIR>
 __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
@@ -124,11 +107,14 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + C::STAGES * C::STAGE_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::STAGING);  // PAIR: the even CTA's are used
+  float* table = reinterpret_cast<float*>(staging + C::STAGING);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::STAGING + 2 * C::TABLE);  // PAIR: the even CTA's are used
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
   uint64_t* acc_empty = acc_full + C::NBUF;  // PAIR: the even CTA's are used
-  uint64_t* drain = acc_empty + C::NBUF;
+  uint64_t* tab_full = acc_empty + C::NBUF;
+  uint64_t* tab_empty = tab_full + 2;
+  uint64_t* drain = tab_empty + 2;
   uint64_t* res_bar = drain + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -154,6 +140,10 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], PAIR ? 16 : 8);
     }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tab_full[b], 64);
+      mbar_init(&tab_empty[b], 8);
+    }
     mbar_init(drain, 1);
     mbar_init(res_bar, 1);
     *abort_flag = 0;
@@ -178,6 +168,10 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
+  // (each setmaxnreg inside its role's own branch: the compiler allocates for
+  // the smaller count where the two could meet)
+  if (warp >= 8) {
+    regs_dec<kIssueRegs>();
   if (warp == 8) {
     // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
@@ -303,7 +297,52 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       mbar_drain(drain, 0);
     }
   } else {
+    // ---------------------------------------------------------- scale table (two warps)
+    // Scales of the tile's rows and weight blocks, kTabK K blocks at a time,
+    // two fills ahead of the sums.  (Read by the promotion warps themselves,
+    // each row of sa is a cache line of its own: 128 lines and the few spills
+    // outgrew the L1 left beside the ring, and a K block took three times as
+    // long.)
+    griddep_wait();
+    const int t64 = static_cast<int>(threadIdx.x) - 320;
+    int fill = 0;
+    bool ok = true;
+    for (int u = first; u < units; u += stride) {
+      const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
+      const int n0 = (u / um) * BN;
+      const int ra = mt * BM + t64, rb = ra + 64;
+      const float* pa = p.sa + static_cast<size_t>(ra < p.M ? ra : 0) * kblocks;
+      const float* pb = p.sa + static_cast<size_t>(rb < p.M ? rb : 0) * kblocks;
+      // weight block j: column half j / 2's gate (or only) block, and its up block
+      const int j = t64 & 3;
+      const int n = n0 + (j >> 1) * (BN == 256 ? 128 : SWIGLU ? 0 : 64) + (SWIGLU ? (j & 1) * 64 : 0);
+      const float* ps =
+          p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n < p.N ? n : p.N - 1)) * kblocks + (t64 >> 2);
+      for (int kb0 = 0; kb0 < kblocks; kb0 += kTabK, ++fill) {
+        float va[kTabK], vb[kTabK];
+#pragma unroll
+        for (int i = 0; i < kTabK; ++i) {
+          const bool in = kb0 + i < kblocks;
+          va[i] = in && ra < p.M ? __ldg(pa + kb0 + i) : 0.f;
+          vb[i] = in && rb < p.M ? __ldg(pb + kb0 + i) : 0.f;
+        }
+        const float vs = t64 < 4 * kTabK && kb0 + (t64 >> 2) < kblocks ? __ldg(ps + kb0) : 0.f;
+        const int b = fill & 1;
+        if (ok) ok = mbar_wait(&tab_empty[b], ((fill >> 1) & 1) ^ 1u, abort_flag, p.status);
+        float* tab = table + b * (C::TABLE / 4);
+#pragma unroll
+        for (int i = 0; i < kTabK; ++i) {
+          tab[i * BM + t64] = va[i];
+          tab[i * BM + t64 + 64] = vb[i];
+        }
+        if (t64 < 4 * kTabK) tab[kTabK * BM + t64] = vs;
+        mbar_arrive(&tab_full[b]);
+      }
+    }
+  }
+  } else {
     // ---------------------------------------------------------- promotion and epilogue
+    regs_inc<kPromoteRegs>();
     griddep_wait();
     const int quarter = warp & 3, half = warp >> 2;
     const bool boss = threadIdx.x == 0;
@@ -316,46 +355,42 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       return half * (BN / 2) + c * 32;
     };
     int buf = 0;
+    int fill = 0;
     uint32_t bphase = 0, rphase = 0;
     bool ok = true;
     bool res_pending = false;  // boss: residual copies in flight
     for (int u = first; u < units; u += stride) {
       const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
       const int n0 = (u / um) * BN;
-      const int row = mt * BM + rloc;
-      const bool row_ok = row < p.M;
       const bool live = mt < m_tiles;  // a pair's odd row tile may lie past M
-      const float* sap = p.sa + static_cast<size_t>(row_ok ? row : 0) * kblocks;
-      // the scale rows of this half's first and second chunk group (columns
-      // past N read the last row: their sums are not stored)
-      auto sb_row = [&](int c) {
-        const int n = n0 + chunk_col(c);
-        return p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n < p.N ? n : p.N - 1)) * kblocks;
-      };
-      const float* sb0 = sb_row(0);
-      const float* sb1 = sb_row(CH / 2);
-      uint64_t acc[CH][16];
+      float acc[CH][32];
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[c][j] = 0;
-      float a_next = row_ok ? __ldg(sap) : 0.f;
-      float b0_next = __ldg(sb0), b1_next = __ldg(sb1);
+        for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
+#pragma unroll 1
       for (int kb = 0; kb < kblocks; ++kb) {
-        const float f0 = __fmul_rn(a_next, b0_next), f1 = __fmul_rn(a_next, b1_next);
-        if (kb + 1 < kblocks) {
-          a_next = row_ok ? __ldg(sap + kb + 1) : 0.f;
-          b0_next = __ldg(sb0 + kb + 1);
-          b1_next = __ldg(sb1 + kb + 1);
+        const int ti = kb % kTabK, tb = fill & 1;
+        if (ti == 0 && ok)
+          ok = __all_sync(0xffffffffu, mbar_wait(&tab_full[tb], (fill >> 1) & 1, abort_flag, p.status));
+        const float* tab = table + tb * (C::TABLE / 4);
+        const float sa = tab[ti * BM + rloc];
+        const float2 sb = *reinterpret_cast<const float2*>(tab + kTabK * BM + ti * 4 + half * 2);
+        const float f0 = __fmul_rn(sa, sb.x), f1 = SWIGLU ? __fmul_rn(sa, sb.y) : f0;
+        if (ti == kTabK - 1 || kb == kblocks - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tab_empty[tb]);
+          ++fill;
         }
         if constexpr (EPI == HB_EPI_RESIDUAL) {
           // the residual tile into the staging slabs, once the previous
           // tile's stores have left them (by now long done)
-          if (boss && live && ok && kb == (kblocks > 2 ? 2 : 0)) {
+          if (boss && live && ok && kb == (kblocks > 4 ? 4 : 0)) {
             bulk_wait_group_read<0>();
             int slabs = (p.N - n0 + 63) / 64;
             if (slabs > BN / 64) slabs = BN / 64;
             mbar_arrive_expect_tx(res_bar, slabs * kSlabBytes);
+#pragma unroll 1
             for (int s = 0; s < slabs; ++s)
               tma_load_2d(staging + s * kSlabBytes, &tmR, res_bar, n0 + s * 64, mt * BM);
             res_pending = true;
@@ -364,8 +399,6 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], bphase, abort_flag, p.status));
         if (ok) {
           tc_fence_after();
-          const uint64_t s0 = pack_f32x2(__float_as_uint(f0), __float_as_uint(f0));
-          const uint64_t s1 = pack_f32x2(__float_as_uint(f1), __float_as_uint(f1));
 #pragma unroll
           for (int c = 0; c < CH; ++c) {
             uint32_t r[32];
@@ -381,9 +414,12 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
                   mbar_arrive(&acc_empty[buf]);
               }
             }
-            const uint64_t s = c < CH / 2 ? s0 : s1;
+            // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
+            // the 32-register TMEM load does not give without moves (620
+            // against 370 clocks per 256-column block, measured)
+            const float f = c < CH / 2 ? f0 : f1;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[c][j] = fma_f32x2(pack_f32x2(r[2 * j], r[2 * j + 1]), s, acc[c][j]);
+            for (int j = 0; j < 32; ++j) acc[c][j] = __fmaf_rn(__uint_as_float(r[j]), f, acc[c][j]);
           }
         }
         if (++buf == C::NBUF) {
@@ -416,8 +452,8 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             uint8_t* slab = staging + (half * PER + i) * kSlabBytes;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const uint64_t lo = acc[rd * PER + i][2 * q], hi = acc[rd * PER + i][2 * q + 1];
-              *reinterpret_cast<ulonglong2*>(slab + slab_off(rloc, q)) = make_ulonglong2(lo, hi);
+              const float* v = &acc[rd * PER + i][4 * q];
+              *reinterpret_cast<float4*>(slab + slab_off(rloc, q)) = make_float4(v[0], v[1], v[2], v[3]);
             }
           }
           fence_proxy_async_smem();
@@ -445,10 +481,9 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
               uint32_t w[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                float g0, g1, u0, u1;
-                unpack_f32x2(acc[i][4 * q + j], g0, g1);
-                unpack_f32x2(acc[G + i][4 * q + j], u0, u1);
-                w[j] = pack_bf16x2(__fmul_rn(silu(g0), u0), __fmul_rn(silu(g1), u1));
+                const int e = 8 * q + 2 * j;
+                w[j] = pack_bf16x2(__fmul_rn(silu(acc[i][e]), acc[G + i][e]),
+                                   __fmul_rn(silu(acc[i][e + 1]), acc[G + i][e + 1]));
               }
               *reinterpret_cast<uint4*>(slab + slab_off(rloc, c0 + q)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -468,18 +503,12 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
                 const uint32_t rr[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  float v0, v1;
-                  unpack_f32x2(acc[c][4 * q + j], v0, v1);
                   const float2 f = unpack_bf16x2(rr[j]);
-                  w[j] = pack_bf16x2(__fadd_rn(f.x, v0), __fadd_rn(f.y, v1));
+                  w[j] = pack_bf16x2(__fadd_rn(f.x, acc[c][8 * q + 2 * j]), __fadd_rn(f.y, acc[c][8 * q + 2 * j + 1]));
                 }
               } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  float v0, v1;
-                  unpack_f32x2(acc[c][4 * q + j], v0, v1);
-                  w[j] = pack_bf16x2(v0, v1);
-                }
+                for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[c][8 * q + 2 * j], acc[c][8 * q + 2 * j + 1]);
               }
               *dst = make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -532,22 +561,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 // is p.rows weight rows (TMEM lanes) x NT tokens (columns), and the rows per
 // tile are chosen so that the tiles fill the SMs.  The MMA always has M =
 // 128: lanes past p.rows multiply whatever follows in shared memory and are
-// not read.
+// not read.  K blocks go through the ring in pairs and through TMEM in
+// groups of four, so that the waits and commits of one block are a quarter
+// of what they would be alone: a single warp adds the blocks of a 32-row
+// tile, and its instructions, not the loads, set the pace.
 //   warps 0-3: promotion and epilogue (those with lanes below p.rows; all
-//              four fill the table of token scales);
+//              four fill the table of scale products);
 //   warp 4   : TMA producer;  warp 5: MMA issuer.
 constexpr int kSkinnyThreads = 192;
-constexpr int kSkinnyBufs = 4;
-constexpr int kTabK = 16;  // K blocks per fill of the token-scale table
+constexpr int kGroup = 4;       // K blocks of one TMEM buffer (two buffers)
+constexpr int kSkinnyTabK = 16; // K blocks per fill of the scale table
 
 template <int NT>
 struct CfgSkinny {
-  static constexpr int TMEM_COLS = NT * kSkinnyBufs < 32 ? 32 : NT * kSkinnyBufs;
-  static constexpr int TAB_BYTES = 2 * kTabK * NT * 4;
-  static constexpr int MAX_STAGES = 32;
-  static constexpr int BAR_BYTES = 1024;
+  static constexpr int TMEM_COLS = 2 * kGroup * NT;
+  static constexpr int TAB = kSkinnyTabK * 2 * NT;  // floats of one buffer: [K block][weight block][token]
+  static constexpr int MAX_STAGES = 16;
+  static constexpr int BAR_BYTES = 512;
   static constexpr int XCH_BYTES = 64 * (NT + 1) * 4;  // SWIGLU: up sums for the gate's threads
-  static constexpr int FIXED = 1024 + BM * 128 + TAB_BYTES + BAR_BYTES + XCH_BYTES;
+  static constexpr int FIXED = 1024 + BM * 128 + 2 * TAB * 4 + BAR_BYTES + XCH_BYTES;
+  static_assert(NT == 16 || NT == 32 || NT == 64, "NT");
 };
 
 template <int NT, int EPI>
@@ -558,21 +591,22 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int w_bytes = p.rows * 128, stage_bytes = w_bytes + NT * 128;
-  // BM * 128 bytes past the ring: the last stage's MMA reads its unused lanes there
+  const int w_bytes = p.rows * 128, kb_bytes = w_bytes + NT * 128, stage_bytes = 2 * kb_bytes;
+  // BM * 128 bytes past the ring: the last stage's MMAs read their unused lanes there
   float* table = reinterpret_cast<float*>(smem + p.stages * stage_bytes + BM * 128);
-  float* xch = table + 2 * kTabK * NT;
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xch) + ((C::XCH_BYTES + 15) & ~15));
+  float* xch = table + 2 * C::TAB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xch) + C::XCH_BYTES);
   uint64_t* empty = full + C::MAX_STAGES;
   uint64_t* acc_full = empty + C::MAX_STAGES;
-  uint64_t* acc_empty = acc_full + kSkinnyBufs;
-  uint64_t* drain = acc_empty + kSkinnyBufs;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int kblocks = p.kblocks;
+  const int pairs = (kblocks + 1) / 2;  // ring stages of a tile (past K the boxes are zeros)
   const int R = p.rows, G = R / 2;
   const int per_block = SWIGLU ? 64 / G : 1;  // SWIGLU tiles of one 128-row gate/up block
   const int tiles = SWIGLU ? (p.N / 128) * per_block : (p.N + R - 1) / R;
@@ -584,7 +618,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < kSkinnyBufs; ++a) {
+    for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], act_warps);
     }
@@ -608,14 +642,18 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
       const uint64_t wpol = policy_evict_first();  // each weight box is read once
-      auto load_w = [&](int s, int kb, int t) {
-        uint8_t* dst = smem + s * stage_bytes;
-        if constexpr (SWIGLU) {
-          const int n = (t / per_block) * 128 + (t % per_block) * G;
-          tma_load_2d_hint(dst, &tmB, &full[s], kb * BK, n, wpol);
-          tma_load_2d_hint(dst + G * 128, &tmB, &full[s], kb * BK, n + 64, wpol);
-        } else {
-          tma_load_2d_hint(dst, &tmB, &full[s], kb * BK, t * R, wpol);
+      auto load_w = [&](int s, int pr, int t) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint8_t* dst = smem + s * stage_bytes + h * kb_bytes;
+          const int k = (2 * pr + h) * BK;
+          if constexpr (SWIGLU) {
+            const int n = (t / per_block) * 128 + (t % per_block) * G;
+            tma_load_2d_hint(dst, &tmB, &full[s], k, n, wpol);
+            tma_load_2d_hint(dst + G * 128, &tmB, &full[s], k, n + 64, wpol);
+          } else {
+            tma_load_2d_hint(dst, &tmB, &full[s], k, t * R, wpol);
+          }
         }
       };
       int stage = 0;
@@ -625,7 +663,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       const int t0 = static_cast<int>(blockIdx.x);
       int pre = 0;
       if (t0 < tiles) {
-        pre = kblocks < ring ? kblocks : ring;
+        pre = pairs < ring ? pairs : ring;
         for (int i = 0; i < pre; ++i) {
           mbar_arrive_expect_tx(&full[i], stage_bytes);
           load_w(i, i, t0);
@@ -633,18 +671,20 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       }
       griddep_wait();
       for (int t = t0; t < tiles && ok; t += gridDim.x) {
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!(t == t0 && kb < pre)) {
+        for (int pr = 0; pr < pairs; ++pr) {
+          if (!(t == t0 && pr < pre)) {
             if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) {
               ok = false;
               break;
             }
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
             mbar_arrive_expect_tx(&full[stage], stage_bytes);
-            load_w(stage, kb, t);
+            load_w(stage, pr, t);
           }
           pending |= 1u << stage;
-          tma_load_2d(smem + stage * stage_bytes + w_bytes, &tmA, &full[stage], kb * BK, 0);
+          uint8_t* dst = smem + stage * stage_bytes + w_bytes;
+          tma_load_2d(dst, &tmA, &full[stage], 2 * pr * BK, 0);
+          tma_load_2d(dst + kb_bytes, &tmA, &full[stage], (2 * pr + 1) * BK, 0);
           if (++stage == ring) {
             stage = 0;
             phase ^= 1u;
@@ -665,28 +705,34 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(&acc_empty[buf], bphase ^ 1u, abort_flag, p.status) ||
-              !mbar_wait(&full[stage], phase, abort_flag, p.status)) {
+        for (int pr = 0; pr < pairs; ++pr) {
+          const int in_group = pr % (kGroup / 2);
+          if (in_group == 0 && !mbar_wait(&acc_empty[buf], bphase ^ 1u, abort_flag, p.status)) ok = false;
+          if (!ok || !mbar_wait(&full[stage], phase, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t w_addr = smem_u32(smem + stage * stage_bytes);
-          const uint32_t x_addr = w_addr + w_bytes;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_e4m3(tmem_base + buf * NT, smem_desc_sw128(w_addr + k * 32), smem_desc_sw128(x_addr + k * 32), kIdesc,
-                     k != 0);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w_addr = smem_u32(smem + stage * stage_bytes + h * kb_bytes);
+            const uint32_t x_addr = w_addr + w_bytes;
+            const uint32_t d = tmem_base + (buf * kGroup + in_group * 2 + h) * NT;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_e4m3(d, smem_desc_sw128(w_addr + k * 32), smem_desc_sw128(x_addr + k * 32), kIdesc, k != 0);
+          }
           mma_commit(&empty[stage]);
-          mma_commit(&acc_full[buf]);
           if (++stage == ring) {
             stage = 0;
             phase ^= 1u;
           }
-          if (++buf == kSkinnyBufs) {
-            buf = 0;
-            bphase ^= 1u;
+          if (in_group == kGroup / 2 - 1 || pr == pairs - 1) {
+            mma_commit(&acc_full[buf]);
+            if (++buf == 2) {
+              buf = 0;
+              bphase ^= 1u;
+            }
           }
         }
       }
@@ -699,81 +745,96 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     const bool active = warp < act_warps;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
     const int e = warp * 32 + lane;  // weight row within the tile
-    constexpr int PER = kTabK * NT / 128;  // table entries a thread fills
-    float pre_s[PER];
-    // token scales of K blocks kb0 .. kb0 + kTabK - 1, entry (i, j): block kb0 + i of token j
+    // Scale products of K block kb0 + fi, fi = threadIdx.x % kSkinnyTabK:
+    // thread's tokens fj, fj + 8, ...; the two weight blocks a tile can touch
+    // (SWIGLU: the gate's and the up's).
+    constexpr int PER = NT / 8;
+    const int fi = threadIdx.x % kSkinnyTabK, fj = threadIdx.x / kSkinnyTabK;
+    float pre_a[PER], pre_b[2];
+    const float* sb_blk[2];
     auto fetch = [&](int kb0) {
+      const bool in = kb0 + fi < kblocks;
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
-        const int idx = x * 128 + static_cast<int>(threadIdx.x);
-        const int i = idx % kTabK, j = idx / kTabK;
-        pre_s[x] = kb0 + i < kblocks && j < p.M ? __ldg(p.sa + static_cast<size_t>(j) * kblocks + kb0 + i) : 0.f;
+        const int j = fj + 8 * x;
+        pre_a[x] = in && j < p.M ? __ldg(p.sa + static_cast<size_t>(j) * kblocks + kb0 + fi) : 0.f;
       }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) pre_b[b] = in ? __ldg(sb_blk[b] + kb0 + fi) : 0.f;
     };
-    auto put = [&](int half) {
+    auto put = [&](int side) {
 #pragma unroll
-      for (int x = 0; x < PER; ++x) {
-        const int idx = x * 128 + static_cast<int>(threadIdx.x);
-        table[(half * kTabK + idx % kTabK) * NT + idx / kTabK] = pre_s[x];
-      }
+      for (int x = 0; x < PER; ++x)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          table[side * C::TAB + (fi * 2 + b) * NT + fj + 8 * x] = __fmul_rn(pre_a[x], pre_b[b]);
     };
     int buf = 0;
     uint32_t bphase = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      int n;  // this thread's row of B
+      int n;    // this thread's row of B
       bool n_ok;
+      int blk;  // which of the tile's two weight blocks scales it
       if constexpr (SWIGLU) {
-        n = (t / per_block) * 128 + (t % per_block) * G + (e < G ? e : 64 + e - G);
+        const int base = (t / per_block) * 128;
+        n = base + (t % per_block) * G + (e < G ? e : 64 + e - G);
         n_ok = e < R;
+        blk = n_ok && e >= G ? 1 : 0;
+        for (int b = 0; b < 2; ++b) sb_blk[b] = p.sb + static_cast<size_t>(scale_row<true>(p, base + 64 * b)) * kblocks;
       } else {
         n = t * R + e;
         n_ok = e < R && n < p.N;
+        const int b0 = t * R / BK, b1 = (p.N - 1) / BK;
+        blk = n_ok ? n / BK - b0 : 0;
+        sb_blk[0] = p.sb + static_cast<size_t>(b0) * kblocks;
+        sb_blk[1] = p.sb + static_cast<size_t>(b0 < b1 ? b0 + 1 : b1) * kblocks;
       }
-      const float* sbp = p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n_ok ? n : 0)) * kblocks;
-      uint64_t acc[NT / 2];
+      float acc[NT];
 #pragma unroll
-      for (int j = 0; j < NT / 2; ++j) acc[j] = 0;
-      float b_next = __ldg(sbp);
+      for (int j = 0; j < NT; ++j) acc[j] = 0.f;
       fetch(0);
       named_barrier_sync(1, 128);  // the previous tile's table reads are done
       put(0);
-      for (int kb = 0; kb < kblocks; ++kb) {
-        const int i = kb % kTabK, half = (kb / kTabK) & 1;
-        if (i == 0) {
-          named_barrier_sync(1, 128);  // this half of the table is filled, the other one is read
-          if (kb + kTabK < kblocks) fetch(kb + kTabK);
+#pragma unroll 1
+      for (int kb0 = 0; kb0 < kblocks; kb0 += kGroup) {
+        const int ti = kb0 % kSkinnyTabK, side = (kb0 / kSkinnyTabK) & 1;
+        if (ti == 0) {
+          named_barrier_sync(1, 128);  // this side of the table is filled, the other one is read
+          if (kb0 + kSkinnyTabK < kblocks) fetch(kb0 + kSkinnyTabK);
         }
-        if (i == kTabK - 1 && kb + 1 < kblocks) put(half ^ 1);
-        const float b = b_next;
-        if (kb + 1 < kblocks) b_next = __ldg(sbp + kb + 1);
+        if (ti == kSkinnyTabK - kGroup && kb0 + kGroup < kblocks) put(side ^ 1);
         if (active) {
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], bphase, abort_flag, p.status));
           if (ok) {
             tc_fence_after();
-            const uint64_t bb = pack_f32x2(__float_as_uint(b), __float_as_uint(b));
-            const ulonglong2* srow = reinterpret_cast<const ulonglong2*>(table + (half * kTabK + i) * NT);
+            // 32 columns at a time: 32 / NT blocks, or half a block of 64 tokens
+            constexpr int STEPS = kGroup * NT / 32;
 #pragma unroll
-            for (int c = 0; c < NT / 16; ++c) {
-              uint32_t r[16];
-              tmem_ld_32x32b_x16(t_lane + buf * NT + c * 16, r);
+            for (int c = 0; c < STEPS; ++c) {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(t_lane + buf * (kGroup * NT) + c * 32, r);
               tmem_ld_wait();
-              if (c == NT / 16 - 1) {
+              if (c == STEPS - 1) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[buf]);
               }
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const ulonglong2 s = srow[c * 4 + j];
-                const int a = c * 8 + 2 * j;
-                acc[a] = fma_f32x2(pack_f32x2(r[4 * j], r[4 * j + 1]), mul_f32x2(s.x, bb), acc[a]);
-                acc[a + 1] = fma_f32x2(pack_f32x2(r[4 * j + 2], r[4 * j + 3]), mul_f32x2(s.y, bb), acc[a + 1]);
+              for (int q = 0; q < 8; ++q) {  // four columns each
+                const int g = (c * 32 + 4 * q) / NT, j = (c * 32 + 4 * q) % NT;
+                if (kb0 + g < kblocks) {
+                  const float4 f = *reinterpret_cast<const float4*>(table + side * C::TAB + ((ti + g) * 2 + blk) * NT + j);
+                  acc[j] = __fmaf_rn(__uint_as_float(r[4 * q]), f.x, acc[j]);
+                  acc[j + 1] = __fmaf_rn(__uint_as_float(r[4 * q + 1]), f.y, acc[j + 1]);
+                  acc[j + 2] = __fmaf_rn(__uint_as_float(r[4 * q + 2]), f.z, acc[j + 2]);
+                  acc[j + 3] = __fmaf_rn(__uint_as_float(r[4 * q + 3]), f.w, acc[j + 3]);
+                }
               }
             }
           }
         }
-        if (++buf == kSkinnyBufs) {
+        if (++buf == 2) {
           buf = 0;
           bphase ^= 1u;
         }
@@ -782,47 +843,30 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       if constexpr (SWIGLU) {
         if (active && e >= G && e < R) {
 #pragma unroll
-          for (int j = 0; j < NT / 2; ++j) {
-            float u0, u1;
-            unpack_f32x2(acc[j], u0, u1);
-            xch[(e - G) * (NT + 1) + 2 * j] = u0;
-            xch[(e - G) * (NT + 1) + 2 * j + 1] = u1;
-          }
+          for (int j = 0; j < NT; ++j) xch[(e - G) * (NT + 1) + j] = acc[j];
         }
         named_barrier_sync(1, 128);
         if (active && ok && e < G) {
           const int f = (t / per_block) * 64 + (t % per_block) * G + e;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + f;
 #pragma unroll
-          for (int j = 0; j < NT / 2; ++j) {
-            float g0, g1;
-            unpack_f32x2(acc[j], g0, g1);
-            if (2 * j < p.M)
-              dst[static_cast<size_t>(2 * j) * p.ldc] =
-                  __float2bfloat16_rn(__fmul_rn(silu(g0), xch[e * (NT + 1) + 2 * j]));
-            if (2 * j + 1 < p.M)
-              dst[static_cast<size_t>(2 * j + 1) * p.ldc] =
-                  __float2bfloat16_rn(__fmul_rn(silu(g1), xch[e * (NT + 1) + 2 * j + 1]));
-          }
+          for (int j = 0; j < NT; ++j)
+            if (j < p.M)
+              dst[static_cast<size_t>(j) * p.ldc] =
+                  __float2bfloat16_rn(__fmul_rn(silu(acc[j]), xch[e * (NT + 1) + j]));
         }
       } else if (active && ok && n_ok) {
 #pragma unroll
-        for (int j = 0; j < NT / 2; ++j) {
-          float v[2];
-          unpack_f32x2(acc[j], v[0], v[1]);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int m = 2 * j + h;
-            if (m >= p.M) continue;
-            const size_t at = static_cast<size_t>(m) * p.ldc + n;
-            if constexpr (EPI == HB_EPI_F32) {
-              static_cast<float*>(p.C)[at] = v[h];
-            } else if constexpr (EPI == HB_EPI_RESIDUAL) {
-              const float r = __bfloat162float(static_cast<const __nv_bfloat16*>(p.R)[at]);
-              static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(__fadd_rn(r, v[h]));
-            } else {
-              static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v[h]);
-            }
+        for (int j = 0; j < NT; ++j) {
+          if (j >= p.M) continue;
+          const size_t at = static_cast<size_t>(j) * p.ldc + n;
+          if constexpr (EPI == HB_EPI_F32) {
+            static_cast<float*>(p.C)[at] = acc[j];
+          } else if constexpr (EPI == HB_EPI_RESIDUAL) {
+            const float r = __bfloat162float(static_cast<const __nv_bfloat16*>(p.R)[at]);
+            static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(__fadd_rn(r, acc[j]));
+          } else {
+            static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(acc[j]);
           }
         }
       }
@@ -893,7 +937,7 @@ hb_status launch_skinny(const DeviceCtx& ctx, const void* A, const void* B, Para
     p.rows = (even + 7) / 8 * 8;
     tiles = (p.N + p.rows - 1) / p.rows;
   }
-  const int stage_bytes = (p.rows + NT) * 128;
+  const int stage_bytes = 2 * (p.rows + NT) * 128;
   const int avail = 232448 - C::FIXED;
   p.stages = avail / stage_bytes < C::MAX_STAGES ? avail / stage_bytes : C::MAX_STAGES;
   const int smem = C::FIXED + p.stages * stage_bytes;
