@@ -245,8 +245,12 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   } else if (warp == 9) {
     // ---------------------------------------------------------- MMA issuer
     griddep_wait();
-    if (leader && lane == 0) {
+    if (leader) {
+      // the whole warp walks the loop and one elected lane issues: inside a
+      // single-lane branch every descriptor would be moved to a uniform
+      // register anew
       constexpr uint32_t kIdesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BN);
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
@@ -255,29 +259,34 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         return mbar_wait(bar, par, abort_flag, p.status);
       };
       for (int u = first; u < units && ok; u += stride) {
+#pragma unroll 1
         for (int kb = 0; kb < kblocks; ++kb) {
-          if (!wait(&acc_empty[buf], bphase ^ 1u) || !wait(&full[stage], phase)) {
-            ok = false;
-            break;
-          }
+          ok = wait(&acc_empty[buf], bphase ^ 1u) && wait(&full[stage], phase);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + stage * C::STAGE_BYTES);
-          const uint32_t b_addr = a_addr + C::A_BYTES;
+          // the start address is the low 14 bits of a descriptor, in 16-byte
+          // units, and shared memory ends below 2^18 bytes: it cannot carry
+          const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+          const uint64_t b_desc = a_desc + (C::A_BYTES >> 4);
           const uint32_t d_tmem = tmem_base + buf * BN;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (PAIR)
-              mma_e4m3_pair(d_tmem, smem_desc_sw128(a_addr + k * 32), smem_desc_sw128(b_addr + k * 32), kIdesc, k != 0);
-            else
-              mma_e4m3(d_tmem, smem_desc_sw128(a_addr + k * 32), smem_desc_sw128(b_addr + k * 32), kIdesc, k != 0);
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (PAIR)
+                mma_e4m3_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
+              else
+                mma_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
+            }
+            if constexpr (PAIR) {
+              mma_commit_pair(&empty[stage], 3);
+              mma_commit_pair(&acc_full[buf], 3);
+            } else {
+              mma_commit(&empty[stage]);
+              mma_commit(&acc_full[buf]);
+            }
           }
-          if constexpr (PAIR) {
-            mma_commit_pair(&empty[stage], 3);
-            mma_commit_pair(&acc_full[buf], 3);
-          } else {
-            mma_commit(&empty[stage]);
-            mma_commit(&acc_full[buf]);
-          }
+          __syncwarp();
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -290,10 +299,13 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       }
       if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
       // no MMA may still read shared memory or write tensor memory when the CTAs leave
-      if constexpr (PAIR)
-        mma_commit_pair(drain, 1);
-      else
-        mma_commit(drain);
+      if (elect_one()) {
+        if constexpr (PAIR)
+          mma_commit_pair(drain, 1);
+        else
+          mma_commit(drain);
+      }
+      __syncwarp();
       mbar_drain(drain, 0);
     }
   } else {
@@ -355,6 +367,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       return half * (BN / 2) + c * 32;
     };
     int buf = 0;
+    const uint32_t acc_empty0 = PAIR ? cluster_addr(acc_empty, 0) : 0u;
     int fill = 0;
     uint32_t bphase = 0, rphase = 0;
     bool ok = true;
@@ -368,20 +381,28 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
-#pragma unroll 1
-      for (int kb = 0; kb < kblocks; ++kb) {
+      // The factors of K block kb, one block ahead of their use.  A wait that
+      // expired raises the abort flag, every later wait gives up at once, and
+      // the loop runs on over whatever TMEM holds: nothing of it is stored.
+      float f0, f1;
+      auto factors = [&](int kb) {
         const int ti = kb % kTabK, tb = fill & 1;
-        if (ti == 0 && ok)
-          ok = __all_sync(0xffffffffu, mbar_wait(&tab_full[tb], (fill >> 1) & 1, abort_flag, p.status));
+        if (ti == 0) ok &= mbar_wait(&tab_full[tb], (fill >> 1) & 1, abort_flag, p.status);
         const float* tab = table + tb * (C::TABLE / 4);
         const float sa = tab[ti * BM + rloc];
         const float2 sb = *reinterpret_cast<const float2*>(tab + kTabK * BM + ti * 4 + half * 2);
-        const float f0 = __fmul_rn(sa, sb.x), f1 = SWIGLU ? __fmul_rn(sa, sb.y) : f0;
+        f0 = __fmul_rn(sa, sb.x);
+        f1 = SWIGLU ? __fmul_rn(sa, sb.y) : f0;
         if (ti == kTabK - 1 || kb == kblocks - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&tab_empty[tb]);
           ++fill;
         }
+      };
+      factors(0);
+#pragma unroll 1
+      for (int kb = 0; kb < kblocks; ++kb) {
+        const float g0 = f0, g1 = f1;
         if constexpr (EPI == HB_EPI_RESIDUAL) {
           // the residual tile into the staging slabs, once the previous
           // tile's stores have left them (by now long done)
@@ -396,37 +417,38 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             res_pending = true;
           }
         }
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], bphase, abort_flag, p.status));
-        if (ok) {
-          tc_fence_after();
+        ok &= mbar_wait(&acc_full[buf], bphase, abort_flag, p.status);
+        __syncwarp();
+        tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < CH; ++c) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(t_lane + buf * BN + chunk_col(c), r);
-            tmem_ld_wait();
-            if (c == CH - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                if constexpr (PAIR)
-                  mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[buf], 0));
-                else
-                  mbar_arrive(&acc_empty[buf]);
-              }
+        for (int c = 0; c < CH; ++c) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t_lane + buf * BN + chunk_col(c), r);
+          if (c == 0 && kb + 1 < kblocks) factors(kb + 1);
+          tmem_ld_wait();
+          if (c == CH - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR)
+                mbar_arrive_cluster_relaxed(acc_empty0 + buf * 8);
+              else
+                mbar_arrive(&acc_empty[buf]);
             }
-            // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
-            // the 32-register TMEM load does not give without moves (620
-            // against 370 clocks per 256-column block, measured)
-            const float f = c < CH / 2 ? f0 : f1;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c][j] = __fmaf_rn(__uint_as_float(r[j]), f, acc[c][j]);
           }
+          // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
+          // the 32-register TMEM load does not give without moves (620
+          // against 370 clocks per 256-column block, measured)
+          const float f = c < CH / 2 ? g0 : g1;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c][j] = __fmaf_rn(__uint_as_float(r[j]), f, acc[c][j]);
         }
         if (++buf == C::NBUF) {
           buf = 0;
           bphase ^= 1u;
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
       // ---- the tile's sums are complete
       if (!live) continue;  // the same for every thread of the CTA
       if constexpr (EPI == HB_EPI_RESIDUAL) {
