@@ -261,15 +261,18 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int u = first; u < units && ok; u += stride) {
 #pragma unroll 1
         for (int kb = 0; kb < kblocks; ++kb) {
-          ok = wait(&acc_empty[buf], bphase ^ 1u) && wait(&full[stage], phase);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
+          // the operands first: the buffer's release is the later event in
+          // the steady state, and nothing but the issue should follow it
+          ok = wait(&full[stage], phase);
           // the start address is the low 14 bits of a descriptor, in 16-byte
           // units, and shared memory ends below 2^18 bytes: it cannot carry
           const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
           const uint64_t b_desc = a_desc + (C::A_BYTES >> 4);
           const uint32_t d_tmem = tmem_base + buf * BN;
+          ok = ok && wait(&acc_empty[buf], bphase ^ 1u);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -381,28 +384,40 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
-      // The factors of K block kb, one block ahead of their use.  A wait that
+      // The sums run over 16 columns at a time, the next 16 on their way from
+      // TMEM meanwhile, across the border of two K blocks too.  A wait that
       // expired raises the abort flag, every later wait gives up at once, and
       // the loop runs on over whatever TMEM holds: nothing of it is stored.
-      float f0, f1;
-      auto factors = [&](int kb) {
+      float sa_next, f0, f1;
+      float2 sb_next;
+      auto load_factors = [&](int kb) {
         const int ti = kb % kTabK, tb = fill & 1;
         if (ti == 0) ok &= mbar_wait(&tab_full[tb], (fill >> 1) & 1, abort_flag, p.status);
         const float* tab = table + tb * (C::TABLE / 4);
-        const float sa = tab[ti * BM + rloc];
-        const float2 sb = *reinterpret_cast<const float2*>(tab + kTabK * BM + ti * 4 + half * 2);
-        f0 = __fmul_rn(sa, sb.x);
-        f1 = SWIGLU ? __fmul_rn(sa, sb.y) : f0;
-        if (ti == kTabK - 1 || kb == kblocks - 1) {
+        sa_next = tab[ti * BM + rloc];
+        sb_next = *reinterpret_cast<const float2*>(tab + kTabK * BM + ti * 4 + half * 2);
+        if (ti == kTabK - 1 || kb == kblocks - 1) ++fill;
+      };
+      // the table side that held block kb's factors goes back to its fillers
+      auto free_factors = [&](int kb) {
+        if (kb % kTabK == kTabK - 1 || kb == kblocks - 1) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tab_empty[tb]);
-          ++fill;
+          if (lane == 0) mbar_arrive(&tab_empty[(fill - 1) & 1]);
         }
       };
-      factors(0);
+      constexpr int NC = 2 * CH;  // 16-column steps
+      uint32_t r[2][16];
+      auto step_col = [&](int c) { return chunk_col(c >> 1) + (c & 1) * 16; };
+      load_factors(0);
+      ok &= mbar_wait(&acc_full[buf], bphase, abort_flag, p.status);
+      __syncwarp();
+      tc_fence_after();
+      tmem_ld_32x32b_x16(t_lane + buf * BN + step_col(0), r[0]);
 #pragma unroll 1
       for (int kb = 0; kb < kblocks; ++kb) {
-        const float g0 = f0, g1 = f1;
+        f0 = __fmul_rn(sa_next, sb_next.x);
+        f1 = SWIGLU ? __fmul_rn(sa_next, sb_next.y) : f0;
+        free_factors(kb);
         if constexpr (EPI == HB_EPI_RESIDUAL) {
           // the residual tile into the staging slabs, once the previous
           // tile's stores have left them (by now long done)
@@ -417,16 +432,13 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             res_pending = true;
           }
         }
-        ok &= mbar_wait(&acc_full[buf], bphase, abort_flag, p.status);
-        __syncwarp();
-        tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(t_lane + buf * BN + chunk_col(c), r);
-          if (c == 0 && kb + 1 < kblocks) factors(kb + 1);
+        for (int c = 0; c < NC; ++c) {
           tmem_ld_wait();
-          if (c == CH - 1) {
+          if (c < NC - 1) {
+            tmem_ld_32x32b_x16(t_lane + buf * BN + step_col(c + 1), r[(c + 1) & 1]);
+            if (c == 0 && kb + 1 < kblocks) load_factors(kb + 1);
+          } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -435,17 +447,25 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
               else
                 mbar_arrive(&acc_empty[buf]);
             }
+            if (++buf == C::NBUF) {
+              buf = 0;
+              bphase ^= 1u;
+            }
+            if (kb + 1 < kblocks) {
+              ok &= mbar_wait(&acc_full[buf], bphase, abort_flag, p.status);
+              __syncwarp();
+              tc_fence_after();
+              tmem_ld_32x32b_x16(t_lane + buf * BN + step_col(0), r[(c + 1) & 1]);
+            }
           }
           // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
-          // the 32-register TMEM load does not give without moves (620
-          // against 370 clocks per 256-column block, measured)
-          const float f = c < CH / 2 ? g0 : g1;
+          // the TMEM load does not give without moves (620 against 370 clocks
+          // per 256-column block, measured)
+          const float f = c < NC / 2 ? f0 : f1;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) acc[c][j] = __fmaf_rn(__uint_as_float(r[j]), f, acc[c][j]);
-        }
-        if (++buf == C::NBUF) {
-          buf = 0;
-          bphase ^= 1u;
+          for (int j = 0; j < 16; ++j)
+            acc[c >> 1][(c & 1) * 16 + j] =
+                __fmaf_rn(__uint_as_float(r[c & 1][j]), f, acc[c >> 1][(c & 1) * 16 + j]);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
