@@ -167,6 +167,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   if constexpr (PAIR) cluster_sync();  // the peer's barriers exist before anything arrives on them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  const uint32_t full0 = PAIR ? cluster_addr(full, 0) : 0u;
 
   // (each setmaxnreg inside its role's own branch: the compiler allocates for
   // the smaller count where the two could meet)
@@ -174,74 +175,77 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     regs_dec<kIssueRegs>();
   if (warp == 8) {
     // ---------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      const uint64_t wpol = um <= 4 ? policy_evict_first() : policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      uint32_t pending = 0, armed_parity = 0;
-      auto load_a = [&](int s, int kb, int m0) {
-        uint8_t* dst = smem + s * C::STAGE_BYTES;
-        if constexpr (PAIR)
-          tma_load_2d_pair(dst, &tmA, cluster_addr(&full[s], 0), kb * BK, m0);
-        else
-          tma_load_2d(dst, &tmA, &full[s], kb * BK, m0);
-      };
-      auto load_b = [&](int s, int kb, int n0) {
-        uint8_t* dst = smem + s * C::STAGE_BYTES + C::A_BYTES;
-        if constexpr (PAIR)
-          tma_load_2d_pair_hint(dst, &tmB, cluster_addr(&full[s], 0), kb * BK, n0, wpol);
-        else
-          tma_load_2d_hint(dst, &tmB, &full[s], kb * BK, n0, wpol);
-      };
-      auto arm = [&](int s) {
-        if (leader) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * C::STAGE_BYTES);  // both CTAs' boxes
-      };
-      // the weights do not come from the kernel ahead: their first ring fill
-      // is issued before waiting for it
-      int pre = 0;
-      if (first < units) {
-        const int n0 = (first / um) * BN + static_cast<int>(rank) * (BN / 2);
-        pre = kblocks < C::STAGES ? kblocks : C::STAGES;
+    // The whole warp walks the loops and one elected lane issues (see the MMA
+    // issuer): a single-lane loop needs twice the time per K block.
+    const uint64_t wpol = um <= 4 ? policy_evict_first() : policy_evict_normal();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    uint32_t pending = 0, armed_parity = 0;
+    auto load_a = [&](int s, int kb, int m0) {
+      uint8_t* dst = smem + s * C::STAGE_BYTES;
+      if constexpr (PAIR)
+        tma_load_2d_pair(dst, &tmA, full0 + s * 8, kb * BK, m0);
+      else
+        tma_load_2d(dst, &tmA, &full[s], kb * BK, m0);
+    };
+    auto load_b = [&](int s, int kb, int n0) {
+      uint8_t* dst = smem + s * C::STAGE_BYTES + C::A_BYTES;
+      if constexpr (PAIR)
+        tma_load_2d_pair_hint(dst, &tmB, full0 + s * 8, kb * BK, n0, wpol);
+      else
+        tma_load_2d_hint(dst, &tmB, &full[s], kb * BK, n0, wpol);
+    };
+    auto arm = [&](int s) {
+      if (leader) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * C::STAGE_BYTES);  // both CTAs' boxes
+    };
+    // the weights do not come from the kernel ahead: their first ring fill
+    // is issued before waiting for it
+    int pre = 0;
+    if (first < units) {
+      const int n0 = (first / um) * BN + static_cast<int>(rank) * (BN / 2);
+      pre = kblocks < C::STAGES ? kblocks : C::STAGES;
+      if (elect_one()) {
         for (int i = 0; i < pre; ++i) {
           arm(i);
           load_b(i, i, n0);
         }
       }
-      griddep_wait();
-      for (int u = first; u < units && ok; u += stride) {
-        const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
-        const int n0 = (u / um) * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (u == first && kb < pre) {
-            pending |= 1u << stage;
-            load_a(stage, kb, mt * BM);
-          } else {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            pending |= 1u << stage;
-            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+      __syncwarp();
+    }
+    griddep_wait();
+    for (int u = first; u < units && ok; u += stride) {
+      const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
+      const int n0 = (u / um) * BN + static_cast<int>(rank) * (BN / 2);
+#pragma unroll 1
+      for (int kb = 0; kb < kblocks; ++kb) {
+        pending |= 1u << stage;
+        if (u == first && kb < pre) {
+          if (elect_one()) load_a(stage, kb, mt * BM);
+        } else {
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status));
+          if (!ok) break;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          if (elect_one()) {
             arm(stage);
             load_a(stage, kb, mt * BM);
             load_b(stage, kb, n0);
           }
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
-      if (!ok) {
-        // let copies already in flight land before the CTA leaves (one CTA:
-        // their own barrier; a pair: the stage is released once consumed)
-        for (int s = 0; s < C::STAGES; ++s)
-          if (pending & (1u << s)) mbar_drain(PAIR ? &empty[s] : &full[s], (armed_parity >> s) & 1u);
-      }
     }
-    if (lane != 0) griddep_wait();
+    if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
+    if (!ok) {
+      // let copies already in flight land before the CTA leaves (one CTA:
+      // their own barrier; a pair: the stage is released once consumed)
+      for (int s = 0; s < C::STAGES; ++s)
+        if (pending & (1u << s)) mbar_drain(PAIR ? &empty[s] : &full[s], (armed_parity >> s) & 1u);
+    }
   } else if (warp == 9) {
     // ---------------------------------------------------------- MMA issuer
     griddep_wait();
@@ -682,105 +686,111 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
 
   if (warp == 4) {
     // ---------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      const uint64_t wpol = policy_evict_first();  // each weight box is read once
-      auto load_w = [&](int s, int pr, int t) {
+    const uint64_t wpol = policy_evict_first();  // each weight box is read once
+    auto load_w = [&](int s, int pr, int t) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint8_t* dst = smem + s * stage_bytes + h * kb_bytes;
-          const int k = (2 * pr + h) * BK;
-          if constexpr (SWIGLU) {
-            const int n = (t / per_block) * 128 + (t % per_block) * G;
-            tma_load_2d_hint(dst, &tmB, &full[s], k, n, wpol);
-            tma_load_2d_hint(dst + G * 128, &tmB, &full[s], k, n + 64, wpol);
-          } else {
-            tma_load_2d_hint(dst, &tmB, &full[s], k, t * R, wpol);
-          }
+      for (int h = 0; h < 2; ++h) {
+        uint8_t* dst = smem + s * stage_bytes + h * kb_bytes;
+        const int k = (2 * pr + h) * BK;
+        if constexpr (SWIGLU) {
+          const int n = (t / per_block) * 128 + (t % per_block) * G;
+          tma_load_2d_hint(dst, &tmB, &full[s], k, n, wpol);
+          tma_load_2d_hint(dst + G * 128, &tmB, &full[s], k, n + 64, wpol);
+        } else {
+          tma_load_2d_hint(dst, &tmB, &full[s], k, t * R, wpol);
         }
-      };
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      uint32_t pending = 0, armed_parity = 0;
-      const int t0 = static_cast<int>(blockIdx.x);
-      int pre = 0;
-      if (t0 < tiles) {
-        pre = pairs < ring ? pairs : ring;
+      }
+    };
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    uint32_t pending = 0, armed_parity = 0;
+    const int t0 = static_cast<int>(blockIdx.x);
+    int pre = 0;
+    if (t0 < tiles) {
+      pre = pairs < ring ? pairs : ring;
+      if (elect_one()) {
         for (int i = 0; i < pre; ++i) {
           mbar_arrive_expect_tx(&full[i], stage_bytes);
           load_w(i, i, t0);
         }
       }
-      griddep_wait();
-      for (int t = t0; t < tiles && ok; t += gridDim.x) {
-        for (int pr = 0; pr < pairs; ++pr) {
-          if (!(t == t0 && pr < pre)) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+      __syncwarp();
+    }
+    griddep_wait();
+    for (int t = t0; t < tiles && ok; t += gridDim.x) {
+#pragma unroll 1
+      for (int pr = 0; pr < pairs; ++pr) {
+        const bool fresh = !(t == t0 && pr < pre);
+        pending |= 1u << stage;
+        if (fresh) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status));
+          if (!ok) break;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        }
+        if (elect_one()) {
+          if (fresh) {
             mbar_arrive_expect_tx(&full[stage], stage_bytes);
             load_w(stage, pr, t);
           }
-          pending |= 1u << stage;
           uint8_t* dst = smem + stage * stage_bytes + w_bytes;
           tma_load_2d(dst, &tmA, &full[stage], 2 * pr * BK, 0);
           tma_load_2d(dst + kb_bytes, &tmA, &full[stage], (2 * pr + 1) * BK, 0);
-          if (++stage == ring) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == ring) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok)
-        for (int s = 0; s < ring; ++s)
-          if (pending & (1u << s)) mbar_drain(&full[s], (armed_parity >> s) & 1u);
     }
-    if (lane != 0) griddep_wait();
+    if (!ok)
+      for (int s = 0; s < ring; ++s)
+        if (pending & (1u << s)) mbar_drain(&full[s], (armed_parity >> s) & 1u);
   } else if (warp == 5) {
     // ---------------------------------------------------------- MMA issuer
     griddep_wait();
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_e4m3_f32(BM, NT);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        for (int pr = 0; pr < pairs; ++pr) {
-          const int in_group = pr % (kGroup / 2);
-          if (in_group == 0 && !mbar_wait(&acc_empty[buf], bphase ^ 1u, abort_flag, p.status)) ok = false;
-          if (!ok || !mbar_wait(&full[stage], phase, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+    constexpr uint32_t kIdesc = idesc_e4m3_f32(BM, NT);
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, bphase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+#pragma unroll 1
+      for (int pr = 0; pr < pairs; ++pr) {
+        const int in_group = pr % (kGroup / 2);
+        ok = mbar_wait(&full[stage], phase, abort_flag, p.status);
+        if (in_group == 0) ok = ok && mbar_wait(&acc_empty[buf], bphase ^ 1u, abort_flag, p.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const bool last = in_group == kGroup / 2 - 1 || pr == pairs - 1;
+        if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t w_addr = smem_u32(smem + stage * stage_bytes + h * kb_bytes);
-            const uint32_t x_addr = w_addr + w_bytes;
+            const uint64_t w_desc = desc0 + static_cast<uint32_t>((stage * stage_bytes + h * kb_bytes) >> 4);
+            const uint64_t x_desc = w_desc + static_cast<uint32_t>(w_bytes >> 4);
             const uint32_t d = tmem_base + (buf * kGroup + in_group * 2 + h) * NT;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_e4m3(d, smem_desc_sw128(w_addr + k * 32), smem_desc_sw128(x_addr + k * 32), kIdesc, k != 0);
+            for (int k = 0; k < 4; ++k) mma_e4m3(d, w_desc + 2 * k, x_desc + 2 * k, kIdesc, k != 0);
           }
           mma_commit(&empty[stage]);
-          if (++stage == ring) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          if (in_group == kGroup / 2 - 1 || pr == pairs - 1) {
-            mma_commit(&acc_full[buf]);
-            if (++buf == 2) {
-              buf = 0;
-              bphase ^= 1u;
-            }
-          }
+          if (last) mma_commit(&acc_full[buf]);
+        }
+        __syncwarp();
+        if (++stage == ring) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (last && ++buf == 2) {
+          buf = 0;
+          bphase ^= 1u;
         }
       }
-      mma_commit(drain);
-      mbar_drain(drain, 0);
     }
+    if (elect_one()) mma_commit(drain);
+    __syncwarp();
+    mbar_drain(drain, 0);
   } else {
     // ---------------------------------------------------------- promotion and epilogue
     griddep_wait();
