@@ -258,22 +258,18 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       int stage = 0, buf = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t par) {
-        if constexpr (PAIR) return mbar_wait_cluster(bar, par, abort_flag, p.status);
-        return mbar_wait(bar, par, abort_flag, p.status);
-      };
       for (int u = first; u < units && ok; u += stride) {
 #pragma unroll 1
         for (int kb = 0; kb < kblocks; ++kb) {
           // the operands first: the buffer's release is the later event in
           // the steady state, and nothing but the issue should follow it
-          ok = wait(&full[stage], phase);
+          ok = mbar_wait(&full[stage], phase, abort_flag, p.status);
           // the start address is the low 14 bits of a descriptor, in 16-byte
           // units, and shared memory ends below 2^18 bytes: it cannot carry
           const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
           const uint64_t b_desc = a_desc + (C::A_BYTES >> 4);
           const uint32_t d_tmem = tmem_base + buf * BN;
-          ok = ok && wait(&acc_empty[buf], bphase ^ 1u);
+          ok = ok && mbar_wait(&acc_empty[buf], bphase ^ 1u, abort_flag, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
