@@ -108,6 +108,58 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// mbar_wait for inner loops, on a shared-memory address: the clock, the abort
+// flag and the time limit come in only after many tries (each holds the
+// thread for a while in hardware), so that a wait costs a few instructions
+// when the phase is there or near.
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+  if (mbar_try_wait_at(bar, parity)) return true;
+  uint64_t t0 = 0;
+#pragma unroll 1
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)
+      if (mbar_try_wait_at(bar, parity)) return true;
+    if (*abort) return false;
+    if (t0 == 0) t0 = globaltimer();
+    if (globaltimer() - t0 > kWaitTimeoutNs) {
+      flag_error(status, kStatusTimeout);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
 // Drain wait used while unwinding after an abort: short limit, no flags.
 constexpr uint64_t kDrainTimeoutNs = 50000000ull;  // 50 ms
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {

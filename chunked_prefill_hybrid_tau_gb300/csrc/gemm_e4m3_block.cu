@@ -69,21 +69,28 @@ __device__ __forceinline__ int scale_row(const Params& p, int n) {
 // together.
 //   warps 0-7 : promotion and epilogue.  Warp w reads TMEM lanes 32 (w % 4)..
 //               (its output rows) and column half w / 4, so a thread holds
-//               BN / 2 fp32 sums of one row and scales a K block with one or
-//               two factors;
+//               BN / 2 fp32 sums of one row and scales a K block with one
+//               factor (SWIGLU: one for its gate, one for its up columns);
 //   warp 8    : TMA producer (128-byte swizzled boxes of one K block);
-//   warp 9    : MMA issuer; one K block per TMEM buffer, NBUF buffers.
+//   warp 9    : MMA issuer.  TMEM holds four buffers of 128 columns; a K block
+//               is BN / 128 of them, each with its own pair of barriers: at BN
+//               = 256 every column half is refilled while the other is read;
+//   warps 10-11: fill the table of scales.
 // The sums leave through shared memory staged apart from the ring and TMA
 // stores, so the next tile's loads and MMAs go on meanwhile.
 constexpr int kTabK = 8;  // K blocks per fill of the scale table
+constexpr int kBufs = 4;  // TMEM buffers of kSub columns
+constexpr int kSub = 128;
 template <int BN, bool PAIR>
 struct Cfg {
+  static constexpr int NSUB = BN / kSub;                            // buffers of a K block
+  static constexpr int NB = kBufs / NSUB;                           // K blocks in TMEM
+  static constexpr int SUB_BYTES = (PAIR ? kSub / 2 : kSub) * 128;  // B rows of one buffer (this CTA's)
   static constexpr int A_BYTES = BM * 128;
-  static constexpr int B_BYTES = (PAIR ? BN / 2 : BN) * 128;
+  static constexpr int B_BYTES = NSUB * SUB_BYTES;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int NBUF = 512 / BN;  // TMEM accumulator buffers
   static constexpr int STAGING = BM * BN * 2;
-  static constexpr int TABLE = kTabK * (BM + 4) * 4;  // one buffer: scales of the rows, then of up to 4 weight blocks
+  static constexpr int TABLE = kTabK * (BM + 4) * 4;  // one side: scales of the rows, then of up to 4 weight blocks
   static constexpr int AVAIL = 232448 - 1024 - 512 - STAGING - 2 * TABLE;
   static constexpr int STAGES = AVAIL / STAGE_BYTES < 8 ? AVAIL / STAGE_BYTES : 8;
   static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING + 2 * TABLE + 512 + 1024;
@@ -111,8 +118,8 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + C::STAGING + 2 * C::TABLE);  // PAIR: the even CTA's are used
   uint64_t* empty = full + C::STAGES;
   uint64_t* acc_full = empty + C::STAGES;
-  uint64_t* acc_empty = acc_full + C::NBUF;  // PAIR: the even CTA's are used
-  uint64_t* tab_full = acc_empty + C::NBUF;
+  uint64_t* acc_empty = acc_full + kBufs;  // PAIR: the even CTA's are used
+  uint64_t* tab_full = acc_empty + kBufs;
   uint64_t* tab_empty = tab_full + 2;
   uint64_t* drain = tab_empty + 2;
   uint64_t* res_bar = drain + 1;
@@ -136,9 +143,9 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < C::NBUF; ++a) {
+    for (int a = 0; a < kBufs; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], PAIR ? 16 : 8);
+      mbar_init(&acc_empty[a], (PAIR ? 16 : 8) / C::NSUB);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tab_full[b], 64);
@@ -191,10 +198,13 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     };
     auto load_b = [&](int s, int kb, int n0) {
       uint8_t* dst = smem + s * C::STAGE_BYTES + C::A_BYTES;
-      if constexpr (PAIR)
-        tma_load_2d_pair_hint(dst, &tmB, full0 + s * 8, kb * BK, n0, wpol);
-      else
-        tma_load_2d_hint(dst, &tmB, &full[s], kb * BK, n0, wpol);
+#pragma unroll
+      for (int i = 0; i < C::NSUB; ++i) {
+        if constexpr (PAIR)
+          tma_load_2d_pair_hint(dst + i * C::SUB_BYTES, &tmB, full0 + s * 8, kb * BK, n0 + i * kSub, wpol);
+        else
+          tma_load_2d_hint(dst + i * C::SUB_BYTES, &tmB, &full[s], kb * BK, n0 + i * kSub, wpol);
+      }
     };
     auto arm = [&](int s) {
       if (leader) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * C::STAGE_BYTES);  // both CTAs' boxes
@@ -203,7 +213,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     // is issued before waiting for it
     int pre = 0;
     if (first < units) {
-      const int n0 = (first / um) * BN + static_cast<int>(rank) * (BN / 2);
+      const int n0 = (first / um) * BN + static_cast<int>(rank) * (kSub / 2);
       pre = kblocks < C::STAGES ? kblocks : C::STAGES;
       if (elect_one()) {
         for (int i = 0; i < pre; ++i) {
@@ -216,7 +226,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     griddep_wait();
     for (int u = first; u < units && ok; u += stride) {
       const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
-      const int n0 = (u / um) * BN + static_cast<int>(rank) * (BN / 2);
+      const int n0 = (u / um) * BN + static_cast<int>(rank) * (kSub / 2);
 #pragma unroll 1
       for (int kb = 0; kb < kblocks; ++kb) {
         pending |= 1u << stage;
@@ -253,49 +263,56 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       // the whole warp walks the loop and one elected lane issues: inside a
       // single-lane branch every descriptor would be moved to a uniform
       // register anew
-      constexpr uint32_t kIdesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, BN);
+      constexpr uint32_t kIdesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, kSub);
       const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
-      int stage = 0, buf = 0;
+      const uint32_t full_at = smem_u32(full), acc_empty_at = smem_u32(acc_empty);
+      int stage = 0, slot = 0;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
       for (int u = first; u < units && ok; u += stride) {
 #pragma unroll 1
         for (int kb = 0; kb < kblocks; ++kb) {
-          // the operands first: the buffer's release is the later event in
-          // the steady state, and nothing but the issue should follow it
-          ok = mbar_wait(&full[stage], phase, abort_flag, p.status);
+          // the operands first: a buffer's release is the later event in the
+          // steady state, and nothing but the issue should follow it
+          ok = mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status);
           // the start address is the low 14 bits of a descriptor, in 16-byte
           // units, and shared memory ends below 2^18 bytes: it cannot carry
           const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
-          const uint64_t b_desc = a_desc + (C::A_BYTES >> 4);
-          const uint32_t d_tmem = tmem_base + buf * BN;
-          ok = ok && mbar_wait(&acc_empty[buf], bphase ^ 1u, abort_flag, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if constexpr (PAIR)
-                mma_e4m3_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
-              else
-                mma_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
+          for (int i = 0; i < C::NSUB; ++i) {
+            const int buf = i * C::NB + slot;
+            const uint32_t d_tmem = tmem_base + buf * kSub;
+            ok = ok && mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint64_t ad = a_desc + 2 * k;
+                const uint64_t bd = ad + ((C::A_BYTES + i * C::SUB_BYTES) >> 4);
+                if constexpr (PAIR)
+                  mma_e4m3_pair(d_tmem, ad, bd, kIdesc, k != 0);
+                else
+                  mma_e4m3(d_tmem, ad, bd, kIdesc, k != 0);
+              }
+              if constexpr (PAIR) {
+                mma_commit_pair(&acc_full[buf], 3);
+                if (i == C::NSUB - 1) mma_commit_pair(&empty[stage], 3);
+              } else {
+                mma_commit(&acc_full[buf]);
+                if (i == C::NSUB - 1) mma_commit(&empty[stage]);
+              }
             }
-            if constexpr (PAIR) {
-              mma_commit_pair(&empty[stage], 3);
-              mma_commit_pair(&acc_full[buf], 3);
-            } else {
-              mma_commit(&empty[stage]);
-              mma_commit(&acc_full[buf]);
-            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
-          if (++buf == C::NBUF) {
-            buf = 0;
+          if (++slot == C::NB) {
+            slot = 0;
             bphase ^= 1u;
           }
         }
@@ -328,7 +345,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       const int ra = mt * BM + t64, rb = ra + 64;
       const float* pa = p.sa + static_cast<size_t>(ra < p.M ? ra : 0) * kblocks;
       const float* pb = p.sa + static_cast<size_t>(rb < p.M ? rb : 0) * kblocks;
-      // weight block j: column half j / 2's gate (or only) block, and its up block
+      // weight block j: column half j / 2's gate (or only) block, and its up block (BN 128: one block's half each)
       const int j = t64 & 3;
       const int n = n0 + (j >> 1) * (BN == 256 ? 128 : SWIGLU ? 0 : 64) + (SWIGLU ? (j & 1) * 64 : 0);
       const float* ps =
@@ -369,9 +386,13 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       if (SWIGLU && BN == 128) return half * 32 + c * 64;
       return half * (BN / 2) + c * 32;
     };
-    int buf = 0;
-    const uint32_t acc_empty0 = PAIR ? cluster_addr(acc_empty, 0) : 0u;
-    int fill = 0;
+    // column half w / 4: at BN 256 a buffer of its own
+    const int sub = BN == 256 ? half : 0;
+    const uint32_t acc_full_at = smem_u32(acc_full) + sub * C::NB * 8;
+    const uint32_t acc_empty_at = (PAIR ? cluster_addr(acc_empty, 0) : smem_u32(acc_empty)) + sub * C::NB * 8;
+    const uint32_t tab_full_at = smem_u32(tab_full), tab_empty_at = smem_u32(tab_empty);
+    const uint32_t sa_at = smem_u32(table) + rloc * 4, sb_at = smem_u32(table) + (kTabK * BM + half * 2) * 4;
+    int fill = 0, slot = 0;
     uint32_t bphase = 0, rphase = 0;
     bool ok = true;
     bool res_pending = false;  // boss: residual copies in flight
@@ -386,42 +407,29 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
       // The sums run over 16 columns at a time, the next 16 on their way from
       // TMEM meanwhile, across the border of two K blocks too.  A wait that
-      // expired raises the abort flag, every later wait gives up at once, and
+      // expired raises the abort flag, every later wait gives up soon, and
       // the loop runs on over whatever TMEM holds: nothing of it is stored.
-      float sa_next, f0, f1;
-      float2 sb_next;
-      auto load_factors = [&](int kb) {
-        const int ti = kb % kTabK, tb = fill & 1;
-        if (ti == 0) ok &= mbar_wait(&tab_full[tb], (fill >> 1) & 1, abort_flag, p.status);
-        const float* tab = table + tb * (C::TABLE / 4);
-        sa_next = tab[ti * BM + rloc];
-        sb_next = *reinterpret_cast<const float2*>(tab + kTabK * BM + ti * 4 + half * 2);
-        if (ti == kTabK - 1 || kb == kblocks - 1) ++fill;
-      };
-      // the table side that held block kb's factors goes back to its fillers
-      auto free_factors = [&](int kb) {
-        if (kb % kTabK == kTabK - 1 || kb == kblocks - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tab_empty[(fill - 1) & 1]);
-        }
-      };
       constexpr int NC = 2 * CH;  // 16-column steps
       uint32_t r[2][16];
+      const uint32_t t_cols = t_lane + sub * C::NB * kSub - sub * kSub;
       auto step_col = [&](int c) { return chunk_col(c >> 1) + (c & 1) * 16; };
-      load_factors(0);
-      ok &= mbar_wait(&acc_full[buf], bphase, abort_flag, p.status);
-      __syncwarp();
-      tc_fence_after();
-      tmem_ld_32x32b_x16(t_lane + buf * BN + step_col(0), r[0]);
+      auto next_block = [&]() {  // waits for the next K block in TMEM and starts its first columns
+        ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
+        __syncwarp();
+        tc_fence_after();
+        tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(0), r[0]);
+      };
+      next_block();
 #pragma unroll 1
-      for (int kb = 0; kb < kblocks; ++kb) {
-        f0 = __fmul_rn(sa_next, sb_next.x);
-        f1 = SWIGLU ? __fmul_rn(sa_next, sb_next.y) : f0;
-        free_factors(kb);
+      for (int kb0 = 0; kb0 < kblocks; kb0 += kTabK, ++fill) {
+        const int side = fill & 1;
+        const int nk = kblocks - kb0 < kTabK ? kblocks - kb0 : kTabK;
+        ok &= mbar_wait_at(tab_full_at + side * 8, (fill >> 1) & 1, abort_flag, p.status);
+        uint32_t sa_next = sa_at + side * C::TABLE, sb_next = sb_at + side * C::TABLE;
         if constexpr (EPI == HB_EPI_RESIDUAL) {
           // the residual tile into the staging slabs, once the previous
-          // tile's stores have left them (by now long done)
-          if (boss && live && ok && kb == (kblocks > 4 ? 4 : 0)) {
+          // tile's stores have left them (in the second round: long done)
+          if (boss && live && ok && kb0 == (kblocks > kTabK ? kTabK : 0)) {
             bulk_wait_group_read<0>();
             int slabs = (p.N - n0 + 63) / 64;
             if (slabs > BN / 64) slabs = BN / 64;
@@ -432,41 +440,45 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             res_pending = true;
           }
         }
+#pragma unroll 1
+        for (int i = 0; i < nk; ++i) {
+          const float sa = lds_f32(sa_next);
+          const float2 sb = lds_f32x2(sb_next);
+          sa_next += BM * 4;
+          sb_next += 16;
+          const float f0 = __fmul_rn(sa, sb.x), f1 = SWIGLU ? __fmul_rn(sa, sb.y) : f0;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          tmem_ld_wait();
-          if (c < NC - 1) {
-            tmem_ld_32x32b_x16(t_lane + buf * BN + step_col(c + 1), r[(c + 1) & 1]);
-            if (c == 0 && kb + 1 < kblocks) load_factors(kb + 1);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (PAIR)
-                mbar_arrive_cluster_relaxed(acc_empty0 + buf * 8);
-              else
-                mbar_arrive(&acc_empty[buf]);
-            }
-            if (++buf == C::NBUF) {
-              buf = 0;
-              bphase ^= 1u;
-            }
-            if (kb + 1 < kblocks) {
-              ok &= mbar_wait(&acc_full[buf], bphase, abort_flag, p.status);
+          for (int c = 0; c < NC; ++c) {
+            tmem_ld_wait();
+            if (c < NC - 1) {
+              tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & 1]);
+            } else {
+              tc_fence_before();
               __syncwarp();
-              tc_fence_after();
-              tmem_ld_32x32b_x16(t_lane + buf * BN + step_col(0), r[(c + 1) & 1]);
+              if (lane == 0) {
+                if constexpr (PAIR)
+                  mbar_arrive_cluster_relaxed(acc_empty_at + slot * 8);
+                else
+                  mbar_arrive_at(acc_empty_at + slot * 8);
+              }
+              if (++slot == C::NB) {
+                slot = 0;
+                bphase ^= 1u;
+              }
+              if (kb0 + i + 1 < kblocks) next_block();
             }
-          }
-          // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
-          // the TMEM load does not give without moves (620 against 370 clocks
-          // per 256-column block, measured)
-          const float f = c < NC / 2 ? f0 : f1;
+            // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
+            // the TMEM load does not give without moves (620 against 370
+            // clocks per 256-column block, measured)
+            const float f = c < NC / 2 ? f0 : f1;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            acc[c >> 1][(c & 1) * 16 + j] =
-                __fmaf_rn(__uint_as_float(r[c & 1][j]), f, acc[c >> 1][(c & 1) * 16 + j]);
+            for (int j = 0; j < 16; ++j)
+              acc[c >> 1][(c & 1) * 16 + j] =
+                  __fmaf_rn(__uint_as_float(r[c & 1][j]), f, acc[c >> 1][(c & 1) * 16 + j]);
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(tab_empty_at + side * 8);
       }
       ok = __all_sync(0xffffffffu, ok);
       // ---- the tile's sums are complete
@@ -936,7 +948,7 @@ hb_status launch_wide(const DeviceCtx& ctx, const void* A, const void* B, const 
   CUtensorMap tmA, tmB, tmC, tmR;
   hb_status st = encode_tmap_2d(&tmA, A, p.K, p.M, p.lda, BK, BM, true, 1);
   if (st != HB_OK) return st;
-  st = encode_tmap_2d(&tmB, B, p.K, p.N, p.K, BK, PAIR ? BN / 2 : BN, true, 1);
+  st = encode_tmap_2d(&tmB, B, p.K, p.N, p.K, BK, PAIR ? kSub / 2 : kSub, true, 1);
   if (st != HB_OK) return st;
   constexpr int ESZ = EPI == HB_EPI_F32 ? 4 : 2;
   st = encode_tmap_2d(&tmC, p.C, p.out_cols, p.M, static_cast<uint64_t>(p.ldc) * ESZ, 128 / ESZ, BM, true, ESZ);
