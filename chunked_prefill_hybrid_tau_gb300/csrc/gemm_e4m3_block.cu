@@ -126,7 +126,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = rank == 0;
@@ -185,6 +185,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     // The whole warp walks the loops and one elected lane issues (see the MMA
     // issuer): a single-lane loop needs twice the time per K block.
     const uint64_t wpol = um <= 4 ? policy_evict_first() : policy_evict_normal();
+    const uint32_t empty_at = smem_u32(empty);
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -233,7 +234,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         if (u == first && kb < pre) {
           if (elect_one()) load_a(stage, kb, mt * BM);
         } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait_at(empty_at + stage * 8, phase ^ 1u, abort_flag, p.status));
           if (!ok) break;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           if (elect_one()) {
@@ -657,7 +658,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform to the compiler
   const int lane = threadIdx.x & 31;
   const int kblocks = p.kblocks;
   const int pairs = (kblocks + 1) / 2;  // ring stages of a tile (past K the boxes are zeros)
@@ -695,6 +696,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   if (warp == 4) {
     // ---------------------------------------------------------- TMA producer
     const uint64_t wpol = policy_evict_first();  // each weight box is read once
+    const uint32_t empty_at = smem_u32(empty);
     auto load_w = [&](int s, int pr, int t) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -732,7 +734,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
         const bool fresh = !(t == t0 && pr < pre);
         pending |= 1u << stage;
         if (fresh) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait_at(empty_at + stage * 8, phase ^ 1u, abort_flag, p.status));
           if (!ok) break;
           armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
         }
@@ -760,6 +762,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     griddep_wait();
     constexpr uint32_t kIdesc = idesc_e4m3_f32(BM, NT);
     const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+    const uint32_t full_at = smem_u32(full), acc_empty_at = smem_u32(acc_empty);
     int stage = 0, buf = 0;
     uint32_t phase = 0, bphase = 0;
     bool ok = true;
@@ -767,8 +770,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
 #pragma unroll 1
       for (int pr = 0; pr < pairs; ++pr) {
         const int in_group = pr % (kGroup / 2);
-        ok = mbar_wait(&full[stage], phase, abort_flag, p.status);
-        if (in_group == 0) ok = ok && mbar_wait(&acc_empty[buf], bphase ^ 1u, abort_flag, p.status);
+        ok = mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status);
+        if (in_group == 0) ok = ok && mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -829,6 +832,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
         for (int b = 0; b < 2; ++b)
           table[side * C::TAB + (fi * 2 + b) * NT + fj + 8 * x] = __fmul_rn(pre_a[x], pre_b[b]);
     };
+    const uint32_t table_at = smem_u32(table);
     int buf = 0;
     uint32_t bphase = 0;
     bool ok = true;
@@ -865,7 +869,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
         }
         if (ti == kSkinnyTabK - kGroup && kb0 + kGroup < kblocks) put(side ^ 1);
         if (active) {
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], bphase, abort_flag, p.status));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_at(smem_u32(&acc_full[buf]), bphase, abort_flag, p.status));
           if (ok) {
             tc_fence_after();
             // 32 columns at a time: 32 / NT blocks, or half a block of 64 tokens
@@ -884,7 +888,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
               for (int q = 0; q < 8; ++q) {  // four columns each
                 const int g = (c * 32 + 4 * q) / NT, j = (c * 32 + 4 * q) % NT;
                 if (kb0 + g < kblocks) {
-                  const float4 f = *reinterpret_cast<const float4*>(table + side * C::TAB + ((ti + g) * 2 + blk) * NT + j);
+                  const float4 f = lds_f32x4(table_at + (side * C::TAB + ((ti + g) * 2 + blk) * NT + j) * 4);
                   acc[j] = __fmaf_rn(__uint_as_float(r[4 * q]), f.x, acc[j]);
                   acc[j + 1] = __fmaf_rn(__uint_as_float(r[4 * q + 1]), f.y, acc[j + 1]);
                   acc[j + 2] = __fmaf_rn(__uint_as_float(r[4 * q + 2]), f.z, acc[j + 2]);
