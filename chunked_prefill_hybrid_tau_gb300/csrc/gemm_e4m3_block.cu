@@ -273,9 +273,17 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int u = first; u < units && ok; u += stride) {
 #pragma unroll 1
         for (int kb = 0; kb < kblocks; ++kb) {
-          // the operands first: a buffer's release is the later event in the
-          // steady state, and nothing but the issue should follow it
-          ok = mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status);
+          // All of the block's barriers are tried at once: one after the
+          // other, three tries and their votes took as long as the MMAs.
+          bool ready[C::NSUB + 1];
+          ready[C::NSUB] = mbar_try_wait_at(full_at + stage * 8, phase);
+#pragma unroll
+          for (int i = 0; i < C::NSUB; ++i)
+            ready[i] = mbar_try_wait_at(acc_empty_at + (i * C::NB + slot) * 8, bphase ^ 1u);
+          if (!__all_sync(0xffffffffu, ready[C::NSUB])) {
+            ok = __all_sync(0xffffffffu, mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status));
+            if (!ok) break;
+          }
           // the start address is the low 14 bits of a descriptor, in 16-byte
           // units, and shared memory ends below 2^18 bytes: it cannot carry
           const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
@@ -283,9 +291,10 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
           for (int i = 0; i < C::NSUB; ++i) {
             const int buf = i * C::NB + slot;
             const uint32_t d_tmem = tmem_base + buf * kSub;
-            ok = ok && mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
+            if (!__all_sync(0xffffffffu, ready[i])) {
+              ok = __all_sync(0xffffffffu, mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status));
+              if (!ok) break;
+            }
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
