@@ -72,10 +72,13 @@ __device__ __forceinline__ int scale_row(const Params& p, int n) {
 //               BN / 2 fp32 sums of one row and scales a K block with one
 //               factor (SWIGLU: one for its gate, one for its up columns);
 //   warp 8    : TMA producer (128-byte swizzled boxes of one K block);
-//   warp 9    : MMA issuer.  TMEM holds four buffers of 128 columns; a K block
+//   warps 9-10: MMA issuers.  TMEM holds four buffers of 128 columns; a K block
 //               is BN / 128 of them, each with its own pair of barriers: at BN
-//               = 256 every column half is refilled while the other is read;
-//   warps 10-11: fill the table of scales.
+//               = 256 every column half is refilled while the other is read.
+//               The two warps take the column halves (BN 128: every second K
+//               block): what one thread needs for its tries, MMAs and commits
+//               is longer than the MMAs themselves;
+//   warp 11   : fills the table of scales.
 // The sums leave through shared memory staged apart from the ring and TMA
 // stores, so the next tile's loads and MMAs go on meanwhile.
 constexpr int kTabK = 8;  // K blocks per fill of the scale table
@@ -141,17 +144,17 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], C::NSUB);
     }
     for (int a = 0; a < kBufs; ++a) {
       mbar_init(&acc_full[a], 1);
       mbar_init(&acc_empty[a], (PAIR ? 16 : 8) / C::NSUB);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&tab_full[b], 64);
+      mbar_init(&tab_full[b], 32);
       mbar_init(&tab_empty[b], 8);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     mbar_init(res_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -257,8 +260,8 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int s = 0; s < C::STAGES; ++s)
         if (pending & (1u << s)) mbar_drain(PAIR ? &empty[s] : &full[s], (armed_parity >> s) & 1u);
     }
-  } else if (warp == 9) {
-    // ---------------------------------------------------------- MMA issuer
+  } else if (warp <= 10) {
+    // ---------------------------------------------------------- MMA issuers
     griddep_wait();
     if (leader) {
       // the whole warp walks the loop and one elected lane issues: inside a
@@ -267,64 +270,62 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       constexpr uint32_t kIdesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, kSub);
       const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
       const uint32_t full_at = smem_u32(full), acc_empty_at = smem_u32(acc_empty);
-      int stage = 0, slot = 0;
+      const int me = warp - 9;
+      // the K blocks (BN 128: every second one; their count runs over the
+      // tiles) and the column half that are this warp's
+      constexpr int STEP = C::NSUB == 2 ? 1 : 2;
+      const int sub = C::NSUB == 2 ? me : 0;
+      const uint32_t b_off = static_cast<uint32_t>((C::A_BYTES + sub * C::SUB_BYTES) >> 4);
+      int stage = C::NSUB == 2 ? 0 : me, slot = stage;
       uint32_t phase = 0, bphase = 0;
       bool ok = true;
-      for (int u = first; u < units && ok; u += stride) {
+      const int mine = (units - first + stride - 1) / stride;  // tiles of this CTA
+      const long long blocks = mine > 0 ? static_cast<long long>(mine) * kblocks : 0;
 #pragma unroll 1
-        for (int kb = 0; kb < kblocks; ++kb) {
-          // All of the block's barriers are tried at once: one after the
-          // other, three tries and their votes took as long as the MMAs.
-          bool ready[C::NSUB + 1];
-          ready[C::NSUB] = mbar_try_wait_at(full_at + stage * 8, phase);
-#pragma unroll
-          for (int i = 0; i < C::NSUB; ++i)
-            ready[i] = mbar_try_wait_at(acc_empty_at + (i * C::NB + slot) * 8, bphase ^ 1u);
-          if (!__all_sync(0xffffffffu, ready[C::NSUB])) {
-            ok = __all_sync(0xffffffffu, mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status));
-            if (!ok) break;
-          }
-          // the start address is the low 14 bits of a descriptor, in 16-byte
-          // units, and shared memory ends below 2^18 bytes: it cannot carry
-          const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
-#pragma unroll
-          for (int i = 0; i < C::NSUB; ++i) {
-            const int buf = i * C::NB + slot;
-            const uint32_t d_tmem = tmem_base + buf * kSub;
-            if (!__all_sync(0xffffffffu, ready[i])) {
-              ok = __all_sync(0xffffffffu, mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status));
-              if (!ok) break;
-            }
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint64_t ad = a_desc + 2 * k;
-                const uint64_t bd = ad + ((C::A_BYTES + i * C::SUB_BYTES) >> 4);
-                if constexpr (PAIR)
-                  mma_e4m3_pair(d_tmem, ad, bd, kIdesc, k != 0);
-                else
-                  mma_e4m3(d_tmem, ad, bd, kIdesc, k != 0);
-              }
-              if constexpr (PAIR) {
-                mma_commit_pair(&acc_full[buf], 3);
-                if (i == C::NSUB - 1) mma_commit_pair(&empty[stage], 3);
-              } else {
-                mma_commit(&acc_full[buf]);
-                if (i == C::NSUB - 1) mma_commit(&empty[stage]);
-              }
-            }
-            __syncwarp();
-          }
+      for (long long kb = C::NSUB == 2 ? 0 : me; kb < blocks; kb += STEP) {
+        const int buf = sub * C::NB + slot;
+        // both barriers are tried at once: one after the other, the tries and
+        // their votes took as long as the MMAs
+        const bool has_data = mbar_try_wait_at(full_at + stage * 8, phase);
+        const bool has_buf = mbar_try_wait_at(acc_empty_at + buf * 8, bphase ^ 1u);
+        if (!__all_sync(0xffffffffu, has_data && has_buf)) {
+          ok = mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status) &&
+               mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        }
+        tc_fence_after();
+        // the start address is the low 14 bits of a descriptor, in 16-byte
+        // units, and shared memory ends below 2^18 bytes: it cannot carry
+        const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+        const uint64_t b_desc = a_desc + b_off;
+        const uint32_t d_tmem = tmem_base + buf * kSub;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (PAIR)
+              mma_e4m3_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
+            else
+              mma_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
           }
-          if (++slot == C::NB) {
-            slot = 0;
-            bphase ^= 1u;
+          if constexpr (PAIR) {
+            mma_commit_pair(&acc_full[buf], 3);
+            mma_commit_pair(&empty[stage], 3);
+          } else {
+            mma_commit(&acc_full[buf]);
+            mma_commit(&empty[stage]);
           }
+        }
+        __syncwarp();
+        stage += STEP;
+        if (stage >= C::STAGES) {
+          stage -= C::STAGES;
+          phase ^= 1u;
+        }
+        slot += STEP;
+        if (slot >= C::NB) {
+          slot -= C::NB;
+          bphase ^= 1u;
         }
       }
       if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
@@ -339,45 +340,46 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       mbar_drain(drain, 0);
     }
   } else {
-    // ---------------------------------------------------------- scale table (two warps)
+    // ---------------------------------------------------------- scale table
     // Scales of the tile's rows and weight blocks, kTabK K blocks at a time,
     // two fills ahead of the sums.  (Read by the promotion warps themselves,
     // each row of sa is a cache line of its own: 128 lines and the few spills
     // outgrew the L1 left beside the ring, and a K block took three times as
     // long.)
     griddep_wait();
-    const int t64 = static_cast<int>(threadIdx.x) - 320;
     int fill = 0;
     bool ok = true;
     for (int u = first; u < units; u += stride) {
       const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
       const int n0 = (u / um) * BN;
-      const int ra = mt * BM + t64, rb = ra + 64;
-      const float* pa = p.sa + static_cast<size_t>(ra < p.M ? ra : 0) * kblocks;
-      const float* pb = p.sa + static_cast<size_t>(rb < p.M ? rb : 0) * kblocks;
-      // weight block j: column half j / 2's gate (or only) block, and its up block (BN 128: one block's half each)
-      const int j = t64 & 3;
-      const int n = n0 + (j >> 1) * (BN == 256 ? 128 : SWIGLU ? 0 : 64) + (SWIGLU ? (j & 1) * 64 : 0);
-      const float* ps =
-          p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n < p.N ? n : p.N - 1)) * kblocks + (t64 >> 2);
-      for (int kb0 = 0; kb0 < kblocks; kb0 += kTabK, ++fill) {
-        float va[kTabK], vb[kTabK];
+      const float* pa[4];
+      bool in_m[4];
 #pragma unroll
-        for (int i = 0; i < kTabK; ++i) {
-          const bool in = kb0 + i < kblocks;
-          va[i] = in && ra < p.M ? __ldg(pa + kb0 + i) : 0.f;
-          vb[i] = in && rb < p.M ? __ldg(pb + kb0 + i) : 0.f;
-        }
-        const float vs = t64 < 4 * kTabK && kb0 + (t64 >> 2) < kblocks ? __ldg(ps + kb0) : 0.f;
+      for (int q = 0; q < 4; ++q) {
+        const int row = mt * BM + q * 32 + lane;
+        in_m[q] = row < p.M;
+        pa[q] = p.sa + static_cast<size_t>(in_m[q] ? row : 0) * kblocks;
+      }
+      // weight block j: buffer j / 2's gate (or only) block, and its up block
+      const int j = lane & 3;
+      const int n = n0 + (BN == 256 ? (j >> 1) * kSub : 0) + (SWIGLU ? (j & 1) * 64 : 0);
+      const float* ps =
+          p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n < p.N ? n : p.N - 1)) * kblocks + (lane >> 2);
+      for (int kb0 = 0; kb0 < kblocks; kb0 += kTabK, ++fill) {
+        float va[4][kTabK];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < kTabK; ++i) va[q][i] = kb0 + i < kblocks && in_m[q] ? __ldg(pa[q] + kb0 + i) : 0.f;
+        const float vs = kb0 + (lane >> 2) < kblocks ? __ldg(ps + kb0) : 0.f;
         const int b = fill & 1;
         if (ok) ok = mbar_wait(&tab_empty[b], ((fill >> 1) & 1) ^ 1u, abort_flag, p.status);
         float* tab = table + b * (C::TABLE / 4);
 #pragma unroll
-        for (int i = 0; i < kTabK; ++i) {
-          tab[i * BM + t64] = va[i];
-          tab[i * BM + t64 + 64] = vb[i];
-        }
-        if (t64 < 4 * kTabK) tab[kTabK * BM + t64] = vs;
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < kTabK; ++i) tab[i * BM + q * 32 + lane] = va[q][i];
+        tab[kTabK * BM + lane] = vs;
         mbar_arrive(&tab_full[b]);
       }
     }
