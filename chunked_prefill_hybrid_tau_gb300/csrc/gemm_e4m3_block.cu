@@ -425,13 +425,15 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       uint32_t r[2][16];
       const uint32_t t_cols = t_lane + sub * C::NB * kSub - sub * kSub;
       auto step_col = [&](int c) { return chunk_col(c >> 1) + (c & 1) * 16; };
-      auto next_block = [&]() {  // waits for the next K block in TMEM and starts its first columns
-        ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
+      // waits for the next K block in TMEM and starts its first columns;
+      // there: an earlier try has found it complete
+      auto next_block = [&](bool there) {
+        if (!__all_sync(0xffffffffu, there)) ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
         __syncwarp();
         tc_fence_after();
         tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(0), r[0]);
       };
-      next_block();
+      next_block(false);
 #pragma unroll 1
       for (int kb0 = 0; kb0 < kblocks; kb0 += kTabK, ++fill) {
         const int side = fill & 1;
@@ -459,9 +461,18 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
           sa_next += BM * 4;
           sb_next += 16;
           const float f0 = __fmul_rn(sa, sb.x), f1 = SWIGLU ? __fmul_rn(sa, sb.y) : f0;
+          const bool more = kb0 + i + 1 < kblocks, wrap = slot + 1 == C::NB;
+          const int next_slot = !more ? slot : wrap ? 0 : slot + 1;
+          const uint32_t next_phase = more && wrap ? bphase ^ 1u : bphase;
+          bool there = false;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             tmem_ld_wait();
+            // Late enough to find it, early enough that its latency passes
+            // under the sums.  Past the tile's last block there is nothing to
+            // find, and a try would hold the thread in vain: it takes the
+            // present block, which is complete.
+            if (c == NC - 2) there = mbar_try_wait_at(acc_full_at + next_slot * 8, next_phase);
             if (c < NC - 1) {
               tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & 1]);
             } else {
@@ -477,7 +488,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
                 slot = 0;
                 bphase ^= 1u;
               }
-              if (kb0 + i + 1 < kblocks) next_block();
+              if (more) next_block(there);
             }
             // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
             // the TMEM load does not give without moves (620 against 370
