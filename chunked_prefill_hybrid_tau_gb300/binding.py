@@ -32,18 +32,42 @@ def _check(status: int, name: str):
         raise HBError(status, f"{name}: {lb.hb_status_string(status).decode()}: {lb.hb_last_error().decode()}")
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """Handle of torch's current stream on the current device.  torch's raw
+    accessors where it has them: the Stream object that current_stream()
+    builds takes 3 us of host time, more than a launch."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if get is None or device is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            _raw_stream = lambda: get(device())  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream):
-    import torch
     if stream is None:
-        return C.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return C.c_void_p(stream)
-    return C.c_void_p(stream.cuda_stream)
+        return _current_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _p(t):
     """Device pointer of a tensor (None -> NULL)."""
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+def _need(call, name, t, size, count):
+    """A contiguous device tensor of at least `count` elements of `size` bytes
+    (the kernels address it by its first element alone)."""
+    if t.numel() < count or t.element_size() != size or not t.is_contiguous() or not t.is_cuda:
+        raise HBError(L.HB_ERR_INVALID_ARG,
+                      f"{call}: {name} must be a contiguous device tensor of at least {count} elements of {size} "
+                      f"bytes, not {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
 
 
 def dims_struct(dims) -> L.hb_layer_dims:
@@ -311,9 +335,16 @@ def hb_kv_append_norm(qkv, row_pos, slot_mapping, rope, max_pos, dims, g_q, g_k,
                       stream=None):
     """hb_kv_append with q and k heads RMS-normed (gains g_q, g_k bf16 [d_head])."""
     ds = dims_struct(dims)
-    _check(lib().hb_kv_append_norm(_p(qkv), int(qkv.shape[0]), _p(row_pos), _p(slot_mapping), _p(rope), int(max_pos),
-                                   C.byref(ds), _p(g_q), _p(g_k), _p(q_out), _p(k_cache), _p(v_cache),
-                                   int(k_cache.shape[0]), _stream(stream)), "hb_kv_append_norm")
+    T, dh, pages = qkv.shape[0], ds.d_head, k_cache.shape[0]
+    slot = ds.n_kv * 16 * dh
+    for name, t, size, count in (("qkv", qkv, 2, T * (ds.n_q + 2 * ds.n_kv) * dh), ("row_pos", row_pos, 4, T),
+                                 ("slot_mapping", slot_mapping, 4, T), ("rope", rope, 4, max_pos * dh),
+                                 ("g_q", g_q, 2, dh), ("g_k", g_k, 2, dh), ("q_out", q_out, 2, T * ds.n_q * dh),
+                                 ("k_cache", k_cache, 2, pages * slot), ("v_cache", v_cache, 2, pages * slot)):
+        _need("hb_kv_append_norm", name, t, size, count)
+    _check(lib().hb_kv_append_norm(_p(qkv), T, _p(row_pos), _p(slot_mapping), _p(rope), int(max_pos), C.byref(ds),
+                                   _p(g_q), _p(g_k), _p(q_out), _p(k_cache), _p(v_cache), pages, _stream(stream)),
+           "hb_kv_append_norm")
 
 
 def hb_attention_workspace_bytes(dims, max_rows, max_seqs, max_kv_len) -> int:
@@ -358,13 +389,16 @@ def hb_quantize_e4m3_block(x, q=None, scale=None, block_rows=1, stream=None):
     """E4M3 codes (uint8 [rows][cols]) of a device bf16 matrix x with one fp32
     scale per 1 x 128 (block_rows=1) or 128 x 128 (block_rows=128) block;
     returns (q, scale [ceil(rows / block_rows)][ceil(cols / 128)])."""
-    import torch
     rows, cols = x.shape
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device) if q is None else q
-    if scale is None:
-        scale = torch.empty((-(-rows // block_rows) if block_rows > 0 else 0, -(-cols // 128)), dtype=torch.float32,
-                            device=x.device)
-    _check(lib().hb_quantize_e4m3_block(_p(x), _p(q), _p(scale), rows, cols, int(block_rows), _stream(stream)),
+    groups = (rows + block_rows - 1) // block_rows if block_rows > 0 else 0, (cols + 127) // 128
+    if q is None or scale is None:
+        import torch
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device) if q is None else q
+        scale = torch.empty(groups, dtype=torch.float32, device=x.device) if scale is None else scale
+    _need("hb_quantize_e4m3_block", "x", x, 2, 0)
+    _need("hb_quantize_e4m3_block", "q", q, 1, rows * cols)
+    _need("hb_quantize_e4m3_block", "scale", scale, 4, groups[0] * groups[1])
+    _check(lib().hb_quantize_e4m3_block(_p(x), _p(q), _p(scale), rows, cols, block_rows, _stream(stream)),
            "hb_quantize_e4m3_block")
     return q, scale
 
@@ -374,8 +408,18 @@ def hb_gemm_e4m3_block(A, s_a, B, s_b, Cout, R=None, epilogue=L.HB_EPI_STORE, st
     scales s_a [M][ceil(K / 128)], s_b [ceil(N / 128)][ceil(K / 128)]."""
     M, K = A.shape
     N = B.shape[0]
+    kb = (K + 127) // 128
+    swiglu = epilogue == L.HB_EPI_SWIGLU
+    call = "hb_gemm_e4m3_block"
+    _need(call, "A", A, 1, 0)
+    _need(call, "B", B, 1, N * K)
+    _need(call, "s_a", s_a, 4, M * kb)
+    _need(call, "s_b", s_b, 4, (2 * ((N + 255) // 256) if swiglu else (N + 127) // 128) * kb)
+    _need(call, "C", Cout, 4 if epilogue == L.HB_EPI_F32 else 2, M * N // 2 if swiglu else M * N)
+    if R is not None:
+        _need(call, "R", R, 2, M * N)
     _check(lib().hb_gemm_e4m3_block(_p(A), _p(s_a), _p(B), _p(s_b), _p(Cout), _p(R), M, N, K, int(epilogue),
-                                    _stream(stream)), "hb_gemm_e4m3_block")
+                                    _stream(stream)), call)
 
 
 def hb_interleave_gate_up(w_gate, w_up, w_gu, stream=None):
