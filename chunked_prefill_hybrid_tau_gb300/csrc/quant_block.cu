@@ -9,12 +9,16 @@
 // a group of zeros gets scale 0 and zero codes.  The floor 2^-112 keeps inv
 // (2^120.8) and scale (2^-120.8) normal fp32 numbers: without it 448 / amax
 // is infinite for amax below 2^-119.2 and a zero beside such a value becomes
-// 0 * inf = NaN.  A NaN or an infinity makes the codes of its own group NaN
-// where it stands (an infinity: in the whole group) and leaves other groups
-// alone.
+// 0 * inf = NaN.  The formulas hold for a NaN and an infinity too: a NaN
+// makes its group's scale and codes NaN, an infinity makes the scale
+// infinite, its own code NaN and the others zero; other groups do not notice.
 //
 // Both kernels read 2 bytes and write 1 byte an element once, so HBM bounds
-// them.
+// them if the instructions an element stay few.  With fp32 maxima and two
+// divisions for every group and lane the token kernel took 66.4 us for 8192 x
+// 14336 (52.6 at the copy rate), most of it issuing.  So the maximum runs
+// over the bit patterns, two at a time (the magnitudes of bf16 numbers order
+// as their bits do, NaN above all), and a lane divides for one group only.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -37,14 +41,20 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float inv) {
   return static_cast<uint32_t>(v);
 }
 
-__device__ __forceinline__ float amax8(const uint4& v, float m) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = unpack_bf16x2(w[j]);
-    m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));
-  }
-  return m;
+// Maxima of the magnitudes of two bf16 numbers, as bit patterns.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t amax8(const uint4& v) {
+  constexpr uint32_t kMag = 0x7fff7fffu;
+  return max2(max2(v.x & kMag, v.y & kMag), max2(v.z & kMag, v.w & kMag));
+}
+// The larger of the two, as fp32.
+__device__ __forceinline__ float amax_value(uint32_t m) {
+  const uint32_t hi = m & 0xffff0000u, lo = m << 16;
+  return __uint_as_float(hi > lo ? hi : lo);
 }
 
 __device__ __forceinline__ uint2 codes8(const uint4& v, float inv) {
@@ -62,17 +72,18 @@ struct GroupScale {
   float inv, scale;
 };
 __device__ __forceinline__ GroupScale group_scale(float amax) {
-  const float top = fmaxf(amax, kAmaxMin);
-  const bool nz = amax > 0.f;
-  return {nz ? __fdiv_rn(448.0f, top) : 0.f, nz ? __fdiv_rn(top, 448.0f) : 0.f};
+  if (amax == 0.f) return {0.f, 0.f};
+  const float top = amax < kAmaxMin ? kAmaxMin : amax;  // a NaN stays
+  return {__fdiv_rn(448.0f, top), __fdiv_rn(top, 448.0f)};
 }
 
 // Tokens: 16 lanes own one group (16 bytes of bf16 each), so the group's
 // maximum is four shuffles and no group meets another.  A CTA's 16 half
 // warps cover 2^gshift groups of 16 >> gshift rows; each takes U groups,
 // 2^gshift apart, with all loads in flight.
+// (40 registers, six CTAs an SM: 55.0 us for 8192 x 14336; 42, five: 57.3.)
 template <int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __maxnreg__(40)
     quant_groups_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int rows,
                         int c8, int kb, int gshift) {
   griddep_launch_dependents();
@@ -88,16 +99,25 @@ __global__ void __launch_bounds__(kThreads)
     const int i = (g0 + (u << gshift)) * 16 + l;
     v[u] = row_ok && i < c8 ? x[base + i] : make_uint4(0, 0, 0, 0);
   }
+  uint32_t m[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float m = amax8(v[u], 0.f);
+    m[u] = amax8(v[u]);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const GroupScale gs = group_scale(m);
-    const int g = g0 + (u << gshift);
-    const int i = g * 16 + l;
-    if (row_ok && i < c8) q[base + i] = codes8(v[u], gs.inv);
-    if (row_ok && g < kb && l == 0) scale[static_cast<size_t>(row) * kb + g] = gs.scale;
+    for (int o = 8; o > 0; o >>= 1) m[u] = max2(m[u], __shfl_xor_sync(0xffffffffu, m[u], o));
+  }
+  // lane l of the group divides for group l % U and hands the factor round
+  uint32_t mine = m[0];
+#pragma unroll
+  for (int u = 1; u < U; ++u) mine = l % U == u ? m[u] : mine;
+  const GroupScale gs = group_scale(amax_value(mine));
+  const int g_mine = g0 + (l << gshift);
+  if (row_ok && l < U && g_mine < kb) scale[static_cast<size_t>(row) * kb + g_mine] = gs.scale;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float inv = __shfl_sync(0xffffffffu, gs.inv, u, 16);
+    const int i = (g0 + (u << gshift)) * 16 + l;
+    if (row_ok && i < c8) q[base + i] = codes8(v[u], inv);
   }
 }
 
@@ -105,11 +125,13 @@ __global__ void __launch_bounds__(kThreads)
 // bytes a thread) between its maximum and its codes.  The launch signals no
 // dependent early: a projection may read its weights before it waits for the
 // kernel ahead of it.
-__global__ void __launch_bounds__(kThreads)
+// (64 registers, four CTAs an SM: 51.8 us for 28672 x 4096, the copy rate;
+// 89 registers, two: 61.2.)
+__global__ void __maxnreg__(64)
     quant_blocks_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int rows,
                         int c8, int kb) {
   griddep_wait();
-  __shared__ float red[kThreads / 32];
+  __shared__ uint32_t red[kThreads / 32];
   const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   const int i = blockIdx.x * 16 + l;
   const int row0 = blockIdx.y * 128 + r0;
@@ -119,16 +141,16 @@ __global__ void __launch_bounds__(kThreads)
     const int r = row0 + 16 * u;
     v[u] = r < rows && i < c8 ? x[static_cast<size_t>(r) * c8 + i] : make_uint4(0, 0, 0, 0);
   }
-  float m = 0.f;
+  uint32_t m = 0;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) m = amax8(v[u], m);
+  for (int u = 0; u < 8; ++u) m = max2(m, amax8(v[u]));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 16; o > 0; o >>= 1) m = max2(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, red[w]);
-  const GroupScale gs = group_scale(m);
+  for (int w = 0; w < kThreads / 32; ++w) m = max2(m, red[w]);
+  const GroupScale gs = group_scale(amax_value(m));
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     const int r = row0 + 16 * u;

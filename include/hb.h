@@ -377,7 +377,8 @@ hb_status hb_gemm_e4m3(const void* A, const float* s_a, const void* B, const flo
  *   scale = top / 448 (correctly rounded fp32 divisions),
  *   q = E4M3(fp32(x * inv)), nearest-even, saturating to +-448;
  * an all-zero block gets scale 0 and zero codes.  The floor 2^-112 keeps inv
- * and scale finite and normal.  A NaN or infinity spoils its own block only.
+ * and scale finite and normal.  A NaN makes the scale and codes of its block
+ * NaN, an infinity makes its block's scale infinite.
  * q: device bytes [rows][cols]; scale: device fp32
  * [ceil(rows / block_rows)][ceil(cols / 128)].  cols % 16 == 0, cols <=
  * 2^24, rows <= 8388480; x and q 16-byte aligned.  Asynchronous on stream.

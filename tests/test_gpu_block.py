@@ -90,8 +90,9 @@ def test_quantize_block_tiny_and_non_finite(block_rows):
     qr, sr = of.quantize_blocks(xf, block_rows)
     assert np.array_equal(q[0, :256], qr[0, :256]) and np.array_equal(s[0, :2], sr[0, :2])
     assert np.array_equal(q[129], qr[129]) and s[-1, 1] == sr[-1, 1]
-    assert (q[0, 256] & 0x7F) == 0x7F and q[0, 257] == 0x7E     # NaN beside the group's 448
-    assert np.all((q[0, 384] & 0x7F) == 0x7F) and np.isinf(s[0, 3])
+    # a NaN: scale and codes of its group; an infinity: infinite scale, NaN where it stands
+    assert np.all((q[0, 256:384] & 0x7F) == 0x7F) and np.isnan(s[0, 2])
+    assert (q[0, 384] & 0x7F) == 0x7F and np.isinf(s[0, 3]) and np.all((q[0, 385:] & 0x7F) == 0)
 
 
 def test_quantize_block_leaves_the_rest_alone():
