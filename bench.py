@@ -47,8 +47,8 @@ def parse():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--tau", type=int, default=512)
     ap.add_argument("--decodes", type=int, default=32)
-    ap.add_argument("--weights", default="bf16", choices=["bf16", "e4m3"],
-                    help="projection weights: bf16, or E4M3 codes with per-row scales (FP8 projections)")
+    ap.add_argument("--weights", default="bf16", choices=["bf16", "e4m3", "e4m3_block"],
+                    help="projection weights: bf16, or E4M3 codes with per-row or per-block scales (FP8 projections)")
     ap.add_argument("--sweep", action="store_true",
                     help="token-budget sweep (tau 64..4096, 64 decodes, c = tau - 64): one JSON line per tau")
     ap.add_argument("--calibrate", type=float, default=None, metavar="SLO_MS",
@@ -89,12 +89,14 @@ def max_over_ranks(v: float, world: int) -> float:
 
 
 # ---------------------------------------------------------------- workload
-def launches_per_layer(dims, f8: bool, n_rows: int) -> int:
+def launches_per_layer(dims, weights, n_rows: int) -> int:
     """Kernels one hb_layer_forward launches, by the library's own rule
     (hb_layer_kernel_count: the chunk and decode attention kernels are both
-    launched whatever the batch holds)."""
+    launched whatever the batch holds).  weights: the format's name, or
+    whether it is E4M3 with per-row scales."""
     import chunked_prefill_hybrid_tau_gb300 as hb
-    return hb.hb_layer_kernel_count(dims, n_rows, 1 if f8 else 0)
+    fmt = {False: 0, True: 1, "bf16": 0, "e4m3": 1, "e4m3_block": 2}[weights]
+    return hb.hb_layer_kernel_count(dims, n_rows, fmt)
 
 
 def make_workload(tau: int, n_dec: int):
@@ -303,7 +305,7 @@ def workload_config(w, weights, world, T, n_dec):
     """The `config` of the bench line, the same for the GPU arm and the
     reference arm (T rows per iteration, n_dec of them decodes)."""
     dims = w.dims
-    return {"workload": WORKLOAD + ("_e4m3" if weights == "e4m3" else ""), "tau": w.tau, "weights": weights,
+    return {"workload": WORKLOAD + ("" if weights == "bf16" else "_" + weights), "tau": w.tau, "weights": weights,
             "chunk_tokens": T - n_dec, "decodes": n_dec, "rows": T, "d_model": dims.d_model,
             "heads": f"{dims.n_q}q/{dims.n_kv}kv", "d_head": dims.d_head, "d_ff": dims.d_ff, "page": 16,
             "parallelism": f"replicas{world}" if world > 1 else "single",
@@ -372,7 +374,7 @@ def run_hb(args, world, rank, local):
     w = make_workload(args.tau, args.decodes)
     st, dims = w.state, w.dims
     max_pos = max(r.done for r in st.decodes + st.prefills) + w.tau + 1
-    f8 = args.weights == "e4m3"
+    f8 = args.weights != "bf16"
     gw = wd.layer_weights_device(w.weights[0], dims, dev, fmt=args.weights)
     kc, vc = wd.bf16_tensor(st.k_pool, dev), wd.bf16_tensor(st.v_pool, dev)
     rope = wd.rope_table_device(max_pos, dims, dev)
@@ -421,9 +423,9 @@ def run_hb(args, world, rank, local):
         layer(runner.step(stream), x_dev, out_dev)
     end.record(stream)
     launches = hb.hb_kernel_launches() - launches0  # this library's kernels in the timed region
-    if launches != launches_per_layer(dims, f8, runner.n_rows) * args.steps:
+    if launches != launches_per_layer(dims, args.weights, runner.n_rows) * args.steps:
         print(f"warning: {launches} kernels launched in the timed region, the library's rule says "
-              f"{launches_per_layer(dims, f8, runner.n_rows) * args.steps}", file=sys.stderr)
+              f"{launches_per_layer(dims, args.weights, runner.n_rows) * args.steps}", file=sys.stderr)
     torch.cuda.synchronize(dev)
     barrier(world)
     hb.hb_check_status(stream)
@@ -592,7 +594,7 @@ def run_sweep(args, taus=None, emit=True):
     w = make_workload(max(taus), 64)
     st, dims = w.state, w.dims
     max_pos = 8192 + max(taus) + 1
-    f8 = args.weights == "e4m3"
+    f8 = args.weights != "bf16"
     gw = wd.layer_weights_device(w.weights[0], dims, fmt=args.weights)
     kc, vc = wd.bf16_tensor(st.k_pool), wd.bf16_tensor(st.v_pool)
     rope = wd.rope_table_device(max_pos, dims)

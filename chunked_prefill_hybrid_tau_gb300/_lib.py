@@ -44,7 +44,7 @@ class hb_device_plan(C.Structure):
 
 class hb_layer_weights(C.Structure):
     _fields_ = [("w_qkv", vp), ("w_o", vp), ("w_gu", vp), ("w_d", vp),
-                ("s_qkv", vp), ("s_o", vp), ("s_gu", vp), ("s_d", vp), ("format", i32)]
+                ("s_qkv", vp), ("s_o", vp), ("s_gu", vp), ("s_d", vp), ("format", i32), ("g_q", vp), ("g_k", vp)]
 
 
 class hb_profile(C.Structure):
@@ -53,7 +53,8 @@ class hb_profile(C.Structure):
 
 HB_LAYER_STAGES = 8
 HB_EPI_STORE, HB_EPI_RESIDUAL, HB_EPI_SWIGLU, HB_EPI_F32 = 0, 1, 2, 3
-HB_WEIGHTS_BF16, HB_WEIGHTS_E4M3 = 0, 1
+HB_WEIGHTS_BF16, HB_WEIGHTS_E4M3, HB_WEIGHTS_E4M3_BLOCK = 0, 1, 2
+HB_LAYER_QK_NORM = 256
 HB_OK, HB_ERR_INVALID_ARG, HB_ERR_CAPACITY, HB_ERR_OUT_OF_PAGES = 0, 1, 2, 3
 HB_ERR_CUDA, HB_ERR_TIMEOUT, HB_ERR_UNSUPPORTED, HB_ERR_DEVICE = 4, 5, 6, 7
 

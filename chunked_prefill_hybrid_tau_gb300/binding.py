@@ -436,28 +436,44 @@ def hb_fold_gamma(w, gamma, out=None, stream=None):
     return out
 
 
-def prepare_layer_weights(w_qkv, w_o, w_g, w_u, w_d, g1, g2, stream=None, fmt="bf16") -> "LayerWeights":
+def prepare_layer_weights(w_qkv, w_o, w_g, w_u, w_d, g1, g2, stream=None, fmt="bf16", g_q=None,
+                          g_k=None) -> "LayerWeights":
     """Raw device bf16 weights of one layer -> the prepared form that
     hb_layer_forward takes: g1 folded into W_qkv, gate/up interleaved and g2
     folded into them (include/hb.h, hb_layer_weights).  w_qkv is folded in
     place; w_g and w_u are left as they are.  fmt="e4m3": each prepared
     matrix is then quantized per row (hb_quantize_e4m3) and the bf16 forms
-    are released."""
+    are released; fmt="e4m3_block": per 128 x 128 block
+    (hb_quantize_e4m3_block), gate and up each on its own before they are
+    interleaved.  g_q, g_k: bf16 [d_head] gains of normed q and k heads."""
     import torch
     F, d = w_g.shape
     f_pad = (F + 63) // 64 * 64
+    gains = dict(g_q=g_q, g_k=g_k)
+    if fmt == "e4m3_block":
+        def block(w):
+            return hb_quantize_e4m3_block(w, block_rows=128, stream=stream)
+
+        hb_fold_gamma(w_qkv, g1, stream=stream)
+        (gate, s_g), (up, s_u) = (block(hb_fold_gamma(w, g2, torch.empty_like(w), stream=stream)) for w in (w_g, w_u))
+        w_gu = torch.empty((2 * f_pad, d), dtype=torch.uint8, device=w_g.device)
+        # codes in pairs: the interleave moves 16-bit elements as they are
+        hb_interleave_gate_up(gate.view(torch.bfloat16), up.view(torch.bfloat16), w_gu.view(torch.bfloat16), stream)
+        q = {k: block(v) for k, v in (("qkv", w_qkv), ("o", w_o), ("d", w_d))}
+        return LayerWeights(w_qkv=q["qkv"][0], w_o=q["o"][0], w_gu=w_gu, w_d=q["d"][0], s_qkv=q["qkv"][1],
+                            s_o=q["o"][1], s_gu=torch.cat([s_g, s_u]), s_d=q["d"][1], fmt=fmt, **gains)
     w_gu = torch.empty((2 * f_pad, d), dtype=torch.bfloat16, device=w_g.device)
     hb_interleave_gate_up(w_g, w_u, w_gu, stream)
     hb_fold_gamma(w_gu, g2, stream=stream)
     hb_fold_gamma(w_qkv, g1, stream=stream)
     if fmt == "bf16":
-        return LayerWeights(w_qkv=w_qkv, w_o=w_o, w_gu=w_gu, w_d=w_d)
+        return LayerWeights(w_qkv=w_qkv, w_o=w_o, w_gu=w_gu, w_d=w_d, **gains)
     if fmt != "e4m3":
         raise ValueError(f"unknown weight format {fmt!r}")
     q = {k: hb_quantize_e4m3(v, stream=stream) for k, v in
          (("qkv", w_qkv), ("o", w_o), ("gu", w_gu), ("d", w_d))}
     return LayerWeights(w_qkv=q["qkv"][0], w_o=q["o"][0], w_gu=q["gu"][0], w_d=q["d"][0], s_qkv=q["qkv"][1],
-                        s_o=q["o"][1], s_gu=q["gu"][1], s_d=q["d"][1], fmt="e4m3")
+                        s_o=q["o"][1], s_gu=q["gu"][1], s_d=q["d"][1], fmt="e4m3", **gains)
 
 
 def hb_layer_workspace_bytes(dims, max_rows, max_seqs, max_kv_len) -> int:
@@ -475,7 +491,8 @@ def hb_layer_kernel_count(dims, n_rows, fmt) -> int:
 @dataclasses.dataclass
 class LayerWeights:
     """Prepared device weights of one layer (prepare_layer_weights): bf16
-    tensors, or E4M3 codes (uint8) with fp32 per-row scales."""
+    tensors, or E4M3 codes (uint8) with fp32 per-row or per-block scales;
+    g_q and g_k where q and k heads are normed."""
     w_qkv: object
     w_o: object
     w_gu: object
@@ -485,13 +502,17 @@ class LayerWeights:
     s_gu: object = None
     s_d: object = None
     fmt: str = "bf16"
+    g_q: object = None
+    g_k: object = None
+
+    FORMATS = {"bf16": L.HB_WEIGHTS_BF16, "e4m3": L.HB_WEIGHTS_E4M3, "e4m3_block": L.HB_WEIGHTS_E4M3_BLOCK}
 
     def struct(self) -> L.hb_layer_weights:
         ptrs = [self.__dict__[k].data_ptr() for k in ("w_qkv", "w_o", "w_gu", "w_d")]
-        if self.fmt == "e4m3":
+        scales = [None] * 4
+        if self.fmt != "bf16":
             scales = [self.__dict__[k].data_ptr() for k in ("s_qkv", "s_o", "s_gu", "s_d")]
-            return L.hb_layer_weights(*ptrs, *scales, L.HB_WEIGHTS_E4M3)
-        return L.hb_layer_weights(*ptrs, None, None, None, None, L.HB_WEIGHTS_BF16)
+        return L.hb_layer_weights(*ptrs, *scales, self.FORMATS[self.fmt], _p(self.g_q), _p(self.g_k))
 
 
 def hb_layer_forward(w: LayerWeights, dims, dplan: DevicePlan, rope, max_pos, x_in, x_out, k_cache, v_cache,

@@ -102,11 +102,11 @@ struct Cfg {
   static_assert(STAGE_BYTES % 1024 == 0 && STAGING % 1024 == 0 && TABLE % 16 == 0, "alignment");
   static_assert(STAGES >= 3, "ring depth");
 };
-// Three warpgroups of 168 registers a thread at launch; the promotion warps
-// take 216 (their sums are 128), the third warpgroup keeps 72:
-// 256 * 216 + 128 * 72 = 384 * 168.
+// 168 registers a thread, the same for every role.  (Moving registers from
+// the issuing to the summing warps with setmaxnreg gave the latter 216, but
+// beside small kernels launched as programmatic dependents a CTA did not
+// finish and the launch failed; it is not used.)
 constexpr int kWideThreads = 384;
-constexpr int kPromoteRegs = 216, kIssueRegs = 72;
 
 template <int BN, int EPI, bool PAIR>
 __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
@@ -179,10 +179,6 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full0 = PAIR ? cluster_addr(full, 0) : 0u;
 
-  // (each setmaxnreg inside its role's own branch: the compiler allocates for
-  // the smaller count where the two could meet)
-  if (warp >= 8) {
-    regs_dec<kIssueRegs>();
   if (warp == 8) {
     // ---------------------------------------------------------- TMA producer
     // The whole warp walks the loops and one elected lane issues (see the MMA
@@ -260,7 +256,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int s = 0; s < C::STAGES; ++s)
         if (pending & (1u << s)) mbar_drain(PAIR ? &empty[s] : &full[s], (armed_parity >> s) & 1u);
     }
-  } else if (warp <= 10) {
+  } else if (warp == 9 || warp == 10) {
     // ---------------------------------------------------------- MMA issuers
     griddep_wait();
     if (leader) {
@@ -284,13 +280,19 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
 #pragma unroll 1
       for (long long kb = C::NSUB == 2 ? 0 : me; kb < blocks; kb += STEP) {
         const int buf = sub * C::NB + slot;
-        // both barriers are tried at once: one after the other, the tries and
-        // their votes took as long as the MMAs
-        const bool has_data = mbar_try_wait_at(full_at + stage * 8, phase);
+        // Both barriers are tried before either vote: one after the other,
+        // the tries and their votes took as long as the MMAs.  The buffer's
+        // comes first, and the operands' counts only behind it: at BN 128 the
+        // other warp may have had the stage before, and a wait by parity
+        // also passes while that earlier phase is still open.  A released
+        // buffer means that block kb - NB has been summed, so every block up
+        // to it has left the ring, kb - STAGES among them (STAGES > NB).
+        static_assert(C::NSUB == 2 || C::STAGES > C::NB, "a stage's earlier phase is over when its buffer is free");
         const bool has_buf = mbar_try_wait_at(acc_empty_at + buf * 8, bphase ^ 1u);
+        const bool has_data = mbar_try_wait_at(full_at + stage * 8, phase);
         if (!__all_sync(0xffffffffu, has_data && has_buf)) {
-          ok = mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status) &&
-               mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status);
+          ok = mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status) &&
+               mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
@@ -308,12 +310,14 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             else
               mma_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
           }
+          // the buffer last: its arrival is the one that the sums, and so the
+          // end of a CTA, wait for
           if constexpr (PAIR) {
-            mma_commit_pair(&acc_full[buf], 3);
             mma_commit_pair(&empty[stage], 3);
+            mma_commit_pair(&acc_full[buf], 3);
           } else {
-            mma_commit(&acc_full[buf]);
             mma_commit(&empty[stage]);
+            mma_commit(&acc_full[buf]);
           }
         }
         __syncwarp();
@@ -339,7 +343,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       __syncwarp();
       mbar_drain(drain, 0);
     }
-  } else {
+  } else if (warp == 11) {
     // ---------------------------------------------------------- scale table
     // Scales of the tile's rows and weight blocks, kTabK K blocks at a time,
     // two fills ahead of the sums.  (Read by the promotion warps themselves,
@@ -383,10 +387,8 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         mbar_arrive(&tab_full[b]);
       }
     }
-  }
   } else {
     // ---------------------------------------------------------- promotion and epilogue
-    regs_inc<kPromoteRegs>();
     griddep_wait();
     const int quarter = warp & 3, half = warp >> 2;
     const bool boss = threadIdx.x == 0;
@@ -417,12 +419,14 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
-      // The sums run over 16 columns at a time, the next 16 on their way from
-      // TMEM meanwhile, across the border of two K blocks too.  A wait that
+      // The sums run over 16 columns at a time; at BN 128 the next 16 are on
+      // their way from TMEM meanwhile, across the border of two K blocks too
+      // (at BN 256 there are no registers left for them).  A wait that
       // expired raises the abort flag, every later wait gives up soon, and
       // the loop runs on over whatever TMEM holds: nothing of it is stored.
       constexpr int NC = 2 * CH;  // 16-column steps
-      uint32_t r[2][16];
+      constexpr bool AHEAD = BN == 128;
+      uint32_t r[AHEAD ? 2 : 1][16];
       const uint32_t t_cols = t_lane + sub * C::NB * kSub - sub * kSub;
       auto step_col = [&](int c) { return chunk_col(c >> 1) + (c & 1) * 16; };
       // waits for the next K block in TMEM and starts its first columns;
@@ -473,9 +477,9 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             // find, and a try would hold the thread in vain: it takes the
             // present block, which is complete.
             if (c == NC - 2) there = mbar_try_wait_at(acc_full_at + next_slot * 8, next_phase);
-            if (c < NC - 1) {
-              tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & 1]);
-            } else {
+            if (AHEAD && c < NC - 1)
+              tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & (AHEAD ? 1 : 0)]);
+            if (c == NC - 1) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) {
@@ -488,7 +492,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
                 slot = 0;
                 bphase ^= 1u;
               }
-              if (more) next_block(there);
+              if (AHEAD && more) next_block(there);
             }
             // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
             // the TMEM load does not give without moves (620 against 370
@@ -497,7 +501,13 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               acc[c >> 1][(c & 1) * 16 + j] =
-                  __fmaf_rn(__uint_as_float(r[c & 1][j]), f, acc[c >> 1][(c & 1) * 16 + j]);
+                  __fmaf_rn(__uint_as_float(r[AHEAD ? c & 1 : 0][j]), f, acc[c >> 1][(c & 1) * 16 + j]);
+            if (!AHEAD) {
+              if (c < NC - 1)
+                tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[0]);
+              else if (more)
+                next_block(there);
+            }
           }
         }
         __syncwarp();

@@ -19,6 +19,13 @@
 // projections run on the tensor cores' FP8 path with the per-row scales of
 // both operands applied in the epilogue; the 1/rms factors still come from
 // the bf16 rows.
+//
+// Block-scaled E4M3 weights: the same with a scale per 128 columns of a token
+// and per 128 x 128 block of a weight; the quantization of x and h multiplies
+// the row's 1/rms into its scales, so the projections carry no statistics.
+//
+// Layers with q/k gains norm every query and key head in the RoPE and KV
+// append kernel, whatever the weights' format.
 #include <cuda_runtime.h>
 
 #include "runtime.h"
@@ -31,8 +38,10 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // SwiGLU width rounded up to the 64-row interleave blocks of w_gu.
 inline int ffn_pad(const hb_layer_dims& dm) { return (dm.d_ff + 63) / 64 * 64; }
 
+inline size_t blocks128(int n) { return static_cast<size_t>((n + 127) / 128); }
+
 struct LayerWs {
-  size_t ss_x, ss_h, qkv, q, o, h, a, part_o, part_d, flags, q8_x, q8_o, q8_h, q8_a, s8, attn, total;
+  size_t ss_x, ss_h, qkv, q, o, h, a, part_o, part_d, flags, q8_x, q8_o, q8_h, q8_a, s8, sb8, attn, total;
 };
 
 LayerWs layer_ws(const hb_layer_dims& dm, int T, int S, int max_kv_len) {
@@ -54,6 +63,9 @@ LayerWs layer_ws(const hb_layer_dims& dm, int T, int S, int max_kv_len) {
   w.q8_h = off; off += align256(t * dm.d_model);
   w.q8_a = off; off += align256(t * ffn_pad(dm));
   w.s8 = off;   off += 4 * align256(t * 4);
+  // block-scaled E4M3: the four projection inputs' scales
+  w.sb8 = off;  off += align256(t * 4 * (2 * blocks128(dm.d_model) + blocks128(dm.n_q * dm.d_head) +
+                                         blocks128(ffn_pad(dm))));
   // split-K counters right before the attention workspace, whose counters
   // come first: one kernel of the layer zeroes both in one range
   w.flags = off;  off += align256(static_cast<size_t>(2) * gemm_split_flags(T, dm.d_model) * 4);
@@ -78,17 +90,22 @@ extern "C" hb_status hb_layer_kernel_count(const hb_layer_dims* dims, int32_t n_
   hb_status st = check_dims(dims);
   if (st != HB_OK) return st;
   HB_REQUIRE(count && n_rows >= 0, "hb_layer_kernel_count: bad arguments");
-  HB_REQUIRE(format == HB_WEIGHTS_BF16 || format == HB_WEIGHTS_E4M3, "hb_layer_kernel_count: unknown format %d",
-             format);
+  const bool qk_norm = (format & HB_LAYER_QK_NORM) != 0;
+  format &= ~HB_LAYER_QK_NORM;
+  HB_REQUIRE(format == HB_WEIGHTS_BF16 || format == HB_WEIGHTS_E4M3 || format == HB_WEIGHTS_E4M3_BLOCK,
+             "hb_layer_kernel_count: unknown format %d", format);
   // the same rules as hb_layer_forward: row statistics, QKV, RoPE/KV
   // append, chunk and decode attention, O, gate/up, down; E4M3: three more
   // quantization kernels, RoPE/KV append inside the QKV projection when
-  // its tiles hold whole heads
+  // its tiles hold whole heads and no head is normed; block-scaled E4M3: the
+  // same four quantizations, the append always on its own
   const int qkv_cols = (dims->n_q + 2 * dims->n_kv) * dims->d_head;
   if (n_rows == 0)
     *count = 0;
   else if (format == HB_WEIGHTS_E4M3)
-    *count = gemm_rope_ok(qkv_cols, *dims) ? 10 : 11;
+    *count = gemm_rope_ok(qkv_cols, *dims) && !qk_norm ? 10 : 11;
+  else if (format == HB_WEIGHTS_E4M3_BLOCK)
+    *count = 11;
   else
     *count = 8;
   return HB_OK;
@@ -101,9 +118,14 @@ namespace {
 hb_status check_weights(const hb_layer_weights* w, const hb_layer_dims* dims) {
   HB_REQUIRE(w, "layer forward: null weights");
   HB_REQUIRE(w->w_qkv && w->w_o && w->w_gu && w->w_d, "layer forward: null weight");
-  HB_REQUIRE(w->format == HB_WEIGHTS_BF16 || w->format == HB_WEIGHTS_E4M3, "layer forward: unknown format %d",
-             w->format);
-  const bool f8 = w->format == HB_WEIGHTS_E4M3;
+  HB_REQUIRE(w->format == HB_WEIGHTS_BF16 || w->format == HB_WEIGHTS_E4M3 || w->format == HB_WEIGHTS_E4M3_BLOCK,
+             "layer forward: unknown format %d", w->format);
+  HB_REQUIRE((w->g_q == nullptr) == (w->g_k == nullptr), "layer forward: q and k gains come together");
+  HB_REQUIRE(w->g_q == nullptr || (aligned16(w->g_q) && aligned16(w->g_k)),
+             "layer forward: q/k gains must be 16-byte aligned");
+  const bool f8 = w->format != HB_WEIGHTS_BF16;
+  HB_REQUIRE(w->format != HB_WEIGHTS_E4M3_BLOCK || dims->d_model <= 16384,
+             "layer forward: block-scaled weights need d_model <= 16384");
   HB_REQUIRE(!f8 || (w->s_qkv && w->s_o && w->s_gu && w->s_d), "layer forward: E4M3 weights need scales");
   HB_REQUIRE(!f8 || (aligned16(w->s_qkv) && aligned16(w->s_o) && aligned16(w->s_gu) && aligned16(w->s_d)),
              "layer forward: E4M3 scales must be 16-byte aligned");
@@ -142,6 +164,7 @@ hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_la
                     const hb_profile* prof, bool x_stats, bool stats_next) {
   hb_status st = HB_OK;
   const bool f8 = w->format == HB_WEIGHTS_E4M3;
+  const bool qk_norm = w->g_q != nullptr;
   const int T = plan->n_rows;
   const hb_layer_dims& dm = *dims;
   const LayerWs lw = layer_ws(dm, T, plan->n_seqs, max_kv_len);
@@ -175,7 +198,15 @@ hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_la
   // fused path is slower at the benchmark shapes: it needs 256-wide tiles
   // (48 CTA pairs) where the plain projection runs 192-wide ones on 64
   // pairs, which costs more than the saved launch.
-  const bool fuse_rope = f8 && gemm_rope_ok(qkv_cols, dm);
+  const bool fuse_rope = f8 && !qk_norm && gemm_rope_ok(qkv_cols, dm);
+  // rotation and KV append as a kernel of its own, with or without the head norms
+  auto append = [&](int* zero, int n) {
+    if (qk_norm)
+      return kv_append_norm_launch(ctx, qkv, T, plan->row_pos, plan->slot_mapping, rope, max_pos, dm, w->g_q, w->g_k,
+                                   q, k_cache, v_cache, num_pages, s, zero, n);
+    return kv_append_launch(ctx, qkv, T, plan->row_pos, plan->slot_mapping, rope, max_pos, dm, q, k_cache, v_cache,
+                            num_pages, s, zero, n);
+  };
   GemmRope rope_qkv;
   rope_qkv.rope = static_cast<const float2*>(rope);
   rope_qkv.row_pos = plan->row_pos;
@@ -223,9 +254,7 @@ hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_la
     HB_STEP(0, quant_rows_launch(ctx, x_in, xq, sx, T, d, ss_x, split_o.flags, n_zero, s));
     HB_STEP(1, gemm_e4m3_launch(ctx, xq, d, sx, w->w_qkv, w->s_qkv, qkv, qkv_cols, nullptr, T, qkv_cols, d, qkv_epi,
                                 s, &norm_x, nullptr, &rope_qkv));
-    HB_STEP(2, fuse_rope ? HB_OK
-                         : kv_append_launch(ctx, qkv, T, plan->row_pos, plan->slot_mapping, rope, max_pos, dm, q,
-                                            k_cache, v_cache, num_pages, s));
+    HB_STEP(2, fuse_rope ? HB_OK : append(nullptr, 0));
     HB_STEP(3, attention_launch(ctx, q, k_cache, v_cache, num_pages, *plan, dm, max_kv_len, o, aws,
                                 lw.total - lw.attn, s, true));
     HB_STEP(4, quant_rows_launch(ctx, o, oq, so, T, hd, nullptr, nullptr, 0, s));
@@ -243,10 +272,38 @@ hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_la
     if (st != HB_OK) return st;
     return mark(HB_LAYER_STAGES);
   }
+  if (w->format == HB_WEIGHTS_E4M3_BLOCK) {
+    uint8_t* xq = ws + lw.q8_x;
+    uint8_t* oq = ws + lw.q8_o;
+    uint8_t* hq = ws + lw.q8_h;
+    uint8_t* aq = ws + lw.q8_a;
+    float* sx = reinterpret_cast<float*>(ws + lw.sb8);
+    float* sh = sx + T * blocks128(d);
+    float* so = sh + T * blocks128(d);
+    float* sa = so + T * blocks128(hd);
+    HB_STEP(0, quant_norm_launch(ctx, x_in, xq, sx, T, d, dm.rms_eps, split_o.flags, n_zero, s));
+    HB_STEP(1, gemm_e4m3_block_launch(ctx, xq, d, sx, w->w_qkv, w->s_qkv, qkv, qkv_cols, nullptr, T, qkv_cols, d,
+                                      HB_EPI_STORE, s));
+    HB_STEP(2, append(nullptr, 0));
+    HB_STEP(3, attention_launch(ctx, q, k_cache, v_cache, num_pages, *plan, dm, max_kv_len, o, aws,
+                                lw.total - lw.attn, s, true));
+    HB_STEP(4, quant_block_launch(ctx, o, oq, so, T, hd, 1, s));
+    st = gemm_e4m3_block_launch(ctx, oq, hd, so, w->w_o, w->s_o, h, d, x_in, T, d, hd, HB_EPI_RESIDUAL, s);
+    if (st != HB_OK) return st;
+    HB_STEP(5, HB_OK);
+    HB_STEP(6, quant_norm_launch(ctx, h, hq, sh, T, d, dm.rms_eps, nullptr, 0, s));
+    st = gemm_e4m3_block_launch(ctx, hq, d, sh, w->w_gu, w->s_gu, a, fp, nullptr, T, 2 * fp, d, HB_EPI_SWIGLU, s);
+    if (st != HB_OK) return st;
+    HB_STEP(7, quant_block_launch(ctx, a, aq, sa, T, fp, 1, s));
+    // d_ff and its padded width fp end in the same block of 128: the scales
+    // of a's rows line up with the weight's
+    st = gemm_e4m3_block_launch(ctx, aq, fp, sa, w->w_d, w->s_d, x_out, d, h, T, d, dm.d_ff, HB_EPI_RESIDUAL, s);
+    if (st != HB_OK) return st;
+    return mark(HB_LAYER_STAGES);
+  }
   HB_STEP(0, x_stats ? HB_OK : row_sumsq_launch(ctx, x_in, ss_x, T, d, nullptr, 0, s));
   HB_STEP(1, gemm_launch(ctx, x_in, d, w->w_qkv, qkv, qkv_cols, nullptr, T, qkv_cols, d, HB_EPI_STORE, s, &norm_x));
-  HB_STEP(2, kv_append_launch(ctx, qkv, T, plan->row_pos, plan->slot_mapping, rope, max_pos, dm, q, k_cache, v_cache,
-                              num_pages, s, split_o.flags, n_zero));
+  HB_STEP(2, append(split_o.flags, n_zero));
   HB_STEP(3, attention_launch(ctx, q, k_cache, v_cache, num_pages, *plan, dm, max_kv_len, o, aws,
                               lw.total - lw.attn, s, true));
   HB_STEP(4, gemm_launch(ctx, o, hd, w->w_o, h, d, x_in, T, d, hd, HB_EPI_RESIDUAL, s, &norm_h_out, &split_o));
@@ -308,8 +365,9 @@ extern "C" hb_status hb_layers_forward(const hb_layer_weights* w, int32_t n_laye
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int l = 0; l < n_layers; ++l) {
     // a bf16 layer takes its input statistics from the layer before it
+    // (block-scaled projections write none)
     const bool next_bf16 = l + 1 < n_layers && w[l + 1].format == HB_WEIGHTS_BF16;
-    const bool x_stats = l > 0 && w[l].format == HB_WEIGHTS_BF16;
+    const bool x_stats = l > 0 && w[l].format == HB_WEIGHTS_BF16 && w[l - 1].format != HB_WEIGHTS_E4M3_BLOCK;
     st = run_layer(ctx, w + l, dims, plan, rope, max_pos, l == 0 ? x_in : x_out, x_out, k_caches[l], v_caches[l],
                    num_pages, max_kv_len, workspace, s, nullptr, x_stats, next_bf16);
     if (st != HB_OK) return st;

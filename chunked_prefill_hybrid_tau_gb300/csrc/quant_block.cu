@@ -159,7 +159,84 @@ __global__ void __maxnreg__(64)
   if (threadIdx.x == 0) scale[static_cast<size_t>(blockIdx.y) * kb + blockIdx.x] = gs.scale;
 }
 
+// Rows that an RMSNorm goes over before their projection (the layer's x and
+// h): the token kernel's codes, and scales that carry the row's 1/rms,
+//   scale[r][b] = fl(scale_b * rsqrt(mean(x[r]^2) + eps)),
+// so that the projection needs no statistics (the gain is in its weights).
+// One CTA per row, which it holds in registers: thread t has the 16-byte
+// pieces t, t + 256, ...; groups lie in 16 neighbouring lanes as above.  The
+// sum of squares is formed in an order of the row length alone.  Also clears
+// n_zero ints (the layer's counters).
+template <int NV>
+__global__ void __launch_bounds__(kThreads)
+    quant_norm_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int c8, int kb,
+                      float inv_d, float eps, int* zero, int n_zero) {
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_zero; i += gridDim.x * blockDim.x) zero[i] = 0;
+  __shared__ float red[kThreads / 32];
+  const int t = threadIdx.x, l = t & 15;
+  const size_t base = static_cast<size_t>(blockIdx.x) * c8;
+  uint4 v[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = t + kThreads * k;
+    v[k] = i < c8 ? x[base + i] : make_uint4(0, 0, 0, 0);
+  }
+  float ss = 0.f;
+  uint32_t m[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = unpack_bf16x2(w[j]);
+      ss = __fmaf_rn(f.x, f.x, ss);
+      ss = __fmaf_rn(f.y, f.y, ss);
+    }
+    m[k] = amax8(v[k]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m[k] = max2(m[k], __shfl_xor_sync(0xffffffffu, m[k], o));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+  if ((t & 31) == 0) red[t >> 5] = ss;
+  __syncthreads();
+  ss = red[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) ss = __fadd_rn(ss, red[w]);
+  const float inv_rms = rsqrtf(__fmaf_rn(ss, inv_d, eps));
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = t + kThreads * k;
+    if (i >= c8) break;
+    const GroupScale gs = group_scale(amax_value(m[k]));
+    q[base + i] = codes8(v[k], gs.inv);
+    if (l == 0) scale[static_cast<size_t>(blockIdx.x) * kb + i / 16] = __fmul_rn(gs.scale, inv_rms);
+  }
+}
+
 }  // namespace
+
+hb_status quant_norm_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int d, float eps,
+                            int* zero, int n_zero, cudaStream_t stream) {
+  (void)ctx;
+  const int c8 = d / 8, kb = (d + 127) / 128;
+  const int nv = (c8 + kThreads - 1) / kThreads;
+  auto* xp = static_cast<const uint4*>(x);
+  auto* qp = static_cast<uint2*>(q);
+#define HB_QN(NV_)                                                                                              \
+  if (nv <= NV_)                                                                                                \
+    return launch_pdl(quant_norm_kernel<NV_>, rows, kThreads, 0, stream, "quant_norm_kernel launch", xp, qp,    \
+                      scale, c8, kb, 1.0f / d, eps, zero, n_zero);
+  HB_QN(1)
+  HB_QN(2)
+  HB_QN(4)
+  HB_QN(8)
+#undef HB_QN
+  set_error("block-scaled layer: d_model = %d above the supported 16384", d);
+  return HB_ERR_UNSUPPORTED;
+}
 
 hb_status quant_block_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int cols,
                              int block_rows, cudaStream_t stream) {

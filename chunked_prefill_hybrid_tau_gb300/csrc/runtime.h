@@ -177,6 +177,11 @@ hb_status quant_rows_launch(const DeviceCtx& ctx, const void* x, void* q, float*
 hb_status quant_block_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int cols,
                              int block_rows, cudaStream_t stream);
 
+// The same for rows that an RMSNorm goes over: block_rows 1, every scale times
+// the row's rsqrt(mean(x^2) + eps), and n_zero ints at `zero` cleared.
+hb_status quant_norm_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int d, float eps,
+                            int* zero, int n_zero, cudaStream_t stream);
+
 // Block-scaled E4M3 projection (hb_gemm_e4m3_block); A has row stride lda
 // bytes, C and R row stride ldc elements.
 hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B,

@@ -439,7 +439,12 @@ hb_status hb_fold_gamma(const void* w, const void* gamma, void* out, int32_t row
  *            projections run as hb_gemm_e4m3; d_ff % 16 == 0 required.  With
  *            E4M3 weights and (n_q + 2 n_kv) d_head % 256 == 0 the RoPE and
  *            KV append run inside the QKV projection (same results; the
- *            rope+kv stage is then empty).
+ *            rope+kv stage is then empty), unless q/k gains are given.
+ *            HB_WEIGHTS_E4M3_BLOCK: x, o, h and the SwiGLU output are
+ *            quantized per token and 128 columns (hb_quantize_e4m3_block's
+ *            rule), the scales of x and h times the row's r, and the
+ *            projections run as hb_gemm_e4m3_block; d_ff % 16 == 0 and
+ *            d_model <= 16384 required.
  *   plan   : device plan; rope: table from hb_rope_table with max_pos rows
  *   x_in   : device bf16 [T][d_model]; x_out may alias x_in
  *   caches : updated in place with this iteration's K/V
@@ -454,8 +459,10 @@ hb_status hb_fold_gamma(const void* w, const void* gamma, void* out, int32_t row
  * ---------------------------------------------------------------------- */
 typedef enum hb_weight_format {
   HB_WEIGHTS_BF16 = 0, /* bf16 matrices */
-  HB_WEIGHTS_E4M3 = 1  /* each matrix as E4M3 codes of its bf16 form (hb_quantize_e4m3) with per-row scales;
+  HB_WEIGHTS_E4M3 = 1, /* each matrix as E4M3 codes of its bf16 form (hb_quantize_e4m3) with per-row scales;
                           the four projection inputs are quantized per token inside the layer */
+  HB_WEIGHTS_E4M3_BLOCK = 2 /* E4M3 codes with a scale per 128 x 128 block (hb_quantize_e4m3_block, block_rows
+                          128); the projection inputs are quantized per token and 128 columns inside the layer */
 } hb_weight_format;
 
 typedef struct hb_layer_weights {
@@ -465,10 +472,12 @@ typedef struct hb_layer_weights {
                          64), then hb_fold_gamma with g2 */
   const void* w_d;    /* [d_model][d_ff] */
   const float* s_qkv; /* HB_WEIGHTS_E4M3: per-row scales of the four matrices (16-byte aligned); */
-  const float* s_o;   /* NULL for HB_WEIGHTS_BF16 */
-  const float* s_gu;
+  const float* s_o;   /* NULL for HB_WEIGHTS_BF16; HB_WEIGHTS_E4M3_BLOCK: block scales [rows / 128][cols / 128] */
+  const float* s_gu;  /* (16-byte aligned), w_gu's as hb_gemm_e4m3_block takes them: the gate's, then the up's */
   const float* s_d;
   int32_t format;     /* hb_weight_format */
+  const void* g_q;    /* bf16 [d_head] gains: every q and k head is RMS-normed before its rotation, as */
+  const void* g_k;    /* hb_kv_append_norm does (16-byte aligned); both NULL: heads are not normed */
 } hb_layer_weights;
 
 #define HB_LAYER_STAGES 8
@@ -496,7 +505,8 @@ hb_status hb_layer_forward(const hb_layer_weights* w, const hb_layer_dims* dims,
  * hb_layer_forward calls, bit for bit: a bf16 layer after the first takes
  * the row statistics of its input from the previous layer's down
  * projection, which writes them in the same order as the statistics
- * kernel, and that kernel is left out (one launch less per layer).
+ * kernel, and that kernel is left out (one launch less per layer; after a
+ * block-scaled layer it runs).
  * Errors as hb_layer_forward; nothing is launched when any layer's
  * arguments are invalid.
  * ---------------------------------------------------------------------- */
@@ -510,8 +520,10 @@ hb_status hb_layers_forward(const hb_layer_weights* w, int32_t n_layers, const h
  * device call; the chunk and decode attention kernels
  * count whatever the batch holds, n_rows == 0 launches nothing).  bf16: 8;
  * E4M3: 11, or 10 when the RoPE and KV append run inside the QKV
- * projection.  *count written on HB_OK; HB_ERR_INVALID_ARG for a null
+ * projection; block-scaled E4M3: 11.  HB_LAYER_QK_NORM may be or-ed into
+ * format: layers with q/k gains.  *count written on HB_OK; HB_ERR_INVALID_ARG for a null
  * pointer, bad dims, n_rows < 0 or an unknown format. */
+#define HB_LAYER_QK_NORM 256
 hb_status hb_layer_kernel_count(const hb_layer_dims* dims, int32_t n_rows, int32_t format, int32_t* count);
 
 /* ------------------------------------------------------------------------

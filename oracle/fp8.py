@@ -167,9 +167,10 @@ def gemm_blocks(qa, sa, qb, sb):
     return dequantize_blocks(qa, sa, 1) @ dequantize_blocks(qb, sb, BLOCK).T
 
 
-def prepare_weights(w):
+def prepare_weights(w, block=False):
     """The prepared bf16 weights (gains folded, rounded once to bf16), then
-    per-row codes and scales: dict name -> (codes, scale) for qkv, o, g, u, d."""
+    per-row (block: per 128 x 128 block) codes and scales: dict name ->
+    (codes, scale) for qkv, o, g, u, d; the q/k head gains as they are."""
     f32 = np.float32
     fold = {
         "qkv": ol.round_bf16(np.asarray(w["w_qkv"], f32) * np.asarray(w["g1"], f32)[None, :]),
@@ -178,17 +179,21 @@ def prepare_weights(w):
         "u": ol.round_bf16(np.asarray(w["w_u"], f32) * np.asarray(w["g2"], f32)[None, :]),
         "d": np.asarray(w["w_d"], f32),
     }
-    def by_rows(m, block=2048):  # rows are independent; blocks only bound the memory in use
-        parts = [quantize_rows(m[i:i + block]) for i in range(0, m.shape[0], block)]
+    def by_rows(m, rows=2048):  # rows (blocks of them) are independent; the parts only bound the memory in use
+        parts = [quantize_blocks(m[i:i + rows], BLOCK) if block else quantize_rows(m[i:i + rows])
+                 for i in range(0, m.shape[0], rows)]
         return np.concatenate([p[0] for p in parts]), np.concatenate([p[1] for p in parts])
 
-    return {k: by_rows(v) for k, v in fold.items()}
+    out = {k: by_rows(v) for k, v in fold.items()}
+    out.update({k: w[k] for k in ("g_q", "g_k") if k in w})
+    return out
 
 
 def layer_forward(wq, dims, plan, x, k_pool, v_pool, cos, sin, storage=None, dtype=np.float32,
-                  return_parts=False):
+                  return_parts=False, block=False):
     """One decoder layer with E4M3 projections (module docstring); wq from
-    prepare_weights.  RMSNorm stays in the projections that consume it:
+    prepare_weights (block: with block scales, on both operands).  RMSNorm
+    stays in the projections that consume it:
     RMSNorm(v; g) W^T = r (v (W diag g)^T), r = 1/sqrt(mean(v^2) + eps) per row,
     with v's quantized codes standing in for v.  storage="bf16" rounds the
     tensors that a bf16 implementation stores, as in oracle.layer."""
@@ -201,8 +206,11 @@ def layer_forward(wq, dims, plan, x, k_pool, v_pool, cos, sin, storage=None, dty
         return 1.0 / np.sqrt(np.mean(v * v, axis=-1) + dtype(dims.eps))
 
     def proj(v, name):
-        qa, sa = quantize_rows(v)
         qb, sb = wq[name]
+        if block:
+            qa, sa = quantize_blocks(v, 1)
+            return gemm_blocks(qa, sa, qb, sb).astype(dtype)
+        qa, sa = quantize_rows(v)
         return gemm(qa, sa, qb, sb).astype(dtype)
 
     x = np.asarray(x, dtype)
@@ -211,6 +219,8 @@ def layer_forward(wq, dims, plan, x, k_pool, v_pool, cos, sin, storage=None, dty
     k = qkv[:, nq * dh:(nq + nkv) * dh].reshape(T, nkv, dh)
     v = qkv[:, (nq + nkv) * dh:].reshape(T, nkv, dh)
     pos = np.asarray(plan.row_pos)
+    if "g_q" in wq:  # normed q and k heads
+        q, k = ol.head_norm(q, wq["g_q"], dims.eps, dtype), ol.head_norm(k, wq["g_k"], dims.eps, dtype)
     q = st(ol.rope(q, pos, cos, sin, dtype))
     k = st(ol.rope(k, pos, cos, sin, dtype))
     ol.kv_append(k, v, plan.slot_mapping, k_pool, v_pool, dims.page)

@@ -16,6 +16,8 @@ block without biases:
     q, k = RoPE(q, k; pos)             rotate-half, inv_freq_i = theta^(-2i/d_head)
     k, v -> paged cache at slot        (k stored after rotation)
     o = softmax(q k^T / sqrt(d_head)) v     per q head h on kv head h*n_kv//n_q
+    (layers with q/k gains g_q, g_k: q and k are RMS-normed per head before
+    the rotation)
     h = x + o W_o^T
     out = h + (silu(hn W_g^T) * (hn W_u^T)) W_d^T,  hn = RMSNorm(h; g2)
 
@@ -147,6 +149,8 @@ def layer_forward(w, dims, plan, x, k_pool, v_pool, cos, sin, dtype=np.float32,
     k = qkv[:, nq * dh:(nq + nkv) * dh].reshape(T, nkv, dh)
     v = qkv[:, (nq + nkv) * dh:].reshape(T, nkv, dh)
     pos = np.asarray(plan.row_pos)
+    if "g_q" in w:  # normed q and k heads
+        q, k = head_norm(q, w["g_q"], dims.eps, dtype), head_norm(k, w["g_k"], dims.eps, dtype)
     q = st(rope(q, pos, cos, sin, dtype))
     k = st(rope(k, pos, cos, sin, dtype))
     kv_append(k, v, plan.slot_mapping, k_pool, v_pool, dims.page)

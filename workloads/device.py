@@ -26,10 +26,12 @@ def to_numpy(t) -> np.ndarray:
 
 def layer_weights_device(w: dict, dims, device="cuda", fmt="bf16"):
     """Upload one layer's weights and prepare them with the library (gains
-    folded, gate/up interleaved; fmt="e4m3": then quantized per row)."""
+    folded, gate/up interleaved; fmt="e4m3": then quantized per row,
+    "e4m3_block": per 128 x 128 block; g_q, g_k: the q/k head gains, if any)."""
     import chunked_prefill_hybrid_tau_gb300 as hb
+    gains = {k: bf16_tensor(w[k], device) for k in ("g_q", "g_k") if k in w}
     return hb.prepare_layer_weights(*[bf16_tensor(w[k], device) for k in ("w_qkv", "w_o", "w_g", "w_u", "w_d",
-                                                                          "g1", "g2")], fmt=fmt)
+                                                                          "g1", "g2")], fmt=fmt, **gains)
 
 
 def rope_table_device(max_pos: int, dims, device="cuda"):
