@@ -102,10 +102,6 @@ struct Cfg {
   static_assert(STAGE_BYTES % 1024 == 0 && STAGING % 1024 == 0 && TABLE % 16 == 0, "alignment");
   static_assert(STAGES >= 3, "ring depth");
 };
-// 168 registers a thread, the same for every role.  (Moving registers from
-// the issuing to the summing warps with setmaxnreg gave the latter 216, but
-// beside small kernels launched as programmatic dependents a CTA did not
-// finish and the launch failed; it is not used.)
 constexpr int kWideThreads = 384;
 
 template <int BN, int EPI, bool PAIR>
@@ -280,22 +276,30 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
 #pragma unroll 1
       for (long long kb = C::NSUB == 2 ? 0 : me; kb < blocks; kb += STEP) {
         const int buf = sub * C::NB + slot;
-        // Both barriers are tried before either vote: one after the other,
-        // the tries and their votes took as long as the MMAs.  The buffer's
-        // comes first, and the operands' counts only behind it: at BN 128 the
-        // other warp may have had the stage before, and a wait by parity
-        // also passes while that earlier phase is still open.  A released
-        // buffer means that block kb - NB has been summed, so every block up
-        // to it has left the ring, kb - STAGES among them (STAGES > NB).
-        static_assert(C::NSUB == 2 || C::STAGES > C::NB, "a stage's earlier phase is over when its buffer is free");
-        const bool has_buf = mbar_try_wait_at(acc_empty_at + buf * 8, bphase ^ 1u);
-        const bool has_data = mbar_try_wait_at(full_at + stage * 8, phase);
-        if (!__all_sync(0xffffffffu, has_data && has_buf)) {
-          ok = mbar_wait_at(acc_empty_at + buf * 8, bphase ^ 1u, abort_flag, p.status) &&
-               mbar_wait_at(full_at + stage * 8, phase, abort_flag, p.status);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+        const uint32_t buf_at = acc_empty_at + buf * 8, data_at = full_at + stage * 8;
+        if constexpr (C::NSUB == 2) {
+          // this warp has waited for every phase of both barriers, so both
+          // are tried before either vote: one after the other, tries and
+          // votes took as long as the MMAs
+          const bool has_buf = mbar_try_wait_at(buf_at, bphase ^ 1u);
+          const bool has_data = mbar_try_wait_at(data_at, phase);
+          ok = __all_sync(0xffffffffu, has_buf && has_data) ||
+               __all_sync(0xffffffffu, mbar_wait_at(buf_at, bphase ^ 1u, abort_flag, p.status) &&
+                                           mbar_wait_at(data_at, phase, abort_flag, p.status));
+        } else {
+          // The buffer first, and the operands only once it is known to be
+          // free: the other warp had this stage before, and a wait by parity
+          // also passes while that earlier phase is still open.  Tried
+          // together, the operands' barrier can be looked at while the
+          // buffer's try is pending; taken for complete one phase early, it
+          // let a block's MMAs run on half a stage and free it twice.  A
+          // released buffer means that block kb - NB has been summed, so
+          // every block up to it has left the ring, kb - STAGES among them.
+          static_assert(C::STAGES > C::NB, "a stage's earlier phase is over when its buffer is free");
+          ok = __all_sync(0xffffffffu, mbar_wait_at(buf_at, bphase ^ 1u, abort_flag, p.status));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_at(data_at, phase, abort_flag, p.status));
         }
+        if (!ok) break;
         tc_fence_after();
         // the start address is the low 14 bits of a descriptor, in 16-byte
         // units, and shared memory ends below 2^18 bytes: it cannot carry
@@ -342,6 +346,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       }
       __syncwarp();
       mbar_drain(drain, 0);
+      __syncwarp();
     }
   } else if (warp == 11) {
     // ---------------------------------------------------------- scale table
@@ -374,8 +379,8 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-          for (int i = 0; i < kTabK; ++i) va[q][i] = kb0 + i < kblocks && in_m[q] ? __ldg(pa[q] + kb0 + i) : 0.f;
-        const float vs = kb0 + (lane >> 2) < kblocks ? __ldg(ps + kb0) : 0.f;
+          for (int i = 0; i < kTabK; ++i) va[q][i] = kb0 + i < kblocks && in_m[q] ? pa[q][kb0 + i] : 0.f;
+        const float vs = kb0 + (lane >> 2) < kblocks ? ps[kb0] : 0.f;
         const int b = fill & 1;
         if (ok) ok = mbar_wait(&tab_empty[b], ((fill >> 1) & 1) ^ 1u, abort_flag, p.status);
         float* tab = table + b * (C::TABLE / 4);
@@ -402,10 +407,12 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     };
     // column half w / 4: at BN 256 a buffer of its own
     const int sub = BN == 256 ? half : 0;
-    const uint32_t acc_full_at = smem_u32(acc_full) + sub * C::NB * 8;
-    const uint32_t acc_empty_at = (PAIR ? cluster_addr(acc_empty, 0) : smem_u32(acc_empty)) + sub * C::NB * 8;
-    const uint32_t tab_full_at = smem_u32(tab_full), tab_empty_at = smem_u32(tab_empty);
-    const uint32_t sa_at = smem_u32(table) + rloc * 4, sb_at = smem_u32(table) + (kTabK * BM + half * 2) * 4;
+    // addresses as one register and constants: at BN = 256 the sums leave few
+    const uint32_t bars = smem_u32(full);
+    const uint32_t acc_full_at = bars + (2 * C::STAGES + sub * C::NB) * 8, acc_empty_at = acc_full_at + kBufs * 8;
+    const uint32_t tab_full_at = bars + (2 * C::STAGES + 2 * kBufs) * 8, tab_empty_at = tab_full_at + 16;
+    const uint32_t sa_at = bars - 2 * C::TABLE + rloc * 4;
+    const uint32_t sb_at = bars - 2 * C::TABLE + (kTabK * BM + half * 2) * 4;
     int fill = 0, slot = 0;
     uint32_t bphase = 0, rphase = 0;
     bool ok = true;
@@ -419,23 +426,34 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
-      // The sums run over 16 columns at a time; at BN 128 the next 16 are on
-      // their way from TMEM meanwhile, across the border of two K blocks too
-      // (at BN 256 there are no registers left for them).  A wait that
-      // expired raises the abort flag, every later wait gives up soon, and
-      // the loop runs on over whatever TMEM holds: nothing of it is stored.
-      constexpr int NC = 2 * CH;  // 16-column steps
-      constexpr bool AHEAD = BN == 128;
-      uint32_t r[AHEAD ? 2 : 1][16];
+      // The sums run over W columns at a time, the next W on their way from
+      // TMEM meanwhile, across the border of two K blocks too.  At BN 256 the
+      // sums leave about 40 registers: two sets of 8 columns, or (STORE and
+      // F32, where the compiler fits it better: 217 against 225 us for
+      // 4096 x 9216 x 7168; SWIGLU the other way round, 384 against 399 us for
+      // 4096 x 28672 x 4096) one set of 16.  A wait that expired raises the
+      // abort flag, every later wait gives up soon, and the loop runs on over
+      // whatever TMEM holds: nothing of it is stored.
+      constexpr bool AHEAD = BN == 128 || EPI == HB_EPI_SWIGLU || EPI == HB_EPI_RESIDUAL;
+      constexpr int W = BN == 256 && AHEAD ? 8 : 16;  // columns of a step
+      constexpr int NC = CH * 32 / W;
+      constexpr bool TRY = BN == 128;  // a register more than BN 256 has
+      uint32_t r[AHEAD ? 2 : 1][W];
       const uint32_t t_cols = t_lane + sub * C::NB * kSub - sub * kSub;
-      auto step_col = [&](int c) { return chunk_col(c >> 1) + (c & 1) * 16; };
+      auto step_col = [&](int c) { return chunk_col(c * W / 32) + c * W % 32; };
+      auto load = [&](uint32_t at, uint32_t (&x)[W]) {
+        if constexpr (W == 8)
+          tmem_ld_32x32b_x8(at, x);
+        else
+          tmem_ld_32x32b_x16(at, x);
+      };
       // waits for the next K block in TMEM and starts its first columns;
       // there: an earlier try has found it complete
       auto next_block = [&](bool there) {
         if (!__all_sync(0xffffffffu, there)) ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
         __syncwarp();
         tc_fence_after();
-        tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(0), r[0]);
+        load(t_cols + slot * kSub + step_col(0), r[0]);
       };
       next_block(false);
 #pragma unroll 1
@@ -443,6 +461,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         const int side = fill & 1;
         const int nk = kblocks - kb0 < kTabK ? kblocks - kb0 : kTabK;
         ok &= mbar_wait_at(tab_full_at + side * 8, (fill >> 1) & 1, abort_flag, p.status);
+        __syncwarp();
         uint32_t sa_next = sa_at + side * C::TABLE, sb_next = sb_at + side * C::TABLE;
         if constexpr (EPI == HB_EPI_RESIDUAL) {
           // the residual tile into the staging slabs, once the previous
@@ -457,6 +476,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
               tma_load_2d(staging + s * kSlabBytes, &tmR, res_bar, n0 + s * 64, mt * BM);
             res_pending = true;
           }
+          __syncwarp();
         }
 #pragma unroll 1
         for (int i = 0; i < nk; ++i) {
@@ -476,15 +496,15 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             // under the sums.  Past the tile's last block there is nothing to
             // find, and a try would hold the thread in vain: it takes the
             // present block, which is complete.
-            if (c == NC - 2) there = mbar_try_wait_at(acc_full_at + next_slot * 8, next_phase);
+            if (TRY && c == NC - 2) there = mbar_try_wait_at(acc_full_at + next_slot * 8, next_phase);
             if (AHEAD && c < NC - 1)
-              tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & (AHEAD ? 1 : 0)]);
+              load(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & (AHEAD ? 1 : 0)]);
             if (c == NC - 1) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) {
                 if constexpr (PAIR)
-                  mbar_arrive_cluster_relaxed(acc_empty_at + slot * 8);
+                  mbar_arrive_cluster_relaxed(cluster_addr_at(acc_empty_at + slot * 8, 0));
                 else
                   mbar_arrive_at(acc_empty_at + slot * 8);
               }
@@ -499,12 +519,13 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             // clocks per 256-column block, measured)
             const float f = c < NC / 2 ? f0 : f1;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[c >> 1][(c & 1) * 16 + j] =
-                  __fmaf_rn(__uint_as_float(r[AHEAD ? c & 1 : 0][j]), f, acc[c >> 1][(c & 1) * 16 + j]);
+            for (int j = 0; j < W; ++j) {
+              float& a = acc[c * W / 32][c * W % 32 + j];
+              a = __fmaf_rn(__uint_as_float(r[AHEAD ? c & 1 : 0][j]), f, a);
+            }
             if (!AHEAD) {
               if (c < NC - 1)
-                tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[0]);
+                load(t_cols + slot * kSub + step_col(c + 1), r[0]);
               else if (more)
                 next_block(there);
             }
@@ -524,6 +545,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         }
       } else {
         if (boss) bulk_wait_group_read<0>();
+        __syncwarp();
         named_barrier_sync(1, 256);
       }
       if constexpr (EPI == HB_EPI_F32) {
@@ -532,6 +554,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         for (int rd = 0; rd < ROUNDS; ++rd) {
           if (rd > 0) {
             if (boss) bulk_wait_group_read<0>();
+            __syncwarp();
             named_barrier_sync(1, 256);
           }
 #pragma unroll
@@ -616,6 +639,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     if (boss) bulk_wait_group<0>();  // the TMA stores have left shared memory and are performed
     if (PAIR && lane == 0 && *abort_flag) raise_peer_abort(abort_flag, rank);
   }
+  __syncwarp();
 
   tc_fence_before();
   __syncthreads();
@@ -834,6 +858,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     if (elect_one()) mma_commit(drain);
     __syncwarp();
     mbar_drain(drain, 0);
+    __syncwarp();
   } else {
     // ---------------------------------------------------------- promotion and epilogue
     griddep_wait();
@@ -852,10 +877,10 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
         const int j = fj + 8 * x;
-        pre_a[x] = in && j < p.M ? __ldg(p.sa + static_cast<size_t>(j) * kblocks + kb0 + fi) : 0.f;
+        pre_a[x] = in && j < p.M ? p.sa[static_cast<size_t>(j) * kblocks + kb0 + fi] : 0.f;
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) pre_b[b] = in ? __ldg(sb_blk[b] + kb0 + fi) : 0.f;
+      for (int b = 0; b < 2; ++b) pre_b[b] = in ? sb_blk[b][kb0 + fi] : 0.f;
     };
     auto put = [&](int side) {
 #pragma unroll
@@ -968,6 +993,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       }
     }
   }
+  __syncwarp();
 
   tc_fence_before();
   __syncthreads();
