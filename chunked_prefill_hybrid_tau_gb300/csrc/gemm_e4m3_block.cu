@@ -102,7 +102,13 @@ struct Cfg {
   static_assert(STAGE_BYTES % 1024 == 0 && STAGING % 1024 == 0 && TABLE % 16 == 0, "alignment");
   static_assert(STAGES >= 3, "ring depth");
 };
+// 168 registers a thread at launch.  A promotion thread of a 256-column tile
+// holds 128 sums and two sets of 16 columns on their way from TMEM; it gets
+// 216 registers, the other warpgroup keeps 72 (4096 x 9216 x 7168: 201 us;
+// 219 with 168 for all, where the next 16 columns cannot be under way).
 constexpr int kWideThreads = 384;
+constexpr int kIssueRegs = 72, kPromoteRegs = 216;
+static_assert(128 * kIssueRegs + 256 * kPromoteRegs <= 168 * kWideThreads, "register split");
 
 template <int BN, int EPI, bool PAIR>
 __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
@@ -175,225 +181,230 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t full0 = PAIR ? cluster_addr(full, 0) : 0u;
 
-  if (warp == 8) {
-    // ---------------------------------------------------------- TMA producer
-    // The whole warp walks the loops and one elected lane issues (see the MMA
-    // issuer): a single-lane loop needs twice the time per K block.
-    const uint64_t wpol = um <= 4 ? policy_evict_first() : policy_evict_normal();
-    const uint32_t empty_at = smem_u32(empty);
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    uint32_t pending = 0, armed_parity = 0;
-    auto load_a = [&](int s, int kb, int m0) {
-      uint8_t* dst = smem + s * C::STAGE_BYTES;
-      if constexpr (PAIR)
-        tma_load_2d_pair(dst, &tmA, full0 + s * 8, kb * BK, m0);
-      else
-        tma_load_2d(dst, &tmA, &full[s], kb * BK, m0);
-    };
-    auto load_b = [&](int s, int kb, int n0) {
-      uint8_t* dst = smem + s * C::STAGE_BYTES + C::A_BYTES;
-#pragma unroll
-      for (int i = 0; i < C::NSUB; ++i) {
-        if constexpr (PAIR)
-          tma_load_2d_pair_hint(dst + i * C::SUB_BYTES, &tmB, full0 + s * 8, kb * BK, n0 + i * kSub, wpol);
-        else
-          tma_load_2d_hint(dst + i * C::SUB_BYTES, &tmB, &full[s], kb * BK, n0 + i * kSub, wpol);
-      }
-    };
-    auto arm = [&](int s) {
-      if (leader) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * C::STAGE_BYTES);  // both CTAs' boxes
-    };
-    // the weights do not come from the kernel ahead: their first ring fill
-    // is issued before waiting for it
-    int pre = 0;
-    if (first < units) {
-      const int n0 = (first / um) * BN + static_cast<int>(rank) * (kSub / 2);
-      pre = kblocks < C::STAGES ? kblocks : C::STAGES;
-      if (elect_one()) {
-        for (int i = 0; i < pre; ++i) {
-          arm(i);
-          load_b(i, i, n0);
-        }
-      }
-      __syncwarp();
-    }
-    griddep_wait();
-    for (int u = first; u < units && ok; u += stride) {
-      const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
-      const int n0 = (u / um) * BN + static_cast<int>(rank) * (kSub / 2);
-#pragma unroll 1
-      for (int kb = 0; kb < kblocks; ++kb) {
-        pending |= 1u << stage;
-        if (u == first && kb < pre) {
-          if (elect_one()) load_a(stage, kb, mt * BM);
-        } else {
-          ok = __all_sync(0xffffffffu, mbar_wait_at(empty_at + stage * 8, phase ^ 1u, abort_flag, p.status));
-          if (!ok) break;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          if (elect_one()) {
-            arm(stage);
-            load_a(stage, kb, mt * BM);
-            load_b(stage, kb, n0);
-          }
-        }
-        __syncwarp();
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
-    if (!ok) {
-      // let copies already in flight land before the CTA leaves (one CTA:
-      // their own barrier; a pair: the stage is released once consumed)
-      for (int s = 0; s < C::STAGES; ++s)
-        if (pending & (1u << s)) mbar_drain(PAIR ? &empty[s] : &full[s], (armed_parity >> s) & 1u);
-    }
-  } else if (warp == 9 || warp == 10) {
-    // ---------------------------------------------------------- MMA issuers
-    griddep_wait();
-    if (leader) {
-      // the whole warp walks the loop and one elected lane issues: inside a
-      // single-lane branch every descriptor would be moved to a uniform
-      // register anew
-      constexpr uint32_t kIdesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, kSub);
-      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
-      const uint32_t full_at = smem_u32(full), acc_empty_at = smem_u32(acc_empty);
-      const int me = warp - 9;
-      // the K blocks (BN 128: every second one; their count runs over the
-      // tiles) and the column half that are this warp's
-      constexpr int STEP = C::NSUB == 2 ? 1 : 2;
-      const int sub = C::NSUB == 2 ? me : 0;
-      const uint32_t b_off = static_cast<uint32_t>((C::A_BYTES + sub * C::SUB_BYTES) >> 4);
-      int stage = C::NSUB == 2 ? 0 : me, slot = stage;
-      uint32_t phase = 0, bphase = 0;
+  // (each setmaxnreg inside its role's own branch: the compiler allocates for
+  // the smaller count where the two could meet)
+  if (warp >= 8) {
+    if constexpr (BN == 256) regs_dec<kIssueRegs>();
+    if (warp == 8) {
+      // ---------------------------------------------------------- TMA producer
+      // The whole warp walks the loops and one elected lane issues (see the MMA
+      // issuer): a single-lane loop needs twice the time per K block.
+      const uint64_t wpol = um <= 4 ? policy_evict_first() : policy_evict_normal();
+      const uint32_t empty_at = smem_u32(empty);
+      int stage = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      const int mine = (units - first + stride - 1) / stride;  // tiles of this CTA
-      const long long blocks = mine > 0 ? static_cast<long long>(mine) * kblocks : 0;
-#pragma unroll 1
-      for (long long kb = C::NSUB == 2 ? 0 : me; kb < blocks; kb += STEP) {
-        const int buf = sub * C::NB + slot;
-        const uint32_t buf_at = acc_empty_at + buf * 8, data_at = full_at + stage * 8;
-        if constexpr (C::NSUB == 2) {
-          // this warp has waited for every phase of both barriers, so both
-          // are tried before either vote: one after the other, tries and
-          // votes took as long as the MMAs
-          const bool has_buf = mbar_try_wait_at(buf_at, bphase ^ 1u);
-          const bool has_data = mbar_try_wait_at(data_at, phase);
-          ok = __all_sync(0xffffffffu, has_buf && has_data) ||
-               __all_sync(0xffffffffu, mbar_wait_at(buf_at, bphase ^ 1u, abort_flag, p.status) &&
-                                           mbar_wait_at(data_at, phase, abort_flag, p.status));
-        } else {
-          // The buffer first, and the operands only once it is known to be
-          // free: the other warp had this stage before, and a wait by parity
-          // also passes while that earlier phase is still open.  Tried
-          // together, the operands' barrier can be looked at while the
-          // buffer's try is pending; taken for complete one phase early, it
-          // let a block's MMAs run on half a stage and free it twice.  A
-          // released buffer means that block kb - NB has been summed, so
-          // every block up to it has left the ring, kb - STAGES among them.
-          static_assert(C::STAGES > C::NB, "a stage's earlier phase is over when its buffer is free");
-          ok = __all_sync(0xffffffffu, mbar_wait_at(buf_at, bphase ^ 1u, abort_flag, p.status));
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_at(data_at, phase, abort_flag, p.status));
-        }
-        if (!ok) break;
-        tc_fence_after();
-        // the start address is the low 14 bits of a descriptor, in 16-byte
-        // units, and shared memory ends below 2^18 bytes: it cannot carry
-        const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
-        const uint64_t b_desc = a_desc + b_off;
-        const uint32_t d_tmem = tmem_base + buf * kSub;
-        if (elect_one()) {
+      uint32_t pending = 0, armed_parity = 0;
+      auto load_a = [&](int s, int kb, int m0) {
+        uint8_t* dst = smem + s * C::STAGE_BYTES;
+        if constexpr (PAIR)
+          tma_load_2d_pair(dst, &tmA, full0 + s * 8, kb * BK, m0);
+        else
+          tma_load_2d(dst, &tmA, &full[s], kb * BK, m0);
+      };
+      auto load_b = [&](int s, int kb, int n0) {
+        uint8_t* dst = smem + s * C::STAGE_BYTES + C::A_BYTES;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if constexpr (PAIR)
-              mma_e4m3_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
-            else
-              mma_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
-          }
-          // the buffer last: its arrival is the one that the sums, and so the
-          // end of a CTA, wait for
-          if constexpr (PAIR) {
-            mma_commit_pair(&empty[stage], 3);
-            mma_commit_pair(&acc_full[buf], 3);
-          } else {
-            mma_commit(&empty[stage]);
-            mma_commit(&acc_full[buf]);
+        for (int i = 0; i < C::NSUB; ++i) {
+          if constexpr (PAIR)
+            tma_load_2d_pair_hint(dst + i * C::SUB_BYTES, &tmB, full0 + s * 8, kb * BK, n0 + i * kSub, wpol);
+          else
+            tma_load_2d_hint(dst + i * C::SUB_BYTES, &tmB, &full[s], kb * BK, n0 + i * kSub, wpol);
+        }
+      };
+      auto arm = [&](int s) {
+        if (leader) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * C::STAGE_BYTES);  // both CTAs' boxes
+      };
+      // the weights do not come from the kernel ahead: their first ring fill
+      // is issued before waiting for it
+      int pre = 0;
+      if (first < units) {
+        const int n0 = (first / um) * BN + static_cast<int>(rank) * (kSub / 2);
+        pre = kblocks < C::STAGES ? kblocks : C::STAGES;
+        if (elect_one()) {
+          for (int i = 0; i < pre; ++i) {
+            arm(i);
+            load_b(i, i, n0);
           }
         }
         __syncwarp();
-        stage += STEP;
-        if (stage >= C::STAGES) {
-          stage -= C::STAGES;
-          phase ^= 1u;
-        }
-        slot += STEP;
-        if (slot >= C::NB) {
-          slot -= C::NB;
-          bphase ^= 1u;
+      }
+      griddep_wait();
+      for (int u = first; u < units && ok; u += stride) {
+        const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
+        const int n0 = (u / um) * BN + static_cast<int>(rank) * (kSub / 2);
+#pragma unroll 1
+        for (int kb = 0; kb < kblocks; ++kb) {
+          pending |= 1u << stage;
+          if (u == first && kb < pre) {
+            if (elect_one()) load_a(stage, kb, mt * BM);
+          } else {
+            ok = __all_sync(0xffffffffu, mbar_wait_at(empty_at + stage * 8, phase ^ 1u, abort_flag, p.status));
+            if (!ok) break;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            if (elect_one()) {
+              arm(stage);
+              load_a(stage, kb, mt * BM);
+              load_b(stage, kb, n0);
+            }
+          }
+          __syncwarp();
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
       if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
-      // no MMA may still read shared memory or write tensor memory when the CTAs leave
-      if (elect_one()) {
-        if constexpr (PAIR)
-          mma_commit_pair(drain, 1);
-        else
-          mma_commit(drain);
+      if (!ok) {
+        // let copies already in flight land before the CTA leaves (one CTA:
+        // their own barrier; a pair: the stage is released once consumed)
+        for (int s = 0; s < C::STAGES; ++s)
+          if (pending & (1u << s)) mbar_drain(PAIR ? &empty[s] : &full[s], (armed_parity >> s) & 1u);
       }
-      __syncwarp();
-      mbar_drain(drain, 0);
-      __syncwarp();
-    }
-  } else if (warp == 11) {
-    // ---------------------------------------------------------- scale table
-    // Scales of the tile's rows and weight blocks, kTabK K blocks at a time,
-    // two fills ahead of the sums.  (Read by the promotion warps themselves,
-    // each row of sa is a cache line of its own: 128 lines and the few spills
-    // outgrew the L1 left beside the ring, and a K block took three times as
-    // long.)
-    griddep_wait();
-    int fill = 0;
-    bool ok = true;
-    for (int u = first; u < units; u += stride) {
-      const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
-      const int n0 = (u / um) * BN;
-      const float* pa[4];
-      bool in_m[4];
+    } else if (warp == 9 || warp == 10) {
+      // ---------------------------------------------------------- MMA issuers
+      griddep_wait();
+      if (leader) {
+        // the whole warp walks the loop and one elected lane issues: inside a
+        // single-lane branch every descriptor would be moved to a uniform
+        // register anew
+        constexpr uint32_t kIdesc = idesc_e4m3_f32(PAIR ? 2 * BM : BM, kSub);
+        const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+        const uint32_t full_at = smem_u32(full), acc_empty_at = smem_u32(acc_empty);
+        const int me = warp - 9;
+        // the K blocks (BN 128: every second one; their count runs over the
+        // tiles) and the column half that are this warp's
+        constexpr int STEP = C::NSUB == 2 ? 1 : 2;
+        const int sub = C::NSUB == 2 ? me : 0;
+        const uint32_t b_off = static_cast<uint32_t>((C::A_BYTES + sub * C::SUB_BYTES) >> 4);
+        int stage = C::NSUB == 2 ? 0 : me, slot = stage;
+        uint32_t phase = 0, bphase = 0;
+        bool ok = true;
+        const int mine = (units - first + stride - 1) / stride;  // tiles of this CTA
+        const long long blocks = mine > 0 ? static_cast<long long>(mine) * kblocks : 0;
+#pragma unroll 1
+        for (long long kb = C::NSUB == 2 ? 0 : me; kb < blocks; kb += STEP) {
+          const int buf = sub * C::NB + slot;
+          const uint32_t buf_at = acc_empty_at + buf * 8, data_at = full_at + stage * 8;
+          if constexpr (C::NSUB == 2) {
+            // this warp has waited for every phase of both barriers, so both
+            // are tried before either vote: one after the other, tries and
+            // votes took as long as the MMAs
+            const bool has_buf = mbar_try_wait_at(buf_at, bphase ^ 1u);
+            const bool has_data = mbar_try_wait_at(data_at, phase);
+            ok = __all_sync(0xffffffffu, has_buf && has_data) ||
+                 __all_sync(0xffffffffu, mbar_wait_at(buf_at, bphase ^ 1u, abort_flag, p.status) &&
+                                             mbar_wait_at(data_at, phase, abort_flag, p.status));
+          } else {
+            // The buffer first, and the operands only once it is known to be
+            // free: the other warp had this stage before, and a wait by parity
+            // also passes while that earlier phase is still open.  Tried
+            // together, the operands' barrier can be looked at while the
+            // buffer's try is pending; taken for complete one phase early, it
+            // let a block's MMAs run on half a stage and free it twice.  A
+            // released buffer means that block kb - NB has been summed, so
+            // every block up to it has left the ring, kb - STAGES among them.
+            static_assert(C::STAGES > C::NB, "a stage's earlier phase is over when its buffer is free");
+            ok = __all_sync(0xffffffffu, mbar_wait_at(buf_at, bphase ^ 1u, abort_flag, p.status));
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_at(data_at, phase, abort_flag, p.status));
+          }
+          if (!ok) break;
+          tc_fence_after();
+          // the start address is the low 14 bits of a descriptor, in 16-byte
+          // units, and shared memory ends below 2^18 bytes: it cannot carry
+          const uint64_t a_desc = desc0 + static_cast<uint32_t>(stage * (C::STAGE_BYTES >> 4));
+          const uint64_t b_desc = a_desc + b_off;
+          const uint32_t d_tmem = tmem_base + buf * kSub;
+          if (elect_one()) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = mt * BM + q * 32 + lane;
-        in_m[q] = row < p.M;
-        pa[q] = p.sa + static_cast<size_t>(in_m[q] ? row : 0) * kblocks;
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (PAIR)
+                mma_e4m3_pair(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
+              else
+                mma_e4m3(d_tmem, a_desc + 2 * k, b_desc + 2 * k, kIdesc, k != 0);
+            }
+            // the buffer last: its arrival is the one that the sums, and so the
+            // end of a CTA, wait for
+            if constexpr (PAIR) {
+              mma_commit_pair(&empty[stage], 3);
+              mma_commit_pair(&acc_full[buf], 3);
+            } else {
+              mma_commit(&empty[stage]);
+              mma_commit(&acc_full[buf]);
+            }
+          }
+          __syncwarp();
+          stage += STEP;
+          if (stage >= C::STAGES) {
+            stage -= C::STAGES;
+            phase ^= 1u;
+          }
+          slot += STEP;
+          if (slot >= C::NB) {
+            slot -= C::NB;
+            bphase ^= 1u;
+          }
+        }
+        if (PAIR && *abort_flag) raise_peer_abort(abort_flag, rank);
+        // no MMA may still read shared memory or write tensor memory when the CTAs leave
+        if (elect_one()) {
+          if constexpr (PAIR)
+            mma_commit_pair(drain, 1);
+          else
+            mma_commit(drain);
+        }
+        __syncwarp();
+        mbar_drain(drain, 0);
       }
-      // weight block j: buffer j / 2's gate (or only) block, and its up block
-      const int j = lane & 3;
-      const int n = n0 + (BN == 256 ? (j >> 1) * kSub : 0) + (SWIGLU ? (j & 1) * 64 : 0);
-      const float* ps =
-          p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n < p.N ? n : p.N - 1)) * kblocks + (lane >> 2);
-      for (int kb0 = 0; kb0 < kblocks; kb0 += kTabK, ++fill) {
-        float va[4][kTabK];
+    } else {
+      // ---------------------------------------------------------- scale table
+      // Scales of the tile's rows and weight blocks, kTabK K blocks at a time,
+      // two fills ahead of the sums.  (Read by the promotion warps themselves,
+      // each row of sa is a cache line of its own: 128 lines and the few spills
+      // outgrew the L1 left beside the ring, and a K block took three times as
+      // long.)
+      griddep_wait();
+      int fill = 0;
+      bool ok = true;
+      for (int u = first; u < units; u += stride) {
+        const int mt = PAIR ? 2 * (u % um) + static_cast<int>(rank) : u % um;
+        const int n0 = (u / um) * BN;
+        const float* pa[4];
+        bool in_m[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 4; ++q) {
+          const int row = mt * BM + q * 32 + lane;
+          in_m[q] = row < p.M;
+          pa[q] = p.sa + static_cast<size_t>(in_m[q] ? row : 0) * kblocks;
+        }
+        // weight block j: buffer j / 2's gate (or only) block, and its up block
+        const int j = lane & 3;
+        const int n = n0 + (BN == 256 ? (j >> 1) * kSub : 0) + (SWIGLU ? (j & 1) * 64 : 0);
+        const float* ps =
+            p.sb + static_cast<size_t>(scale_row<SWIGLU>(p, n < p.N ? n : p.N - 1)) * kblocks + (lane >> 2);
+        for (int kb0 = 0; kb0 < kblocks; kb0 += kTabK, ++fill) {
+          float va[4][kTabK];
 #pragma unroll
-          for (int i = 0; i < kTabK; ++i) va[q][i] = kb0 + i < kblocks && in_m[q] ? pa[q][kb0 + i] : 0.f;
-        const float vs = kb0 + (lane >> 2) < kblocks ? ps[kb0] : 0.f;
-        const int b = fill & 1;
-        if (ok) ok = mbar_wait(&tab_empty[b], ((fill >> 1) & 1) ^ 1u, abort_flag, p.status);
-        float* tab = table + b * (C::TABLE / 4);
+          for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+            for (int i = 0; i < kTabK; ++i) va[q][i] = kb0 + i < kblocks && in_m[q] ? ld_f32(pa[q] + kb0 + i) : 0.f;
+          const float vs = kb0 + (lane >> 2) < kblocks ? ld_f32(ps + kb0) : 0.f;
+          const int b = fill & 1;
+          if (ok) ok = mbar_wait(&tab_empty[b], ((fill >> 1) & 1) ^ 1u, abort_flag, p.status);
+          float* tab = table + b * (C::TABLE / 4);
 #pragma unroll
-          for (int i = 0; i < kTabK; ++i) tab[i * BM + q * 32 + lane] = va[q][i];
-        tab[kTabK * BM + lane] = vs;
-        mbar_arrive(&tab_full[b]);
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < kTabK; ++i) tab[i * BM + q * 32 + lane] = va[q][i];
+          tab[kTabK * BM + lane] = vs;
+          mbar_arrive(&tab_full[b]);
+        }
       }
     }
   } else {
     // ---------------------------------------------------------- promotion and epilogue
+    if constexpr (BN == 256) regs_inc<kPromoteRegs>();
     griddep_wait();
     const int quarter = warp & 3, half = warp >> 2;
     const bool boss = threadIdx.x == 0;
@@ -426,34 +437,21 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
-      // The sums run over W columns at a time, the next W on their way from
-      // TMEM meanwhile, across the border of two K blocks too.  At BN 256 the
-      // sums leave about 40 registers: two sets of 8 columns, or (STORE and
-      // F32, where the compiler fits it better: 217 against 225 us for
-      // 4096 x 9216 x 7168; SWIGLU the other way round, 384 against 399 us for
-      // 4096 x 28672 x 4096) one set of 16.  A wait that expired raises the
-      // abort flag, every later wait gives up soon, and the loop runs on over
-      // whatever TMEM holds: nothing of it is stored.
-      constexpr bool AHEAD = BN == 128 || EPI == HB_EPI_SWIGLU || EPI == HB_EPI_RESIDUAL;
-      constexpr int W = BN == 256 && AHEAD ? 8 : 16;  // columns of a step
-      constexpr int NC = CH * 32 / W;
-      constexpr bool TRY = BN == 128;  // a register more than BN 256 has
-      uint32_t r[AHEAD ? 2 : 1][W];
+      // The sums run over 16 columns at a time, the next 16 on their way from
+      // TMEM meanwhile, across the border of two K blocks too.  A wait that
+      // expired raises the abort flag, every later wait gives up soon, and
+      // the loop runs on over whatever TMEM holds: nothing of it is stored.
+      constexpr int NC = CH * 2;
+      uint32_t r[2][16];
       const uint32_t t_cols = t_lane + sub * C::NB * kSub - sub * kSub;
-      auto step_col = [&](int c) { return chunk_col(c * W / 32) + c * W % 32; };
-      auto load = [&](uint32_t at, uint32_t (&x)[W]) {
-        if constexpr (W == 8)
-          tmem_ld_32x32b_x8(at, x);
-        else
-          tmem_ld_32x32b_x16(at, x);
-      };
+      auto step_col = [&](int c) { return chunk_col(c >> 1) + (c & 1) * 16; };
       // waits for the next K block in TMEM and starts its first columns;
       // there: an earlier try has found it complete
       auto next_block = [&](bool there) {
         if (!__all_sync(0xffffffffu, there)) ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
         __syncwarp();
         tc_fence_after();
-        load(t_cols + slot * kSub + step_col(0), r[0]);
+        tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(0), r[0]);
       };
       next_block(false);
 #pragma unroll 1
@@ -496,9 +494,8 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             // under the sums.  Past the tile's last block there is nothing to
             // find, and a try would hold the thread in vain: it takes the
             // present block, which is complete.
-            if (TRY && c == NC - 2) there = mbar_try_wait_at(acc_full_at + next_slot * 8, next_phase);
-            if (AHEAD && c < NC - 1)
-              load(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & (AHEAD ? 1 : 0)]);
+            if (c == NC - 2) there = mbar_try_wait_at(acc_full_at + next_slot * 8, next_phase);
+            if (c < NC - 1) tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & 1]);
             if (c == NC - 1) {
               tc_fence_before();
               __syncwarp();
@@ -512,22 +509,16 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
                 slot = 0;
                 bphase ^= 1u;
               }
-              if (AHEAD && more) next_block(there);
+              if (more) next_block(there);
             }
             // scalar FMAs: the packed fma.rn.f32x2 needs register pairs that
             // the TMEM load does not give without moves (620 against 370
             // clocks per 256-column block, measured)
             const float f = c < NC / 2 ? f0 : f1;
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-              float& a = acc[c * W / 32][c * W % 32 + j];
-              a = __fmaf_rn(__uint_as_float(r[AHEAD ? c & 1 : 0][j]), f, a);
-            }
-            if (!AHEAD) {
-              if (c < NC - 1)
-                load(t_cols + slot * kSub + step_col(c + 1), r[0]);
-              else if (more)
-                next_block(there);
+            for (int j = 0; j < 16; ++j) {
+              float& a = acc[c >> 1][(c & 1) * 16 + j];
+              a = __fmaf_rn(__uint_as_float(r[c & 1][j]), f, a);
             }
           }
         }
@@ -639,12 +630,12 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     if (boss) bulk_wait_group<0>();  // the TMA stores have left shared memory and are performed
     if (PAIR && lane == 0 && *abort_flag) raise_peer_abort(abort_flag, rank);
   }
-  __syncwarp();
 
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();
   if (warp == 9) {
+    __syncwarp();
     tc_fence_after();
     if constexpr (PAIR)
       tmem_dealloc_pair(tmem_base, 512);
@@ -676,16 +667,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 // groups of four, so that the waits and commits of one block are a quarter
 // of what they would be alone: a single warp adds the blocks of a 32-row
 // tile, and its instructions, not the loads, set the pace.
-//   warps 0-3: promotion and epilogue (those with lanes below p.rows; all
-//              four fill the table of scale products);
-//   warp 4   : TMA producer;  warp 5: MMA issuer.
-constexpr int kSkinnyThreads = 192;
-constexpr int kGroup = 4;       // K blocks of one TMEM buffer (two buffers)
+//   warps 0-7: promotion and epilogue, warp w for TMEM lanes 32 (w % 4).. (those
+//              below p.rows) and half w / 4 of the tokens; all eight fill the
+//              table of scale products;
+//   warp 8   : TMA producer;  warp 9: MMA issuer.
+constexpr int kSkinnyThreads = 320;
+constexpr int kGroup = 4;       // K blocks of one TMEM buffer
 constexpr int kSkinnyTabK = 16; // K blocks per fill of the scale table
 
 template <int NT>
 struct CfgSkinny {
-  static constexpr int TMEM_COLS = 2 * kGroup * NT;
+  static constexpr int NBUF = NT == 64 ? 2 : 4;
+  static constexpr int TMEM_COLS = NBUF * kGroup * NT;
+  static constexpr int TH = NT / 2;                 // tokens of a promotion thread
+  static constexpr int LOADS = NT == 64 ? 2 : kGroup;  // K blocks read from TMEM at a time
   static constexpr int TAB = kSkinnyTabK * 2 * NT;  // floats of one buffer: [K block][weight block][token]
   static constexpr int MAX_STAGES = 16;
   static constexpr int BAR_BYTES = 512;
@@ -693,6 +688,10 @@ struct CfgSkinny {
   static constexpr int FIXED = 1024 + BM * 128 + 2 * TAB * 4 + BAR_BYTES + XCH_BYTES;
   static_assert(NT == 16 || NT == 32 || NT == 64, "NT");
 };
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[8]) { tmem_ld_32x32b_x8(at, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(at, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(at, r); }
 
 template <int NT, int EPI>
 __global__ void __launch_bounds__(kSkinnyThreads, 1)
@@ -709,8 +708,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(xch) + C::XCH_BYTES);
   uint64_t* empty = full + C::MAX_STAGES;
   uint64_t* acc_full = empty + C::MAX_STAGES;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + C::NBUF;
+  uint64_t* drain = acc_empty + C::NBUF;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -729,9 +728,9 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < C::NBUF; ++a) {
       mbar_init(&acc_full[a], 1);
-      mbar_init(&acc_empty[a], act_warps);
+      mbar_init(&acc_empty[a], 2 * act_warps);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -739,7 +738,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -749,7 +748,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ---------------------------------------------------------- TMA producer
     const uint64_t wpol = policy_evict_first();  // each weight box is read once
     const uint32_t empty_at = smem_u32(empty);
@@ -813,7 +812,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     if (!ok)
       for (int s = 0; s < ring; ++s)
         if (pending & (1u << s)) mbar_drain(&full[s], (armed_parity >> s) & 1u);
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---------------------------------------------------------- MMA issuer
     griddep_wait();
     constexpr uint32_t kIdesc = idesc_e4m3_f32(BM, NT);
@@ -849,7 +848,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
           stage = 0;
           phase ^= 1u;
         }
-        if (last && ++buf == 2) {
+        if (last && ++buf == C::NBUF) {
           buf = 0;
           bphase ^= 1u;
         }
@@ -858,17 +857,18 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     if (elect_one()) mma_commit(drain);
     __syncwarp();
     mbar_drain(drain, 0);
-    __syncwarp();
   } else {
     // ---------------------------------------------------------- promotion and epilogue
     griddep_wait();
-    const bool active = warp < act_warps;
-    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-    const int e = warp * 32 + lane;  // weight row within the tile
+    constexpr int TH = C::TH;
+    const int quarter = warp & 3, j0 = (warp >> 2) * TH;  // this warp's first token
+    const bool active = quarter < act_warps;
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + j0;
+    const int e = quarter * 32 + lane;  // weight row within the tile
     // Scale products of K block kb0 + fi, fi = threadIdx.x % kSkinnyTabK:
-    // thread's tokens fj, fj + 8, ...; the two weight blocks a tile can touch
+    // thread's tokens fj, fj + 16, ...; the two weight blocks a tile can touch
     // (SWIGLU: the gate's and the up's).
-    constexpr int PER = NT / 8;
+    constexpr int PER = NT / 16;
     const int fi = threadIdx.x % kSkinnyTabK, fj = threadIdx.x / kSkinnyTabK;
     float pre_a[PER], pre_b[2];
     const float* sb_blk[2];
@@ -876,20 +876,21 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       const bool in = kb0 + fi < kblocks;
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
-        const int j = fj + 8 * x;
-        pre_a[x] = in && j < p.M ? p.sa[static_cast<size_t>(j) * kblocks + kb0 + fi] : 0.f;
+        const int j = fj + 16 * x;
+        pre_a[x] = in && j < p.M ? ld_f32(p.sa + static_cast<size_t>(j) * kblocks + kb0 + fi) : 0.f;
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) pre_b[b] = in ? sb_blk[b][kb0 + fi] : 0.f;
+      for (int b = 0; b < 2; ++b) pre_b[b] = in ? ld_f32(sb_blk[b] + kb0 + fi) : 0.f;
     };
     auto put = [&](int side) {
 #pragma unroll
       for (int x = 0; x < PER; ++x)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          table[side * C::TAB + (fi * 2 + b) * NT + fj + 8 * x] = __fmul_rn(pre_a[x], pre_b[b]);
+          table[side * C::TAB + (fi * 2 + b) * NT + fj + 16 * x] = __fmul_rn(pre_a[x], pre_b[b]);
     };
-    const uint32_t table_at = smem_u32(table);
+    const uint32_t table_at = smem_u32(table) + j0 * 4;
+    const uint32_t acc_full_at = smem_u32(acc_full), acc_empty_at = smem_u32(acc_empty);
     int buf = 0;
     uint32_t bphase = 0;
     bool ok = true;
@@ -911,51 +912,52 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
         sb_blk[0] = p.sb + static_cast<size_t>(b0) * kblocks;
         sb_blk[1] = p.sb + static_cast<size_t>(b0 < b1 ? b0 + 1 : b1) * kblocks;
       }
-      float acc[NT];
+      float acc[TH];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) acc[j] = 0.f;
+      for (int j = 0; j < TH; ++j) acc[j] = 0.f;
       fetch(0);
-      named_barrier_sync(1, 128);  // the previous tile's table reads are done
+      named_barrier_sync(1, 256);  // the previous tile's table reads are done
       put(0);
 #pragma unroll 1
       for (int kb0 = 0; kb0 < kblocks; kb0 += kGroup) {
         const int ti = kb0 % kSkinnyTabK, side = (kb0 / kSkinnyTabK) & 1;
         if (ti == 0) {
-          named_barrier_sync(1, 128);  // this side of the table is filled, the other one is read
+          named_barrier_sync(1, 256);  // this side of the table is filled, the other one is read
           if (kb0 + kSkinnyTabK < kblocks) fetch(kb0 + kSkinnyTabK);
         }
         if (ti == kSkinnyTabK - kGroup && kb0 + kGroup < kblocks) put(side ^ 1);
         if (active) {
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_at(smem_u32(&acc_full[buf]), bphase, abort_flag, p.status));
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait_at(acc_full_at + buf * 8, bphase, abort_flag, p.status));
           if (ok) {
             tc_fence_after();
-            // 32 columns at a time: 32 / NT blocks, or half a block of 64 tokens
-            constexpr int STEPS = kGroup * NT / 32;
 #pragma unroll
-            for (int c = 0; c < STEPS; ++c) {
-              uint32_t r[32];
-              tmem_ld_32x32b_x32(t_lane + buf * (kGroup * NT) + c * 32, r);
+            for (int g0 = 0; g0 < kGroup; g0 += C::LOADS) {
+              uint32_t r[C::LOADS][TH];
+#pragma unroll
+              for (int g = 0; g < C::LOADS; ++g) tmem_ld_cols(t_lane + (buf * kGroup + g0 + g) * NT, r[g]);
               tmem_ld_wait();
-              if (c == STEPS - 1) {
+              if (g0 + C::LOADS == kGroup) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty[buf]);
+                if (lane == 0) mbar_arrive_at(acc_empty_at + buf * 8);
               }
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {  // four columns each
-                const int g = (c * 32 + 4 * q) / NT, j = (c * 32 + 4 * q) % NT;
-                if (kb0 + g < kblocks) {
-                  const float4 f = lds_f32x4(table_at + (side * C::TAB + ((ti + g) * 2 + blk) * NT + j) * 4);
-                  acc[j] = __fmaf_rn(__uint_as_float(r[4 * q]), f.x, acc[j]);
-                  acc[j + 1] = __fmaf_rn(__uint_as_float(r[4 * q + 1]), f.y, acc[j + 1]);
-                  acc[j + 2] = __fmaf_rn(__uint_as_float(r[4 * q + 2]), f.z, acc[j + 2]);
-                  acc[j + 3] = __fmaf_rn(__uint_as_float(r[4 * q + 3]), f.w, acc[j + 3]);
+              for (int g = 0; g < C::LOADS; ++g) {
+                if (kb0 + g0 + g >= kblocks) break;
+                const uint32_t at = table_at + (side * C::TAB + ((ti + g0 + g) * 2 + blk) * NT) * 4;
+#pragma unroll
+                for (int j = 0; j < TH; j += 4) {
+                  const float4 f = lds_f32x4(at + j * 4);
+                  acc[j] = __fmaf_rn(__uint_as_float(r[g][j]), f.x, acc[j]);
+                  acc[j + 1] = __fmaf_rn(__uint_as_float(r[g][j + 1]), f.y, acc[j + 1]);
+                  acc[j + 2] = __fmaf_rn(__uint_as_float(r[g][j + 2]), f.z, acc[j + 2]);
+                  acc[j + 3] = __fmaf_rn(__uint_as_float(r[g][j + 3]), f.w, acc[j + 3]);
                 }
               }
             }
           }
         }
-        if (++buf == 2) {
+        if (++buf == C::NBUF) {
           buf = 0;
           bphase ^= 1u;
         }
@@ -964,23 +966,23 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       if constexpr (SWIGLU) {
         if (active && e >= G && e < R) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) xch[(e - G) * (NT + 1) + j] = acc[j];
+          for (int j = 0; j < TH; ++j) xch[(e - G) * (NT + 1) + j0 + j] = acc[j];
         }
-        named_barrier_sync(1, 128);
+        named_barrier_sync(1, 256);
         if (active && ok && e < G) {
           const int f = (t / per_block) * 64 + (t % per_block) * G + e;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + f;
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
-            if (j < p.M)
-              dst[static_cast<size_t>(j) * p.ldc] =
-                  __float2bfloat16_rn(__fmul_rn(silu(acc[j]), xch[e * (NT + 1) + j]));
+          for (int j = 0; j < TH; ++j)
+            if (j0 + j < p.M)
+              dst[static_cast<size_t>(j0 + j) * p.ldc] =
+                  __float2bfloat16_rn(__fmul_rn(silu(acc[j]), xch[e * (NT + 1) + j0 + j]));
         }
       } else if (active && ok && n_ok) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (j >= p.M) continue;
-          const size_t at = static_cast<size_t>(j) * p.ldc + n;
+        for (int j = 0; j < TH; ++j) {
+          if (j0 + j >= p.M) continue;
+          const size_t at = static_cast<size_t>(j0 + j) * p.ldc + n;
           if constexpr (EPI == HB_EPI_F32) {
             static_cast<float*>(p.C)[at] = acc[j];
           } else if constexpr (EPI == HB_EPI_RESIDUAL) {
@@ -993,11 +995,11 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       }
     }
   }
-  __syncwarp();
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
