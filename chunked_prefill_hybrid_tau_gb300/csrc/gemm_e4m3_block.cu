@@ -670,8 +670,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 //   warps 0-7: promotion and epilogue, warp w for TMEM lanes 32 (w % 4).. (those
 //              below p.rows) and half w / 4 of the tokens; all eight fill the
 //              table of scale products;
-//   warp 8   : TMA producer;  warp 9: MMA issuer.
-constexpr int kSkinnyThreads = 320;
+//   warp 8   : TMA producer;  warps 9-10: MMA issuers.
+constexpr int kSkinnyThreads = 352;
 constexpr int kGroup = 4;       // K blocks of one TMEM buffer
 constexpr int kSkinnyTabK = 16; // K blocks per fill of the scale table
 
@@ -720,19 +720,20 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   const int R = p.rows, G = R / 2;
   const int per_block = SWIGLU ? 64 / G : 1;  // SWIGLU tiles of one 128-row gate/up block
   const int tiles = SWIGLU ? (p.N / 128) * per_block : (p.N + R - 1) / R;
-  const int act_warps = (R + 31) / 32;
+  const bool m64 = R <= 64;
+  const int act_warps = m64 ? (R + 15) / 16 : (R + 31) / 32;
   const int ring = p.stages;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < ring; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);
     }
     for (int a = 0; a < C::NBUF; ++a) {
-      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_full[a], 2);
       mbar_init(&acc_empty[a], 2 * act_warps);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
@@ -812,11 +813,14 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     if (!ok)
       for (int s = 0; s < ring; ++s)
         if (pending & (1u << s)) mbar_drain(&full[s], (armed_parity >> s) & 1u);
-  } else if (warp == 9) {
-    // ---------------------------------------------------------- MMA issuer
+  } else if (warp >= 9) {
+    // ---------------------------------------------------------- MMA issuers
     griddep_wait();
-    constexpr uint32_t kIdesc = idesc_e4m3_f32(BM, NT);
-    const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+    const uint32_t idesc = m64 ? idesc_e4m3_f32(64, NT) : idesc_e4m3_f32(BM, NT);
+    // the two warps take one K block of every stage each
+    const int me = warp - 9;
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(smem) + me * kb_bytes);
+    const uint32_t tmem_me = tmem_base + me * NT;
     const uint32_t full_at = smem_u32(full), acc_empty_at = smem_u32(acc_empty);
     int stage = 0, buf = 0;
     uint32_t phase = 0, bphase = 0;
@@ -832,14 +836,11 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
         tc_fence_after();
         const bool last = in_group == kGroup / 2 - 1 || pr == pairs - 1;
         if (elect_one()) {
+          const uint64_t w_desc = desc0 + static_cast<uint32_t>((stage * stage_bytes) >> 4);
+          const uint64_t x_desc = w_desc + static_cast<uint32_t>(w_bytes >> 4);
+          const uint32_t d = tmem_me + (buf * kGroup + in_group * 2) * NT;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint64_t w_desc = desc0 + static_cast<uint32_t>((stage * stage_bytes + h * kb_bytes) >> 4);
-            const uint64_t x_desc = w_desc + static_cast<uint32_t>(w_bytes >> 4);
-            const uint32_t d = tmem_base + (buf * kGroup + in_group * 2 + h) * NT;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_e4m3(d, w_desc + 2 * k, x_desc + 2 * k, kIdesc, k != 0);
-          }
+          for (int k = 0; k < 4; ++k) mma_e4m3(d, w_desc + 2 * k, x_desc + 2 * k, idesc, k != 0);
           mma_commit(&empty[stage]);
           if (last) mma_commit(&acc_full[buf]);
         }
@@ -864,7 +865,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     const int quarter = warp & 3, j0 = (warp >> 2) * TH;  // this warp's first token
     const bool active = quarter < act_warps;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + j0;
-    const int e = quarter * 32 + lane;  // weight row within the tile
+    // weight row within the tile (M = 64: rows 16 w.. in lanes 32 w..)
+    const int e = m64 ? (lane < 16 ? quarter * 16 + lane : BM) : quarter * 32 + lane;
     // Scale products of K block kb0 + fi, fi = threadIdx.x % kSkinnyTabK:
     // thread's tokens fj, fj + 16, ...; the two weight blocks a tile can touch
     // (SWIGLU: the gate's and the up's).
