@@ -40,6 +40,7 @@ struct Params {
   int kblocks;
   int* status;
   int rows;      // skinny kernel: weight rows of a tile
+  int groups;    // skinny kernel: groups of NT tokens
   int stages;    // skinny kernel: ring depth
 };
 
@@ -61,6 +62,10 @@ __device__ __forceinline__ int scale_row(const Params& p, int n) {
   }
   return n >> 7;
 }
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[8]) { tmem_ld_32x32b_x8(at, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(at, r); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(at, r); }
 
 // ================================================================ wide tiles
 // 128 x BN output tiles (PAIR: 256 x BN on a cluster of two CTAs with
@@ -441,17 +446,17 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       // TMEM meanwhile, across the border of two K blocks too.  A wait that
       // expired raises the abort flag, every later wait gives up soon, and
       // the loop runs on over whatever TMEM holds: nothing of it is stored.
-      constexpr int NC = CH * 2;
-      uint32_t r[2][16];
+      constexpr int W = BN == 256 && EPI != HB_EPI_F32 ? 32 : 16, NC = CH * 32 / W;
+      uint32_t r[2][W];
       const uint32_t t_cols = t_lane + sub * C::NB * kSub - sub * kSub;
-      auto step_col = [&](int c) { return chunk_col(c >> 1) + (c & 1) * 16; };
+      auto step_col = [&](int c) { return chunk_col(c * W / 32) + c * W % 32; };
       // waits for the next K block in TMEM and starts its first columns;
       // there: an earlier try has found it complete
       auto next_block = [&](bool there) {
         if (!__all_sync(0xffffffffu, there)) ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
         __syncwarp();
         tc_fence_after();
-        tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(0), r[0]);
+        tmem_ld_cols(t_cols + slot * kSub + step_col(0), r[0]);
       };
       next_block(false);
 #pragma unroll 1
@@ -495,7 +500,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             // find, and a try would hold the thread in vain: it takes the
             // present block, which is complete.
             if (c == NC - 2) there = mbar_try_wait_at(acc_full_at + next_slot * 8, next_phase);
-            if (c < NC - 1) tmem_ld_32x32b_x16(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & 1]);
+            if (c < NC - 1) tmem_ld_cols(t_cols + slot * kSub + step_col(c + 1), r[(c + 1) & 1]);
             if (c == NC - 1) {
               tc_fence_before();
               __syncwarp();
@@ -516,8 +521,8 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             // clocks per 256-column block, measured)
             const float f = c < NC / 2 ? f0 : f1;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float& a = acc[c >> 1][(c & 1) * 16 + j];
+            for (int j = 0; j < W; ++j) {
+              float& a = acc[c * W / 32][c * W % 32 + j];
               a = __fmaf_rn(__uint_as_float(r[c & 1][j]), f, a);
             }
           }
@@ -689,10 +694,6 @@ struct CfgSkinny {
   static_assert(NT == 16 || NT == 32 || NT == 64, "NT");
 };
 
-__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[8]) { tmem_ld_32x32b_x8(at, r); }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[16]) { tmem_ld_32x32b_x16(at, r); }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[32]) { tmem_ld_32x32b_x32(at, r); }
-
 template <int NT, int EPI>
 __global__ void __launch_bounds__(kSkinnyThreads, 1)
     block_gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -719,7 +720,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   const int pairs = (kblocks + 1) / 2;  // ring stages of a tile (past K the boxes are zeros)
   const int R = p.rows, G = R / 2;
   const int per_block = SWIGLU ? 64 / G : 1;  // SWIGLU tiles of one 128-row gate/up block
-  const int tiles = SWIGLU ? (p.N / 128) * per_block : (p.N + R - 1) / R;
+  // the groups of one weight tile run side by side
+  const int tiles = (SWIGLU ? (p.N / 128) * per_block : (p.N + R - 1) / R) * p.groups;
   const bool m64 = R <= 64;
   const int act_warps = m64 ? (R + 15) / 16 : (R + 31) / 32;
   const int ring = p.stages;
@@ -754,16 +756,17 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     const uint64_t wpol = policy_evict_first();  // each weight box is read once
     const uint32_t empty_at = smem_u32(empty);
     auto load_w = [&](int s, int pr, int t) {
+      const int wt = t / p.groups;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint8_t* dst = smem + s * stage_bytes + h * kb_bytes;
         const int k = (2 * pr + h) * BK;
         if constexpr (SWIGLU) {
-          const int n = (t / per_block) * 128 + (t % per_block) * G;
+          const int n = (wt / per_block) * 128 + (wt % per_block) * G;
           tma_load_2d_hint(dst, &tmB, &full[s], k, n, wpol);
           tma_load_2d_hint(dst + G * 128, &tmB, &full[s], k, n + 64, wpol);
         } else {
-          tma_load_2d_hint(dst, &tmB, &full[s], k, t * R, wpol);
+          tma_load_2d_hint(dst, &tmB, &full[s], k, wt * R, wpol);
         }
       }
     };
@@ -785,6 +788,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     }
     griddep_wait();
     for (int t = t0; t < tiles && ok; t += gridDim.x) {
+      const int m0 = t % p.groups * NT;
 #pragma unroll 1
       for (int pr = 0; pr < pairs; ++pr) {
         const bool fresh = !(t == t0 && pr < pre);
@@ -800,8 +804,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
             load_w(stage, pr, t);
           }
           uint8_t* dst = smem + stage * stage_bytes + w_bytes;
-          tma_load_2d(dst, &tmA, &full[stage], 2 * pr * BK, 0);
-          tma_load_2d(dst + kb_bytes, &tmA, &full[stage], (2 * pr + 1) * BK, 0);
+          tma_load_2d(dst, &tmA, &full[stage], 2 * pr * BK, m0);
+          tma_load_2d(dst + kb_bytes, &tmA, &full[stage], (2 * pr + 1) * BK, m0);
         }
         __syncwarp();
         if (++stage == ring) {
@@ -874,11 +878,12 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     const int fi = threadIdx.x % kSkinnyTabK, fj = threadIdx.x / kSkinnyTabK;
     float pre_a[PER], pre_b[2];
     const float* sb_blk[2];
+    int m0 = 0;  // the tile's first token
     auto fetch = [&](int kb0) {
       const bool in = kb0 + fi < kblocks;
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
-        const int j = fj + 16 * x;
+        const int j = m0 + fj + 16 * x;
         pre_a[x] = in && j < p.M ? ld_f32(p.sa + static_cast<size_t>(j) * kblocks + kb0 + fi) : 0.f;
       }
 #pragma unroll
@@ -897,19 +902,21 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     uint32_t bphase = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const int wt = t / p.groups;
+      m0 = (t - wt * p.groups) * NT;
       int n;    // this thread's row of B
       bool n_ok;
       int blk;  // which of the tile's two weight blocks scales it
       if constexpr (SWIGLU) {
-        const int base = (t / per_block) * 128;
-        n = base + (t % per_block) * G + (e < G ? e : 64 + e - G);
+        const int base = (wt / per_block) * 128;
+        n = base + (wt % per_block) * G + (e < G ? e : 64 + e - G);
         n_ok = e < R;
         blk = n_ok && e >= G ? 1 : 0;
         for (int b = 0; b < 2; ++b) sb_blk[b] = p.sb + static_cast<size_t>(scale_row<true>(p, base + 64 * b)) * kblocks;
       } else {
-        n = t * R + e;
+        n = wt * R + e;
         n_ok = e < R && n < p.N;
-        const int b0 = t * R / BK, b1 = (p.N - 1) / BK;
+        const int b0 = wt * R / BK, b1 = (p.N - 1) / BK;
         blk = n_ok ? n / BK - b0 : 0;
         sb_blk[0] = p.sb + static_cast<size_t>(b0) * kblocks;
         sb_blk[1] = p.sb + static_cast<size_t>(b0 < b1 ? b0 + 1 : b1) * kblocks;
@@ -972,19 +979,19 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
         }
         named_barrier_sync(1, 256);
         if (active && ok && e < G) {
-          const int f = (t / per_block) * 64 + (t % per_block) * G + e;
+          const int f = (wt / per_block) * 64 + (wt % per_block) * G + e;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + f;
 #pragma unroll
           for (int j = 0; j < TH; ++j)
-            if (j0 + j < p.M)
-              dst[static_cast<size_t>(j0 + j) * p.ldc] =
+            if (m0 + j0 + j < p.M)
+              dst[static_cast<size_t>(m0 + j0 + j) * p.ldc] =
                   __float2bfloat16_rn(__fmul_rn(silu(acc[j]), xch[e * (NT + 1) + j0 + j]));
         }
       } else if (active && ok && n_ok) {
 #pragma unroll
         for (int j = 0; j < TH; ++j) {
-          if (j0 + j >= p.M) continue;
-          const size_t at = static_cast<size_t>(j0 + j) * p.ldc + n;
+          if (m0 + j0 + j >= p.M) continue;
+          const size_t at = static_cast<size_t>(m0 + j0 + j) * p.ldc + n;
           if constexpr (EPI == HB_EPI_F32) {
             static_cast<float*>(p.C)[at] = acc[j];
           } else if constexpr (EPI == HB_EPI_RESIDUAL) {
@@ -1050,18 +1057,20 @@ hb_status launch_skinny(const DeviceCtx& ctx, const void* A, const void* B, Para
   constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;
   int tiles;
   if (SWIGLU) {
-    // G gate and G up rows of one 128-row block: the largest G that still
-    // gives every SM a tile
+    // G gate and G up rows of one 128-row block: as small as the waves that
+    // whole blocks take allow
+    auto waves = [&](int g) { return (p.N / 128 * (64 / g) * p.groups + ctx.num_sms - 1) / ctx.num_sms; };
     int g = 64;
-    while (g > 8 && (p.N / 128) * (64 / g) < ctx.num_sms) g /= 2;
+    while (g > 8 && waves(g / 2) <= waves(g)) g /= 2;
     p.rows = 2 * g;
-    tiles = p.N / 128 * (64 / g);
+    tiles = p.N / 128 * (64 / g) * p.groups;
   } else {
     // as few waves as 128-row tiles allow, their rows spread evenly
-    const int waves = (p.N + 128 * ctx.num_sms - 1) / (128 * ctx.num_sms);
-    const int even = (p.N + waves * ctx.num_sms - 1) / (waves * ctx.num_sms);
+    const int per_wave = ctx.num_sms / p.groups;  // weight tiles
+    const int waves = (p.N + 128 * per_wave - 1) / (128 * per_wave);
+    const int even = (p.N + waves * per_wave - 1) / (waves * per_wave);
     p.rows = (even + 7) / 8 * 8;
-    tiles = (p.N + p.rows - 1) / p.rows;
+    tiles = (p.N + p.rows - 1) / p.rows * p.groups;
   }
   const int stage_bytes = 2 * (p.rows + NT) * 128;
   const int avail = 232448 - C::FIXED;
@@ -1084,7 +1093,8 @@ template <int EPI>
 hb_status launch_epi(const DeviceCtx& ctx, const void* A, const void* B, const Params& p, cudaStream_t stream) {
   if (p.M <= 16) return launch_skinny<16, EPI>(ctx, A, B, p, stream);
   if (p.M <= 32) return launch_skinny<32, EPI>(ctx, A, B, p, stream);
-  if (p.M <= 64) return launch_skinny<64, EPI>(ctx, A, B, p, stream);
+  if (p.M <= 64 || (p.groups <= ctx.num_sms && p.N <= ctx.num_sms / p.groups * 64))
+    return launch_skinny<64, EPI>(ctx, A, B, p, stream);
   if (p.M <= BM) return launch_wide<128, EPI, false>(ctx, A, B, p, stream);
   const int pm = (p.M + 2 * BM - 1) / (2 * BM), pairs = ctx.num_sms / 2;
   auto waves = [&](int bn) { return (pm * ((p.N + bn - 1) / bn) + pairs - 1) / pairs; };
@@ -1111,6 +1121,7 @@ hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, c
   p.f_blocks = (N / 2 + 127) / 128;
   p.kblocks = (K + BK - 1) / BK;
   p.status = ctx.status;
+  p.groups = (M + 63) / 64;
   switch (epi) {
     case HB_EPI_STORE: return launch_epi<HB_EPI_STORE>(ctx, A, B, p, stream);
     case HB_EPI_RESIDUAL: return launch_epi<HB_EPI_RESIDUAL>(ctx, A, B, p, stream);

@@ -222,6 +222,45 @@ def test_gemm_block_rows_do_not_depend_on_the_batch(n, k, epi):
         assert torch.equal(part, whole[lo:hi]), (lo, hi)
 
 
+# More outputs than one wave of 64-row weight tiles takes: the 128-row tiles of
+# one CTA (65 to 128 tokens) and of CTA pairs, 128 and 256 columns wide.
+WIDE_CASES = [
+    (65, 4872, 144, F32), (128, 5000, 688, RESIDUAL), (100, 4992, 400, SWIGLU), (127, 8200, 1152, STORE),
+    (66, 19592, 2064, STORE), (80, 28672, 4096, SWIGLU), (96, 20000, 272, F32),
+    (129, 3256, 272, F32), (200, 4104, 688, RESIDUAL), (201, 6144, 2048, STORE), (300, 2432, 1040, SWIGLU),
+    (385, 5000, 400, STORE), (512, 9728, 656, F32), (700, 10248, 1296, RESIDUAL), (1100, 9728, 400, SWIGLU),
+]
+
+
+@pytest.mark.parametrize("m,n,k,epi", WIDE_CASES)
+def test_gemm_block_many_outputs(m, n, k, epi):
+    pr = Projection(m, n, k, epi)
+    rel = pr.check(pr.run())
+    if epi == F32:
+        assert rel < 1e-5
+
+
+@pytest.mark.parametrize("n,k,epi", [(10248, 528, STORE), (9984, 1168, SWIGLU), (5000, 688, F32), (20000, 272, RESIDUAL)])
+def test_gemm_block_rows_do_not_depend_on_the_batch_many_outputs(n, k, epi):
+    pr = Projection(700, n, k, epi)
+    whole = pr.run()
+    for lo, hi in [(0, 1), (5, 21), (100, 130), (333, 397), (400, 465), (200, 300), (128, 384), (0, 513)]:
+        part = pr.run(slice(lo, hi))
+        assert torch.equal(part, whole[lo:hi]), (lo, hi)
+
+
+def test_gemm_block_tokens_in_groups():
+    """Few outputs and many tokens: groups of 64 tokens, the last one partly
+    empty, neighbours untouched."""
+    for m, n, epi in [(65, 8, F32), (1000, 136, STORE), (577, 264, RESIDUAL), (130, 1152, SWIGLU), (4000, 128, SWIGLU),
+                      (9730, 8, F32)]:
+        pr = Projection(m, n, 400, epi)
+        buf = torch.full((m + 1, n // 2 if epi == SWIGLU else n), 7.0, device="cuda",
+                         dtype=torch.float32 if epi == F32 else torch.bfloat16)
+        pr.check(pr.run(out=buf[:m]))
+        assert bool((buf[m] == 7).all())
+
+
 def test_gemm_block_in_place_residual_and_neighbours():
     """R may be C; rows past M and whatever follows the output stay as they were."""
     for m in (9, 100, 300):
