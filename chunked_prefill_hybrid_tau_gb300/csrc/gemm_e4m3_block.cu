@@ -86,6 +86,15 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[32]) { t
 //   warp 11   : fills the table of scales.
 // The sums leave through shared memory staged apart from the ring and TMA
 // stores, so the next tile's loads and MMAs go on meanwhile.
+//
+// A K block of a 256 x 256 pair tile is 512 clocks of MMAs; all of its 128 x 256
+// partial sums then cross from TMEM to registers (256 clocks at 4 bytes a lane
+// and clock) while the other half's MMAs update TMEM.  Measured: 750 clocks
+// (394 ns).  4096 x 9216 x 7168: 191 us, 2.83 PFLOP/s, 145 at twice the measured
+// bf16 rate; 512 x 28672 x 4096 (SWIGLU): 51 us, 2.35 PFLOP/s.  Tried and
+// slower: twice the promotion warps with half the sums each (255 against 225
+// us, their waits and table reads double), packed fp32 FMAs, one issuing warp
+// (207), 128-column tiles throughout (222).
 constexpr int kTabK = 8;  // K blocks per fill of the scale table
 constexpr int kBufs = 4;  // TMEM buffers of kSub columns
 constexpr int kSub = 128;
@@ -442,11 +451,12 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
-      // The sums run over 16 columns at a time, the next 16 on their way from
+      // The sums run over W columns at a time, the next W on their way from
       // TMEM meanwhile, across the border of two K blocks too.  A wait that
       // expired raises the abort flag, every later wait gives up soon, and
       // the loop runs on over whatever TMEM holds: nothing of it is stored.
-      constexpr int W = BN == 256 && EPI != HB_EPI_F32 ? 32 : 16, NC = CH * 32 / W;
+      constexpr int W = BN == 256 && EPI != HB_EPI_F32 ? 32 : 16;  // (F32 at 32: 246 us against 229, it spills)
+      constexpr int NC = CH * 32 / W;
       uint32_t r[2][W];
       const uint32_t t_cols = t_lane + sub * C::NB * kSub - sub * kSub;
       auto step_col = [&](int c) { return chunk_col(c * W / 32) + c * W % 32; };
@@ -664,14 +674,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 }
 
 // ================================================================ few tokens
-// M <= NT: the weights are the bound, so the operands change places: a tile
-// is p.rows weight rows (TMEM lanes) x NT tokens (columns), and the rows per
-// tile are chosen so that the tiles fill the SMs.  The MMA always has M =
-// 128: lanes past p.rows multiply whatever follows in shared memory and are
-// not read.  K blocks go through the ring in pairs and through TMEM in
-// groups of four, so that the waits and commits of one block are a quarter
-// of what they would be alone: a single warp adds the blocks of a 32-row
-// tile, and its instructions, not the loads, set the pace.
+// The weights are the bound, so the operands change places: a tile is p.rows
+// weight rows (TMEM lanes) x NT tokens (columns), and the rows per tile are
+// chosen so that the tiles fill the SMs; more than 64 tokens make groups of 64,
+// the tiles of one weight box side by side.  The MMA has M = 64, or 128 above 64
+// rows: lanes past p.rows multiply whatever follows in shared memory and are
+// not read.
+//
+// What a K block costs is not its bytes but the steps in turn of one warp: a
+// wait, four MMAs of 32 columns of K (about 75 clocks each at M = 128 whatever
+// N, less at 64), a commit.  So K blocks go through the ring in pairs, one for
+// each of two issuing warps, and through TMEM in groups of four, and the sums
+// of a lane are shared by two warps.  32 x 4096 x 14336: 16.7 us, 126 ns a block
+// (25.4 us with one issuing warp, M = 128 and one warp a lane; 8.8 at the copy
+// rate); 1 x 6144 x 4096: 7.1 us; 1 x 28672 x 4096 (SWIGLU): 18.9 us, 6.2 TB/s.
 //   warps 0-7: promotion and epilogue, warp w for TMEM lanes 32 (w % 4).. (those
 //              below p.rows) and half w / 4 of the tokens; all eight fill the
 //              table of scale products;
@@ -1089,16 +1105,25 @@ hb_status launch_skinny(const DeviceCtx& ctx, const void* A, const void* B, Para
                     stream, "block_gemm_skinny_kernel launch", tmA, tmB, p);
 }
 
+// Up to 64 tokens take tiles of weight rows spread over the SMs.  More tokens
+// do so in groups of 64 while one wave of tiles of up to 128 weight rows
+// (SWIGLU: 64) holds them all, where 256 x 128 tiles would leave most SMs idle:
+// 128 x 4096 x 4096 8.6 us against 11.0, 201 x 1536 x 2048 5.4 against 7.1, 128 x
+// 9728 x 4096 10.9 against 11.9 (SWIGLU 13.1 against 12.2), 512 x 2400 x 4096
+// 10.1 against 11.2.  Beyond that one CTA's 128 rows, then pairs; a K block of a
+// pair's tile takes 237 ns at 128 columns and 394 at 256, so the narrow tiles
+// win where they need less than 5 / 3 of the waves.
 template <int EPI>
 hb_status launch_epi(const DeviceCtx& ctx, const void* A, const void* B, const Params& p, cudaStream_t stream) {
+  constexpr int ROWS = EPI == HB_EPI_SWIGLU ? 64 : 128;
   if (p.M <= 16) return launch_skinny<16, EPI>(ctx, A, B, p, stream);
   if (p.M <= 32) return launch_skinny<32, EPI>(ctx, A, B, p, stream);
-  if (p.M <= 64 || (p.groups <= ctx.num_sms && p.N <= ctx.num_sms / p.groups * 64))
+  if (p.M <= 64 || (p.groups <= ctx.num_sms && p.N <= ctx.num_sms / p.groups * ROWS))
     return launch_skinny<64, EPI>(ctx, A, B, p, stream);
   if (p.M <= BM) return launch_wide<128, EPI, false>(ctx, A, B, p, stream);
   const int pm = (p.M + 2 * BM - 1) / (2 * BM), pairs = ctx.num_sms / 2;
   auto waves = [&](int bn) { return (pm * ((p.N + bn - 1) / bn) + pairs - 1) / pairs; };
-  if (waves(128) * 128 < waves(256) * 256) return launch_wide<128, EPI, true>(ctx, A, B, p, stream);
+  if (waves(128) * 3 < waves(256) * 5) return launch_wide<128, EPI, true>(ctx, A, B, p, stream);
   return launch_wide<256, EPI, true>(ctx, A, B, p, stream);
 }
 

@@ -222,13 +222,15 @@ def test_gemm_block_rows_do_not_depend_on_the_batch(n, k, epi):
         assert torch.equal(part, whole[lo:hi]), (lo, hi)
 
 
-# More outputs than one wave of 64-row weight tiles takes: the 128-row tiles of
+# More outputs than one wave of tiles of weight rows takes, or nearly so: the 128-row tiles of
 # one CTA (65 to 128 tokens) and of CTA pairs, 128 and 256 columns wide.
 WIDE_CASES = [
     (65, 4872, 144, F32), (128, 5000, 688, RESIDUAL), (100, 4992, 400, SWIGLU), (127, 8200, 1152, STORE),
     (66, 19592, 2064, STORE), (80, 28672, 4096, SWIGLU), (96, 20000, 272, F32),
     (129, 3256, 272, F32), (200, 4104, 688, RESIDUAL), (201, 6144, 2048, STORE), (300, 2432, 1040, SWIGLU),
-    (385, 5000, 400, STORE), (512, 9728, 656, F32), (700, 10248, 1296, RESIDUAL), (1100, 9728, 400, SWIGLU),
+    (65, 9736, 144, F32), (128, 10000, 688, RESIDUAL), (127, 12296, 1152, STORE), (129, 6408, 272, F32),
+    (200, 5000, 688, RESIDUAL), (385, 5000, 400, STORE), (512, 9728, 656, F32), (700, 10248, 1296, RESIDUAL),
+    (1100, 9728, 400, SWIGLU),
 ]
 
 
@@ -240,7 +242,8 @@ def test_gemm_block_many_outputs(m, n, k, epi):
         assert rel < 1e-5
 
 
-@pytest.mark.parametrize("n,k,epi", [(10248, 528, STORE), (9984, 1168, SWIGLU), (5000, 688, F32), (20000, 272, RESIDUAL)])
+@pytest.mark.parametrize("n,k,epi", [(10248, 528, STORE), (9984, 1168, SWIGLU), (5000, 688, F32),
+                                     (20000, 272, RESIDUAL)])
 def test_gemm_block_rows_do_not_depend_on_the_batch_many_outputs(n, k, epi):
     pr = Projection(700, n, k, epi)
     whole = pr.run()
