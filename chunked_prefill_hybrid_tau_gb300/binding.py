@@ -62,12 +62,14 @@ def _p(t):
 
 
 def _need(call, name, t, size, count):
-    """A contiguous device tensor of at least `count` elements of `size` bytes
-    (the kernels address it by its first element alone)."""
+    """Device pointer of a contiguous device tensor of at least `count`
+    elements of `size` bytes (the kernels address it by its first element
+    alone)."""
     if t.numel() < count or t.element_size() != size or not t.is_contiguous() or not t.is_cuda:
         raise HBError(L.HB_ERR_INVALID_ARG,
                       f"{call}: {name} must be a contiguous device tensor of at least {count} elements of {size} "
                       f"bytes, not {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
 def dims_struct(dims) -> L.hb_layer_dims:
@@ -335,16 +337,14 @@ def hb_kv_append_norm(qkv, row_pos, slot_mapping, rope, max_pos, dims, g_q, g_k,
                       stream=None):
     """hb_kv_append with q and k heads RMS-normed (gains g_q, g_k bf16 [d_head])."""
     ds = dims_struct(dims)
-    T, dh, pages = qkv.shape[0], ds.d_head, k_cache.shape[0]
-    slot = ds.n_kv * 16 * dh
-    for name, t, size, count in (("qkv", qkv, 2, T * (ds.n_q + 2 * ds.n_kv) * dh), ("row_pos", row_pos, 4, T),
-                                 ("slot_mapping", slot_mapping, 4, T), ("rope", rope, 4, max_pos * dh),
-                                 ("g_q", g_q, 2, dh), ("g_k", g_k, 2, dh), ("q_out", q_out, 2, T * ds.n_q * dh),
-                                 ("k_cache", k_cache, 2, pages * slot), ("v_cache", v_cache, 2, pages * slot)):
-        _need("hb_kv_append_norm", name, t, size, count)
-    _check(lib().hb_kv_append_norm(_p(qkv), T, _p(row_pos), _p(slot_mapping), _p(rope), int(max_pos), C.byref(ds),
-                                   _p(g_q), _p(g_k), _p(q_out), _p(k_cache), _p(v_cache), pages, _stream(stream)),
-           "hb_kv_append_norm")
+    T, dh, pages, call = qkv.shape[0], ds.d_head, k_cache.shape[0], "hb_kv_append_norm"
+    cache = pages * ds.n_kv * 16 * dh
+    _check(lib().hb_kv_append_norm(
+        _need(call, "qkv", qkv, 2, T * (ds.n_q + 2 * ds.n_kv) * dh), T, _need(call, "row_pos", row_pos, 4, T),
+        _need(call, "slot_mapping", slot_mapping, 4, T), _need(call, "rope", rope, 4, max_pos * dh), int(max_pos),
+        C.byref(ds), _need(call, "g_q", g_q, 2, dh), _need(call, "g_k", g_k, 2, dh),
+        _need(call, "q_out", q_out, 2, T * ds.n_q * dh), _need(call, "k_cache", k_cache, 2, cache),
+        _need(call, "v_cache", v_cache, 2, cache), pages, _stream(stream)), call)
 
 
 def hb_attention_workspace_bytes(dims, max_rows, max_seqs, max_kv_len) -> int:
@@ -395,11 +395,10 @@ def hb_quantize_e4m3_block(x, q=None, scale=None, block_rows=1, stream=None):
         import torch
         q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device) if q is None else q
         scale = torch.empty(groups, dtype=torch.float32, device=x.device) if scale is None else scale
-    _need("hb_quantize_e4m3_block", "x", x, 2, 0)
-    _need("hb_quantize_e4m3_block", "q", q, 1, rows * cols)
-    _need("hb_quantize_e4m3_block", "scale", scale, 4, groups[0] * groups[1])
-    _check(lib().hb_quantize_e4m3_block(_p(x), _p(q), _p(scale), rows, cols, block_rows, _stream(stream)),
-           "hb_quantize_e4m3_block")
+    call = "hb_quantize_e4m3_block"
+    _check(lib().hb_quantize_e4m3_block(_need(call, "x", x, 2, 0), _need(call, "q", q, 1, rows * cols),
+                                        _need(call, "scale", scale, 4, groups[0] * groups[1]), rows, cols,
+                                        block_rows, _stream(stream)), call)
     return q, scale
 
 
@@ -411,15 +410,11 @@ def hb_gemm_e4m3_block(A, s_a, B, s_b, Cout, R=None, epilogue=L.HB_EPI_STORE, st
     kb = (K + 127) // 128
     swiglu = epilogue == L.HB_EPI_SWIGLU
     call = "hb_gemm_e4m3_block"
-    _need(call, "A", A, 1, 0)
-    _need(call, "B", B, 1, N * K)
-    _need(call, "s_a", s_a, 4, M * kb)
-    _need(call, "s_b", s_b, 4, (2 * ((N + 255) // 256) if swiglu else (N + 127) // 128) * kb)
-    _need(call, "C", Cout, 4 if epilogue == L.HB_EPI_F32 else 2, M * N // 2 if swiglu else M * N)
-    if R is not None:
-        _need(call, "R", R, 2, M * N)
-    _check(lib().hb_gemm_e4m3_block(_p(A), _p(s_a), _p(B), _p(s_b), _p(Cout), _p(R), M, N, K, int(epilogue),
-                                    _stream(stream)), call)
+    _check(lib().hb_gemm_e4m3_block(
+        _need(call, "A", A, 1, 0), _need(call, "s_a", s_a, 4, M * kb), _need(call, "B", B, 1, N * K),
+        _need(call, "s_b", s_b, 4, (2 * ((N + 255) // 256) if swiglu else (N + 127) // 128) * kb),
+        _need(call, "C", Cout, 4 if epilogue == L.HB_EPI_F32 else 2, M * N // 2 if swiglu else M * N),
+        None if R is None else _need(call, "R", R, 2, M * N), M, N, K, int(epilogue), _stream(stream)), call)
 
 
 def hb_interleave_gate_up(w_gate, w_up, w_gu, stream=None):
