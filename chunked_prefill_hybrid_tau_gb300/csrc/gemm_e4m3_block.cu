@@ -681,13 +681,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 // rows: lanes past p.rows multiply whatever follows in shared memory and are
 // not read.
 //
-// What a K block costs is not its bytes but the steps in turn of one warp: a
-// wait, four MMAs of 32 columns of K (about 75 clocks each at M = 128 whatever
-// N, less at 64), a commit.  So K blocks go through the ring in pairs, one for
-// each of two issuing warps, and through TMEM in groups of four, and the sums
-// of a lane are shared by two warps.  32 x 4096 x 14336: 16.7 us, 126 ns a block
-// (25.4 us with one issuing warp, M = 128 and one warp a lane; 8.8 at the copy
-// rate); 1 x 6144 x 4096: 7.1 us; 1 x 28672 x 4096 (SWIGLU): 18.9 us, 6.2 TB/s.
+// With one issuing warp, M = 128 and one promotion warp a lane, a K block cost
+// the steps in turn of one warp (wait, four MMAs, commit; 290 clocks).  So K
+// blocks go through the ring in pairs, one for each of two issuing warps, and
+// through TMEM in groups of four, and the sums of a lane are shared by two
+// warps.  What is left is about 107 clocks and 2.2 for each 128-byte row of
+// weights and tokens (48, 64 and 96 rows: 213, 240 and 320 clocks): an SM takes
+// in 64 bytes a clock from L2, the tokens' rows included.  Four issuing warps are
+// no faster.  32 x 4096 x 14336: 16.7 us (25.4 before; 8.8 at the copy rate);
+// 1 x 6144 x 4096: 7.1 us; 1 x 28672 x 4096 (SWIGLU): 18.9 us, 6.2 TB/s; 32 x
+// 128256 x 4096 (F32): 74.5 us, 7.2 TB/s.
 //   warps 0-7: promotion and epilogue, warp w for TMEM lanes 32 (w % 4).. (those
 //              below p.rows) and half w / 4 of the tokens; all eight fill the
 //              table of scale products;
