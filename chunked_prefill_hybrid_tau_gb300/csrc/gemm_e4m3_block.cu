@@ -1166,6 +1166,7 @@ extern "C" hb_status hb_gemm_e4m3_block(const void* A, const float* s_a, const v
   hb::clear_error();
   HB_REQUIRE(A && s_a && B && s_b && C, "hb_gemm_e4m3_block: null operand");
   HB_REQUIRE(M >= 1 && N >= 8 && K >= 16, "hb_gemm_e4m3_block: bad shape M=%d N=%d K=%d", M, N, K);
+  HB_REQUIRE(M <= 1 << 30 && N <= 1 << 30 && K <= 1 << 30, "hb_gemm_e4m3_block: sizes up to 2^30");
   HB_REQUIRE(K % 16 == 0 && N % 8 == 0, "hb_gemm_e4m3_block: K %% 16 and N %% 8 required (K=%d N=%d)", K, N);
   HB_REQUIRE(epilogue >= HB_EPI_STORE && epilogue <= HB_EPI_F32, "hb_gemm_e4m3_block: unknown epilogue %d", epilogue);
   HB_REQUIRE(epilogue != HB_EPI_SWIGLU || N % 128 == 0, "hb_gemm_e4m3_block: SWIGLU needs N %% 128 == 0");

@@ -399,8 +399,8 @@ hb_status hb_quantize_e4m3_block(const void* x, void* q, float* scale, int32_t r
  * blocks of 64 (N / 2 rows of each, as hb_interleave_gate_up lays them out),
  * and s_b holds the block scales of the gate [ceil(N / 256)][ceil(K / 128)]
  * followed by those of the up matrix, each quantized on its own.
- * K % 16 == 0, N % 8 == 0 (N % 128 for SWIGLU); A, B, C and R 16-byte
- * aligned.  B must be complete before the kernel ahead of this call on the
+ * K % 16 == 0, N % 8 == 0 (N % 128 for SWIGLU), each size at most 2^30; A, B,
+ * C and R 16-byte aligned.  B must be complete before the kernel ahead of this call on the
  * stream starts, unless that kernel is hb_quantize_e4m3_block with
  * block_rows 128 or not one of this library's.
  * ---------------------------------------------------------------------- */

@@ -439,3 +439,61 @@ def test_chain_on_a_side_stream_and_in_a_graph():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(eager, again))
     hb.hb_check_status()
+
+
+def test_gemm_block_calls_at_once():
+    """Every kernel on two streams at a time, and a captured graph replayed
+    beside eager calls: the bits of the calls one after the other."""
+    cases = [Projection(m, n, k, e) for m, n, k, e in
+             [(1, 6144, 4096, STORE), (40, 1000, 688, F32), (64, 4096, 2064, RESIDUAL), (90, 12296, 1152, STORE),
+              (300, 2432, 1040, SWIGLU), (600, 10248, 400, RESIDUAL), (1100, 9728, 656, F32)]]
+    ref = [pr.run() for pr in cases]
+    outs = [[pr.out() for pr in cases] for _ in range(3)]
+
+    def call(pr, out):
+        hb.hb_gemm_e4m3_block(pr.a, pr.sa, pr.b, pr.sb, out, pr.r, pr.epi)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        for pr, out in zip(cases, outs[0]):
+            call(pr, out)
+    for rep in range(20):
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        with torch.cuda.stream(streams[1]):
+            for i in range(len(cases)):
+                call(cases[-1 - i], outs[1][-1 - i])
+        for pr, out in zip(cases, outs[2]):
+            call(pr, out)
+        torch.cuda.synchronize()
+        hb.hb_check_status()
+        for got in outs:
+            for o, r in zip(got, ref):
+                assert torch.equal(o, r), rep
+                o.fill_(3)
+
+
+@pytest.mark.parametrize("m", [65, 80, 128, 200, 520])
+def test_gemm_block_behind_quantizations_many_times(m):
+    """Projections and the quantizations between them, each launched while its
+    predecessors still run, over and over: always the same bits.  (One-CTA
+    tiles once took a stage's operands for complete one phase early here.)"""
+    g = gen(m)
+    x = randn((m, 4096), g)
+    up, su = hb.hb_quantize_e4m3_block(randn((28672, 4096), g, 0.02), block_rows=128)
+    down, sd = hb.hb_quantize_e4m3_block(randn((10240, 14336), g, 0.02), block_rows=128)
+    q, s = hb.hb_quantize_e4m3_block(x)
+    a = torch.empty((m, 14336), dtype=torch.bfloat16, device="cuda")
+    qa, sa = torch.empty_like(a, dtype=torch.uint8), torch.empty((m, 112), device="cuda")
+    first = None
+    for _ in range(40):
+        out = torch.empty((m, 10240), dtype=torch.bfloat16, device="cuda")
+        hb.hb_quantize_e4m3_block(x, q, s)
+        hb.hb_gemm_e4m3_block(q, s, up, su, a, epilogue=SWIGLU)
+        hb.hb_quantize_e4m3_block(a, qa, sa)
+        hb.hb_gemm_e4m3_block(qa, sa, down, sd, out)
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    hb.hb_check_status()

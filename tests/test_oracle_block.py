@@ -164,6 +164,8 @@ def test_gemm_block_refusals(lib):
         refused(lib, f(**{missing: None}), "null")
     refused(lib, f(m=0), "bad shape")
     refused(lib, f(k=24), "K % 16")
+    for size in ("m", "n", "k"):
+        refused(lib, f(**{size: 2 ** 31 - 128}), "2^30")
     refused(lib, f(n=100), "N % 8")
     refused(lib, f(epi=4), "epilogue")
     refused(lib, f(epi=-1), "epilogue")
