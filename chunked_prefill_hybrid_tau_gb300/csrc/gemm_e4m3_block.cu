@@ -944,6 +944,21 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
 #pragma unroll
       for (int j = 0; j < TH; ++j) acc[j] = 0.f;
       fetch(0);
+      // the residuals of this thread's outputs, read while the first boxes
+      // arrive (each read behind the last output's store, which may alias it,
+      // they cost 5 us for 64 tokens)
+      [[maybe_unused]] uint32_t res[TH / 2];
+      if constexpr (EPI == HB_EPI_RESIDUAL) {
+        const auto* rp = static_cast<const uint16_t*>(p.R) + (n_ok ? n : 0);
+        uint32_t v[TH];
+#pragma unroll
+        for (int j = 0; j < TH; ++j) {
+          const int row = m0 + j0 + j < p.M ? m0 + j0 + j : p.M - 1;
+          v[j] = rp[static_cast<size_t>(row) * p.ldc];
+        }
+#pragma unroll
+        for (int j = 0; j < TH; j += 2) res[j / 2] = v[j] | (v[j + 1] << 16);
+      }
       named_barrier_sync(1, 256);  // the previous tile's table reads are done
       put(0);
 #pragma unroll 1
@@ -1014,7 +1029,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
           if constexpr (EPI == HB_EPI_F32) {
             static_cast<float*>(p.C)[at] = acc[j];
           } else if constexpr (EPI == HB_EPI_RESIDUAL) {
-            const float r = __bfloat162float(static_cast<const __nv_bfloat16*>(p.R)[at]);
+            const float2 pair = unpack_bf16x2(res[j / 2]);
+            const float r = j & 1 ? pair.y : pair.x;
             static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(__fadd_rn(r, acc[j]));
           } else {
             static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(acc[j]);
@@ -1074,6 +1090,7 @@ template <int NT, int EPI>
 hb_status launch_skinny(const DeviceCtx& ctx, const void* A, const void* B, Params p, cudaStream_t stream) {
   using C = CfgSkinny<NT>;
   constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;
+  p.groups = (p.M + NT - 1) / NT;
   int tiles;
   if (SWIGLU) {
     // G gate and G up rows of one 128-row block: as small as the waves that
@@ -1108,21 +1125,44 @@ hb_status launch_skinny(const DeviceCtx& ctx, const void* A, const void* B, Para
                     stream, "block_gemm_skinny_kernel launch", tmA, tmB, p);
 }
 
-// Up to 64 tokens take tiles of weight rows spread over the SMs.  More tokens
-// do so in groups of 64 while one wave of tiles of up to 128 weight rows
-// (SWIGLU: 64) holds them all, where 256 x 128 tiles would leave most SMs idle:
-// 128 x 4096 x 4096 8.6 us against 11.0, 201 x 1536 x 2048 5.4 against 7.1, 128 x
-// 9728 x 4096 10.9 against 11.9 (SWIGLU 13.1 against 12.2), 512 x 2400 x 4096
-// 10.1 against 11.2.  Beyond that one CTA's 128 rows, then pairs; a K block of a
-// pair's tile takes 237 ns at 128 columns and 394 at 256, so the narrow tiles
-// win where they need less than 5 / 3 of the waves.
+// Rows of weights of a tile, with groups of nt tokens, if one wave of tiles
+// holds the output; 0 if it does not.
+template <bool SWIGLU>
+int one_wave_rows(const DeviceCtx& ctx, const Params& p, int nt) {
+  const int groups = (p.M + nt - 1) / nt;
+  if (groups > ctx.num_sms) return 0;
+  const int per_wave = ctx.num_sms / groups;  // weight tiles
+  if (SWIGLU) {
+    int g = 8;
+    while (g < 64 && p.N / 128 * (64 / g) > per_wave) g *= 2;
+    return p.N / 128 * (64 / g) <= per_wave ? 2 * g : 0;
+  }
+  const int rows = ((p.N + per_wave - 1) / per_wave + 7) / 8 * 8;
+  return rows <= BM ? rows : 0;
+}
+
+// Where one wave of tiles of weight rows x 16, 32 or 64 tokens holds the output,
+// 256 x 128 tiles would leave most SMs idle: 128 x 4096 x 4096 8.6 us against
+// 11.0, 128 x 9728 x 4096 10.9 against 11.9 (SWIGLU with 128 rows 13.1 against
+// 12.2: up to 64), 512 x 2400 x 4096 10.1 against 11.2.  Of the token counts the
+// one whose tile has the fewest rows of weights and tokens to load.  Up to 64
+// tokens take such tiles in several waves too.  Beyond that one CTA's 128
+// rows, then pairs; a K block of a pair's tile takes 237 ns at 128 columns and
+// 394 at 256, so the narrow tiles win where they need less than 5 / 3 of the
+// waves.
 template <int EPI>
 hb_status launch_epi(const DeviceCtx& ctx, const void* A, const void* B, const Params& p, cudaStream_t stream) {
-  constexpr int ROWS = EPI == HB_EPI_SWIGLU ? 64 : 128;
-  if (p.M <= 16) return launch_skinny<16, EPI>(ctx, A, B, p, stream);
-  if (p.M <= 32) return launch_skinny<32, EPI>(ctx, A, B, p, stream);
-  if (p.M <= 64 || (p.groups <= ctx.num_sms && p.N <= ctx.num_sms / p.groups * ROWS))
-    return launch_skinny<64, EPI>(ctx, A, B, p, stream);
+  constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;
+  int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 0, best = 0;
+  for (int t = 16; t <= 64; t *= 2) {
+    const int rows = one_wave_rows<SWIGLU>(ctx, p, t);
+    if (rows == 0 || (SWIGLU && rows > 64 && t < p.M) || (best != 0 && rows + t >= best)) continue;
+    nt = t;
+    best = rows + t;
+  }
+  if (nt == 16) return launch_skinny<16, EPI>(ctx, A, B, p, stream);
+  if (nt == 32) return launch_skinny<32, EPI>(ctx, A, B, p, stream);
+  if (nt == 64) return launch_skinny<64, EPI>(ctx, A, B, p, stream);
   if (p.M <= BM) return launch_wide<128, EPI, false>(ctx, A, B, p, stream);
   const int pm = (p.M + 2 * BM - 1) / (2 * BM), pairs = ctx.num_sms / 2;
   auto waves = [&](int bn) { return (pm * ((p.N + bn - 1) / bn) + pairs - 1) / pairs; };
@@ -1149,7 +1189,6 @@ hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, c
   p.f_blocks = (N / 2 + 127) / 128;
   p.kblocks = (K + BK - 1) / BK;
   p.status = ctx.status;
-  p.groups = (M + 63) / 64;
   switch (epi) {
     case HB_EPI_STORE: return launch_epi<HB_EPI_STORE>(ctx, A, B, p, stream);
     case HB_EPI_RESIDUAL: return launch_epi<HB_EPI_RESIDUAL>(ctx, A, B, p, stream);
