@@ -1146,10 +1146,9 @@ int one_wave_rows(const DeviceCtx& ctx, const Params& p, int nt) {
 // 11.0, 128 x 9728 x 4096 10.9 against 11.9 (SWIGLU with 128 rows 13.1 against
 // 12.2: up to 64), 512 x 2400 x 4096 10.1 against 11.2.  Of the token counts the
 // one whose tile has the fewest rows of weights and tokens to load.  Up to 64
-// tokens take such tiles in several waves too.  Beyond that one CTA's 128
-// rows, then pairs; a K block of a pair's tile takes 237 ns at 128 columns and
-// 394 at 256, so the narrow tiles win where they need less than 5 / 3 of the
-// waves.
+// tokens take such tiles in several waves too.  Else tiles of 128 rows (one
+// CTA) or 256 (a pair), by the waves they need and the time of a K block: 286
+// ns for 128 x 128, 237 for 256 x 128, 394 for 256 x 256.
 template <int EPI>
 hb_status launch_epi(const DeviceCtx& ctx, const void* A, const void* B, const Params& p, cudaStream_t stream) {
   constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;
@@ -1163,10 +1162,15 @@ hb_status launch_epi(const DeviceCtx& ctx, const void* A, const void* B, const P
   if (nt == 16) return launch_skinny<16, EPI>(ctx, A, B, p, stream);
   if (nt == 32) return launch_skinny<32, EPI>(ctx, A, B, p, stream);
   if (nt == 64) return launch_skinny<64, EPI>(ctx, A, B, p, stream);
-  if (p.M <= BM) return launch_wide<128, EPI, false>(ctx, A, B, p, stream);
-  const int pm = (p.M + 2 * BM - 1) / (2 * BM), pairs = ctx.num_sms / 2;
-  auto waves = [&](int bn) { return (pm * ((p.N + bn - 1) / bn) + pairs - 1) / pairs; };
-  if (waves(128) * 3 < waves(256) * 5) return launch_wide<128, EPI, true>(ctx, A, B, p, stream);
+  // ns of a K block of all waves
+  auto time = [&](int ns, int rows, int cols, int slots) {
+    const long long tiles = static_cast<long long>((p.M + rows - 1) / rows) * ((p.N + cols - 1) / cols);
+    return (tiles + slots - 1) / slots * ns;
+  };
+  const long long one = time(286, BM, 128, ctx.num_sms), narrow = time(237, 2 * BM, 128, ctx.num_sms / 2);
+  const long long broad = time(394, 2 * BM, 256, ctx.num_sms / 2);
+  if (p.M <= BM || (one < narrow && one < broad)) return launch_wide<128, EPI, false>(ctx, A, B, p, stream);
+  if (narrow < broad) return launch_wide<128, EPI, true>(ctx, A, B, p, stream);
   return launch_wide<256, EPI, true>(ctx, A, B, p, stream);
 }
 

@@ -230,7 +230,8 @@ WIDE_CASES = [
     (129, 3256, 272, F32), (200, 4104, 688, RESIDUAL), (201, 6144, 2048, STORE), (300, 2432, 1040, SWIGLU),
     (65, 9736, 144, F32), (128, 10000, 688, RESIDUAL), (127, 12296, 1152, STORE), (129, 6408, 272, F32),
     (200, 5000, 688, RESIDUAL), (385, 5000, 400, STORE), (512, 9728, 656, F32), (700, 10248, 1296, RESIDUAL),
-    (1100, 9728, 400, SWIGLU),
+    (1100, 9728, 400, SWIGLU), (293, 10728, 400, RESIDUAL), (600, 7168, 272, STORE), (290, 10752, 1296, SWIGLU),
+    (257, 11008, 656, F32),
 ]
 
 
@@ -243,11 +244,11 @@ def test_gemm_block_many_outputs(m, n, k, epi):
 
 
 @pytest.mark.parametrize("n,k,epi", [(10248, 528, STORE), (9984, 1168, SWIGLU), (5000, 688, F32),
-                                     (20000, 272, RESIDUAL)])
+                                     (20000, 272, RESIDUAL), (10728, 656, RESIDUAL)])
 def test_gemm_block_rows_do_not_depend_on_the_batch_many_outputs(n, k, epi):
     pr = Projection(700, n, k, epi)
     whole = pr.run()
-    for lo, hi in [(0, 1), (5, 21), (100, 130), (333, 397), (400, 465), (200, 300), (128, 384), (0, 513)]:
+    for lo, hi in [(0, 1), (5, 21), (100, 130), (333, 397), (400, 465), (200, 300), (128, 384), (0, 293), (0, 513)]:
         part = pr.run(slice(lo, hi))
         assert torch.equal(part, whole[lo:hi]), (lo, hi)
 
