@@ -688,8 +688,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 // warps.  What is left is about 107 clocks and 2.2 for each 128-byte row of
 // weights and tokens (48, 64 and 96 rows: 213, 240 and 320 clocks): an SM takes
 // in 64 bytes a clock from L2, the tokens' rows included.  Four issuing warps are
-// no faster.  32 x 4096 x 14336: 16.7 us (25.4 before; 8.8 at the copy rate);
-// 1 x 6144 x 4096: 7.1 us; 1 x 28672 x 4096 (SWIGLU): 18.9 us, 6.2 TB/s; 32 x
+// no faster.  32 x 4096 x 14336: 17.3 us (25.4 before; 8.8 at the copy rate);
+// 1 x 6144 x 4096: 6.6 us; 1 x 28672 x 4096 (SWIGLU): 18.9 us, 6.2 TB/s; 32 x
 // 128256 x 4096 (F32): 74.5 us, 7.2 TB/s.
 //   warps 0-7: promotion and epilogue, warp w for TMEM lanes 32 (w % 4).. (those
 //              below p.rows) and half w / 4 of the tokens; all eight fill the
