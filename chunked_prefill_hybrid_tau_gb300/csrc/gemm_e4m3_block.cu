@@ -676,8 +676,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 // ================================================================ few tokens
 // The weights are the bound, so the operands change places: a tile is p.rows
 // weight rows (TMEM lanes) x NT tokens (columns), and the rows per tile are
-// chosen so that the tiles fill the SMs; more than 64 tokens make groups of 64,
-// the tiles of one weight box side by side.  The MMA has M = 64, or 128 above 64
+// chosen so that the tiles fill the SMs; more than NT tokens make groups, the
+// tiles of one weight box side by side.  The MMA has M = 64, or 128 above 64
 // rows: lanes past p.rows multiply whatever follows in shared memory and are
 // not read.
 //
@@ -694,7 +694,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 //   warps 0-7: promotion and epilogue, warp w for TMEM lanes 32 (w % 4).. (those
 //              below p.rows) and half w / 4 of the tokens; all eight fill the
 //              table of scale products;
-//   warp 8   : TMA producer;  warps 9-10: MMA issuers.
+//   warp 8   : TMA producer;
+//   warps 9-10: MMA issuers, one K block of every stage each.
 constexpr int kSkinnyThreads = 352;
 constexpr int kGroup = 4;       // K blocks of one TMEM buffer
 constexpr int kSkinnyTabK = 16; // K blocks per fill of the scale table
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
 
   if (warp == 8) {
     // ---------------------------------------------------------- TMA producer
-    const uint64_t wpol = policy_evict_first();  // each weight box is read once
+    const uint64_t wpol = policy_evict_first();  // a weight box is read once, or by its groups side by side
     const uint32_t empty_at = smem_u32(empty);
     auto load_w = [&](int s, int pr, int t) {
       const int wt = t / p.groups;
