@@ -91,7 +91,9 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[32]) { t
 // partial sums then cross from TMEM to registers (256 clocks at 4 bytes a lane
 // and clock) while the other half's MMAs update TMEM.  Measured: 750 clocks
 // (394 ns).  4096 x 9216 x 7168: 191 us, 2.83 PFLOP/s, 145 at twice the measured
-// bf16 rate; 512 x 28672 x 4096 (SWIGLU): 51 us, 2.35 PFLOP/s.  Tried and
+// bf16 rate; 512 x 28672 x 4096 (SWIGLU): 51 us, 2.35 PFLOP/s.  (Without the
+// epilogue 2% less, without A's loads 4%; the per-row scaled projection, the
+// same MMAs without these sums: 156 and 41 us.)  Tried and
 // slower: twice the promotion warps with half the sums each (255 against 225
 // us, their waits and table reads double), packed fp32 FMAs, one issuing warp
 // (207), 128-column tiles throughout (222).
