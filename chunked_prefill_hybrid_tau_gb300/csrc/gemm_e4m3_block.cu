@@ -437,6 +437,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
     // addresses as one register and constants: at BN = 256 the sums leave few
     const uint32_t bars = smem_u32(full);
     const uint32_t acc_full_at = bars + (2 * C::STAGES + sub * C::NB) * 8, acc_empty_at = acc_full_at + kBufs * 8;
+    const uint32_t acc_empty_peer = PAIR ? cluster_addr_at(acc_empty_at, 0) : 0u;
     const uint32_t tab_full_at = bars + (2 * C::STAGES + 2 * kBufs) * 8, tab_empty_at = tab_full_at + 16;
     const uint32_t sa_at = bars - 2 * C::TABLE + rloc * 4;
     const uint32_t sb_at = bars - 2 * C::TABLE + (kTabK * BM + half * 2) * 4;
@@ -457,7 +458,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       // TMEM meanwhile, across the border of two K blocks too.  A wait that
       // expired raises the abort flag, every later wait gives up soon, and
       // the loop runs on over whatever TMEM holds: nothing of it is stored.
-      constexpr int W = BN == 256 && EPI != HB_EPI_F32 ? 32 : 16;  // (F32 at 32: 246 us against 229, it spills)
+      constexpr int W = BN == 256 && EPI != HB_EPI_F32 ? 32 : 16;  // (F32 at 32 spilled: 246 us against 229)
       constexpr int NC = CH * 32 / W;
       uint32_t r[2][W];
       const uint32_t t_cols = t_lane + sub * C::NB * kSub - sub * kSub;
@@ -465,8 +466,10 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       // waits for the next K block in TMEM and starts its first columns;
       // there: an earlier try has found it complete
       auto next_block = [&](bool there) {
-        if (!__all_sync(0xffffffffu, there)) ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
-        __syncwarp();
+        if (!__all_sync(0xffffffffu, there)) {
+          ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
+          __syncwarp();
+        }
         tc_fence_after();
         tmem_ld_cols(t_cols + slot * kSub + step_col(0), r[0]);
       };
@@ -518,7 +521,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
               __syncwarp();
               if (lane == 0) {
                 if constexpr (PAIR)
-                  mbar_arrive_cluster_relaxed(cluster_addr_at(acc_empty_at + slot * 8, 0));
+                  mbar_arrive_cluster_relaxed(acc_empty_peer + slot * 8);
                 else
                   mbar_arrive_at(acc_empty_at + slot * 8);
               }
