@@ -457,7 +457,8 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       // The sums run over W columns at a time, the next W on their way from
       // TMEM meanwhile, across the border of two K blocks too.  A wait that
       // expired raises the abort flag, every later wait gives up soon, and
-      // the loop runs on over whatever TMEM holds: nothing of it is stored.
+      // the loop runs on over whatever TMEM holds: nothing of it is stored,
+      // and no buffer is released any more.
       constexpr int W = BN == 256 && EPI != HB_EPI_F32 ? 32 : 16;  // (F32 at 32 spilled: 246 us against 229)
       constexpr int NC = CH * 32 / W;
       uint32_t r[2][W];
@@ -519,7 +520,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
             if (c == NC - 1) {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) {
+              if (lane == 0 && ok) {
                 if constexpr (PAIR)
                   mbar_arrive_cluster_relaxed(acc_empty_peer + slot * 8);
                 else
