@@ -56,6 +56,22 @@ def _stream(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """Uninitialised device tensor for calls on `stream`.  torch takes it from
+    the current stream's memory.  Where `stream` is another one, work queued
+    on the current stream may still be using that memory, so `stream` waits
+    for it; and the tensor is recorded there, so that its memory is not given
+    out again before `stream` is done with it, however early it is dropped."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and _stream(stream) != _current_stream():
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+        stream.wait_stream(torch.cuda.current_stream(device))
+        t.record_stream(stream)
+    return t
+
+
 def _p(t):
     """Device pointer of a tensor (None -> NULL)."""
     return None if t is None else t.data_ptr()
@@ -379,8 +395,8 @@ def hb_quantize_e4m3(x, q=None, scale=None, stream=None):
     device bf16 matrix x; returns (q, scale)."""
     import torch
     rows, cols = x.shape
-    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device) if q is None else q
-    scale = torch.empty(max(rows, 4), dtype=torch.float32, device=x.device) if scale is None else scale
+    q = _empty((rows, cols), torch.uint8, x.device, stream) if q is None else q
+    scale = _empty(max(rows, 4), torch.float32, x.device, stream) if scale is None else scale
     _check(lib().hb_quantize_e4m3(_p(x), _p(q), _p(scale), rows, cols, _stream(stream)), "hb_quantize_e4m3")
     return q, scale[:rows]
 
@@ -393,8 +409,8 @@ def hb_quantize_e4m3_block(x, q=None, scale=None, block_rows=1, stream=None):
     groups = (rows + block_rows - 1) // block_rows if block_rows > 0 else 0, (cols + 127) // 128
     if q is None or scale is None:
         import torch
-        q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device) if q is None else q
-        scale = torch.empty(groups, dtype=torch.float32, device=x.device) if scale is None else scale
+        q = _empty((rows, cols), torch.uint8, x.device, stream) if q is None else q
+        scale = _empty(groups, torch.float32, x.device, stream) if scale is None else scale
     call = "hb_quantize_e4m3_block"
     _check(lib().hb_quantize_e4m3_block(_need(call, "x", x, 2, 0), _need(call, "q", q, 1, rows * cols),
                                         _need(call, "scale", scale, 4, groups[0] * groups[1]), rows, cols,
@@ -446,18 +462,23 @@ def prepare_layer_weights(w_qkv, w_o, w_g, w_u, w_d, g1, g2, stream=None, fmt="b
     f_pad = (F + 63) // 64 * 64
     gains = dict(g_q=g_q, g_k=g_k)
     if fmt == "e4m3_block":
-        def block(w):
-            return hb_quantize_e4m3_block(w, block_rows=128, stream=stream)
+        def block(w, scale=None):
+            return hb_quantize_e4m3_block(w, scale=scale, block_rows=128, stream=stream)
+
+        def folded(w):
+            return hb_fold_gamma(w, g2, _empty((F, d), torch.bfloat16, w.device, stream), stream=stream)
 
         hb_fold_gamma(w_qkv, g1, stream=stream)
-        (gate, s_g), (up, s_u) = (block(hb_fold_gamma(w, g2, torch.empty_like(w), stream=stream)) for w in (w_g, w_u))
-        w_gu = torch.empty((2 * f_pad, d), dtype=torch.uint8, device=w_g.device)
+        # the gate's scales, then the up matrix's, each written in place: `stream` alone touches them
+        s_gu = _empty((2, (F + 127) // 128, (d + 127) // 128), torch.float32, w_g.device, stream)
+        gate, up = (block(folded(w), s_gu[i])[0] for i, w in enumerate((w_g, w_u)))
+        w_gu = _empty((2 * f_pad, d), torch.uint8, w_g.device, stream)
         # codes in pairs: the interleave moves 16-bit elements as they are
         hb_interleave_gate_up(gate.view(torch.bfloat16), up.view(torch.bfloat16), w_gu.view(torch.bfloat16), stream)
         q = {k: block(v) for k, v in (("qkv", w_qkv), ("o", w_o), ("d", w_d))}
         return LayerWeights(w_qkv=q["qkv"][0], w_o=q["o"][0], w_gu=w_gu, w_d=q["d"][0], s_qkv=q["qkv"][1],
-                            s_o=q["o"][1], s_gu=torch.cat([s_g, s_u]), s_d=q["d"][1], fmt=fmt, **gains)
-    w_gu = torch.empty((2 * f_pad, d), dtype=torch.bfloat16, device=w_g.device)
+                            s_o=q["o"][1], s_gu=s_gu.view(-1, s_gu.shape[2]), s_d=q["d"][1], fmt=fmt, **gains)
+    w_gu = _empty((2 * f_pad, d), torch.bfloat16, w_g.device, stream)
     hb_interleave_gate_up(w_g, w_u, w_gu, stream)
     hb_fold_gamma(w_gu, g2, stream=stream)
     hb_fold_gamma(w_qkv, g1, stream=stream)
