@@ -35,6 +35,12 @@ def _check(status: int, name: str):
 _raw_stream = None
 
 
+def _current_device() -> int:
+    import torch
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    return torch.cuda.current_device() if get is None else get()
+
+
 def _current_stream() -> int:
     """Handle of torch's current stream on the current device.  torch's raw
     accessors where it has them: the Stream object that current_stream()
@@ -77,15 +83,33 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _need(call, name, t, size, count):
-    """Device pointer of a contiguous device tensor of at least `count`
-    elements of `size` bytes (the kernels address it by its first element
-    alone)."""
-    if t.numel() < count or t.element_size() != size or not t.is_contiguous() or not t.is_cuda:
-        raise HBError(L.HB_ERR_INVALID_ARG,
-                      f"{call}: {name} must be a contiguous device tensor of at least {count} elements of {size} "
-                      f"bytes, not {tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+_operand_types = {}
+
+
+def _operands(call):
+    """-> need(name, t, kind, count): the device pointer of operand `t` of
+    `call`, a contiguous tensor on the current device of the given kind (bf16,
+    e4m3 codes, f32, i32) with at least `count` elements.  The kernels see an
+    address alone, so anything else is refused here."""
+    if not _operand_types:
+        import torch
+        _operand_types.update(bf16=(torch.bfloat16,), e4m3=(torch.uint8, torch.float8_e4m3fn), f32=(torch.float32,),
+                              i32=(torch.int32,))
+    device = None
+
+    def need(name, t, kind, count):
+        nonlocal device
+        where = t.get_device()
+        if where >= 0 and device is None:
+            device = _current_device()
+        if t.numel() < count or t.dtype not in _operand_types[kind] or not t.is_contiguous() or where != device:
+            raise HBError(L.HB_ERR_INVALID_ARG,
+                          f"{call}: {name} must be a contiguous device tensor of at least {count} elements of type "
+                          f"{' or '.join(str(d) for d in _operand_types[kind])} on the current device, not "
+                          f"{tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
+        return t.data_ptr()
+
+    return need
 
 
 def dims_struct(dims) -> L.hb_layer_dims:
@@ -355,12 +379,15 @@ def hb_kv_append_norm(qkv, row_pos, slot_mapping, rope, max_pos, dims, g_q, g_k,
     ds = dims_struct(dims)
     T, dh, pages, call = qkv.shape[0], ds.d_head, k_cache.shape[0], "hb_kv_append_norm"
     cache = pages * ds.n_kv * 16 * dh
+    need = _operands(call)
+    if qkv.numel() != T * (ds.n_q + 2 * ds.n_kv) * dh:
+        raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: qkv {tuple(qkv.shape)} does not have rows of {ds.n_q} q and "
+                                            f"2 x {ds.n_kv} kv heads of {dh}")
     _check(lib().hb_kv_append_norm(
-        _need(call, "qkv", qkv, 2, T * (ds.n_q + 2 * ds.n_kv) * dh), T, _need(call, "row_pos", row_pos, 4, T),
-        _need(call, "slot_mapping", slot_mapping, 4, T), _need(call, "rope", rope, 4, max_pos * dh), int(max_pos),
-        C.byref(ds), _need(call, "g_q", g_q, 2, dh), _need(call, "g_k", g_k, 2, dh),
-        _need(call, "q_out", q_out, 2, T * ds.n_q * dh), _need(call, "k_cache", k_cache, 2, cache),
-        _need(call, "v_cache", v_cache, 2, cache), pages, _stream(stream)), call)
+        need("qkv", qkv, "bf16", 0), T, need("row_pos", row_pos, "i32", T), need("slot_mapping", slot_mapping, "i32", T),
+        need("rope", rope, "f32", max_pos * dh), int(max_pos), C.byref(ds), need("g_q", g_q, "bf16", dh),
+        need("g_k", g_k, "bf16", dh), need("q_out", q_out, "bf16", T * ds.n_q * dh),
+        need("k_cache", k_cache, "bf16", cache), need("v_cache", v_cache, "bf16", cache), pages, _stream(stream)), call)
 
 
 def hb_attention_workspace_bytes(dims, max_rows, max_seqs, max_kv_len) -> int:
@@ -412,9 +439,10 @@ def hb_quantize_e4m3_block(x, q=None, scale=None, block_rows=1, stream=None):
         q = _empty((rows, cols), torch.uint8, x.device, stream) if q is None else q
         scale = _empty(groups, torch.float32, x.device, stream) if scale is None else scale
     call = "hb_quantize_e4m3_block"
-    _check(lib().hb_quantize_e4m3_block(_need(call, "x", x, 2, 0), _need(call, "q", q, 1, rows * cols),
-                                        _need(call, "scale", scale, 4, groups[0] * groups[1]), rows, cols,
-                                        block_rows, _stream(stream)), call)
+    need = _operands(call)
+    _check(lib().hb_quantize_e4m3_block(need("x", x, "bf16", 0), need("q", q, "e4m3", rows * cols),
+                                        need("scale", scale, "f32", groups[0] * groups[1]), rows, cols, block_rows,
+                                        _stream(stream)), call)
     return q, scale
 
 
@@ -422,15 +450,18 @@ def hb_gemm_e4m3_block(A, s_a, B, s_b, Cout, R=None, epilogue=L.HB_EPI_STORE, st
     """Block-scaled E4M3 codes A [M][K], B [N][K] (uint8 tensors) with fp32
     scales s_a [M][ceil(K / 128)], s_b [ceil(N / 128)][ceil(K / 128)]."""
     M, K = A.shape
-    N = B.shape[0]
+    N, KB = B.shape
     kb = (K + 127) // 128
     swiglu = epilogue == L.HB_EPI_SWIGLU
     call = "hb_gemm_e4m3_block"
+    need = _operands(call)
+    if KB != K:
+        raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: A has rows of {K} codes, B of {KB}")
     _check(lib().hb_gemm_e4m3_block(
-        _need(call, "A", A, 1, 0), _need(call, "s_a", s_a, 4, M * kb), _need(call, "B", B, 1, N * K),
-        _need(call, "s_b", s_b, 4, (2 * ((N + 255) // 256) if swiglu else (N + 127) // 128) * kb),
-        _need(call, "C", Cout, 4 if epilogue == L.HB_EPI_F32 else 2, M * N // 2 if swiglu else M * N),
-        None if R is None else _need(call, "R", R, 2, M * N), M, N, K, int(epilogue), _stream(stream)), call)
+        need("A", A, "e4m3", 0), need("s_a", s_a, "f32", M * kb), need("B", B, "e4m3", 0),
+        need("s_b", s_b, "f32", (2 * ((N + 255) // 256) if swiglu else (N + 127) // 128) * kb),
+        need("C", Cout, "f32" if epilogue == L.HB_EPI_F32 else "bf16", M * N // 2 if swiglu else M * N),
+        None if R is None else need("R", R, "bf16", M * N), M, N, K, int(epilogue), _stream(stream)), call)
 
 
 def hb_interleave_gate_up(w_gate, w_up, w_gu, stream=None):

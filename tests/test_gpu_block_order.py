@@ -33,6 +33,7 @@ def test_prepare_on_a_side_stream(fmt, as_handle):
         churn = [torch.full((3 << 20,), 7.0, device="cuda") for _ in range(4)]
         del churn
         copies = [t.clone() for t in raw]
+        side.wait_stream(torch.cuda.current_stream())  # the caller's tensors are the caller's to order
         lw = hb.prepare_layer_weights(*copies, stream=handle, fmt=fmt)
         churn = [torch.full((3 << 20,), 9.0, device="cuda") for _ in range(4)]
         del churn
