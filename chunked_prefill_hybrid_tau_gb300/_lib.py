@@ -51,6 +51,7 @@ class hb_profile(C.Structure):
     _fields_ = [("events", C.POINTER(vp)), ("n_events", i32)]
 
 
+HB_VERSION = 200  # the header's: the structures above are laid out as in this version
 HB_LAYER_STAGES = 8
 HB_EPI_STORE, HB_EPI_RESIDUAL, HB_EPI_SWIGLU, HB_EPI_F32 = 0, 1, 2, 3
 HB_WEIGHTS_BF16, HB_WEIGHTS_E4M3, HB_WEIGHTS_E4M3_BLOCK = 0, 1, 2
@@ -123,6 +124,8 @@ def load():
             if not os.path.exists(path):
                 raise RuntimeError(f"libhb.so missing at {path}")
             lib = C.CDLL(path)
+            if lib.hb_version() != HB_VERSION:
+                raise RuntimeError(f"{path} is version {lib.hb_version()}, this binding is for {HB_VERSION}")
             for name, (res, args) in PROTOTYPES.items():
                 fn = getattr(lib, name)
                 fn.restype = res

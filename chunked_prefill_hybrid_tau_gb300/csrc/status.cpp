@@ -34,4 +34,4 @@ extern "C" const char* hb_status_string(int status) {
 
 extern "C" const char* hb_last_error(void) { return hb::g_last_error.c_str(); }
 
-extern "C" int32_t hb_version(void) { return 200; }
+extern "C" int32_t hb_version(void) { return HB_VERSION; }

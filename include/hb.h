@@ -50,7 +50,13 @@ typedef enum hb_status {
 const char* hb_status_string(int status);
 /* Message of the last failing call on this thread ("" if none). */
 const char* hb_last_error(void);
-/* Library version as 10000*major + 100*minor + patch. */
+/* Library version as 10000*major + 100*minor + patch.  HB_VERSION is the one
+ * that this header describes.  Structures may grow with the minor version
+ * (hb_layer_weights has g_q and g_k since 200), and the library cannot tell
+ * what its caller was compiled against: a caller compares hb_version() with
+ * HB_VERSION before its first other call and goes no further where they
+ * differ (the Python binding does). */
+#define HB_VERSION 200
 int32_t hb_version(void);
 
 /* ------------------------------------------------------------------------
