@@ -140,6 +140,11 @@ __device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, vola
     }
   }
 }
+// Whether every wait of the CTA so far has held: asked by a thread whose own
+// have (ok), once the threads that it asks for have met it at a barrier.  A
+// wait that expired, or gave up because another one had, leaves `abort` raised.
+__device__ __forceinline__ bool all_waits_held(bool ok, volatile int* abort) { return ok && *abort == 0; }
+
 __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -361,14 +361,27 @@ namespace {
 // One thread waits on a barrier that nothing ever completes: the bounded
 // wait gives up after timeout_ns and records a timeout in the status word,
 // the path every kernel takes when a copy or a partner never arrives.
+// Then two warps share a tile's work: the first one's wait is over at once,
+// the second one's expires.  They meet, and the first asks whether it may
+// store; an index error in the status word says that it would have.
 __global__ void wait_selftest_kernel(int* status, unsigned long long timeout_ns) {
-  __shared__ __align__(8) uint64_t bar;
+  __shared__ __align__(8) uint64_t bars[2];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
   if (threadIdx.x == 0) {
-    mbar_init(&bar, 1);
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    abort_word = 0;
     fence_barrier_init();
+    mbar_arrive(&bars[1]);
   }
   __syncthreads();
-  if (threadIdx.x == 0) mbar_wait(&bar, 0, nullptr, status, timeout_ns);
+  if (threadIdx.x == 0) mbar_wait(&bars[0], 0, nullptr, status, timeout_ns);
+  __syncthreads();
+  const int warp = threadIdx.x >> 5;
+  const bool ok = mbar_wait(&bars[1 - warp], 0, abort_flag, status, timeout_ns);
+  named_barrier_sync(1, 64);
+  if (warp == 0 && all_waits_held(ok, abort_flag)) atomicExch(status, kStatusIndex);
 }
 }  // namespace
 }  // namespace hb
@@ -379,7 +392,7 @@ extern "C" hb_status hb_selftest_wait_timeout(int32_t timeout_us, void* stream) 
   hb::DeviceCtx ctx;
   hb_status st = hb::device_context(&ctx);
   if (st != HB_OK) return st;
-  hb::wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(
+  hb::wait_selftest_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(
       ctx.status, static_cast<unsigned long long>(timeout_us) * 1000ull);
   return hb::launch_status("wait_selftest_kernel launch");
 }

@@ -457,8 +457,11 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       // The sums run over W columns at a time, the next W on their way from
       // TMEM meanwhile, across the border of two K blocks too.  A wait that
       // expired raises the abort flag, every later wait gives up soon, and
-      // the loop runs on over whatever TMEM holds: nothing of it is stored,
-      // and no buffer is released any more.
+      // the loop runs on over whatever TMEM holds: no buffer is released any
+      // more, and nothing of the tile is stored.  A tile is the work of all
+      // eight warps, whose waits need not expire together (at BN 256 the
+      // halves have buffers of their own), so the store asks the flag, which
+      // every warp has had its chance to raise before the barrier ahead of it.
       constexpr int W = BN == 256 && EPI != HB_EPI_F32 ? 32 : 16;  // (F32 at 32 spilled: 246 us against 229)
       constexpr int NC = CH * 32 / W;
       uint32_t r[2][W];
@@ -580,7 +583,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
           }
           fence_proxy_async_smem();
           named_barrier_sync(2, 256);
-          if (boss && ok) {
+          if (boss && all_waits_held(ok, abort_flag)) {
             for (int h = 0; h < 2; ++h)
               for (int i = 0; i < PER; ++i) {
                 const int x = n0 + h * (BN / 2) + (rd * PER + i) * 32;
@@ -638,7 +641,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         }
         fence_proxy_async_smem();
         named_barrier_sync(2, 256);
-        if (boss && ok) {
+        if (boss && all_waits_held(ok, abort_flag)) {
           constexpr int SLABS = SWIGLU ? BN / 128 : BN / 64;
           const int x0 = SWIGLU ? n0 / 2 : n0;
           for (int s = 0; s < SLABS; ++s)
@@ -1019,7 +1022,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
           for (int j = 0; j < TH; ++j) xch[(e - G) * (NT + 1) + j0 + j] = acc[j];
         }
         named_barrier_sync(1, 256);
-        if (active && ok && e < G) {
+        // the up sums are another warp's
+        if (active && e < G && all_waits_held(ok, abort_flag)) {
           const int f = (wt / per_block) * 64 + (wt % per_block) * G + e;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.C) + f;
 #pragma unroll

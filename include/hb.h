@@ -564,11 +564,12 @@ uint64_t hb_kernel_launches(void);
 /* ------------------------------------------------------------------------
  * hb_selftest_wait_timeout - exercise the failure path of the bounded
  * device waits without faulting the GPU.  The pages define no such
- * operation: it checks this library's own error reporting.  One thread of
- * one CTA waits on a shared-memory barrier that nothing completes; after
+ * operation: it checks this library's own error reporting.  One thread of a
+ * CTA waits on a shared-memory barrier that nothing completes; after
  * timeout_us microseconds (1 .. 1 000 000) the wait gives up, records a
- * timeout in the device status word and the kernel returns.  The next
- * hb_check_status on `stream` returns HB_ERR_TIMEOUT and clears the word;
+ * timeout in the device status word and the kernel returns, after a second
+ * such wait whose expiry must keep another warp from storing what the two
+ * had in common.  The next hb_check_status on `stream` returns HB_ERR_TIMEOUT and clears the word;
  * the context stays usable.  Argument errors return HB_ERR_INVALID_ARG
  * before any device work.
  * ---------------------------------------------------------------------- */
