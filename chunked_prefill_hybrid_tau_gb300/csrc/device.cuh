@@ -109,9 +109,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // mbar_wait for inner loops, on a shared-memory address: the clock, the abort
-// flag and the time limit come in only after many tries (each holds the
+// flag and the time limit come in only after a number of tries (each holds the
 // thread for a while in hardware), so that a wait costs a few instructions
-// when the phase is there or near.
+// when the phase is there or near.  Once the abort flag is raised it gives up
+// after the one try.
 __device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -123,23 +124,26 @@ __device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) 
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+constexpr int kTriesPerLook = 64;
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, volatile int* abort, int* status,
+                                             uint64_t timeout_ns = kWaitTimeoutNs) {
   if (mbar_try_wait_at(bar, parity)) return true;
   uint64_t t0 = 0;
 #pragma unroll 1
   while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 1024; ++i)
-      if (mbar_try_wait_at(bar, parity)) return true;
     if (*abort) return false;
+#pragma unroll 1
+    for (int i = 0; i < kTriesPerLook; ++i)
+      if (mbar_try_wait_at(bar, parity)) return true;
     if (t0 == 0) t0 = globaltimer();
-    if (globaltimer() - t0 > kWaitTimeoutNs) {
+    if (globaltimer() - t0 > timeout_ns) {
       flag_error(status, kStatusTimeout);
       *abort = 1;
       return false;
     }
   }
 }
+
 // Whether every wait of the CTA so far has held: asked by a thread whose own
 // have (ok), once the threads that it asks for have met it at a barrier.  A
 // wait that expired, or gave up because another one had, leaves `abort` raised.

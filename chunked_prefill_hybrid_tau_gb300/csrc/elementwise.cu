@@ -364,6 +364,9 @@ namespace {
 // Then two warps share a tile's work: the first one's wait is over at once,
 // the second one's expires.  They meet, and the first asks whether it may
 // store; an index error in the status word says that it would have.
+// Last, the wait of the inner loops: it expires as the other does, and 200
+// more of them, the flag raised, must not wait again (half a second in all:
+// an index error).
 __global__ void wait_selftest_kernel(int* status, unsigned long long timeout_ns) {
   __shared__ __align__(8) uint64_t bars[2];
   __shared__ int abort_word;
@@ -382,6 +385,16 @@ __global__ void wait_selftest_kernel(int* status, unsigned long long timeout_ns)
   const bool ok = mbar_wait(&bars[1 - warp], 0, abort_flag, status, timeout_ns);
   named_barrier_sync(1, 64);
   if (warp == 0 && all_waits_held(ok, abort_flag)) atomicExch(status, kStatusIndex);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  abort_word = 0;
+  const uint32_t bar = smem_u32(&bars[0]);
+  bool held = mbar_wait_at(bar, 0, abort_flag, status, timeout_ns);
+  const uint64_t t0 = globaltimer();
+#pragma unroll 1
+  for (int i = 0; i < 200 && globaltimer() - t0 < 500000000ull; ++i)
+    held = held || mbar_wait_at(bar, 0, abort_flag, status, 50000000ull);
+  if (held || globaltimer() - t0 > 500000000ull) atomicExch(status, kStatusIndex);
 }
 }  // namespace
 }  // namespace hb

@@ -456,9 +456,10 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
         for (int j = 0; j < 32; ++j) acc[c][j] = 0.f;
       // The sums run over W columns at a time, the next W on their way from
       // TMEM meanwhile, across the border of two K blocks too.  A wait that
-      // expired raises the abort flag, every later wait gives up soon, and
-      // the loop runs on over whatever TMEM holds: no buffer is released any
-      // more, and nothing of the tile is stored.  A tile is the work of all
+      // expired raises the abort flag, a thread whose wait has failed waits
+      // for nothing any more (a tile more then costs its arithmetic, however
+      // many K blocks are left), and the loop runs on over whatever TMEM
+      // holds: no buffer is released any more, and nothing of the tile is stored.  A tile is the work of all
       // eight warps, whose waits need not expire together (at BN 256 the
       // halves have buffers of their own), so the store asks the flag, which
       // every warp has had its chance to raise before the barrier ahead of it.
@@ -471,7 +472,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       // there: an earlier try has found it complete
       auto next_block = [&](bool there) {
         if (!__all_sync(0xffffffffu, there)) {
-          ok &= mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
+          if (ok) ok = mbar_wait_at(acc_full_at + slot * 8, bphase, abort_flag, p.status);
           __syncwarp();
         }
         tc_fence_after();
@@ -482,7 +483,7 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       for (int kb0 = 0; kb0 < kblocks; kb0 += kTabK, ++fill) {
         const int side = fill & 1;
         const int nk = kblocks - kb0 < kTabK ? kblocks - kb0 : kTabK;
-        ok &= mbar_wait_at(tab_full_at + side * 8, (fill >> 1) & 1, abort_flag, p.status);
+        if (ok) ok = mbar_wait_at(tab_full_at + side * 8, (fill >> 1) & 1, abort_flag, p.status);
         __syncwarp();
         uint32_t sa_next = sa_at + side * C::TABLE, sb_next = sb_at + side * C::TABLE;
         if constexpr (EPI == HB_EPI_RESIDUAL) {

@@ -567,11 +567,13 @@ uint64_t hb_kernel_launches(void);
  * operation: it checks this library's own error reporting.  One thread of a
  * CTA waits on a shared-memory barrier that nothing completes; after
  * timeout_us microseconds (1 .. 1 000 000) the wait gives up, records a
- * timeout in the device status word and the kernel returns, after a second
- * such wait whose expiry must keep another warp from storing what the two
- * had in common.  The next hb_check_status on `stream` returns HB_ERR_TIMEOUT and clears the word;
- * the context stays usable.  Argument errors return HB_ERR_INVALID_ARG
- * before any device work.
+ * timeout in the device status word.  Two more expiries follow, of the same
+ * limit: one that must keep another warp from storing what the two warps had
+ * in common, and one of the inner loops' wait, after which later waits must
+ * give up at once.  The next hb_check_status on `stream` returns
+ * HB_ERR_TIMEOUT and clears the word (HB_ERR_DEVICE: the self-test failed);
+ * the context stays usable.  Argument errors return HB_ERR_INVALID_ARG before
+ * any device work.
  * ---------------------------------------------------------------------- */
 hb_status hb_selftest_wait_timeout(int32_t timeout_us, void* stream);
 
