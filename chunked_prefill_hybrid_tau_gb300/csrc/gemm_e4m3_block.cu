@@ -39,6 +39,7 @@ struct Params {
   int f_blocks;  // SWIGLU: rows of sb that belong to the gate
   int kblocks;
   int* status;
+  bool preload;  // B was complete before the kernel ahead of this one: its first boxes do not wait for that kernel
   int rows;      // skinny kernel: weight rows of a tile
   int groups;    // skinny kernel: groups of NT tokens
   int stages;    // skinny kernel: ring depth
@@ -231,10 +232,10 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       auto arm = [&](int s) {
         if (leader) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * C::STAGE_BYTES);  // both CTAs' boxes
       };
-      // the weights do not come from the kernel ahead: their first ring fill
+      // weights that do not come from the kernel ahead: their first ring fill
       // is issued before waiting for it
       int pre = 0;
-      if (first < units) {
+      if (p.preload && first < units) {
         const int n0 = (first / um) * BN + static_cast<int>(rank) * (kSub / 2);
         pre = kblocks < C::STAGES ? kblocks : C::STAGES;
         if (elect_one()) {
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     uint32_t pending = 0, armed_parity = 0;
     const int t0 = static_cast<int>(blockIdx.x);
     int pre = 0;
-    if (t0 < tiles) {
+    if (p.preload && t0 < tiles) {
       pre = pairs < ring ? pairs : ring;
       if (elect_one()) {
         for (int i = 0; i < pre; ++i) {
@@ -1190,8 +1191,9 @@ hb_status launch_epi(const DeviceCtx& ctx, const void* A, const void* B, const P
 
 hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B,
                                  const float* sb, void* C, int ldc, const void* R, int M, int N, int K, int epi,
-                                 cudaStream_t stream) {
+                                 cudaStream_t stream, bool weights_ready) {
   Params p = {};
+  p.preload = weights_ready;
   p.M = M;
   p.N = N;
   p.K = K;
@@ -1233,6 +1235,7 @@ extern "C" hb_status hb_gemm_e4m3_block(const void* A, const float* s_a, const v
   hb_status st = hb::device_context(&ctx);
   if (st != HB_OK) return st;
   const int ldc = epilogue == HB_EPI_SWIGLU ? N / 2 : N;
+  // whatever is ahead on the stream may have written B
   return hb::gemm_e4m3_block_launch(ctx, A, K, s_a, B, s_b, C, ldc, R, M, N, K, epilogue,
-                                    static_cast<cudaStream_t>(stream));
+                                    static_cast<cudaStream_t>(stream), false);
 }

@@ -283,21 +283,21 @@ hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_la
     float* sa = so + T * blocks128(hd);
     HB_STEP(0, quant_norm_launch(ctx, x_in, xq, sx, T, d, dm.rms_eps, split_o.flags, n_zero, s));
     HB_STEP(1, gemm_e4m3_block_launch(ctx, xq, d, sx, w->w_qkv, w->s_qkv, qkv, qkv_cols, nullptr, T, qkv_cols, d,
-                                      HB_EPI_STORE, s));
+                                      HB_EPI_STORE, s, true));
     HB_STEP(2, append(nullptr, 0));
     HB_STEP(3, attention_launch(ctx, q, k_cache, v_cache, num_pages, *plan, dm, max_kv_len, o, aws,
                                 lw.total - lw.attn, s, true));
     HB_STEP(4, quant_block_launch(ctx, o, oq, so, T, hd, 1, s));
-    st = gemm_e4m3_block_launch(ctx, oq, hd, so, w->w_o, w->s_o, h, d, x_in, T, d, hd, HB_EPI_RESIDUAL, s);
+    st = gemm_e4m3_block_launch(ctx, oq, hd, so, w->w_o, w->s_o, h, d, x_in, T, d, hd, HB_EPI_RESIDUAL, s, true);
     if (st != HB_OK) return st;
     HB_STEP(5, HB_OK);
     HB_STEP(6, quant_norm_launch(ctx, h, hq, sh, T, d, dm.rms_eps, nullptr, 0, s));
-    st = gemm_e4m3_block_launch(ctx, hq, d, sh, w->w_gu, w->s_gu, a, fp, nullptr, T, 2 * fp, d, HB_EPI_SWIGLU, s);
+    st = gemm_e4m3_block_launch(ctx, hq, d, sh, w->w_gu, w->s_gu, a, fp, nullptr, T, 2 * fp, d, HB_EPI_SWIGLU, s, true);
     if (st != HB_OK) return st;
     HB_STEP(7, quant_block_launch(ctx, a, aq, sa, T, fp, 1, s));
     // d_ff and its padded width fp end in the same block of 128: the scales
     // of a's rows line up with the weight's
-    st = gemm_e4m3_block_launch(ctx, aq, fp, sa, w->w_d, w->s_d, x_out, d, h, T, d, dm.d_ff, HB_EPI_RESIDUAL, s);
+    st = gemm_e4m3_block_launch(ctx, aq, fp, sa, w->w_d, w->s_d, x_out, d, h, T, d, dm.d_ff, HB_EPI_RESIDUAL, s, true);
     if (st != HB_OK) return st;
     return mark(HB_LAYER_STAGES);
   }

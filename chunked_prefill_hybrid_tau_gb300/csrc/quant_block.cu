@@ -123,8 +123,8 @@ __global__ void __maxnreg__(40)
 
 // Weights: one CTA per 128 x 128 block, held in registers (8 pieces of 16
 // bytes a thread) between its maximum and its codes.  The launch signals no
-// dependent early: a projection may read its weights before it waits for the
-// kernel ahead of it.
+// dependent early and its threads end with release_weights(): a layer's
+// projection reads its weights before it waits for the kernel ahead of it.
 // (64 registers, four CTAs an SM: 51.8 us for 28672 x 4096, the copy rate;
 // 89 registers, two: 61.2.)
 __global__ void __maxnreg__(64)
@@ -157,6 +157,7 @@ __global__ void __maxnreg__(64)
     if (r < rows && i < c8) q[static_cast<size_t>(r) * c8 + i] = codes8(v[u], gs.inv);
   }
   if (threadIdx.x == 0) scale[static_cast<size_t>(blockIdx.y) * kb + blockIdx.x] = gs.scale;
+  release_weights();
 }
 
 // Rows that an RMSNorm goes over before their projection (the layer's x and

@@ -183,10 +183,13 @@ hb_status quant_norm_launch(const DeviceCtx& ctx, const void* x, void* q, float*
                             int* zero, int n_zero, cudaStream_t stream);
 
 // Block-scaled E4M3 projection (hb_gemm_e4m3_block); A has row stride lda
-// bytes, C and R row stride ldc elements.
+// bytes, C and R row stride ldc elements.  weights_ready: B was complete
+// before the kernel ahead on the stream started, or comes from one of the
+// weight preparation kernels (release_weights); its first boxes are then
+// fetched while that kernel still runs.
 hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B,
                                  const float* sb, void* C, int ldc, const void* R, int M, int N, int K, int epi,
-                                 cudaStream_t stream);
+                                 cudaStream_t stream, bool weights_ready);
 
 // A [M][K] with row stride lda, B [N][K], C/R with row stride ldc (elements).
 hb_status gemm_launch(const DeviceCtx& ctx, const void* A, int lda, const void* B, void* C, int ldc, const void* R,

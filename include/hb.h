@@ -406,9 +406,8 @@ hb_status hb_quantize_e4m3_block(const void* x, void* q, float* scale, int32_t r
  * and s_b holds the block scales of the gate [ceil(N / 256)][ceil(K / 128)]
  * followed by those of the up matrix, each quantized on its own.
  * K % 16 == 0, N % 8 == 0 (N % 128 for SWIGLU), each size at most 2^30; A, B,
- * C and R 16-byte aligned.  B must be complete before the kernel ahead of this call on the
- * stream starts, unless that kernel is hb_quantize_e4m3_block with
- * block_rows 128 or not one of this library's.
+ * C and R 16-byte aligned.  Any operand may come from the call right ahead on
+ * the stream.
  * ---------------------------------------------------------------------- */
 hb_status hb_gemm_e4m3_block(const void* A, const float* s_a, const void* B, const float* s_b, void* C,
                              const void* R, int32_t M, int32_t N, int32_t K, int32_t epilogue, void* stream);
@@ -451,6 +450,12 @@ hb_status hb_fold_gamma(const void* w, const void* gamma, void* out, int32_t row
  *            rule), the scales of x and h times the row's r, and the
  *            projections run as hb_gemm_e4m3_block; d_ff % 16 == 0 and
  *            d_model <= 16384 required.
+ *            The matrices must be complete before the kernel ahead of this
+ *            call on the stream starts, unless that kernel is one of the
+ *            weight preparation calls: the layer fetches the first of them
+ *            while that kernel may still run.  (Written by other work,
+ *            synchronise once, or let an event or a copy of the stream come
+ *            between.)
  *   plan   : device plan; rope: table from hb_rope_table with max_pos rows
  *   x_in   : device bf16 [T][d_model]; x_out may alias x_in
  *   caches : updated in place with this iteration's K/V

@@ -42,3 +42,74 @@ def test_prepare_on_a_side_stream(fmt, as_handle):
             assert torch.equal(getattr(lw, k).view(torch.uint8), getattr(ref, k).view(torch.uint8)), k
         torch.cuda.synchronize()
     hb.hb_check_status()
+
+
+# one shape for each kernel that hb_gemm_e4m3_block may choose: few tokens, one
+# CTA's 128 x 128 tiles, a pair's 256 x 128 and 256 x 256
+SHAPES = [(4, 8192, 4096), (100, 20096, 512), (256, 9728, 512), (640, 10240, 1024)]
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+@pytest.mark.parametrize("writer", ["quantize", "copy", "cat"])
+def test_projection_straight_after_its_weights(m, n, k, writer):
+    """B and its scales rewritten by the call right ahead, over and over."""
+    gen = wd.device_generator(m + n)
+    ws = [hb.hb_quantize_e4m3_block(wd.randn_bf16((n, k), gen, 0.05), block_rows=128) for _ in range(2)]
+    raw = [wd.randn_bf16((n, k), gen, 0.05) for _ in range(2)]
+    if writer == "quantize":
+        ws = [hb.hb_quantize_e4m3_block(w, block_rows=128) for w in raw]
+    a, sa = hb.hb_quantize_e4m3_block(wd.randn_bf16((m, k), gen))
+    ref = []
+    for q, s in ws:
+        torch.cuda.synchronize()
+        o = torch.empty((m, n), dtype=torch.bfloat16, device="cuda")
+        hb.hb_gemm_e4m3_block(a, sa, q, s, o)
+        ref.append(o)
+    assert not torch.equal(*ref)
+    q, s = torch.empty_like(ws[0][0]), torch.empty_like(ws[0][1])
+    outs = torch.empty((24, m, n), dtype=torch.bfloat16, device="cuda")
+    for i in range(24):
+        j = i % 3 % 2
+        if writer == "quantize":
+            hb.hb_quantize_e4m3_block(raw[j], q, s, block_rows=128)
+        elif writer == "copy":
+            s.copy_(ws[j][1])
+            q.copy_(ws[j][0])
+        else:
+            torch.add(ws[j][1], 0, out=s)
+            torch.cat([ws[j][0][:n // 2], ws[j][0][n // 2:]], out=q)
+        hb.hb_gemm_e4m3_block(a, sa, q, s, outs[i])
+    hb.hb_check_status()
+    for i in range(24):
+        assert torch.equal(outs[i], ref[i % 3 % 2]), i
+
+
+def test_layer_straight_after_its_preparation():
+    """The layer called right behind the preparation of its weights, in buffers
+    that held other weights before."""
+    dims = wl.TINY
+    gen = wd.device_generator(77)
+    shapes = ((dims.qkv_cols, 256), (256, 256), (dims.d_ff, 256), (dims.d_ff, 256), (256, dims.d_ff), (256,), (256,))
+    raws = [[wd.randn_bf16(s, gen, 0.05) for s in shapes] for _ in range(2)]
+    T = 40
+    hp = hb.hb_plan_batch([], [], [T], [0], [[]], list(range(4)), T, T)
+    dp = hb.DevicePlan(hp)
+    rope = wd.rope_table_device(64, dims)
+    x = wd.randn_bf16((T, 256), gen)
+    k, v = (torch.zeros((4, dims.n_kv, 16, dims.d_head), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = wd.workspace(hb.hb_layer_workspace_bytes(dims, T, 1, T))
+    for fmt in ("e4m3_block",):
+        ref, outs = [], []
+        for i in range(12):
+            copies = [t.clone() for t in raws[i % 3 % 2]]
+            torch.cuda.synchronize()
+            lw = hb.prepare_layer_weights(*copies, fmt=fmt)
+            if i < 2:
+                torch.cuda.synchronize()
+            out = torch.empty_like(x)
+            hb.hb_layer_forward(lw, dims, dp, rope, 64, x, out, k, v, T, ws)
+            (ref if i < 2 else outs).append(out)
+        hb.hb_check_status()
+        assert not torch.equal(*ref)
+        for i, out in enumerate(outs):
+            assert torch.equal(out, ref[(i + 2) % 3 % 2]), (fmt, i)
