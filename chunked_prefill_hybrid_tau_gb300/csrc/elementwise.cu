@@ -130,6 +130,7 @@ __global__ void fold_gamma_kernel(const uint4* w, const uint4* __restrict__ gamm
     }
     out[i] = make_uint4(o[0], o[1], o[2], o[3]);
   }
+  release_weights();
 }
 
 // ---------------------------------------------------------------- RoPE table

@@ -52,27 +52,29 @@ int gemm_pair_bn(int M, int N, int epi, bool split, int num_sms) {
 }
 
 hb_status gemm_launch(const DeviceCtx& ctx, const void* A, int lda, const void* B, void* C, int ldc, const void* R,
-                      int M, int N, int K, int epi, cudaStream_t stream, const GemmNorm* norm, const GemmSplit* split) {
+                      int M, int N, int K, int epi, cudaStream_t stream, const GemmNorm* norm, const GemmSplit* split,
+                      bool weights_ready) {
   if (split != nullptr && !gemm_split_k(N, K, epi)) split = nullptr;
   const int pbn = gemm_pair_bn(M, N, epi, split != nullptr, ctx.num_sms);
   if (pbn != 0) {
     if (epi == HB_EPI_SWIGLU)
       return launch_pair<kPairBN, HB_EPI_SWIGLU, false>(ctx, A, lda, nullptr, B, nullptr, C, ldc, R, M, N, K, norm, split,
-                                                      stream);
+                                                      stream, weights_ready);
     if (epi == HB_EPI_RESIDUAL)
       return launch_pair<kPairBN, HB_EPI_RESIDUAL, false>(ctx, A, lda, nullptr, B, nullptr, C, ldc, R, M, N, K, norm,
-                                                        split, stream);
+                                                        split, stream, weights_ready);
     if (pbn == 192)
       return launch_pair<192, HB_EPI_STORE, false>(ctx, A, lda, nullptr, B, nullptr, C, ldc, R, M, N, K, norm, split,
-                                                   stream);
+                                                   stream, weights_ready);
     return launch_pair<256, HB_EPI_STORE, false>(ctx, A, lda, nullptr, B, nullptr, C, ldc, R, M, N, K, norm, split,
-                                                 stream);
+                                                 stream, weights_ready);
   }
   // split-K units use the widest tile (N = 256 MMAs run near the tensor peak)
   const int bn = split ? 256 : choose_bn(M, N, epi, ctx.num_sms);
-#define HB_GEMM_CASE(BN_, EPI_)                                                                                \
-  if (bn == BN_ && epi == EPI_)                                                                                \
-    return launch<BN_, EPI_, false>(ctx, A, lda, nullptr, B, nullptr, C, ldc, R, M, N, K, norm, split, stream);
+#define HB_GEMM_CASE(BN_, EPI_)                                                                               \
+  if (bn == BN_ && epi == EPI_)                                                                               \
+    return launch<BN_, EPI_, false>(ctx, A, lda, nullptr, B, nullptr, C, ldc, R, M, N, K, norm, split, stream, \
+                                    weights_ready);
   HB_GEMM_CASE(256, HB_EPI_STORE)
   HB_GEMM_CASE(192, HB_EPI_STORE)
   HB_GEMM_CASE(128, HB_EPI_STORE)
@@ -116,6 +118,7 @@ __global__ void interleave_gate_up_kernel(const uint4* __restrict__ wg, const ui
     const int src = blk * 64 + (e & 63);
     out[i] = src < F ? (e < 64 ? wg : wu)[static_cast<size_t>(src) * d8 + c] : make_uint4(0, 0, 0, 0);
   }
+  dev::release_weights();
 }
 }  // namespace
 
@@ -130,7 +133,9 @@ extern "C" hb_status hb_gemm(const void* A, const void* B, void* C, const void* 
   st = hb::device_context(&ctx);
   if (st != HB_OK) return st;
   const int ldc = epilogue == HB_EPI_SWIGLU ? N / 2 : N;
-  return hb::gemm_launch(ctx, A, K, B, C, ldc, R, M, N, K, epilogue, static_cast<cudaStream_t>(stream));
+  // whatever is ahead on the stream may have written B
+  return hb::gemm_launch(ctx, A, K, B, C, ldc, R, M, N, K, epilogue, static_cast<cudaStream_t>(stream), nullptr,
+                         nullptr, false);
 }
 
 extern "C" hb_status hb_interleave_gate_up(const void* w_gate, const void* w_up, void* w_gu, int32_t F, int32_t d,

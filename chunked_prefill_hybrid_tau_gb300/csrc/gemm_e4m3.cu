@@ -15,7 +15,8 @@ namespace hb {
 
 hb_status gemm_e4m3_launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B,
                            const float* sb, void* C, int ldc, const void* R, int M, int N, int K, int epi,
-                           cudaStream_t stream, const GemmNorm* norm, const GemmSplit* split, const GemmRope* rope) {
+                           cudaStream_t stream, const GemmNorm* norm, const GemmSplit* split, const GemmRope* rope,
+                           bool weights_ready) {
   if (split != nullptr && !gemm_split_k(N, K, epi)) split = nullptr;
   const int pbn = gemm_pair_bn(M, N, epi, split != nullptr, ctx.num_sms);
   if (epi == kEpiRope) {
@@ -25,26 +26,30 @@ hb_status gemm_e4m3_launch(const DeviceCtx& ctx, const void* A, int lda, const f
     }
     if (pbn != 0)
       return launch_pair<kPairBN, kEpiRope, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream,
-                                                  rope);
+                                                  weights_ready, rope);
     if (choose_bn(M, N, epi, ctx.num_sms) == 256)
-      return launch<256, kEpiRope, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream, rope);
-    return launch<128, kEpiRope, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream, rope);
+      return launch<256, kEpiRope, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream, weights_ready,
+                                         rope);
+    return launch<128, kEpiRope, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream, weights_ready,
+                                         rope);
   }
   if (pbn != 0) {
     if (epi == HB_EPI_SWIGLU)
       return launch_pair<kPairBN, HB_EPI_SWIGLU, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split,
-                                                      stream);
+                                                      stream, weights_ready);
     if (epi == HB_EPI_RESIDUAL)
       return launch_pair<kPairBN, HB_EPI_RESIDUAL, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split,
-                                                        stream);
+                                                        stream, weights_ready);
     if (pbn == 192)
-      return launch_pair<192, HB_EPI_STORE, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream);
-    return launch_pair<256, HB_EPI_STORE, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream);
+      return launch_pair<192, HB_EPI_STORE, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream,
+                                                   weights_ready);
+    return launch_pair<256, HB_EPI_STORE, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream,
+                                                 weights_ready);
   }
   const int bn = split ? 256 : choose_bn(M, N, epi, ctx.num_sms);
 #define HB_GEMM_CASE(BN_, EPI_) \
   if (bn == BN_ && epi == EPI_) \
-    return launch<BN_, EPI_, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream);
+    return launch<BN_, EPI_, true>(ctx, A, lda, sa, B, sb, C, ldc, R, M, N, K, norm, split, stream, weights_ready);
   HB_GEMM_CASE(256, HB_EPI_STORE)
   HB_GEMM_CASE(192, HB_EPI_STORE)
   HB_GEMM_CASE(128, HB_EPI_STORE)
@@ -85,6 +90,7 @@ extern "C" hb_status hb_gemm_e4m3(const void* A, const float* s_a, const void* B
   st = hb::device_context(&ctx);
   if (st != HB_OK) return st;
   const int ldc = epilogue == HB_EPI_SWIGLU ? N / 2 : N;
+  // whatever is ahead on the stream may have written B
   return hb::gemm_e4m3_launch(ctx, A, K, s_a, B, s_b, C, ldc, R, M, N, K, epilogue,
-                              static_cast<cudaStream_t>(stream));
+                              static_cast<cudaStream_t>(stream), nullptr, nullptr, nullptr, false);
 }

@@ -75,6 +75,7 @@ struct Params {
   const float* sa;  // E4M3 operands: per-row scales of A [M] and of B [N] (null for bf16)
   const float* sb;
   GemmRope rope;    // kEpiRope: destinations and RoPE table of the fused QKV epilogue
+  bool preload;     // B was complete before the kernel ahead of this one: its first boxes do not wait for that kernel
 };
 
 // Work unit u: tile u / ksplit, K half u % ksplit (k-blocks [kb0, kb1)).
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t pending = 0;  // stages armed and not yet seen consumed (bit mask)
       uint32_t armed_parity = 0;
-      // The weights do not come from the previous kernel: the first ring
+      // Weights that do not come from the previous kernel: the first ring
       // fill of B is issued before waiting for it, then A follows.  Up to 8
       // row tiles, a weight box is read by the CTAs of its column tile at
       // about the same time and not again in the layer: first out of L2.
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 4096 rows).
       const uint64_t wpol = m_tiles <= 8 ? policy_evict_first() : policy_evict_normal();
       int pre = 0;
-      if (static_cast<int>(blockIdx.x) < units) {
+      if (p.preload && static_cast<int>(blockIdx.x) < units) {
         const Unit w = unit_of<BN>(p, blockIdx.x, m_tiles, kblocks);
         pre = w.kb1 - w.kb0 < C::STAGES ? w.kb1 - w.kb0 : C::STAGES;
         for (int i = 0; i < pre; ++i) {
@@ -975,7 +976,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       uint32_t pending = 0, armed_parity = 0;  // stages loaded and not yet seen released
-      // The weights do not come from the previous kernel: the first ring
+      // Weights that do not come from the previous kernel: the first ring
       // fill of B is issued before waiting for it, then A follows.  Up to 4
       // pair row tiles (1024 rows), a weight box is read by the clusters of
       // its column tile at about the same time and not again in the layer:
@@ -984,7 +985,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // the box out between its readers, and the default policy is faster.
       const uint64_t wpol = pm_tiles <= 4 ? policy_evict_first() : policy_evict_normal();
       int pre = 0;
-      if (cluster < units) {
+      if (p.preload && cluster < units) {
         const PairUnit w = pair_unit_of(p, cluster, pm_tiles, kblocks);
         const int n0 = w.n_blk * BN + static_cast<int>(rank) * (BN / 2);
         pre = w.kb1 - w.kb0 < C::STAGES ? w.kb1 - w.kb0 : C::STAGES;
@@ -1148,7 +1149,7 @@ hb_status encode_out_maps(CUtensorMap* tmC, CUtensorMap* tmR, void* Cp, const vo
 template <int BN, int EPI, bool F8>
 hb_status launch_pair(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B, const float* sb,
                       void* Cp, int ldc, const void* R, int M, int N, int K, const GemmNorm* norm,
-                      const GemmSplit* split, cudaStream_t stream, const GemmRope* rope = nullptr) {
+                      const GemmSplit* split, cudaStream_t stream, bool weights_ready, const GemmRope* rope = nullptr) {
   using C = CfgPair<BN>;
   constexpr int BK = bk_elems<F8>();
   constexpr int ESZ = F8 ? 1 : 2;
@@ -1183,6 +1184,7 @@ hb_status launch_pair(const DeviceCtx& ctx, const void* A, int lda, const float*
   p.sa = sa;
   p.sb = sb;
   p.rope = rope ? *rope : GemmRope{};
+  p.preload = weights_ready;
   const int m_tiles = (M + BM - 1) / BM;
   const int units = ((m_tiles + 1) / 2) * ((N + BN - 1) / BN) * p.ksplit;
   const int pairs = ctx.num_sms / 2;
@@ -1195,7 +1197,7 @@ hb_status launch_pair(const DeviceCtx& ctx, const void* A, int lda, const float*
 template <int BN, int EPI, bool F8>
 hb_status launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B, const float* sb,
                  void* Cp, int ldc, const void* R, int M, int N, int K, const GemmNorm* norm, const GemmSplit* split,
-                 cudaStream_t stream, const GemmRope* rope = nullptr) {
+                 cudaStream_t stream, bool weights_ready, const GemmRope* rope = nullptr) {
   using C = Cfg<BN>;
   constexpr int BK = bk_elems<F8>();
   constexpr int ESZ = F8 ? 1 : 2;
@@ -1230,6 +1232,7 @@ hb_status launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, 
   p.sa = sa;
   p.sb = sb;
   p.rope = rope ? *rope : GemmRope{};
+  p.preload = weights_ready;
   const int tiles = ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
   const int units = tiles * p.ksplit;
   const int grid = units < ctx.num_sms ? units : ctx.num_sms;

@@ -161,7 +161,7 @@ int gemm_split_flags(int M, int N);          // arrival counters (ints)
 hb_status gemm_e4m3_launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B,
                            const float* sb, void* C, int ldc, const void* R, int M, int N, int K, int epi,
                            cudaStream_t stream, const GemmNorm* norm = nullptr, const GemmSplit* split = nullptr,
-                           const GemmRope* rope = nullptr);
+                           const GemmRope* rope = nullptr, bool weights_ready = true);
 hb_status gemm_e4m3_check(const void* A, const float* sa, const void* B, const float* sb, void* C, const void* R,
                           int M, int N, int K, int epi);
 
@@ -169,8 +169,10 @@ hb_status gemm_e4m3_check(const void* A, const float* sa, const void* B, const f
 // codes q [rows][cols], scales [rows]; with ss != nullptr also the row
 // statistics of x in the GemmNorm layout (cols % 32 == 0), and n_zero ints
 // at `zero` cleared (as row_sumsq_launch).
+// early: the kernel behind may start while this one runs; not where the codes
+// may be weights that it reads ahead of its wait.
 hb_status quant_rows_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int cols,
-                            float* ss, int* zero, int n_zero, cudaStream_t stream);
+                            float* ss, int* zero, int n_zero, cudaStream_t stream, bool early = true);
 
 // Block-scaled E4M3 quantization of bf16 x [rows][cols]: codes q, scales
 // [ceil(rows / block_rows)][ceil(cols / 128)]; block_rows 1 or 128.
@@ -192,9 +194,10 @@ hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, c
                                  cudaStream_t stream, bool weights_ready);
 
 // A [M][K] with row stride lda, B [N][K], C/R with row stride ldc (elements).
+// weights_ready as for gemm_e4m3_block_launch.
 hb_status gemm_launch(const DeviceCtx& ctx, const void* A, int lda, const void* B, void* C, int ldc, const void* R,
                       int M, int N, int K, int epi, cudaStream_t stream, const GemmNorm* norm = nullptr,
-                      const GemmSplit* split = nullptr);
+                      const GemmSplit* split = nullptr, bool weights_ready = true);
 
 // Row statistics of x [rows][d] bf16 in the GemmNorm layout; also zeroes
 // n_zero ints at `zero` (split-K counters of the launches that follow).

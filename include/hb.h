@@ -332,7 +332,8 @@ hb_status hb_attention_noalloc(const void* q, const void* k_cache, const void* v
  *                    silu(A Bg^T) * (A Bu^T)
  *   HB_EPI_F32     : C fp32 [M][N] = AB^T
  * Requires K % 8 == 0 and N % 8 == 0 (N % 128 for SWIGLU), 16-byte aligned
- * pointers.
+ * pointers.  Any operand may come from the call right ahead on the stream (so
+ * too in hb_gemm_e4m3).
  * ---------------------------------------------------------------------- */
 typedef enum hb_epilogue {
   HB_EPI_STORE = 0,

@@ -98,7 +98,7 @@ def test_layer_straight_after_its_preparation():
     x = wd.randn_bf16((T, 256), gen)
     k, v = (torch.zeros((4, dims.n_kv, 16, dims.d_head), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     ws = wd.workspace(hb.hb_layer_workspace_bytes(dims, T, 1, T))
-    for fmt in ("e4m3_block",):
+    for fmt in ("e4m3_block", "e4m3", "bf16"):
         ref, outs = [], []
         for i in range(12):
             copies = [t.clone() for t in raws[i % 3 % 2]]
@@ -113,3 +113,29 @@ def test_layer_straight_after_its_preparation():
         assert not torch.equal(*ref)
         for i, out in enumerate(outs):
             assert torch.equal(out, ref[(i + 2) % 3 % 2]), (fmt, i)
+
+
+@pytest.mark.parametrize("m,n,k", [(4, 4096, 4096), (300, 6144, 1024)])
+def test_row_scaled_and_bf16_projections_straight_after_their_weights(m, n, k):
+    gen = wd.device_generator(m * 3 + n)
+    raw = [wd.randn_bf16((n, k), gen, 0.05) for _ in range(2)]
+    x = wd.randn_bf16((m, k), gen)
+    a, sa = hb.hb_quantize_e4m3(x)
+    ones = torch.ones(k, dtype=torch.bfloat16, device="cuda")
+    q, s, w = torch.empty((n, k), dtype=torch.uint8, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(raw[0])
+    ref, outs = [], []
+    for i in range(20):
+        o8, o16 = (torch.empty((m, n), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        hb.hb_quantize_e4m3(raw[i % 3 % 2], q, s)
+        if i < 2:
+            torch.cuda.synchronize()
+        hb.hb_gemm_e4m3(a, sa, q, s, o8)
+        hb.hb_fold_gamma(raw[i % 3 % 2], ones, w)
+        if i < 2:
+            torch.cuda.synchronize()
+        hb.hb_gemm(x, w, o16)
+        (ref if i < 2 else outs).append((o8, o16))
+    hb.hb_check_status()
+    for i, (o8, o16) in enumerate(outs):
+        r8, r16 = ref[(i + 2) % 3 % 2]
+        assert torch.equal(o8, r8) and torch.equal(o16, r16), i
