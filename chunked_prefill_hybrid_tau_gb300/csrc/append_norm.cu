@@ -36,11 +36,10 @@ constexpr int kRegs = 72;
 
 template <int DH>
 __global__ void __maxnreg__(kRegs)
-    kv_append_norm_kernel(const __nv_bfloat16* __restrict__ qkv, const int* __restrict__ row_pos,
-                          const int* __restrict__ slots, const float2* __restrict__ rope, int T, int max_pos, int n_q,
-                          int n_kv, const __nv_bfloat16* __restrict__ g_q, const __nv_bfloat16* __restrict__ g_k,
-                          float eps, __nv_bfloat16* __restrict__ q_out, __nv_bfloat16* __restrict__ kc,
-                          __nv_bfloat16* __restrict__ vc, long long num_slots, int* status, int* zero, int n_zero) {
+    kv_append_norm_kernel(const __nv_bfloat16* qkv, const int* row_pos, const int* slots, const float2* rope, int T,
+                          int max_pos, int n_q, int n_kv, const __nv_bfloat16* g_q, const __nv_bfloat16* g_k, float eps,
+                          __nv_bfloat16* q_out, __nv_bfloat16* kc, __nv_bfloat16* vc, long long num_slots, int* status,
+                          int* zero, int n_zero) {
   constexpr int HALF = DH / 2;
   constexpr int RC = HALF / 8;  // threads per head
   griddep_launch_dependents();
@@ -52,7 +51,7 @@ __global__ void __maxnreg__(kRegs)
   // the lanes of one head; they take every branch below together
   const unsigned group = ((1u << RC) - 1u) << ((threadIdx.x & 31) & ~(RC - 1));
   int r = blockIdx.x;
-  int pos = row_pos[r], slot = slots[r];
+  int pos = ld_s32(row_pos + r), slot = ld_s32(slots + r);
   while (r < T) {
     const __nv_bfloat16* src_row = qkv + static_cast<size_t>(r) * heads * DH + c * 8;
     const bool pos_ok = pos >= 0 && pos < max_pos;
@@ -68,15 +67,15 @@ __global__ void __maxnreg__(kRegs)
       for (int u = 0; u < U; ++u) {
         const int h = h0 + u * hp;
         if (h < heads) {
-          a[u] = *reinterpret_cast<const uint4*>(src_row + h * DH);
-          b[u] = *reinterpret_cast<const uint4*>(src_row + h * DH + HALF);
+          a[u] = ld_u4(src_row + h * DH);
+          b[u] = ld_u4(src_row + h * DH + HALF);
         }
       }
       if (!pos_ok) break;
       if (h0 < hp) {
-        const float4* csp = reinterpret_cast<const float4*>(rope + static_cast<size_t>(pos) * HALF + c * 8);
+        const float2* csp = rope + static_cast<size_t>(pos) * HALF + c * 8;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) cs[j] = __ldg(csp + j);
+        for (int j = 0; j < 4; ++j) cs[j] = ld_f4(csp + 2 * j);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -92,8 +91,7 @@ __global__ void __maxnreg__(kRegs)
         uint4 o1 = a[u], o2 = b[u];
         if (h < n_q + n_kv) {
           const __nv_bfloat16* g = (h < n_q ? g_q : g_k) + c * 8;
-          const uint4 ga = __ldg(reinterpret_cast<const uint4*>(g));
-          const uint4 gb = __ldg(reinterpret_cast<const uint4*>(g + HALF));
+          const uint4 ga = ld_u4(g), gb = ld_u4(g + HALF);
           const uint32_t aw[4] = {o1.x, o1.y, o1.z, o1.w}, bw[4] = {o2.x, o2.y, o2.z, o2.w};
           const uint32_t gaw[4] = {ga.x, ga.y, ga.z, ga.w}, gbw[4] = {gb.x, gb.y, gb.z, gb.w};
           float ss = 0.f;
@@ -127,8 +125,8 @@ __global__ void __maxnreg__(kRegs)
       }
     }
     if (r_next < T) {
-      pos_next = row_pos[r_next];
-      slot_next = slots[r_next];
+      pos_next = ld_s32(row_pos + r_next);
+      slot_next = ld_s32(slots + r_next);
     }
     r = r_next;
     pos = pos_next;

@@ -84,8 +84,7 @@ __device__ __forceinline__ GroupScale group_scale(float amax) {
 // (40 registers, six CTAs an SM: 55.0 us for 8192 x 14336; 42, five: 57.3.)
 template <int U>
 __global__ void __maxnreg__(40)
-    quant_groups_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int rows,
-                        int c8, int kb, int gshift) {
+    quant_groups_kernel(const uint4* x, uint2* q, float* scale, int rows, int c8, int kb, int gshift) {
   griddep_launch_dependents();
   griddep_wait();
   const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
@@ -97,7 +96,7 @@ __global__ void __maxnreg__(40)
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int i = (g0 + (u << gshift)) * 16 + l;
-    v[u] = row_ok && i < c8 ? x[base + i] : make_uint4(0, 0, 0, 0);
+    v[u] = row_ok && i < c8 ? ld_u4(x + base + i) : make_uint4(0, 0, 0, 0);
   }
   uint32_t m[U];
 #pragma unroll
@@ -128,8 +127,7 @@ __global__ void __maxnreg__(40)
 // (64 registers, four CTAs an SM: 51.8 us for 28672 x 4096, the copy rate;
 // 89 registers, two: 61.2.)
 __global__ void __maxnreg__(64)
-    quant_blocks_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int rows,
-                        int c8, int kb) {
+    quant_blocks_kernel(const uint4* x, uint2* q, float* scale, int rows, int c8, int kb) {
   griddep_wait();
   __shared__ uint32_t red[kThreads / 32];
   const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4;
@@ -139,7 +137,7 @@ __global__ void __maxnreg__(64)
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
     const int r = row0 + 16 * u;
-    v[u] = r < rows && i < c8 ? x[static_cast<size_t>(r) * c8 + i] : make_uint4(0, 0, 0, 0);
+    v[u] = r < rows && i < c8 ? ld_u4(x + static_cast<size_t>(r) * c8 + i) : make_uint4(0, 0, 0, 0);
   }
   uint32_t m = 0;
 #pragma unroll
@@ -170,8 +168,8 @@ __global__ void __maxnreg__(64)
 // n_zero ints (the layer's counters).
 template <int NV>
 __global__ void __launch_bounds__(kThreads)
-    quant_norm_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int c8, int kb,
-                      float inv_d, float eps, int* zero, int n_zero) {
+    quant_norm_kernel(const uint4* x, uint2* q, float* scale, int c8, int kb, float inv_d, float eps, int* zero,
+                      int n_zero) {
   griddep_launch_dependents();
   griddep_wait();
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_zero; i += gridDim.x * blockDim.x) zero[i] = 0;
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = t + kThreads * k;
-    v[k] = i < c8 ? x[base + i] : make_uint4(0, 0, 0, 0);
+    v[k] = i < c8 ? ld_u4(x + base + i) : make_uint4(0, 0, 0, 0);
   }
   float ss = 0.f;
   uint32_t m[NV];
