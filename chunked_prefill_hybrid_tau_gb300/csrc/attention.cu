@@ -174,7 +174,7 @@ __device__ __forceinline__ void warp_page(uint32_t k_base, uint32_t v_base, int 
 }
 
 __device__ __forceinline__ uint32_t ld_q2(const __nv_bfloat16* rowp, int col, bool ok) {
-  return ok ? __ldg(reinterpret_cast<const unsigned int*>(rowp + col)) : 0u;
+  return ok ? static_cast<uint32_t>(ld_s32(reinterpret_cast<const int*>(rowp + col))) : 0u;
 }
 
 // ---------------------------------------------------------------- decode rows

@@ -221,7 +221,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // loaded four blocks ahead and checked at use
       auto load_page = [&](int j) {
         const int npg = j < w.nblk ? min(8, (key_end - j * TK + 15) / 16) : 0;
-        return lane < 8 && my_pg < npg ? __ldg(bt + j * 8 + my_pg) : 0;
+        return lane < 8 && my_pg < npg ? ld_s32(bt + j * 8 + my_pg) : 0;
       };
       int pf0 = load_page(0), pf1 = load_page(1), pf2 = load_page(2), pf3 = load_page(3);
       for (int j = 0; j < w.nblk; ++j) {

@@ -20,8 +20,8 @@ constexpr int kNormWarps = 4;
 
 template <int NV>
 __global__ void __launch_bounds__(kNormWarps * 32)
-    rmsnorm_kernel(const uint4* __restrict__ x, const int* __restrict__ rows, const uint4* __restrict__ gamma,
-                   uint4* __restrict__ y, int n_rows, int d8, float inv_d, float eps, int n_src, int* status) {
+    rmsnorm_kernel(const uint4* x, const int* rows, const uint4* gamma, uint4* y, int n_rows, int d8, float inv_d,
+                   float eps, int n_src, int* status) {
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kNormWarps * 32)
   if (r >= n_rows) return;
   int src = r;
   if (rows) {
-    src = rows[r];
+    src = ld_s32(rows + r);
     if (src < 0 || src >= n_src) {
       if (lane == 0) flag_error(status, kStatusIndex);
       return;
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kNormWarps * 32)
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = lane + 32 * k;
-    v[k] = i < d8 ? xr[i] : make_uint4(0, 0, 0, 0);
+    v[k] = i < d8 ? ld_u4(xr + i) : make_uint4(0, 0, 0, 0);
   }
   float ss = 0.f;
 #pragma unroll
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kNormWarps * 32)
   for (int k = 0; k < NV; ++k) {
     const int i = lane + 32 * k;
     if (i >= d8) break;
-    const uint4 g = gamma[i];
+    const uint4 g = ld_u4(gamma + i);
     const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, gw[4] = {g.x, g.y, g.z, g.w};
     uint32_t o[4];
 #pragma unroll
@@ -79,8 +79,7 @@ __global__ void __launch_bounds__(kNormWarps * 32)
 // xor pattern.
 template <int NV>
 __global__ void __launch_bounds__(kNormWarps * 32)
-    row_sumsq_kernel(const uint4* __restrict__ x, float* __restrict__ ss, int n_rows, int d8, int* zero,
-                     int n_zero) {
+    row_sumsq_kernel(const uint4* x, float* ss, int n_rows, int d8, int* zero, int n_zero) {
   griddep_launch_dependents();
   griddep_wait();
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_zero; i += gridDim.x * blockDim.x) zero[i] = 0;
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(kNormWarps * 32)
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = lane + 32 * k;
-    v[k] = i < d8 ? xr[i] : make_uint4(0, 0, 0, 0);
+    v[k] = i < d8 ? ld_u4(xr + i) : make_uint4(0, 0, 0, 0);
   }
   float* out = ss + static_cast<size_t>(r) * (d8 / 4);
 #pragma unroll
@@ -154,11 +153,9 @@ __global__ void rope_table_kernel(float2* __restrict__ t, int max_pos, int half,
 // accesses are 16 bytes.  K/V land at slot = page*16 + offset of the
 // [page][kv head][16][d_head] pools.
 template <int DH>
-__global__ void kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, const int* __restrict__ row_pos,
-                                 const int* __restrict__ slots, const float2* __restrict__ rope, int max_pos, int n_q,
-                                 int n_kv, __nv_bfloat16* __restrict__ q_out, __nv_bfloat16* __restrict__ kc,
-                                 __nv_bfloat16* __restrict__ vc, long long num_slots, int* status, int* zero,
-                                 int n_zero) {
+__global__ void kv_append_kernel(const __nv_bfloat16* qkv, const int* row_pos, const int* slots, const float2* rope,
+                                 int max_pos, int n_q, int n_kv, __nv_bfloat16* q_out, __nv_bfloat16* kc,
+                                 __nv_bfloat16* vc, long long num_slots, int* status, int* zero, int n_zero) {
   constexpr int HALF = DH / 2;
   constexpr int RC = HALF / 8;  // rotating threads per head
   constexpr int VC = DH / 8;    // copy threads per v head
@@ -166,8 +163,8 @@ __global__ void kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, const in
   griddep_wait();
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_zero; i += gridDim.x * blockDim.x) zero[i] = 0;
   const int r = blockIdx.x;
-  const int pos = row_pos[r];
-  const int slot = slots[r];
+  const int pos = ld_s32(row_pos + r);
+  const int slot = ld_s32(slots + r);
   const int ld = (n_q + 2 * n_kv) * DH;
   const bool pos_ok = pos >= 0 && pos < max_pos;
   const bool slot_ok = slot >= 0 && slot < num_slots;
@@ -183,9 +180,11 @@ __global__ void kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, const in
     if (t < rot) {
       const int h = t / RC, c = t % RC;
       const __nv_bfloat16* src = src_row + h * DH + c * 8;
-      uint4 a = *reinterpret_cast<const uint4*>(src);
-      uint4 b = *reinterpret_cast<const uint4*>(src + HALF);
-      const float4* cs = reinterpret_cast<const float4*>(rope + static_cast<size_t>(pos) * HALF + c * 8);
+      const uint4 a = ld_u4(src), b = ld_u4(src + HALF);
+      const float2* csp = rope + static_cast<size_t>(pos) * HALF + c * 8;
+      float4 cs[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cs[j] = ld_f4(csp + 2 * j);
       uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w}, o1[4], o2[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -211,7 +210,7 @@ __global__ void kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, const in
       if (!slot_ok) continue;
       const int t2 = t - rot;
       const int g = t2 / VC, c = t2 % VC;
-      const uint4 v = *reinterpret_cast<const uint4*>(src_row + (n_q + n_kv + g) * DH + c * 8);
+      const uint4 v = ld_u4(src_row + (n_q + n_kv + g) * DH + c * 8);
       *reinterpret_cast<uint4*>(vc + ((static_cast<size_t>(page) * n_kv + g) * 16 + off) * DH + c * 8) = v;
     }
   }

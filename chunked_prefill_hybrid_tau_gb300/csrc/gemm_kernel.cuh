@@ -192,10 +192,9 @@ __device__ __forceinline__ void residual_chunk(const Params& p, int row, int col
 // The products are rounded explicitly (no contraction into a later add), so
 // every epilogue path produces the same bits.
 __device__ __forceinline__ void scale_cols(uint32_t (&r)[32], float rowf, const float* sb, int col, int N) {
-  const float4* s4 = reinterpret_cast<const float4*>(sb + col);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float4 s = col + 4 * i < N ? __ldg(s4 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 s = col + 4 * i < N ? ld_f4(sb + col + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
     r[4 * i] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(r[4 * i]), rowf), s.x));
     r[4 * i + 1] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(r[4 * i + 1]), rowf), s.y));
     r[4 * i + 2] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(r[4 * i + 2]), rowf), s.z));
@@ -580,8 +579,8 @@ __device__ __forceinline__ void epilogue_rope(const Params& p, uint32_t t_base, 
                                               float scale, float rowf) {
   const GemmRope& rp = p.rope;
   const int DH = rp.d_head, HALF = DH / 2;
-  const int pos = row_ok ? __ldg(rp.row_pos + row) : 0;
-  const int slot = row_ok ? __ldg(rp.slots + row) : 0;
+  const int pos = row_ok ? ld_s32(rp.row_pos + row) : 0;
+  const int slot = row_ok ? ld_s32(rp.slots + row) : 0;
   const bool pos_ok = row_ok && pos >= 0 && pos < rp.max_pos;
   const bool slot_ok = pos_ok && slot >= 0 && slot < rp.num_slots;
   if (row_ok && (!pos_ok || slot >= rp.num_slots)) flag_error(p.status, kStatusIndex);
@@ -609,9 +608,9 @@ __device__ __forceinline__ void epilogue_rope(const Params& p, uint32_t t_base, 
       // (cos, sin) of dimensions c .. c + 31 at the row's position, all loads
       // in flight together (the accumulator loads overlap them)
       float4 cs[16];
-      const float4* csp = reinterpret_cast<const float4*>(rp.rope + static_cast<size_t>(pos) * HALF + c);
+      const float2* csp = rp.rope + static_cast<size_t>(pos) * HALF + c;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) cs[i] = rot && pos_ok ? __ldg(csp + i) : make_float4(1.f, 0.f, 1.f, 0.f);
+      for (int i = 0; i < 16; ++i) cs[i] = rot && pos_ok ? ld_f4(csp + 2 * i) : make_float4(1.f, 0.f, 1.f, 0.f);
       uint32_t r1[32], r2[32];
       tmem_ld_32x32b_x32(t_base + hb + c, r1);
       tmem_ld_32x32b_x32(t_base + hb + HALF + c, r2);

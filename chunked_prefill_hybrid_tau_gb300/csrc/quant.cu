@@ -35,8 +35,7 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float inv) {
 // lanes by a fixed xor pattern, the same arithmetic as row_sumsq_kernel).
 template <int NV, bool SS>
 __global__ void __launch_bounds__(kQuantThreads)
-    quant_rows_kernel(const uint4* __restrict__ x, uint2* __restrict__ q, float* __restrict__ scale, int c8,
-                      float* __restrict__ ss, int* zero, int n_zero, bool early) {
+    quant_rows_kernel(const uint4* x, uint2* q, float* scale, int c8, float* ss, int* zero, int n_zero, bool early) {
   if (early) griddep_launch_dependents();
   griddep_wait();
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_zero; i += gridDim.x * blockDim.x) zero[i] = 0;
@@ -48,7 +47,7 @@ __global__ void __launch_bounds__(kQuantThreads)
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = t + kQuantThreads * k;
-    v[k] = i < c8 ? xr[i] : make_uint4(0, 0, 0, 0);
+    v[k] = i < c8 ? ld_u4(xr + i) : make_uint4(0, 0, 0, 0);
   }
   float amax = 0.f;
 #pragma unroll
