@@ -320,16 +320,6 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 }
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// At the end of a kernel that writes what a projection may read ahead of its
-// griddep_wait() (prepared weights): the thread's stores are performed for
-// the whole device, and for the asynchronous copies (TMA) that read them,
-// before it exits.  griddep_wait() would order them; such a reader is started
-// by the exit of these threads alone.
-__device__ __forceinline__ void release_weights() {
-  __threadfence();
-  asm volatile("fence.proxy.async.global;" ::: "memory");
-}
-
 // Registers a thread of this warpgroup may use from here on (every warp of the
 // warpgroup executes it; the sum over the block stays within what the block
 // was launched with).

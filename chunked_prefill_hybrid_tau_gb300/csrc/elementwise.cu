@@ -129,7 +129,6 @@ __global__ void fold_gamma_kernel(const uint4* w, const uint4* __restrict__ gamm
     }
     out[i] = make_uint4(o[0], o[1], o[2], o[3]);
   }
-  release_weights();
 }
 
 // ---------------------------------------------------------------- RoPE table
@@ -219,7 +218,7 @@ __global__ void kv_append_kernel(const __nv_bfloat16* qkv, const int* row_pos, c
 }  // namespace
 
 hb_status rmsnorm_launch(const DeviceCtx& ctx, const void* x, const int* rows, const void* gamma, void* y,
-                         int n_rows, int d, float eps, int n_src, cudaStream_t stream) {
+                         int n_rows, int d, float eps, int n_src, cudaStream_t stream, bool overlap) {
   if (n_rows == 0) return HB_OK;
   const int blocks = (n_rows + kNormWarps - 1) / kNormWarps;
   const int d8 = d / 8;
@@ -229,8 +228,8 @@ hb_status rmsnorm_launch(const DeviceCtx& ctx, const void* x, const int* rows, c
   auto* yp = static_cast<uint4*>(y);
 #define HB_NORM(NV_)                                                                                           \
   if (nv <= NV_) {                                                                                             \
-    return launch_pdl(rmsnorm_kernel<NV_>, blocks, kNormWarps * 32, 0, stream, "rmsnorm_kernel launch", xp, rows, \
-                      gp, yp, n_rows, d8, 1.0f / d, eps, n_src, ctx.status);                                     \
+    return launch(overlap, rmsnorm_kernel<NV_>, blocks, kNormWarps * 32, 0, stream, "rmsnorm_kernel launch", xp, \
+                  rows, gp, yp, n_rows, d8, 1.0f / d, eps, n_src, ctx.status);                                  \
   }
   HB_NORM(1)
   HB_NORM(2)
@@ -244,7 +243,7 @@ hb_status rmsnorm_launch(const DeviceCtx& ctx, const void* x, const int* rows, c
 }
 
 hb_status row_sumsq_launch(const DeviceCtx& ctx, const void* x, float* ss, int rows, int d, int* zero, int n_zero,
-                           cudaStream_t stream) {
+                           cudaStream_t stream, bool overlap) {
   if (rows == 0) return HB_OK;
   const int blocks = (rows + kNormWarps - 1) / kNormWarps;
   const int d8 = d / 8;
@@ -253,8 +252,8 @@ hb_status row_sumsq_launch(const DeviceCtx& ctx, const void* x, float* ss, int r
   (void)ctx;
 #define HB_SS(NV_)                                                                                                 \
   if (nv <= NV_)                                                                                                   \
-    return launch_pdl(row_sumsq_kernel<NV_>, blocks, kNormWarps * 32, 0, stream, "row_sumsq_kernel launch", xp, ss, \
-                      rows, d8, zero, n_zero);
+    return launch(overlap, row_sumsq_kernel<NV_>, blocks, kNormWarps * 32, 0, stream, "row_sumsq_kernel launch",   \
+                  xp, ss, rows, d8, zero, n_zero);
   HB_SS(1)
   HB_SS(2)
   HB_SS(4)

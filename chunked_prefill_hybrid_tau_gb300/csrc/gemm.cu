@@ -118,7 +118,6 @@ __global__ void interleave_gate_up_kernel(const uint4* __restrict__ wg, const ui
     const int src = blk * 64 + (e & 63);
     out[i] = src < F ? (e < 64 ? wg : wu)[static_cast<size_t>(src) * d8 + c] : make_uint4(0, 0, 0, 0);
   }
-  dev::release_weights();
 }
 }  // namespace
 

@@ -157,11 +157,13 @@ hb_status check_call(const hb_layer_dims* dims, const hb_device_plan* plan, cons
 // wrote them), so the statistics kernel is left out; stats_next: the down
 // projection also writes the statistics of x_out, for the next layer.
 // Both are formed in the same order, so the results do not depend on which
-// kernel produced them.
+// kernel produced them.  first: the call's first layer, whose first kernel
+// starts once everything ahead on the stream is complete; so the weights are,
+// which every projection here begins to fetch ahead of its wait.
 hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_layer_dims* dims,
                     const hb_device_plan* plan, const void* rope, int max_pos, const void* x_in, void* x_out,
                     void* k_cache, void* v_cache, int num_pages, int max_kv_len, void* workspace, cudaStream_t s,
-                    const hb_profile* prof, bool x_stats, bool stats_next) {
+                    const hb_profile* prof, bool x_stats, bool stats_next, bool first) {
   hb_status st = HB_OK;
   const bool f8 = w->format == HB_WEIGHTS_E4M3;
   const bool qk_norm = w->g_q != nullptr;
@@ -251,7 +253,7 @@ hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_la
     float* so = sx + align256(static_cast<size_t>(T) * 4) / 4;
     float* sh = so + align256(static_cast<size_t>(T) * 4) / 4;
     float* sa = sh + align256(static_cast<size_t>(T) * 4) / 4;
-    HB_STEP(0, quant_rows_launch(ctx, x_in, xq, sx, T, d, ss_x, split_o.flags, n_zero, s));
+    HB_STEP(0, quant_rows_launch(ctx, x_in, xq, sx, T, d, ss_x, split_o.flags, n_zero, s, !first));
     HB_STEP(1, gemm_e4m3_launch(ctx, xq, d, sx, w->w_qkv, w->s_qkv, qkv, qkv_cols, nullptr, T, qkv_cols, d, qkv_epi,
                                 s, &norm_x, nullptr, &rope_qkv));
     HB_STEP(2, fuse_rope ? HB_OK : append(nullptr, 0));
@@ -281,7 +283,7 @@ hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_la
     float* sh = sx + T * blocks128(d);
     float* so = sh + T * blocks128(d);
     float* sa = so + T * blocks128(hd);
-    HB_STEP(0, quant_norm_launch(ctx, x_in, xq, sx, T, d, dm.rms_eps, split_o.flags, n_zero, s));
+    HB_STEP(0, quant_norm_launch(ctx, x_in, xq, sx, T, d, dm.rms_eps, split_o.flags, n_zero, s, !first));
     HB_STEP(1, gemm_e4m3_block_launch(ctx, xq, d, sx, w->w_qkv, w->s_qkv, qkv, qkv_cols, nullptr, T, qkv_cols, d,
                                       HB_EPI_STORE, s, true));
     HB_STEP(2, append(nullptr, 0));
@@ -301,7 +303,7 @@ hb_status run_layer(const DeviceCtx& ctx, const hb_layer_weights* w, const hb_la
     if (st != HB_OK) return st;
     return mark(HB_LAYER_STAGES);
   }
-  HB_STEP(0, x_stats ? HB_OK : row_sumsq_launch(ctx, x_in, ss_x, T, d, nullptr, 0, s));
+  HB_STEP(0, x_stats ? HB_OK : row_sumsq_launch(ctx, x_in, ss_x, T, d, nullptr, 0, s, !first));
   HB_STEP(1, gemm_launch(ctx, x_in, d, w->w_qkv, qkv, qkv_cols, nullptr, T, qkv_cols, d, HB_EPI_STORE, s, &norm_x));
   HB_STEP(2, append(split_o.flags, n_zero));
   HB_STEP(3, attention_launch(ctx, q, k_cache, v_cache, num_pages, *plan, dm, max_kv_len, o, aws,
@@ -339,7 +341,7 @@ extern "C" hb_status hb_layer_forward(const hb_layer_weights* w, const hb_layer_
   st = device_context(&ctx);
   if (st != HB_OK) return st;
   return run_layer(ctx, w, dims, plan, rope, max_pos, x_in, x_out, k_cache, v_cache, num_pages, max_kv_len, workspace,
-                   static_cast<cudaStream_t>(stream), prof, false, false);
+                   static_cast<cudaStream_t>(stream), prof, false, false, true);
 }
 
 extern "C" hb_status hb_layers_forward(const hb_layer_weights* w, int32_t n_layers, const hb_layer_dims* dims,
@@ -369,7 +371,7 @@ extern "C" hb_status hb_layers_forward(const hb_layer_weights* w, int32_t n_laye
     const bool next_bf16 = l + 1 < n_layers && w[l + 1].format == HB_WEIGHTS_BF16;
     const bool x_stats = l > 0 && w[l].format == HB_WEIGHTS_BF16 && w[l - 1].format != HB_WEIGHTS_E4M3_BLOCK;
     st = run_layer(ctx, w + l, dims, plan, rope, max_pos, l == 0 ? x_in : x_out, x_out, k_caches[l], v_caches[l],
-                   num_pages, max_kv_len, workspace, s, nullptr, x_stats, next_bf16);
+                   num_pages, max_kv_len, workspace, s, nullptr, x_stats, next_bf16, l == 0);
     if (st != HB_OK) return st;
   }
   return HB_OK;
@@ -392,7 +394,7 @@ extern "C" hb_status hb_final_logits(const void* x, int32_t T, const int32_t* ro
   st = device_context(&ctx);
   if (st != HB_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = rmsnorm_launch(ctx, x, rows, g_f, workspace, n_sel, d, eps, T, s);
+  st = rmsnorm_launch(ctx, x, rows, g_f, workspace, n_sel, d, eps, T, s, false);
   if (st != HB_OK) return st;
   return gemm_launch(ctx, workspace, d, w_lm, logits, vocab, nullptr, n_sel, vocab, d, HB_EPI_F32, s);
 }

@@ -35,8 +35,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float inv) {
 // lanes by a fixed xor pattern, the same arithmetic as row_sumsq_kernel).
 template <int NV, bool SS>
 __global__ void __launch_bounds__(kQuantThreads)
-    quant_rows_kernel(const uint4* x, uint2* q, float* scale, int c8, float* ss, int* zero, int n_zero, bool early) {
-  if (early) griddep_launch_dependents();
+    quant_rows_kernel(const uint4* x, uint2* q, float* scale, int c8, float* ss, int* zero, int n_zero) {
+  griddep_launch_dependents();
   griddep_wait();
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_zero; i += gridDim.x * blockDim.x) zero[i] = 0;
   __shared__ float red[kQuantThreads / 32];
@@ -93,13 +93,12 @@ __global__ void __launch_bounds__(kQuantThreads)
     }
     qr[i] = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
   }
-  if (!early) release_weights();
 }
 
 }  // namespace
 
 hb_status quant_rows_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int cols,
-                            float* ss, int* zero, int n_zero, cudaStream_t stream, bool early) {
+                            float* ss, int* zero, int n_zero, cudaStream_t stream, bool overlap) {
   (void)ctx;
   if (rows == 0) return HB_OK;
   const int c8 = cols / 8;
@@ -109,10 +108,10 @@ hb_status quant_rows_launch(const DeviceCtx& ctx, const void* x, void* q, float*
 #define HB_Q(NV_)                                                                                               \
   if (nv <= NV_) {                                                                                              \
     if (ss)                                                                                                     \
-      return launch_pdl(quant_rows_kernel<NV_, true>, rows, kQuantThreads, 0, stream, "quant_rows_kernel launch", \
-                        xp, qp, scale, c8, ss, zero, n_zero, early);                                            \
-    return launch_pdl(quant_rows_kernel<NV_, false>, rows, kQuantThreads, 0, stream, "quant_rows_kernel launch",  \
-                      xp, qp, scale, c8, ss, zero, n_zero, early);                                              \
+      return launch(overlap, quant_rows_kernel<NV_, true>, rows, kQuantThreads, 0, stream,                      \
+                    "quant_rows_kernel launch", xp, qp, scale, c8, ss, zero, n_zero);                           \
+    return launch(overlap, quant_rows_kernel<NV_, false>, rows, kQuantThreads, 0, stream,                       \
+                  "quant_rows_kernel launch", xp, qp, scale, c8, ss, zero, n_zero);                             \
   }
   HB_Q(1)
   HB_Q(2)
@@ -136,6 +135,5 @@ extern "C" hb_status hb_quantize_e4m3(const void* x, void* q, float* scale, int3
   hb::DeviceCtx ctx;
   hb_status st = hb::device_context(&ctx);
   if (st != HB_OK) return st;
-  return hb::quant_rows_launch(ctx, x, q, scale, rows, cols, nullptr, nullptr, 0, static_cast<cudaStream_t>(stream),
-                               false);
+  return hb::quant_rows_launch(ctx, x, q, scale, rows, cols, nullptr, nullptr, 0, static_cast<cudaStream_t>(stream));
 }

@@ -121,9 +121,7 @@ __global__ void __maxnreg__(40)
 }
 
 // Weights: one CTA per 128 x 128 block, held in registers (8 pieces of 16
-// bytes a thread) between its maximum and its codes.  The launch signals no
-// dependent early and its threads end with release_weights(): a layer's
-// projection reads its weights before it waits for the kernel ahead of it.
+// bytes a thread) between its maximum and its codes.
 // (64 registers, four CTAs an SM: 51.8 us for 28672 x 4096, the copy rate;
 // 89 registers, two: 61.2.)
 __global__ void __maxnreg__(64)
@@ -155,7 +153,6 @@ __global__ void __maxnreg__(64)
     if (r < rows && i < c8) q[static_cast<size_t>(r) * c8 + i] = codes8(v[u], gs.inv);
   }
   if (threadIdx.x == 0) scale[static_cast<size_t>(blockIdx.y) * kb + blockIdx.x] = gs.scale;
-  release_weights();
 }
 
 // Rows that an RMSNorm goes over before their projection (the layer's x and
@@ -218,7 +215,7 @@ __global__ void __launch_bounds__(kThreads)
 }  // namespace
 
 hb_status quant_norm_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int d, float eps,
-                            int* zero, int n_zero, cudaStream_t stream) {
+                            int* zero, int n_zero, cudaStream_t stream, bool overlap) {
   (void)ctx;
   const int c8 = d / 8, kb = (d + 127) / 128;
   const int nv = (c8 + kThreads - 1) / kThreads;
@@ -226,8 +223,8 @@ hb_status quant_norm_launch(const DeviceCtx& ctx, const void* x, void* q, float*
   auto* qp = static_cast<uint2*>(q);
 #define HB_QN(NV_)                                                                                              \
   if (nv <= NV_)                                                                                                \
-    return launch_pdl(quant_norm_kernel<NV_>, rows, kThreads, 0, stream, "quant_norm_kernel launch", xp, qp,    \
-                      scale, c8, kb, 1.0f / d, eps, zero, n_zero);
+    return launch(overlap, quant_norm_kernel<NV_>, rows, kThreads, 0, stream, "quant_norm_kernel launch", xp,   \
+                  qp, scale, c8, kb, 1.0f / d, eps, zero, n_zero);
   HB_QN(1)
   HB_QN(2)
   HB_QN(4)

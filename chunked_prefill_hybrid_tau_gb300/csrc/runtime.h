@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <utility>
 
 #include "common.h"
 
@@ -55,11 +56,16 @@ hb_status smem_limit_once(std::atomic<bool>* done, int device, Kernel kernel, in
 // has signalled griddepcontrol.launch_dependents) and must execute
 // griddepcontrol.wait before it touches memory the predecessor writes or
 // reads.  Every kernel of this library does both, so kernels complete in
-// stream order.  Behind anything that is not such a kernel (a copy, an event,
-// another library's kernel) the launch waits as usual.
+// stream order.  Behind another library's kernel, which gives no such signal,
+// the launch waits for its CTAs to end.
+// Without overlap, an ordinary launch: everything ahead on the stream is
+// complete, and its writes are seen by every read of the kernel and of those
+// launched behind it, ahead of their own waits too.  The first kernel of a
+// call whose projections fetch weights ahead of their wait is launched so,
+// whoever wrote the weights.
 template <typename... KArgs, typename... Args>
-hb_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                     const char* what, Args&&... args) {
+hb_status launch(bool overlap, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                 const char* what, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -69,10 +75,15 @@ hb_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = overlap ? 1 : 0;
   const hb_status st = cuda_status(cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...), what);
   if (st == HB_OK) count_launch();
   return st;
+}
+template <typename... KArgs, typename... Args>
+hb_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                     const char* what, Args&&... args) {
+  return launch(true, kernel, grid, block, smem, stream, what, std::forward<Args>(args)...);
 }
 
 hb_status encode_tmap_q3d(CUtensorMap* map, const void* q, int T, int n_q, int d_head);
@@ -89,9 +100,10 @@ hb_status chunk_tc_launch(const DeviceCtx& ctx, const void* q, const CUtensorMap
 // Shape checks shared by the layer entry points.
 hb_status check_dims(const hb_layer_dims* dims);
 
-// Launchers (arguments already checked; asynchronous on `stream`).
+// Launchers (arguments already checked; asynchronous on `stream`; overlap as
+// for launch()).
 hb_status rmsnorm_launch(const DeviceCtx& ctx, const void* x, const int* rows, const void* gamma, void* y,
-                         int n_rows, int d, float eps, int n_src, cudaStream_t stream);
+                         int n_rows, int d, float eps, int n_src, cudaStream_t stream, bool overlap = true);
 // zero / n_zero: ints cleared after the kernel's wait for its inputs (the
 // layer's split-K and attention counters; nullptr, 0 for none).
 hb_status kv_append_launch(const DeviceCtx& ctx, const void* qkv, int T, const int* row_pos, const int* slots,
@@ -169,10 +181,8 @@ hb_status gemm_e4m3_check(const void* A, const float* sa, const void* B, const f
 // codes q [rows][cols], scales [rows]; with ss != nullptr also the row
 // statistics of x in the GemmNorm layout (cols % 32 == 0), and n_zero ints
 // at `zero` cleared (as row_sumsq_launch).
-// early: the kernel behind may start while this one runs; not where the codes
-// may be weights that it reads ahead of its wait.
 hb_status quant_rows_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int cols,
-                            float* ss, int* zero, int n_zero, cudaStream_t stream, bool early = true);
+                            float* ss, int* zero, int n_zero, cudaStream_t stream, bool overlap = true);
 
 // Block-scaled E4M3 quantization of bf16 x [rows][cols]: codes q, scales
 // [ceil(rows / block_rows)][ceil(cols / 128)]; block_rows 1 or 128.
@@ -182,12 +192,11 @@ hb_status quant_block_launch(const DeviceCtx& ctx, const void* x, void* q, float
 // The same for rows that an RMSNorm goes over: block_rows 1, every scale times
 // the row's rsqrt(mean(x^2) + eps), and n_zero ints at `zero` cleared.
 hb_status quant_norm_launch(const DeviceCtx& ctx, const void* x, void* q, float* scale, int rows, int d, float eps,
-                            int* zero, int n_zero, cudaStream_t stream);
+                            int* zero, int n_zero, cudaStream_t stream, bool overlap = true);
 
 // Block-scaled E4M3 projection (hb_gemm_e4m3_block); A has row stride lda
 // bytes, C and R row stride ldc elements.  weights_ready: B was complete
-// before the kernel ahead on the stream started, or comes from one of the
-// weight preparation kernels (release_weights); its first boxes are then
+// before the kernel ahead on the stream started; its first boxes are then
 // fetched while that kernel still runs.
 hb_status gemm_e4m3_block_launch(const DeviceCtx& ctx, const void* A, int lda, const float* sa, const void* B,
                                  const float* sb, void* C, int ldc, const void* R, int M, int N, int K, int epi,
@@ -202,7 +211,7 @@ hb_status gemm_launch(const DeviceCtx& ctx, const void* A, int lda, const void* 
 // Row statistics of x [rows][d] bf16 in the GemmNorm layout; also zeroes
 // n_zero ints at `zero` (split-K counters of the launches that follow).
 hb_status row_sumsq_launch(const DeviceCtx& ctx, const void* x, float* ss, int rows, int d, int* zero, int n_zero,
-                           cudaStream_t stream);
+                           cudaStream_t stream, bool overlap = true);
 size_t attention_workspace_bytes(const hb_layer_dims& dims, int max_seqs, int max_kv_len);
 // Bytes at the start of the attention workspace that must be zero when the
 // attention kernels start (work and combine counters).

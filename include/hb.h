@@ -451,12 +451,8 @@ hb_status hb_fold_gamma(const void* w, const void* gamma, void* out, int32_t row
  *            rule), the scales of x and h times the row's r, and the
  *            projections run as hb_gemm_e4m3_block; d_ff % 16 == 0 and
  *            d_model <= 16384 required.
- *            The matrices must be complete before the kernel ahead of this
- *            call on the stream starts, unless that kernel is one of the
- *            weight preparation calls: the layer fetches the first of them
- *            while that kernel may still run.  (Written by other work,
- *            synchronise once, or let an event or a copy of the stream come
- *            between.)
+ *            Like every operand they may come from the work right ahead on
+ *            the stream.
  *   plan   : device plan; rope: table from hb_rope_table with max_pos rows
  *   x_in   : device bf16 [T][d_model]; x_out may alias x_in
  *   caches : updated in place with this iteration's K/V
