@@ -32,13 +32,19 @@ def _check(status: int, name: str):
         raise HBError(status, f"{name}: {lb.hb_status_string(status).decode()}: {lb.hb_last_error().decode()}")
 
 
-_raw_stream = None
+_raw_stream = _raw_device = None
 
 
 def _current_device() -> int:
-    import torch
-    get = getattr(torch._C, "_cuda_getDevice", None)
-    return torch.cuda.current_device() if get is None else get()
+    """torch's current device; -2 where there is none (no tensor lies there)."""
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        if not torch.cuda.is_available():
+            return -2
+        _raw_device = get
+    return _raw_device()
 
 
 def _current_stream() -> int:
@@ -83,33 +89,29 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-_operand_types = {}
+_types = None
 
 
-def _operands(call):
-    """-> need(name, t, kind, count): the device pointer of operand `t` of
-    `call`, a contiguous tensor on the current device of the given kind (bf16,
-    e4m3 codes, f32, i32) with at least `count` elements.  The kernels see an
-    address alone, so anything else is refused here."""
-    if not _operand_types:
+def _operand_types():
+    """Accepted element types of the operand kinds: bf16, e4m3 (codes), f32, i32."""
+    global _types
+    if _types is None:
         import torch
-        _operand_types.update(bf16=(torch.bfloat16,), e4m3=(torch.uint8, torch.float8_e4m3fn), f32=(torch.float32,),
-                              i32=(torch.int32,))
-    device = None
+        _types = {"bf16": (torch.bfloat16,), "e4m3": (torch.uint8, torch.float8_e4m3fn), "f32": (torch.float32,),
+                  "i32": (torch.int32,)}
+    return _types
 
-    def need(name, t, kind, count):
-        nonlocal device
-        where = t.get_device()
-        if where >= 0 and device is None:
-            device = _current_device()
-        if t.numel() < count or t.dtype not in _operand_types[kind] or not t.is_contiguous() or where != device:
-            raise HBError(L.HB_ERR_INVALID_ARG,
-                          f"{call}: {name} must be a contiguous device tensor of at least {count} elements of type "
-                          f"{' or '.join(str(d) for d in _operand_types[kind])} on the current device, not "
-                          f"{tuple(t.shape)} {t.dtype} with strides {t.stride()} on {t.device}")
-        return t.data_ptr()
 
-    return need
+def _need(call, name, t, types, count, device):
+    """Device pointer of operand `t`, a contiguous tensor on `device` (the
+    current one) of one of `types` with at least `count` elements.  The
+    kernels see an address alone, so anything else is refused here."""
+    if t.numel() < count or t.dtype not in types or not t.is_contiguous() or t.get_device() != device:
+        raise HBError(L.HB_ERR_INVALID_ARG,
+                      f"{call}: {name} must be a contiguous device tensor of at least {count} elements of type "
+                      f"{' or '.join(str(d) for d in types)} on the current device, not {tuple(t.shape)} {t.dtype} "
+                      f"with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
 def dims_struct(dims) -> L.hb_layer_dims:
@@ -379,15 +381,17 @@ def hb_kv_append_norm(qkv, row_pos, slot_mapping, rope, max_pos, dims, g_q, g_k,
     ds = dims_struct(dims)
     T, dh, pages, call = qkv.shape[0], ds.d_head, k_cache.shape[0], "hb_kv_append_norm"
     cache = pages * ds.n_kv * 16 * dh
-    need = _operands(call)
     if qkv.numel() != T * (ds.n_q + 2 * ds.n_kv) * dh:
         raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: qkv {tuple(qkv.shape)} does not have rows of {ds.n_q} q and "
                                             f"2 x {ds.n_kv} kv heads of {dh}")
+    types, dev = _operand_types(), _current_device()
+    bf16, i32 = types["bf16"], types["i32"]
     _check(lib().hb_kv_append_norm(
-        need("qkv", qkv, "bf16", 0), T, need("row_pos", row_pos, "i32", T), need("slot_mapping", slot_mapping, "i32", T),
-        need("rope", rope, "f32", max_pos * dh), int(max_pos), C.byref(ds), need("g_q", g_q, "bf16", dh),
-        need("g_k", g_k, "bf16", dh), need("q_out", q_out, "bf16", T * ds.n_q * dh),
-        need("k_cache", k_cache, "bf16", cache), need("v_cache", v_cache, "bf16", cache), pages, _stream(stream)), call)
+        _need(call, "qkv", qkv, bf16, 0, dev), T, _need(call, "row_pos", row_pos, i32, T, dev),
+        _need(call, "slot_mapping", slot_mapping, i32, T, dev),
+        _need(call, "rope", rope, types["f32"], max_pos * dh, dev), int(max_pos), C.byref(ds), _need(call, "g_q", g_q, bf16, dh, dev), _need(call, "g_k", g_k, bf16, dh, dev),
+        _need(call, "q_out", q_out, bf16, T * ds.n_q * dh, dev), _need(call, "k_cache", k_cache, bf16, cache, dev),
+        _need(call, "v_cache", v_cache, bf16, cache, dev), pages, _stream(stream)), call)
 
 
 def hb_attention_workspace_bytes(dims, max_rows, max_seqs, max_kv_len) -> int:
@@ -439,10 +443,11 @@ def hb_quantize_e4m3_block(x, q=None, scale=None, block_rows=1, stream=None):
         q = _empty((rows, cols), torch.uint8, x.device, stream) if q is None else q
         scale = _empty(groups, torch.float32, x.device, stream) if scale is None else scale
     call = "hb_quantize_e4m3_block"
-    need = _operands(call)
-    _check(lib().hb_quantize_e4m3_block(need("x", x, "bf16", 0), need("q", q, "e4m3", rows * cols),
-                                        need("scale", scale, "f32", groups[0] * groups[1]), rows, cols, block_rows,
-                                        _stream(stream)), call)
+    types, dev = _operand_types(), _current_device()
+    _check(lib().hb_quantize_e4m3_block(_need(call, "x", x, types["bf16"], 0, dev),
+                                        _need(call, "q", q, types["e4m3"], rows * cols, dev),
+                                        _need(call, "scale", scale, types["f32"], groups[0] * groups[1], dev), rows,
+                                        cols, block_rows, _stream(stream)), call)
     return q, scale
 
 
@@ -454,14 +459,15 @@ def hb_gemm_e4m3_block(A, s_a, B, s_b, Cout, R=None, epilogue=L.HB_EPI_STORE, st
     kb = (K + 127) // 128
     swiglu = epilogue == L.HB_EPI_SWIGLU
     call = "hb_gemm_e4m3_block"
-    need = _operands(call)
     if KB != K:
         raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: A has rows of {K} codes, B of {KB}")
+    types, dev = _operand_types(), _current_device()
+    bf16, e4m3, f32 = types["bf16"], types["e4m3"], types["f32"]
     _check(lib().hb_gemm_e4m3_block(
-        need("A", A, "e4m3", 0), need("s_a", s_a, "f32", M * kb), need("B", B, "e4m3", 0),
-        need("s_b", s_b, "f32", (2 * ((N + 255) // 256) if swiglu else (N + 127) // 128) * kb),
-        need("C", Cout, "f32" if epilogue == L.HB_EPI_F32 else "bf16", M * N // 2 if swiglu else M * N),
-        None if R is None else need("R", R, "bf16", M * N), M, N, K, int(epilogue), _stream(stream)), call)
+        _need(call, "A", A, e4m3, 0, dev), _need(call, "s_a", s_a, f32, M * kb, dev), _need(call, "B", B, e4m3, 0, dev),
+        _need(call, "s_b", s_b, f32, (2 * ((N + 255) // 256) if swiglu else (N + 127) // 128) * kb, dev),
+        _need(call, "C", Cout, f32 if epilogue == L.HB_EPI_F32 else bf16, M * N // 2 if swiglu else M * N, dev),
+        None if R is None else _need(call, "R", R, bf16, M * N, dev), M, N, K, int(epilogue), _stream(stream)), call)
 
 
 def hb_interleave_gate_up(w_gate, w_up, w_gu, stream=None):
