@@ -389,7 +389,8 @@ def hb_kv_append_norm(qkv, row_pos, slot_mapping, rope, max_pos, dims, g_q, g_k,
     _check(lib().hb_kv_append_norm(
         _need(call, "qkv", qkv, bf16, 0, dev), T, _need(call, "row_pos", row_pos, i32, T, dev),
         _need(call, "slot_mapping", slot_mapping, i32, T, dev),
-        _need(call, "rope", rope, types["f32"], max_pos * dh, dev), int(max_pos), C.byref(ds), _need(call, "g_q", g_q, bf16, dh, dev), _need(call, "g_k", g_k, bf16, dh, dev),
+        _need(call, "rope", rope, types["f32"], max_pos * dh, dev), int(max_pos), C.byref(ds),
+        _need(call, "g_q", g_q, bf16, dh, dev), _need(call, "g_k", g_k, bf16, dh, dev),
         _need(call, "q_out", q_out, bf16, T * ds.n_q * dh, dev), _need(call, "k_cache", k_cache, bf16, cache, dev),
         _need(call, "v_cache", v_cache, bf16, cache, dev), pages, _stream(stream)), call)
 
