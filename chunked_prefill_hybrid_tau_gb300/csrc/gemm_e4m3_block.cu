@@ -91,8 +91,10 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t at, uint32_t (&r)[32]) { t
 // A K block of a 256 x 256 pair tile is 512 clocks of MMAs; all of its 128 x 256
 // partial sums then cross from TMEM to registers (256 clocks at 4 bytes a lane
 // and clock) while the other half's MMAs update TMEM.  Measured: 750 clocks
-// (394 ns).  4096 x 9216 x 7168: 191 us, 2.83 PFLOP/s, 145 at twice the measured
-// bf16 rate; 512 x 28672 x 4096 (SWIGLU): 51 us, 2.35 PFLOP/s.  (Without the
+// (394 ns).  4096 x 9216 x 7168: 191 us, 2.84 PFLOP/s, 145 at twice the measured
+// bf16 rate; 512 x 28672 x 4096 (SWIGLU): 52 us, 2.31 PFLOP/s; both in a
+// replayed graph.  Called one after the other for long, under the card's power
+// limit: 212 and 56 us, 2.55 and 2.14 PFLOP/s.  (Without the
 // epilogue 2% less, without A's loads 4%; the per-row scaled projection, the
 // same MMAs without these sums: 156 and 41 us.)  Tried and
 // slower: twice the promotion warps with half the sums each (255 against 225
@@ -699,9 +701,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
 // warps.  What is left is about 107 clocks and 2.2 for each 128-byte row of
 // weights and tokens (48, 64 and 96 rows: 213, 240 and 320 clocks): an SM takes
 // in 64 bytes a clock from L2, the tokens' rows included.  Four issuing warps are
-// no faster.  32 x 4096 x 14336: 17.3 us (25.4 before; 8.8 at the copy rate);
-// 1 x 6144 x 4096: 6.6 us; 1 x 28672 x 4096 (SWIGLU): 18.9 us, 6.2 TB/s; 32 x
-// 128256 x 4096 (F32): 74.5 us, 7.2 TB/s.
+// no faster.  Calls in a replayed graph, and in brackets with the weights'
+// first boxes fetched ahead of the wait, as in a layer: 32 x 4096 x 14336 18.7
+// us (17.3; 8.8 at the copy rate), 1 x 6144 x 4096 7.1 (7.2), 1 x 28672 x 4096
+// (SWIGLU) 20.8, 5.7 TB/s (19.3), 32 x 128256 x 4096 (F32) 75.9, 7.0 TB/s
+// (74.4).
 //   warps 0-7: promotion and epilogue, warp w for TMEM lanes 32 (w % 4).. (those
 //              below p.rows) and half w / 4 of the tokens; all eight fill the
 //              table of scale products;
@@ -1157,11 +1161,17 @@ int one_wave_rows(const DeviceCtx& ctx, const Params& p, int nt) {
 // Where one wave of tiles of weight rows x 16, 32 or 64 tokens holds the output,
 // 256 x 128 tiles would leave most SMs idle: 128 x 4096 x 4096 8.6 us against
 // 11.0, 128 x 9728 x 4096 10.9 against 11.9 (SWIGLU with 128 rows 13.1 against
-// 12.2: up to 64), 512 x 2400 x 4096 10.1 against 11.2.  Of the token counts the
+// 12.2: up to 64), 512 x 2400 x 4096 10.1 against 11.2 (measured with the
+// weights fetched ahead of the wait).  Of the token counts the
 // one whose tile has the fewest rows of weights and tokens to load.  Up to 64
 // tokens take such tiles in several waves too.  Else tiles of 128 rows (one
 // CTA) or 256 (a pair), by the waves they need and the time of a K block: 286
-// ns for 128 x 128, 237 for 256 x 128, 394 for 256 x 256.
+// ns for 128 x 128, 237 for 256 x 128, 394 for 256 x 256.  All three measured
+// (us, in this order; * the rule's): 512 x 4096 x 14336 32.0, 31.5*, 54.8;
+// 512 x 4096 x 4096 12.3, 12.7*, 19.7 (both RESIDUAL); 512 x 6144 x 4096 22.8,
+// 22.2, 18.7*; 512 x 28672 x 4096 SWIGLU 66.5, 65.7, 52.1*; 1024 x 4096 x 14336
+// 62.6, 58.5, 55.5*; 2048 x 4096 x 4096 39.2, 38.3, 36.8*; 4096 x 9216 x 7168
+// 232, 225, 190*.
 template <int EPI>
 hb_status launch_epi(const DeviceCtx& ctx, const void* A, const void* B, const Params& p, cudaStream_t stream) {
   constexpr bool SWIGLU = EPI == HB_EPI_SWIGLU;

@@ -400,8 +400,9 @@ hb_status hb_quantize_e4m3_block(const void* x, void* q, float* scale, int32_t r
  * smaller); s_a fp32 [M][ceil(K / 128)] (hb_quantize_e4m3_block of the
  * tokens, block_rows 1), s_b fp32 [ceil(N / 128)][ceil(K / 128)] (of the
  * weights, block_rows 128).  Each block's products are summed on the tensor
- * cores (kind::f8f6f4) and added, scaled, in fp32, block by block in K
- * order, whatever M is: a token's result does not depend on the batch.
+ * cores (kind::f8f6f4) and added in fp32, acc = fma(sum, fl(s_a s_b), acc),
+ * block by block in K order, whatever M is: a token's result does not depend
+ * on the batch.
  * The epilogues are hb_gemm's.  SWIGLU: B's rows interleave gate and up in
  * blocks of 64 (N / 2 rows of each, as hb_interleave_gate_up lays them out),
  * and s_b holds the block scales of the gate [ceil(N / 256)][ceil(K / 128)]
@@ -469,8 +470,10 @@ typedef enum hb_weight_format {
   HB_WEIGHTS_BF16 = 0, /* bf16 matrices */
   HB_WEIGHTS_E4M3 = 1, /* each matrix as E4M3 codes of its bf16 form (hb_quantize_e4m3) with per-row scales;
                           the four projection inputs are quantized per token inside the layer */
-  HB_WEIGHTS_E4M3_BLOCK = 2 /* E4M3 codes with a scale per 128 x 128 block (hb_quantize_e4m3_block, block_rows
-                          128); the projection inputs are quantized per token and 128 columns inside the layer */
+  HB_WEIGHTS_E4M3_BLOCK = 2 /* E4M3 codes with a scale per 128 x 128 block of the prepared bf16 matrix, its RMSNorm
+                          gain folded in (hb_quantize_e4m3_block, block_rows 128); the projection inputs are
+                          quantized per token and 128 columns inside the layer.  Block codes made without the gain
+                          fit only where the gain is 1: it varies inside a block, so no scale can carry it */
 } hb_weight_format;
 
 typedef struct hb_layer_weights {
