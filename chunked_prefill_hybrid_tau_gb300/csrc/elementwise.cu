@@ -152,9 +152,10 @@ __global__ void rope_table_kernel(float2* __restrict__ t, int max_pos, int half,
 // accesses are 16 bytes.  K/V land at slot = page*16 + offset of the
 // [page][kv head][16][d_head] pools.
 template <int DH>
-__global__ void kv_append_kernel(const __nv_bfloat16* qkv, const int* row_pos, const int* slots, const float2* rope,
-                                 int max_pos, int n_q, int n_kv, __nv_bfloat16* q_out, __nv_bfloat16* kc,
-                                 __nv_bfloat16* vc, long long num_slots, int* status, int* zero, int n_zero) {
+__global__ void __maxnreg__(32)
+    kv_append_kernel(const __nv_bfloat16* qkv, const int* row_pos, const int* slots, const float2* rope, int max_pos,
+                     int n_q, int n_kv, __nv_bfloat16* q_out, __nv_bfloat16* kc, __nv_bfloat16* vc, long long num_slots,
+                     int* status, int* zero, int n_zero) {
   constexpr int HALF = DH / 2;
   constexpr int RC = HALF / 8;  // rotating threads per head
   constexpr int VC = DH / 8;    // copy threads per v head
@@ -167,19 +168,18 @@ __global__ void kv_append_kernel(const __nv_bfloat16* qkv, const int* row_pos, c
   const int ld = (n_q + 2 * n_kv) * DH;
   const bool pos_ok = pos >= 0 && pos < max_pos;
   const bool slot_ok = slot >= 0 && slot < num_slots;
-  if (threadIdx.x == 0) {
-    if (!pos_ok || slot >= num_slots) flag_error(status, kStatusIndex);
-  }
-  if (!pos_ok) return;
+  if (threadIdx.x == 0 && (!pos_ok || slot >= num_slots)) flag_error(status, kStatusIndex);
   const int page = slot / 16, off = slot % 16;
   const __nv_bfloat16* src_row = qkv + static_cast<size_t>(r) * ld;
   const int rot = (n_q + n_kv) * RC;
   const int total = rot + n_kv * VC;
   for (int t = threadIdx.x; t < total; t += blockDim.x) {
+    // the row's pieces do not wait for its position and slot
     if (t < rot) {
       const int h = t / RC, c = t % RC;
       const __nv_bfloat16* src = src_row + h * DH + c * 8;
       const uint4 a = ld_u4(src), b = ld_u4(src + HALF);
+      if (!pos_ok) break;
       const float2* csp = rope + static_cast<size_t>(pos) * HALF + c * 8;
       float4 cs[4];
 #pragma unroll
@@ -206,10 +206,11 @@ __global__ void kv_append_kernel(const __nv_bfloat16* qkv, const int* row_pos, c
       *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
       *reinterpret_cast<uint4*>(dst + HALF + c * 8) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
     } else {
-      if (!slot_ok) continue;
       const int t2 = t - rot;
       const int g = t2 / VC, c = t2 % VC;
       const uint4 v = ld_u4(src_row + (n_q + n_kv + g) * DH + c * 8);
+      if (!pos_ok) break;
+      if (!slot_ok) continue;
       *reinterpret_cast<uint4*>(vc + ((static_cast<size_t>(page) * n_kv + g) * 16 + off) * DH + c * 8) = v;
     }
   }
