@@ -209,24 +209,26 @@ __device__ __forceinline__ void scale_cols(uint32_t (&r)[32], float rowf, const 
 // in place.  Own + partner is commutative, so either half's sum has the same
 // bits.  The counters must be zero at launch (the layer clears them in a
 // kernel ahead of its projections); both halves of a tile run in the same round of the
-// persistent grid (consecutive units on an even number of clusters).
+// persistent grid (consecutive units on an even number of clusters).  All 128
+// epilogue threads call it, those whose waits have failed too: with the abort
+// flag raised this CTA does not arrive, and the result is false in all of them.
 __device__ __forceinline__ bool split_exchange(const Params& p, int stile, bool leader, volatile int* ep_flag,
                                                volatile int* abort_flag) {
   __threadfence();
   named_barrier_sync(1, 128);
   if (leader) {
     int* arrive = p.flags + stile * 4;
-    atomicAdd(arrive, 1);
-    int ok = 1;
+    int ok = *abort_flag == 0;
+    if (ok) atomicAdd(arrive, 1);
     const uint64_t t0 = globaltimer();
-    while (*reinterpret_cast<volatile int*>(arrive) < 2) {
+    while (ok && *reinterpret_cast<volatile int*>(arrive) < 2) {
       if (*abort_flag || globaltimer() - t0 > kWaitTimeoutNs) {
         if (!*abort_flag) flag_error(p.status, kStatusTimeout);
         *abort_flag = 1;
         ok = 0;
-        break;
+      } else {
+        __nanosleep(32);
       }
-      __nanosleep(32);
     }
     __threadfence();
     *ep_flag = ok;
@@ -368,8 +370,11 @@ constexpr int kSlabBytes = 128 * 128;
 //   it writes its fp32 partial of the other half (column-major, coalesced),
 //   meets the partner on the tile's counter and fetches the partner's partial
 //   of its own half with one bulk copy.
-// Called by the 128 epilogue threads; `leader` is one of them.  Returns
-// false when a bounded wait expired.  This code runs once per CTA and
+// Called by the 128 epilogue threads; `leader` is one of them.  ok: the
+// thread's waits so far have held (the same in a warp).  Threads whose waits
+// have failed come too, or fail in here: the named barriers count on all 128.
+// They work on whatever is there, and the tile is stored only if no wait has
+// failed.  Returns whether this thread's have held.  This code runs once per CTA and
 // often cold, so its instruction fetches weigh as much as its arithmetic:
 // the 32-column steps of the residual path are not unrolled (bf16 layer
 // 233.0 -> 231.7 us), those of the SwiGLU and store paths only with E4M3
@@ -380,7 +385,7 @@ template <int BN, int EPI, bool F8>
 __device__ __forceinline__ bool epilogue_last(const Params& p, const CUtensorMap* tmC, const CUtensorMap* tmR,
                                               uint8_t* ring, uint64_t* ep_bar, volatile int* ep_flag, uint32_t t_base,
                                               int m0, int row, bool row_ok, int rloc, int n_blk, int stile, int half,
-                                              bool leader, float scale, float rowf, volatile int* abort_flag) {
+                                              bool leader, float scale, float rowf, volatile int* abort_flag, bool ok) {
   if constexpr (EPI == HB_EPI_RESIDUAL) {
     // the columns this CTA finishes: all, or with split K its half (the
     // other half's partial goes to the partner CTA, whose partial of these
@@ -395,7 +400,8 @@ __device__ __forceinline__ bool epilogue_last(const Params& p, const CUtensorMap
     uint8_t* part_smem = ring + NS_ALL * kSlabBytes;
     // this thread's row statistics, collected here and written as one vector
     float* ss_sm = reinterpret_cast<float*>(part_smem + (BN / 2) * BM * 4) + rloc * NP;
-    if (leader) {
+    const bool issued = leader && ok;  // residual copies in flight
+    if (issued) {
       mbar_arrive_expect_tx(&ep_bar[0], ns * kSlabBytes);
       for (int s = 0; s < ns; ++s) tma_load_2d(ring + s * kSlabBytes, tmR, &ep_bar[0], n_blk * BN + cl0 + s * 64, m0);
     }
@@ -410,8 +416,11 @@ __device__ __forceinline__ bool epilogue_last(const Params& p, const CUtensorMap
 #pragma unroll
         for (int j = 0; j < 32; ++j) mine[static_cast<size_t>(o0 + c * 32 + j) * BM + rloc] = __uint_as_float(r[j]);
       }
-      const bool ok = split_exchange(p, stile, leader, ep_flag, abort_flag);
-      if (leader && ok) {
+      if (!split_exchange(p, stile, leader, ep_flag, abort_flag)) {  // the same in all threads
+        if (issued) mbar_wait(&ep_bar[0], 0, nullptr, nullptr);  // the residual copies land before the CTA leaves
+        return false;
+      }
+      if (issued) {
         fence_proxy_async_global();
         const float* other = p.part + (static_cast<size_t>(stile) * 2 + (1 - half)) * BN * BM + cl0 * BM;
         constexpr uint32_t kPiece = (BN / 2) * BM * 4 / 2;
@@ -419,13 +428,14 @@ __device__ __forceinline__ bool epilogue_last(const Params& p, const CUtensorMap
         for (int i = 0; i < 2; ++i)
           bulk_load(part_smem + i * kPiece, reinterpret_cast<const uint8_t*>(other) + i * kPiece, kPiece, &ep_bar[1]);
       }
-      if (!ok) {
-        mbar_wait(&ep_bar[0], 0, nullptr, nullptr);  // the residual copies land before the CTA leaves
-        return false;
-      }
     }
-    if (!mbar_wait(&ep_bar[0], 0, abort_flag, p.status)) return false;
-    if (split && !mbar_wait(&ep_bar[1], 0, abort_flag, p.status)) return false;
+    if (ok) ok = mbar_wait(&ep_bar[0], 0, abort_flag, p.status);
+    if (ok && split) ok = mbar_wait(&ep_bar[1], 0, abort_flag, p.status);
+    if (issued && !ok) {  // the copies land before the CTA leaves
+      mbar_wait(&ep_bar[0], 0, nullptr, nullptr);
+      if (split) mbar_wait(&ep_bar[1], 0, nullptr, nullptr);
+    }
+    __syncwarp();
     const float* other = reinterpret_cast<const float*>(part_smem);  // partner's partial of this CTA's columns
 #pragma unroll 1
     for (int s = 0; s < ns; ++s) {
@@ -461,7 +471,7 @@ __device__ __forceinline__ bool epilogue_last(const Params& p, const CUtensorMap
         ss_sm[2 * s + h] = sumsq32(w);
       }
     }
-    if (p.norm.ss_out != nullptr && row_ok) {
+    if (p.norm.ss_out != nullptr && row_ok && ok) {
       // parts (n_blk BN + cl0) / 32 .. + 2 ns - 1 of the row, consecutive
       const int col0 = n_blk * BN + cl0;
       float* dst = p.norm.ss_out + static_cast<size_t>(row) * p.norm.parts + col0 / 32;
@@ -476,11 +486,11 @@ __device__ __forceinline__ bool epilogue_last(const Params& p, const CUtensorMap
     }
     fence_proxy_async_smem();
     named_barrier_sync(1, 128);
-    if (leader) {
+    if (leader && all_waits_held(ok, abort_flag)) {
       for (int s = 0; s < ns; ++s) tma_store_2d(tmC, ring + s * kSlabBytes, n_blk * BN + cl0 + s * 64, m0);
       bulk_commit_group();
     }
-    return true;
+    return ok;
   } else if constexpr (EPI == HB_EPI_SWIGLU) {
     constexpr int NS = BN / 128;  // each 128 accumulator columns (gate 64 | up 64) give a 64-column slab
 #pragma unroll 1
@@ -514,11 +524,11 @@ __device__ __forceinline__ bool epilogue_last(const Params& p, const CUtensorMap
     }
     fence_proxy_async_smem();
     named_barrier_sync(1, 128);
-    if (leader) {
+    if (leader && all_waits_held(ok, abort_flag)) {
       for (int s = 0; s < NS; ++s) tma_store_2d(tmC, ring + s * kSlabBytes, n_blk * (BN / 2) + s * 64, m0);
       bulk_commit_group();
     }
-    return true;
+    return ok;
   } else {
     // STORE (bf16, 64 columns per slab) or F32 (fp32, 32 columns per slab)
     constexpr int SC = EPI == HB_EPI_F32 ? 32 : 64;
@@ -554,11 +564,11 @@ __device__ __forceinline__ bool epilogue_last(const Params& p, const CUtensorMap
     }
     fence_proxy_async_smem();
     named_barrier_sync(1, 128);
-    if (leader) {
+    if (leader && all_waits_held(ok, abort_flag)) {
       for (int s = 0; s < NS; ++s) tma_store_2d(tmC, ring + s * kSlabBytes, n_blk * BN + s * SC, m0);
       bulk_commit_group();
     }
-    return true;
+    return ok;
   }
 }
 
@@ -780,7 +790,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Unit w = unit_of<BN>(p, u, m_tiles, kblocks);
         const int acc = t & 1;
         const uint32_t acc_phase = (t >> 1) & 1;
-        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status)) break;
+        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -820,6 +833,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();
     const int quarter = warp & 3;
     const bool leader = warp == 2 && lane == 0;
+    // once a wait of the warp has failed it waits for nothing and stores
+    // nothing more, but goes on through the tiles: the others may meet it at
+    // a named barrier
+    bool ok = true;
     int t = 0;
     for (int un = blockIdx.x; un < units; un += gridDim.x, ++t) {
       const Unit wu = unit_of<BN>(p, un, m_tiles, kblocks);
@@ -833,24 +850,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the row's folded RMSNorm factor, read before the accumulator is ready
       const float scale = (p.norm.ss_in != nullptr && row_ok) ? row_inv_rms(p.norm, row) : 1.f;
       const float rowf = F8 && row_ok ? scale * p.sa[row] : scale;
-      bool ok = mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.status));
       tc_fence_after();
       const uint32_t t_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
       if constexpr (EPI == kEpiRope) {
-        epilogue_rope<BN, F8>(p, t_base, row, row_ok, n_blk, scale, rowf);
+        epilogue_rope<BN, F8>(p, t_base, row, row_ok && ok, n_blk, scale, rowf);
       } else if (un + static_cast<int>(gridDim.x) >= units) {
         // the CTA's last tile: the ring is idle, stage through it
         ok = epilogue_last<BN, EPI, F8>(p, &tmC, &tmR, smem, ep_bar, ep_flag, t_base, m0, row, row_ok, rloc, n_blk,
-                                        wu.tile, wu.half, leader, scale, rowf, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) break;
+                                        wu.tile, wu.half, leader, scale, rowf, abort_flag, ok);
+        ok = __all_sync(0xffffffffu, ok);
       } else {
-        epilogue_tile<BN, EPI, F8>(p, t_base, row, row_ok, rloc, n_blk, wu.tile, wu.half, leader, ep_flag, abort_flag,
-                                   scale, rowf);
+        epilogue_tile<BN, EPI, F8>(p, t_base, row, row_ok && ok, rloc, n_blk, wu.tile, wu.half, leader, ep_flag,
+                                   abort_flag, scale, rowf);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[acc]);
+      if (lane == 0 && ok) mbar_arrive(&acc_empty[acc]);
     }
     if (leader) bulk_wait_group<0>();  // the TMA stores have left shared memory and are performed
   }
@@ -1084,6 +1100,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     griddep_wait();
     const int quarter = warp & 3;
     const bool leader_thread = warp == 2 && lane == 0;
+    bool ok = true;  // as in gemm_kernel
     int t = 0;
     for (int un = cluster; un < units; un += n_clusters, ++t) {
       const PairUnit wu = pair_unit_of(p, un, pm_tiles, kblocks);
@@ -1095,27 +1112,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool row_ok = row < p.M;
       const float scale = (p.norm.ss_in != nullptr && row_ok) ? row_inv_rms(p.norm, row) : 1.f;
       const float rowf = F8 && row_ok ? scale * p.sa[row] : scale;
-      bool ok = mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[acc], acc_phase, abort_flag, p.status));
       tc_fence_after();
       if (mt < m_tiles) {  // a 128-row tile wholly past M (odd tile count) has nothing to write
         const uint32_t t_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
         const int stile = mt + m_tiles * wu.n_blk;
         if constexpr (EPI == kEpiRope) {
-          epilogue_rope<BN, F8>(p, t_base, row, row_ok, wu.n_blk, scale, rowf);
+          epilogue_rope<BN, F8>(p, t_base, row, row_ok && ok, wu.n_blk, scale, rowf);
         } else if (un + n_clusters >= units) {
           // the CTA's last tile: its ring is idle, stage through it
           ok = epilogue_last<BN, EPI, F8>(p, &tmC, &tmR, smem, ep_bar, ep_flag, t_base, mt * BM, row, row_ok, rloc,
-                                          wu.n_blk, stile, wu.half, leader_thread, scale, rowf, abort_flag);
+                                          wu.n_blk, stile, wu.half, leader_thread, scale, rowf, abort_flag, ok);
+          ok = __all_sync(0xffffffffu, ok);
         } else {
-          epilogue_tile<BN, EPI, F8>(p, t_base, row, row_ok, rloc, wu.n_blk, stile, wu.half, leader_thread, ep_flag,
-                                     abort_flag, scale, rowf);
+          epilogue_tile<BN, EPI, F8>(p, t_base, row, row_ok && ok, rloc, wu.n_blk, stile, wu.half, leader_thread,
+                                     ep_flag, abort_flag, scale, rowf);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0 && ok) mbar_arrive_cluster(cluster_addr(&acc_empty[acc], 0));
     }
     if (leader_thread) bulk_wait_group<0>();  // the TMA stores have left shared memory and are performed
     if (lane == 0 && *abort_flag) raise_peer_abort(abort_flag, rank);

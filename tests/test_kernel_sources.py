@@ -1,8 +1,13 @@
-"""A rule that the kernels' sources have to keep, checked as text (no GPU): a
-kernel that starts while the kernel ahead of it still runs (griddep_wait)
-reads nothing through the read-only path.  Its loads of what that kernel
+"""Rules that the kernels' sources have to keep, checked as text (no GPU).
+
+A kernel that starts while the kernel ahead of it still runs (griddep_wait)
+reads nothing through the read-only path: its loads of what that kernel
 writes could be moved ahead of the wait by the compiler, and the data is not
-constant while it runs."""
+constant while it runs.
+
+A warp whose bounded wait has expired still meets the others at the named
+barriers ahead of it: it leaves no loop that holds one, or the others wait
+there for ever."""
 import os
 import re
 
@@ -44,3 +49,36 @@ def test_no_read_only_path_behind_a_wait(name):
             continue  # an ordinary launch: starts once the kernel ahead is complete
         bad = [p.strip() for p in params.split(",") if "const" in p and "__restrict__" in p]
         assert not bad, (kernel, bad)
+
+
+def block_from(text, start):
+    """The statement block whose opening brace follows position `start`."""
+    i = text.index("{", start)
+    depth, j = 1, i + 1
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[j], 0)
+        j += 1
+    return text[i:j]
+
+
+def test_no_warp_leaves_the_others_at_a_named_barrier():
+    text = source("gemm_kernel.cuh")
+    last = block_from(text, text.index("bool epilogue_last("))
+    assert last.count("named_barrier_sync") == 3
+    # one way out ahead of a barrier, taken by all threads or none (split_exchange meets them)
+    assert last.count("return false") == 1
+    assert last.index("split_exchange(") < last.index("return false") < last.index("named_barrier_sync")
+    loops = [m.start() for m in re.finditer(r"for \(int un = ", text)]
+    assert len(loops) == 2
+    for at in loops:
+        body = block_from(text, text.index(")", text.index("++t", at)))
+        assert "epilogue_last<" in body and not re.search(r"\bbreak\b|\breturn\b", body)
+    block = source("gemm_e4m3_block.cu")
+    roles = [m.start() for m in re.finditer(r"for \(int [ut] = (?:first; u < units|blockIdx\.x; t < tiles); [ut] \+= \w+"
+                                            r"(?:\.x)?\)", block)]
+    met = [b for b in (block_from(block, at) for at in roles) if "named_barrier_sync" in b]
+    assert len(met) == 2
+    for body in met:
+        # leaving the sums of a group past the last K block, and a lambda's value
+        outer = body.replace("if (kb0 + g0 + g >= kblocks) break;", "").replace("{ return chunk_col(", "{ chunk_col(")
+        assert not re.search(r"\bbreak\b|\breturn\b", outer)
