@@ -68,18 +68,25 @@ def _stream(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _capturing(stream) -> bool:
+    import torch
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _empty(shape, dtype, device, stream):
     """Uninitialised device tensor for calls on `stream`.  torch takes it from
     the current stream's memory.  Where `stream` is another one, work queued
     on the current stream may still be using that memory, so `stream` waits
-    for it; and the tensor is recorded there, so that its memory is not given
+    for it (not in a capture, which runs later); and the tensor is recorded there, so that its memory is not given
     out again before `stream` is done with it, however early it is dropped."""
     import torch
     t = torch.empty(shape, dtype=dtype, device=device)
     if stream is not None and _stream(stream) != _current_stream():
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-        stream.wait_stream(torch.cuda.current_stream(device))
+        if not _capturing(stream):
+            stream.wait_stream(torch.cuda.current_stream(device))
         t.record_stream(stream)
     return t
 

@@ -462,10 +462,11 @@ __device__ __forceinline__ void wide_body(const CUtensorMap& tmA, const CUtensor
       // expired raises the abort flag, a thread whose wait has failed waits
       // for nothing any more (a tile more then costs its arithmetic, however
       // many K blocks are left), and the loop runs on over whatever TMEM
-      // holds: no buffer is released any more, and nothing of the tile is stored.  A tile is the work of all
-      // eight warps, whose waits need not expire together (at BN 256 the
-      // halves have buffers of their own), so the store asks the flag, which
-      // every warp has had its chance to raise before the barrier ahead of it.
+      // holds: no buffer is released any more, and nothing of the tile is
+      // stored.  A tile is the work of all eight warps, whose waits need not
+      // expire together (at BN 256 the halves have buffers of their own), so
+      // the store asks the flag, which every warp has had its chance to raise
+      // before the barrier ahead of it.
       constexpr int W = BN == 256 && EPI != HB_EPI_F32 ? 32 : 16;  // (F32 at 32 spilled: 246 us against 229)
       constexpr int NC = CH * 32 / W;
       uint32_t r[2][W];

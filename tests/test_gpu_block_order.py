@@ -139,3 +139,23 @@ def test_row_scaled_and_bf16_projections_straight_after_their_weights(m, n, k):
     for i, (o8, o16) in enumerate(outs):
         r8, r16 = ref[(i + 2) % 3 % 2]
         assert torch.equal(o8, r8) and torch.equal(o16, r16), i
+
+
+def test_quantize_captured_on_a_stream_that_is_not_the_current_one():
+    """Buffers of the call's own, taken while another stream captures: the
+    capture is not tied to the current stream's work."""
+    gen = wd.device_generator(3)
+    x = wd.randn_bf16((130, 512), gen)
+    ref = hb.hb_quantize_e4m3_block(x, block_rows=128)
+    hb.hb_check_status()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    # relaxed: the other stream's memory comes from cudaMalloc, which a capture otherwise forbids the thread
+    with torch.cuda.graph(graph, stream=side, capture_error_mode="relaxed"):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            q, s = hb.hb_quantize_e4m3_block(x, block_rows=128, stream=side)
+    q.zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(q, ref[0]) and torch.equal(s, ref[1])

@@ -84,6 +84,7 @@ def late(monkeypatch):
     monkeypatch.setattr(B, "hb_quantize_e4m3", quantize)
     monkeypatch.setattr(B, "hb_quantize_e4m3_block", quantize)
     monkeypatch.setattr(B, "_current_stream", lambda: 3)
+    monkeypatch.setattr(B, "_capturing", lambda st: False, raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: object())
     monkeypatch.setattr(torch, "empty", poisoned)
     monkeypatch.setattr(torch.Tensor, "record_stream",
