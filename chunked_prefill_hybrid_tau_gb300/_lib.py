@@ -51,11 +51,14 @@ class hb_profile(C.Structure):
     _fields_ = [("events", C.POINTER(vp)), ("n_events", i32)]
 
 
-HB_VERSION = 200  # the header's: the structures above are laid out as in this version
+HB_VERSION = 300  # the header's: the structures above are laid out as in this version
 HB_LAYER_STAGES = 8
 HB_EPI_STORE, HB_EPI_RESIDUAL, HB_EPI_SWIGLU, HB_EPI_F32 = 0, 1, 2, 3
 HB_WEIGHTS_BF16, HB_WEIGHTS_E4M3, HB_WEIGHTS_E4M3_BLOCK = 0, 1, 2
 HB_LAYER_QK_NORM = 256
+HB_NORM_BF16, HB_NORM_E4M3, HB_NORM_E4M3_BLOCK = 0, 1, 2
+HB_LOGITS_F32, HB_LOGITS_BF16 = 0, 1
+HB_MAX_TOP_K = 32  # hb_logprobs
 HB_OK, HB_ERR_INVALID_ARG, HB_ERR_CAPACITY, HB_ERR_OUT_OF_PAGES = 0, 1, 2, 3
 HB_ERR_CUDA, HB_ERR_TIMEOUT, HB_ERR_UNSUPPORTED, HB_ERR_DEVICE = 4, 5, 6, 7
 
@@ -83,11 +86,17 @@ PROTOTYPES = {
                                C.c_size_t, vp]),
     "hb_attention_noalloc": (C.c_int, [vp, vp, vp, i32, C.POINTER(hb_device_plan), C.POINTER(hb_layer_dims), i32,
                                        vp, vp]),
+    "hb_kv_append_e4m3": (C.c_int, [vp, i32, vp, vp, vp, i32, C.POINTER(hb_layer_dims), vp, vp, vp, vp, vp, vp, vp, i32,
+                                    vp]),
+    "hb_attention_e4m3_workspace_bytes": (C.c_size_t, [C.POINTER(hb_layer_dims), i32, i32, i32]),
+    "hb_attention_e4m3": (C.c_int, [vp, vp, vp, vp, vp, i32, C.POINTER(hb_device_plan), C.POINTER(hb_layer_dims), i32,
+                                    vp, vp, C.c_size_t, vp]),
     "hb_gemm": (C.c_int, [vp, vp, vp, vp, i32, i32, i32, i32, vp]),
     "hb_gemm_e4m3": (C.c_int, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp]),
     "hb_quantize_e4m3": (C.c_int, [vp, vp, vp, i32, i32, vp]),
     "hb_quantize_e4m3_block": (C.c_int, [vp, vp, vp, i32, i32, i32, vp]),
     "hb_gemm_e4m3_block": (C.c_int, [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp]),
+    "hb_add_rmsnorm": (C.c_int, [vp, vp, vp, vp, vp, vp, i32, i32, C.c_float, i32, vp]),
     "hb_interleave_gate_up": (C.c_int, [vp, vp, vp, i32, i32, vp]),
     "hb_fold_gamma": (C.c_int, [vp, vp, vp, i32, i32, vp]),
     "hb_layer_workspace_bytes": (C.c_size_t, [C.POINTER(hb_layer_dims), i32, i32, i32]),
@@ -99,6 +108,7 @@ PROTOTYPES = {
                                    C.POINTER(hb_device_plan), vp, i32, vp, vp, vp, vp, i32, i32, vp, C.c_size_t, vp,
                                    C.POINTER(hb_profile)]),
     "hb_final_logits": (C.c_int, [vp, i32, vp, i32, vp, vp, i32, i32, C.c_float, vp, vp, C.c_size_t, vp]),
+    "hb_logprobs": (C.c_int, [vp, i32, i32, i32, C.c_int64, vp, i32, vp, vp, i32, vp, vp, vp]),
     "hb_check_status": (C.c_int, [vp]),
     "hb_device_info": (C.c_int, [p_i32, p_i32]),
     "hb_kernel_launches": (C.c_uint64, []),

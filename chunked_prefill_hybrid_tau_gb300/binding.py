@@ -100,12 +100,13 @@ _types = None
 
 
 def _operand_types():
-    """Accepted element types of the operand kinds: bf16, e4m3 (codes), f32, i32."""
+    """Accepted element types of the operand kinds: bf16, e4m3 (codes), e8m0
+    (scale exponents), f32, i32."""
     global _types
     if _types is None:
         import torch
-        _types = {"bf16": (torch.bfloat16,), "e4m3": (torch.uint8, torch.float8_e4m3fn), "f32": (torch.float32,),
-                  "i32": (torch.int32,)}
+        _types = {"bf16": (torch.bfloat16,), "e4m3": (torch.uint8, torch.float8_e4m3fn),
+                  "e8m0": (torch.uint8, torch.float8_e8m0fnu), "f32": (torch.float32,), "i32": (torch.int32,)}
     return _types
 
 
@@ -415,6 +416,60 @@ def hb_attention(q, k_cache, v_cache, dplan: DevicePlan, dims, max_kv_len, out, 
                               _stream(stream)), "hb_attention")
 
 
+def _cache_e4m3(call, ds, k_cache, k_scale, v_cache, v_scale, types, dev):
+    """Pages of an E4M3 cache and its four pointers, each pool's size checked
+    against the dims and the page count of k_cache."""
+    pages, rows = k_cache.shape[0], k_cache.shape[0] * ds.n_kv * 16
+    return pages, (_need(call, "k_cache", k_cache, types["e4m3"], rows * ds.d_head, dev),
+                   _need(call, "k_scale", k_scale, types["e8m0"], rows, dev),
+                   _need(call, "v_cache", v_cache, types["e4m3"], rows * ds.d_head, dev),
+                   _need(call, "v_scale", v_scale, types["e8m0"], rows, dev))
+
+
+def hb_kv_append_e4m3(qkv, row_pos, slot_mapping, rope, max_pos, dims, q_out, k_cache, k_scale, v_cache, v_scale,
+                      g_q=None, g_k=None, stream=None):
+    """hb_kv_append into E4M3 codes k_cache, v_cache [pages][n_kv][16][d_head]
+    with power-of-two scales k_scale, v_scale [pages][n_kv][16] (exponent
+    bytes); with gains g_q, g_k (bf16 [d_head]) q and k heads are normed."""
+    ds = dims_struct(dims)
+    T, dh, call = qkv.shape[0], ds.d_head, "hb_kv_append_e4m3"
+    if qkv.numel() != T * (ds.n_q + 2 * ds.n_kv) * dh:
+        raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: qkv {tuple(qkv.shape)} does not have rows of {ds.n_q} q and "
+                                            f"2 x {ds.n_kv} kv heads of {dh}")
+    types, dev = _operand_types(), _current_device()
+    bf16, i32 = types["bf16"], types["i32"]
+    pages, cache = _cache_e4m3(call, ds, k_cache, k_scale, v_cache, v_scale, types, dev)
+    _check(lib().hb_kv_append_e4m3(
+        _need(call, "qkv", qkv, bf16, 0, dev), T, _need(call, "row_pos", row_pos, i32, T, dev),
+        _need(call, "slot_mapping", slot_mapping, i32, T, dev),
+        _need(call, "rope", rope, types["f32"], max_pos * dh, dev), int(max_pos), C.byref(ds),
+        None if g_q is None else _need(call, "g_q", g_q, bf16, dh, dev),
+        None if g_k is None else _need(call, "g_k", g_k, bf16, dh, dev),
+        _need(call, "q_out", q_out, bf16, T * ds.n_q * dh, dev), *cache, pages, _stream(stream)), call)
+
+
+def hb_attention_e4m3_workspace_bytes(dims, max_rows, max_seqs, max_kv_len) -> int:
+    ds = dims_struct(dims)
+    return int(lib().hb_attention_e4m3_workspace_bytes(C.byref(ds), int(max_rows), int(max_seqs), int(max_kv_len)))
+
+
+def hb_attention_e4m3(q, k_cache, k_scale, v_cache, v_scale, dplan: DevicePlan, dims, max_kv_len, out, workspace,
+                      stream=None):
+    """hb_attention over the E4M3 cache that hb_kv_append_e4m3 writes."""
+    ds = dims_struct(dims)
+    ps = dplan.struct()
+    call = "hb_attention_e4m3"
+    types, dev = _operand_types(), _current_device()
+    pages, cache = _cache_e4m3(call, ds, k_cache, k_scale, v_cache, v_scale, types, dev)
+    count = ps.n_rows * ds.n_q * ds.d_head
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: workspace must be a contiguous tensor on the current device")
+    _check(lib().hb_attention_e4m3(
+        _need(call, "q", q, types["bf16"], count, dev), *cache, pages, C.byref(ps), C.byref(ds), int(max_kv_len),
+        _need(call, "out", out, types["bf16"], count, dev), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)), call)
+
+
 def hb_gemm(A, B, Cout, R=None, epilogue=L.HB_EPI_STORE, stream=None):
     M, K = A.shape
     N = B.shape[0]
@@ -476,6 +531,36 @@ def hb_gemm_e4m3_block(A, s_a, B, s_b, Cout, R=None, epilogue=L.HB_EPI_STORE, st
         _need(call, "s_b", s_b, f32, (2 * ((N + 255) // 256) if swiglu else (N + 127) // 128) * kb, dev),
         _need(call, "C", Cout, f32 if epilogue == L.HB_EPI_F32 else bf16, M * N // 2 if swiglu else M * N, dev),
         None if R is None else _need(call, "R", R, bf16, M * N, dev), M, N, K, int(epilogue), _stream(stream)), call)
+
+
+NORM_FORMATS = {"bf16": L.HB_NORM_BF16, "e4m3": L.HB_NORM_E4M3, "e4m3_block": L.HB_NORM_E4M3_BLOCK}
+
+
+def hb_add_rmsnorm(x, residual, gamma, eps, h_out=None, y=None, scale=None, fmt="bf16", stream=None):
+    """h = bf16(x + residual) (into h_out unless that is None; residual may be
+    None) and its RMS norm y: bf16, or E4M3 codes with an fp32 scale per row
+    (fmt="e4m3") or per 128 columns ("e4m3_block"); returns (y, scale), made
+    here where they are None (scale stays None for bf16)."""
+    rows, d = x.shape
+    call = "hb_add_rmsnorm"
+    if fmt not in NORM_FORMATS:
+        raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: unknown format {fmt!r}")
+    coded = fmt != "bf16"
+    scales = (rows,) if fmt == "e4m3" else (rows, (d + 127) // 128)
+    if y is None or (coded and scale is None):
+        import torch
+        y = _empty((rows, d), torch.uint8 if coded else torch.bfloat16, x.device, stream) if y is None else y
+        scale = _empty(scales, torch.float32, x.device, stream) if coded and scale is None else scale
+    types, dev = _operand_types(), _current_device()
+    bf16, n = types["bf16"], rows * d
+    _check(lib().hb_add_rmsnorm(
+        _need(call, "x", x, bf16, 0, dev), None if residual is None else _need(call, "residual", residual, bf16, n, dev),
+        _need(call, "gamma", gamma, bf16, d, dev), None if h_out is None else _need(call, "h_out", h_out, bf16, n, dev),
+        _need(call, "y", y, types["e4m3"] if coded else bf16, n, dev),
+        None if scale is None else _need(call, "scale", scale, types["f32"],
+                                         rows if fmt == "e4m3" else rows * scales[-1], dev),
+        rows, d, float(eps), NORM_FORMATS[fmt], _stream(stream)), call)
+    return y, scale
 
 
 def hb_interleave_gate_up(w_gate, w_up, w_gu, stream=None):
@@ -617,3 +702,35 @@ def hb_final_logits(x, rows, g_f, w_lm, logits, workspace, eps, stream=None):
     _check(lib().hb_final_logits(_p(x), T, _p(rows), int(rows.numel()), _p(g_f), _p(w_lm), vocab, d, float(eps),
                                  _p(logits), _p(workspace), workspace.numel() * workspace.element_size(),
                                  _stream(stream)), "hb_final_logits")
+
+
+def hb_logprobs(logits, tokens=None, token_logprobs=None, entropy=None, top_ids=None, top_logprobs=None, stream=None):
+    """Log probabilities of tokens (int32 [rows][n]) under logits (fp32 or
+    bf16 [rows][vocab], rows any stride of at least vocab apart), each row's
+    entropy and its top_ids.shape[1] best alternatives, into the fp32 tensors
+    token_logprobs [rows][n], entropy [rows], top_logprobs [rows][k] and the
+    int32 top_ids [rows][k].  What is None is left out."""
+    rows, vocab = logits.shape
+    call = "hb_logprobs"
+    types, dev = _operand_types(), _current_device()
+    f32, i32 = types["f32"], types["i32"]
+    if logits.dtype not in f32 + types["bf16"] or logits.get_device() != dev or (vocab > 1 and logits.stride(1) != 1) \
+            or (rows > 1 and logits.stride(0) < vocab):
+        raise HBError(L.HB_ERR_INVALID_ARG,
+                      f"{call}: logits must be an fp32 or bf16 device matrix with adjacent columns on the current "
+                      f"device, not {tuple(logits.shape)} {logits.dtype} with strides {logits.stride()} on "
+                      f"{logits.device}")
+    if (tokens is None) != (token_logprobs is None) or (top_ids is None) != (top_logprobs is None):
+        raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: tokens go with token_logprobs, top_ids with top_logprobs")
+    for name, t in (("tokens", tokens), ("top_ids", top_ids)):
+        if t is not None and (t.dim() != 2 or t.shape[0] != rows):
+            raise HBError(L.HB_ERR_INVALID_ARG, f"{call}: {name} must have {rows} rows, not {tuple(t.shape)}")
+    n = 0 if tokens is None else tokens.shape[1]
+    k = 0 if top_ids is None else top_ids.shape[1]
+    _check(lib().hb_logprobs(
+        logits.data_ptr(), L.HB_LOGITS_F32 if logits.dtype in f32 else L.HB_LOGITS_BF16, rows, vocab,
+        logits.stride(0) if rows > 1 else vocab, None if n == 0 else _need(call, "tokens", tokens, i32, rows * n, dev), n,
+        None if n == 0 else _need(call, "token_logprobs", token_logprobs, f32, rows * n, dev),
+        None if entropy is None else _need(call, "entropy", entropy, f32, rows, dev), k,
+        None if k == 0 else _need(call, "top_ids", top_ids, i32, rows * k, dev),
+        None if k == 0 else _need(call, "top_logprobs", top_logprobs, f32, rows * k, dev), _stream(stream)), call)

@@ -1,0 +1,454 @@
+// Log probabilities of given tokens, the entropy and the k best alternatives
+// of every row of logits, in one read of the logits.
+//
+// With m = max x_i, s = sum exp(x_i - m), t = sum exp(x_i - m) (x_i - m):
+//   lse = m + log s,  log p_i = (x_i - m) - log s,  entropy = log s - t / s,
+// so one pass that carries (m, s, t) has everything but the order; two parts
+// of a row join by rescaling to the larger m.  The differences x - m are
+// formed before the product with log2(e): rounding m log2(e) first would put
+// an error of m * 2^-24 into every term.
+//
+// The k best: every thread keeps the largest of its elements.  Four lanes'
+// largest make a group; of the CTA's 128 groups the k-th largest is a bound
+// that at least k elements reach, and only the groups that reach it (k, and
+// ties) can hold one of the k best.  Their elements are read again (a 128th of
+// the row each, from L2), those at or above the bound are collected (a few
+// more than k) and ranked by counting.
+//
+// A row has 8 fixed segments, and thread t of a segment fixed elements; states
+// join over segments first, in a fixed tree, then over threads.  1, 2, 4 or 8
+// CTAs (a cluster) share a row's segments, more the fewer rows there are: the
+// arithmetic, and so every bit, is the same.
+//
+// Reads 4 or 2 bytes an element once: HBM bounds it for many rows.
+#include <cuda_bf16.h>
+
+#include "device.cuh"
+#include "runtime.h"
+
+namespace hb {
+namespace {
+
+using namespace dev;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kSegs = 8;
+constexpr int kElems = 16;            // elements a thread takes at a time
+constexpr int kGroups = kThreads / 4;
+constexpr int kMaxTop = 32;
+constexpr int kCap = 1024;            // collected candidates
+constexpr float kLeast = -1e30f;      // stands for differences of -infinity, where the factor is 0
+constexpr float kLog2e = 1.44269504088896341f;
+
+struct Args {
+  const void* logits;
+  long long stride;
+  int vocab;
+  const int* tokens;
+  int n_tokens;
+  float* token_lp;
+  float* entropy;
+  int top_k;
+  int* top_ids;
+  float* top_lp;
+  int* status;
+};
+
+struct State {
+  float m, s, t;
+};
+
+// The states of two parts of a row as one.
+__device__ __forceinline__ State join(const State& a, const State& b) {
+  const float m = fmaxf(a.m, b.m);
+  // a part without a finite logit, or an empty one, has m = -inf and s = 0
+  // (and a difference that overflows meets a factor of 0)
+  const float da = a.m == -INFINITY ? 0.f : fmaxf(__fsub_rn(a.m, m), kLeast);
+  const float db = b.m == -INFINITY ? 0.f : fmaxf(__fsub_rn(b.m, m), kLeast);
+  const float fa = ex2_approx(__fmul_rn(da, kLog2e)), fb = ex2_approx(__fmul_rn(db, kLog2e));
+  State c;
+  c.m = m;
+  c.s = __fmaf_rn(a.s, fa, __fmul_rn(b.s, fb));
+  c.t = __fmaf_rn(__fmaf_rn(a.s, da, a.t), fa, __fmul_rn(__fmaf_rn(b.s, db, b.t), fb));
+  return c;
+}
+
+// Logits as whole numbers in their order, equal ones alike (-0 as +0), NaN
+// above all; a candidate's key also orders equal logits by the lower index.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  if (x != x) return 0xffffffffu;
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long key_of(float x, int i) {
+  return static_cast<unsigned long long>(order_of(x)) << 32 | (0xffffffffu - static_cast<uint32_t>(i));
+}
+
+template <typename T>
+struct Row {
+  static constexpr int E = 16 / sizeof(T);  // elements of a 16-byte piece
+  static constexpr int P = kElems / E;      // pieces a thread takes at a time
+  const T* x;
+  int vocab;
+  int shift;   // elements by which the row starts behind a 16-byte boundary
+  int pieces;  // 16-byte pieces that the row touches; piece v holds elements v E - shift ...
+  int per_seg;
+
+  __device__ Row(const void* base, long long stride, int row, int n) {
+    x = static_cast<const T*>(base) + static_cast<long long>(row) * stride;
+    vocab = n;
+    shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+    pieces = (shift + n + E - 1) / E;
+    per_seg = (pieces + kSegs - 1) / kSegs;
+  }
+  __device__ static float one(const T* p) {
+    if (sizeof(T) == 4) return ld_f32(reinterpret_cast<const float*>(p));
+    unsigned short b;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(b) : "l"(p));
+    return __uint_as_float(static_cast<uint32_t>(b) << 16);
+  }
+  // The elements of piece v; those outside the row are -inf.
+  __device__ __forceinline__ void load(int v, float (&f)[E]) const {
+    const int i0 = v * E - shift;
+    if (i0 >= 0 && i0 + E <= vocab) {
+      if (sizeof(T) == 4) {
+        const float4 w = ld_f4(x + i0);
+        f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
+      } else {
+        const uint4 w = ld_u4(x + i0);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[(2 * j) % E] = __uint_as_float(u[j] << 16);
+          f[(2 * j + 1) % E] = __uint_as_float(u[j] & 0xffff0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; ++j) f[j] = i0 + j >= 0 && i0 + j < vocab ? one(x + i0 + j) : -INFINITY;
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_dsmem_f32(const void* p, uint32_t rank) {
+  return __uint_as_float(ld_dsmem_u32(p, rank));
+}
+
+// Binary tree over a power of two of states, in place; the result is a[0].
+template <int N>
+__device__ __forceinline__ void join_tree(State (&a)[N]) {
+#pragma unroll
+  for (int w = 1; w < N; w *= 2)
+#pragma unroll
+    for (int i = 0; i + w < N; i += 2 * w) a[i] = join(a[i], a[i + w]);
+}
+
+struct Shared {
+  State state[kThreads];
+  float best[kGroups];
+  unsigned long long best_key[kGroups];
+  int winners[kGroups];
+  unsigned long long cand[kCap];
+  unsigned long long top[kMaxTop];
+  unsigned long long all[8 * kMaxTop];
+  State warp_state[kWarps];
+  unsigned long long bound;
+  int n_winners, n_cand;
+};
+
+template <typename T, int CL>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
+  constexpr int E = Row<T>::E, P = Row<T>::P, SEGS = kSegs / CL;
+  griddep_launch_dependents();
+  griddep_wait();
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = CL > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int row = blockIdx.x / CL;
+  const Row<T> x(a.logits, a.stride, row, a.vocab);
+
+  // ---- one pass: (m, s, t) of each segment's elements of this thread, the
+  // segments joined as the leaves of a binary tree; and the largest element
+  State seg[SEGS];
+  float best = -INFINITY;
+#pragma unroll 1
+  for (int i = 0; i < SEGS; ++i) {
+    const int v0 = (rank * SEGS + i) * x.per_seg, v1 = min(v0 + x.per_seg, x.pieces);
+    State st = {-INFINITY, 0.f, 0.f};
+#pragma unroll 1
+    for (int v = v0 + tid; v < v1; v += kThreads * P) {
+      float f[P][E];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (v + p * kThreads < v1) {
+          x.load(v + p * kThreads, f[p]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j) f[p][j] = -INFINITY;
+        }
+      }
+      float mt = f[0][0];
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < E; ++j) mt = fmaxf(mt, f[p][j]);
+      if (mt > st.m) {
+        if (st.m != -INFINITY) {
+          const float d = fmaxf(__fsub_rn(st.m, mt), kLeast), c = ex2_approx(__fmul_rn(d, kLog2e));
+          st.t = __fmul_rn(__fmaf_rn(st.s, d, st.t), c);
+          st.s = __fmul_rn(st.s, c);
+        }
+        st.m = mt;
+      }
+      const float m = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const float d = __fsub_rn(f[p][j], m), e = ex2_approx(__fmul_rn(d, kLog2e));
+          st.s = __fadd_rn(st.s, e);
+          st.t = __fmaf_rn(e, fmaxf(d, kLeast), st.t);  // e = 0 at d = -inf: the product is 0
+        }
+    }
+    best = fmaxf(best, st.m);
+    // a NaN among the elements has made s a NaN: carry it on whatever m is
+#pragma unroll
+    for (int k = 0; k < SEGS; ++k)
+      if (k == i) seg[k] = st;
+  }
+  join_tree(seg);
+  sh.state[tid] = seg[0];
+
+  // ---- the k best of this CTA's segments, in falling order in sh.top
+  const int k = a.top_k;
+  if (k > 0) {
+    float g = best;
+    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
+    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+    if ((lane & 3) == 0) sh.best[tid >> 2] = g;
+    if (tid < kMaxTop) sh.top[tid] = 0;
+    if (tid == 0) sh.n_winners = sh.n_cand = 0;
+    // fmaxf passes over a NaN: with one about, the bound goes by exact keys
+    bool by_key = __syncthreads_or(seg[0].s != seg[0].s) != 0;
+    // rank of each group among the groups, equal ones by the lower group
+    if (tid < kGroups) {
+      const float mine = sh.best[tid];
+      int above = 0;
+#pragma unroll 8
+      for (int i = 0; i < kGroups; ++i) above += sh.best[i] > mine || (sh.best[i] == mine && i < tid);
+      if (above == k - 1) sh.bound = static_cast<unsigned long long>(order_of(mine)) << 32;
+    }
+    __syncthreads();
+    bool keyed = false;
+#pragma unroll 1
+    while (true) {
+      if (by_key && !keyed) {
+        // the exact largest key of each group's elements, and the k-th of them
+        unsigned long long mine = 0;
+        for (int v0 = rank * SEGS * x.per_seg, i = 0; i < SEGS; ++i, v0 += x.per_seg)
+          for (int v = v0 + tid; v < min(v0 + x.per_seg, x.pieces); v += kThreads) {
+            float f[E];
+            x.load(v, f);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+              const int at = v * E - x.shift + j;
+              if (at >= 0 && at < x.vocab) mine = max(mine, key_of(f[j], at));
+            }
+          }
+        mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+        mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
+        if ((lane & 3) == 0) sh.best_key[tid >> 2] = mine;
+        __syncthreads();
+        if (tid < kGroups) {
+          mine = sh.best_key[tid];
+          int above = 0;
+          for (int i = 0; i < kGroups; ++i) above += sh.best_key[i] > mine || (sh.best_key[i] == mine && i < tid);
+          if (above == k - 1) sh.bound = max(sh.bound, mine);
+        }
+        keyed = true;
+        __syncthreads();
+      }
+      const unsigned long long bound = sh.bound;
+      if (tid < kGroups) {
+        const bool wins = by_key ? sh.best_key[tid] >= bound && sh.best_key[tid] != 0
+                                 : order_of(sh.best[tid]) >= static_cast<uint32_t>(bound >> 32);
+        if (wins) sh.winners[atomicAdd(&sh.n_winners, 1)] = tid;
+      }
+      __syncthreads();
+      // the winners' elements at or above the bound: a warp takes a winner
+      for (int w = warp; w < sh.n_winners; w += kWarps) {
+        const int grp = sh.winners[w];
+        for (int i = 0; i < SEGS; ++i) {
+          const int v0 = (rank * SEGS + i) * x.per_seg, v1 = min(v0 + x.per_seg, x.pieces);
+          for (int v = v0 + 4 * grp + (lane & 3) + (lane >> 2) * kThreads; v < v1; v += 8 * kThreads) {
+            float f[E];
+            x.load(v, f);
+#pragma unroll
+            for (int j = 0; j < E; ++j) {
+              const int at = v * E - x.shift + j;
+              if (at < 0 || at >= x.vocab) continue;
+              const unsigned long long key = key_of(f[j], at);
+              if (key >= bound) {
+                const int n = atomicAdd(&sh.n_cand, 1);
+                if (n < kCap) sh.cand[n] = key;
+              }
+            }
+          }
+        }
+      }
+      __syncthreads();
+      const int found = sh.n_cand, n = min(found, kCap);
+      // rank by counting: keys differ, so the ranks do
+      for (int c = tid; c < n; c += kThreads) {
+        const unsigned long long key = sh.cand[c];
+        int above = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) above += sh.cand[i] > key;
+        if (above < k) sh.top[above] = key;
+      }
+      __syncthreads();
+      if (found <= kCap) break;
+      // more candidates than fit: ties at the bound (many equal logits), or a
+      // few groups with most of the large ones.  First find the bound by exact
+      // keys, then take the k-th of those collected, which leaves at most
+      // found - (kCap - k) for the next round.
+      if (tid == 0) {
+        if (keyed) sh.bound = sh.top[k - 1];
+        sh.n_winners = sh.n_cand = 0;
+      }
+      by_key = true;
+      __syncthreads();
+    }
+  }
+
+  // ---- the row: states of the cluster's CTAs, thread by thread, then over
+  // the threads; and the best of each CTA's k best
+  if (CL > 1) cluster_sync();
+  else __syncthreads();
+  if (rank == 0) {
+    State c[CL];
+#pragma unroll
+    for (int i = 0; i < CL; ++i) {
+      if (i == 0) {
+        c[i] = sh.state[tid];
+      } else {
+        c[i].m = ld_dsmem_f32(&sh.state[tid].m, i);
+        c[i].s = ld_dsmem_f32(&sh.state[tid].s, i);
+        c[i].t = ld_dsmem_f32(&sh.state[tid].t, i);
+      }
+    }
+    unsigned long long key = 0;
+    if (CL > 1 && tid < CL * k) {
+      const unsigned long long* p = &sh.top[tid % k];
+      const uint32_t lo = ld_dsmem_u32(p, tid / k), hi = ld_dsmem_u32(reinterpret_cast<const uint32_t*>(p) + 1, tid / k);
+      key = static_cast<unsigned long long>(hi) << 32 | lo;
+      sh.all[tid] = key;
+    }
+    join_tree(c);
+    State st = c[0];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      State other;
+      other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+      other.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+      other.t = __shfl_xor_sync(0xffffffffu, st.t, o);
+      st = (lane & o) ? join(other, st) : join(st, other);
+    }
+    if (lane == 0) sh.warp_state[warp] = st;
+    __syncthreads();
+    State ws[kWarps];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) ws[i] = sh.warp_state[i];
+    join_tree(ws);
+    const float m = ws[0].m, log_s = logf(ws[0].s);
+    if (a.entropy && tid == 0) a.entropy[row] = __fsub_rn(log_s, __fdiv_rn(ws[0].t, ws[0].s));
+    for (int j = tid; j < a.n_tokens; j += kThreads) {
+      const size_t at = static_cast<size_t>(row) * a.n_tokens + j;
+      const int id = ld_s32(a.tokens + at);
+      if (id >= a.vocab) flag_error(a.status, kStatusIndex);
+      if (id >= 0 && id < a.vocab) a.token_lp[at] = __fsub_rn(__fsub_rn(Row<T>::one(x.x + id), m), log_s);
+    }
+    auto put = [&](int at, unsigned long long best_key) {
+      const int id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best_key));
+      const size_t to = static_cast<size_t>(row) * k + at;
+      a.top_ids[to] = id;
+      a.top_lp[to] = __fsub_rn(__fsub_rn(Row<T>::one(x.x + id), m), log_s);
+    };
+    if (CL == 1) {
+      if (tid < k) put(tid, sh.top[tid]);
+    } else if (tid < CL * k && key != 0) {
+      int above = 0;
+      for (int i = 0; i < CL * k; ++i) above += sh.all[i] > key;
+      if (above < k) put(above, key);
+    }
+  }
+  if (CL > 1) cluster_sync();  // this CTA's shared memory has been read
+}
+
+template <typename T, int CL>
+hb_status logprobs_launch(const Args& a, int rows, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * CL);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CL;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CL > 1 ? 2 : 1;
+  const hb_status st = cuda_status(cudaLaunchKernelEx(&cfg, logprobs_kernel<T, CL>, a), "logprobs_kernel launch");
+  if (st == HB_OK) count_launch();
+  return st;
+}
+
+template <typename T>
+hb_status logprobs_rows(const Args& a, int rows, int num_sms, cudaStream_t stream) {
+  // as many CTAs a row as keep the grid within two a SM
+  const long long room = 2ll * num_sms;
+  if (rows * 8ll <= room) return logprobs_launch<T, 8>(a, rows, stream);
+  if (rows * 4ll <= room) return logprobs_launch<T, 4>(a, rows, stream);
+  if (rows * 2ll <= room) return logprobs_launch<T, 2>(a, rows, stream);
+  return logprobs_launch<T, 1>(a, rows, stream);
+}
+
+}  // namespace
+}  // namespace hb
+
+extern "C" hb_status hb_logprobs(const void* logits, int32_t logits_type, int32_t n_rows, int32_t vocab,
+                                 int64_t row_stride, const int32_t* tokens, int32_t n_tokens, float* token_logprobs,
+                                 float* entropy, int32_t top_k, int32_t* top_ids, float* top_logprobs, void* stream) {
+  using namespace hb;
+  clear_error();
+  HB_REQUIRE(logits_type == HB_LOGITS_F32 || logits_type == HB_LOGITS_BF16, "hb_logprobs: unknown logits type %d",
+             logits_type);
+  HB_REQUIRE(n_rows >= 0 && vocab > 0 && row_stride >= vocab, "hb_logprobs: n_rows >= 0, vocab > 0, row_stride >= vocab");
+  HB_REQUIRE(vocab <= (1 << 30) && n_rows <= (1 << 28), "hb_logprobs: at most 2^30 logits a row and 2^28 rows");
+  HB_REQUIRE(n_tokens >= 0, "hb_logprobs: n_tokens >= 0");
+  HB_REQUIRE(top_k >= 0 && top_k <= vocab && top_k <= kMaxTop, "hb_logprobs: top_k must be in 0 .. min(vocab, %d)",
+             kMaxTop);
+  if (n_rows == 0) return HB_OK;
+  HB_REQUIRE(logits != nullptr, "hb_logprobs: null pointer");
+  HB_REQUIRE(n_tokens == 0 || (tokens && token_logprobs), "hb_logprobs: null tokens or token_logprobs");
+  HB_REQUIRE(top_k == 0 || (top_ids && top_logprobs), "hb_logprobs: null top_ids or top_logprobs");
+  HB_REQUIRE((reinterpret_cast<uintptr_t>(logits) & (logits_type == HB_LOGITS_F32 ? 3u : 1u)) == 0 && aligned4(tokens) &&
+                 aligned4(token_logprobs) && aligned4(entropy) && aligned4(top_ids) && aligned4(top_logprobs),
+             "hb_logprobs: operands aligned to their elements");
+  if (n_tokens == 0 && top_k == 0 && !entropy) return HB_OK;
+  DeviceCtx ctx;
+  hb_status st = device_context(&ctx);
+  if (st != HB_OK) return st;
+  const Args a = {logits, row_stride, vocab, tokens, n_tokens, token_logprobs, entropy, top_k, top_ids, top_logprobs,
+                  ctx.status};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return logits_type == HB_LOGITS_F32 ? logprobs_rows<float>(a, n_rows, ctx.num_sms, s)
+                                      : logprobs_rows<__nv_bfloat16>(a, n_rows, ctx.num_sms, s);
+}

@@ -56,7 +56,7 @@ const char* hb_last_error(void);
  * what its caller was compiled against: a caller compares hb_version() with
  * HB_VERSION before its first other call and goes no further where they
  * differ (the Python binding does). */
-#define HB_VERSION 200
+#define HB_VERSION 300
 int32_t hb_version(void);
 
 /* ------------------------------------------------------------------------
@@ -321,6 +321,61 @@ hb_status hb_attention_noalloc(const void* q, const void* k_cache, const void* v
                                void* out, void* stream);
 
 /* ------------------------------------------------------------------------
+ * hb_kv_append_e4m3 - hb_kv_append into a cache of E4M3 codes (half the bytes
+ * that decode rows stream; the pages name no quantized cache: an addition).
+ * Per row and kv head the rotated key y (fp32, not rounded before) and the
+ * raw value are each quantized with a scale of their own:
+ *   amax = max |y|, e = the smallest integer >= -100 with amax <= 448 * 2^e,
+ *   code = E4M3(y * 2^-e), nearest-even (OCP E4M3), scale byte = e + 127.
+ * The scale is a power of two (an exponent byte with bias 127, OCP E8M0), so
+ * code * 2^e is exact in bf16 and in fp32: reading the cache rounds nothing.
+ * A vector with a NaN or an infinity gets scale byte 255 (NaN) and NaN codes
+ * (0x7f) throughout.
+ *   g_q, g_k : bf16 [d_head] gains: every q and k head is RMS-normed before
+ *              its rotation as hb_kv_append_norm does; both NULL: not normed
+ *   k_cache, v_cache : device bytes [num_pages][n_kv][page_size][d_head]
+ *   k_scale, v_scale : device bytes [num_pages][n_kv][page_size]
+ * Everything else (qkv, rope, q_out, padding rows, HB_ERR_DEVICE) as
+ * hb_kv_append.  qkv, rope, q_out, the caches and the gains are 16-byte
+ * aligned; the scales need no alignment here, 16 bytes in hb_attention_e4m3.
+ * A row's results do not depend on the other rows of the call.
+ * ---------------------------------------------------------------------- */
+hb_status hb_kv_append_e4m3(const void* qkv, int32_t T, const int32_t* row_pos, const int32_t* slot_mapping,
+                            const void* rope, int32_t max_pos, const hb_layer_dims* dims, const void* g_q,
+                            const void* g_k, void* q_out, void* k_cache, void* k_scale, void* v_cache, void* v_scale,
+                            int32_t num_pages, void* stream);
+
+/* ------------------------------------------------------------------------
+ * hb_attention_e4m3 - hb_attention over a cache of hb_kv_append_e4m3: row r
+ * of a sequence at position p attends to its keys 0..p,
+ *   out = sum_j P_j 2^ev_j V_j / sum_j P_j,
+ *   P_j = exp(2^ek_j (q . K_j) / sqrt(d_head) - m),
+ * with codes K, V, scales 2^ek, 2^ev of key j and the q row in bf16; products
+ * are summed and the softmax is kept in fp32, P is rounded to bf16 for its
+ * product with V.  What lies behind a sequence's last key, in its last page
+ * or in pages of the block table behind it, is never used, whatever it holds.
+ * A key or value of scale byte 255 reads as NaN.  Codes 0x7f and 0xff under
+ * another scale byte (the append writes none) are outside the format and may
+ * read as any value up to 480 times the scale or as NaN.
+ *   k_cache, v_cache, k_scale, v_scale : as in hb_kv_append_e4m3 (after this
+ *     iteration's append), each 16-byte aligned
+ *   q, plan, out, max_kv_len : as hb_attention.  Every sequence of the plan
+ *     has at least one row; a plan with another count is reported as
+ *     HB_ERR_DEVICE by hb_check_status, and rows may be left unwritten.
+ *   workspace: device scratch of hb_attention_e4m3_workspace_bytes(...)
+ *     bytes, 256-byte aligned, contents need not be initialised; calls that
+ *     may overlap (other streams, graphs replayed side by side) need one each
+ * Requires d_head == 64 or 128, page_size == 16, at most 1024 sequences.
+ * A row's result does not depend on the other sequences of the batch.
+ * ---------------------------------------------------------------------- */
+size_t hb_attention_e4m3_workspace_bytes(const hb_layer_dims* dims, int32_t max_rows, int32_t max_seqs,
+                                         int32_t max_kv_len);
+hb_status hb_attention_e4m3(const void* q, const void* k_cache, const void* k_scale, const void* v_cache,
+                            const void* v_scale, int32_t num_pages, const hb_device_plan* plan,
+                            const hb_layer_dims* dims, int32_t max_kv_len, void* out, void* workspace,
+                            size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * hb_gemm - C = epilogue(A B^T) on the tensor cores (bf16 in, fp32
  * accumulate): the packed-token projections whose roofline the pages use
  * (Sarathi-Serve reading notes, section 1.6: T = max(T_math, T_mem)).
@@ -413,6 +468,33 @@ hb_status hb_quantize_e4m3_block(const void* x, void* q, float* scale, int32_t r
  * ---------------------------------------------------------------------- */
 hb_status hb_gemm_e4m3_block(const void* A, const float* s_a, const void* B, const float* s_b, void* C,
                              const void* R, int32_t M, int32_t N, int32_t K, int32_t epilogue, void* stream);
+
+/* ------------------------------------------------------------------------
+ * hb_add_rmsnorm - residual addition and RMS norm in one pass over the rows:
+ *   h[r] = bf16(x[r] + residual[r])               (residual NULL: h = x)
+ *   y[r] = h[r] / sqrt(mean(h[r]^2) + eps) * gamma, in fp32 from the rounded h
+ * with y in one of three forms:
+ *   HB_NORM_BF16       : y bf16 [rows][d]; y_scale NULL
+ *   HB_NORM_E4M3       : codes [rows][d], y_scale fp32 [rows]: the operand of
+ *                        hb_gemm_e4m3, hb_quantize_e4m3's rule on the fp32 y
+ *   HB_NORM_E4M3_BLOCK : codes [rows][d], y_scale fp32 [rows][ceil(d / 128)]:
+ *                        the operand of hb_gemm_e4m3_block,
+ *                        hb_quantize_e4m3_block's rule (block_rows 1) on y
+ * Where weights carry no folded gain (block codes cannot take one afterwards)
+ * this is the operand preparation with the gain on the tokens' side.  The
+ * fp32 y is quantized directly, without a rounding to bf16 between; maxima
+ * below 2^-112 count as 2^-112 in both coded forms.  NaN and infinities
+ * follow the formulas: a NaN in h makes the whole row's y NaN, an infinity its
+ * own y NaN and the row's others 0; a NaN among a scale's y makes that scale
+ * and its codes NaN.  Other rows do not notice.
+ * x, residual, h_out: device bf16 [rows][d]; h_out may be NULL (h is not
+ * stored), or be x or residual; gamma: device bf16 [d]; y aliases nothing.
+ * d % 8 == 0 (codes: d % 16 == 0), d <= 32768; 16-byte aligned (y_scale: 4).
+ * A row's results do not depend on the other rows of the call.
+ * ---------------------------------------------------------------------- */
+typedef enum hb_norm_format { HB_NORM_BF16 = 0, HB_NORM_E4M3 = 1, HB_NORM_E4M3_BLOCK = 2 } hb_norm_format;
+hb_status hb_add_rmsnorm(const void* x, const void* residual, const void* gamma, void* h_out, void* y, float* y_scale,
+                         int32_t rows, int32_t d, float eps, int32_t format, void* stream);
 
 /* Weight preparation: w_gu[2 Fp][d], Fp = F rounded up to a multiple of 64,
  * from w_gate[F][d] and w_up[F][d] (device bf16): rows interleaved in blocks
@@ -549,6 +631,35 @@ hb_status hb_layer_kernel_count(const hb_layer_dims* dims, int32_t n_rows, int32
 hb_status hb_final_logits(const void* x, int32_t T, const int32_t* rows, int32_t n_sel, const void* g_f,
                           const void* w_lm, int32_t vocab, int32_t d, float eps, void* logits, void* workspace,
                           size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * hb_logprobs - log probabilities of given tokens, the entropy and the best
+ * alternatives of every row of logits (hb_final_logits' rows), one read of
+ * the logits.  With lse = log sum_i exp(x_i) of row r over the vocabulary:
+ *   token_logprobs[r][j] = x[tokens[r][j]] - lse
+ *   entropy[r]           = lse - sum_i p_i x_i,  p_i = exp(x_i - lse)
+ *   top_ids[r][0..k-1]   = the k largest logits' indices in falling order,
+ *                          equal ones by the lower index (-0 equals +0)
+ *   top_logprobs[r][j]   = x[top_ids[r][j]] - lse
+ * in fp32, from the logits as they are (no temperature).
+ *   logits : device fp32 (HB_LOGITS_F32) or bf16 (HB_LOGITS_BF16)
+ *            [n_rows][vocab], rows `row_stride` elements apart (>= vocab);
+ *            aligned to an element
+ *   tokens : device int32 [n_rows][n_tokens]; a negative id is padding, its
+ *            entry is left as it was; an id >= vocab sets HB_ERR_DEVICE and
+ *            is skipped.  n_tokens 0: tokens and token_logprobs may be NULL
+ *   entropy: fp32 [n_rows] or NULL
+ *   top_k  : 0..min(vocab, 32); 0: top_ids, top_logprobs may be NULL
+ * Logits of -infinity (masked tokens) have probability 0 and log probability
+ * -infinity.  A row without a finite logit, or with a NaN or +infinity, has
+ * no distribution: its log probabilities and entropy are NaN, and its
+ * top_ids take a NaN as larger than every number.
+ * A row's results do not depend on the other rows of the call, bit for bit.
+ * ---------------------------------------------------------------------- */
+typedef enum hb_logits_type { HB_LOGITS_F32 = 0, HB_LOGITS_BF16 = 1 } hb_logits_type;
+hb_status hb_logprobs(const void* logits, int32_t logits_type, int32_t n_rows, int32_t vocab, int64_t row_stride,
+                      const int32_t* tokens, int32_t n_tokens, float* token_logprobs, float* entropy, int32_t top_k,
+                      int32_t* top_ids, float* top_logprobs, void* stream);
 
 /* ------------------------------------------------------------------------
  * hb_check_status - synchronise `stream`, then read and clear the device
