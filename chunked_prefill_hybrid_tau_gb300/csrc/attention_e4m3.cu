@@ -3,8 +3,22 @@
 //
 //   out = sum_j P_j 2^ev_j V_j / sum_j P_j,  P_j = exp(2^ek_j (q . K_j) / sqrt(d) - m)
 //
-// One warp takes one row and q head, lanes share the head dimension, keys one
-// after another with a running maximum and sum.
+// Decode rows (sequences of one row): HBM bounds them, 2 n_kv (d + 1) bytes a
+// key.  A unit is one row x one kv head x one range of kSplit keys at fixed
+// positions, so a row's result does not depend on its batch; a warp owns whole
+// units and streams their 16-token pages through a ring of its own.
+//
+// Both products run on m16n8k16 MMAs with the keys (S) or the head dimension
+// (O) as rows and the kv head's q heads as the 8 columns:
+//   S^T = K Q^T  : 16 keys x 8 heads, one MMA per 16 dims,
+//   O^T += V^T P^T : 16 dims x 8 heads, one MMA per 16 dims of the output,
+// half the MMAs and half the accumulators of the other way round.  More than 8
+// q heads a kv head take a second column tile.  The codes are widened to bf16
+// in registers, exactly; a 16-bit ldmatrix of 8-bit codes hands a lane four
+// neighbouring dims of a key (K), or two dims of two keys (V, transposed), and
+// taking bytes (0, 2) and (1, 3) of them as the pairs permutes the dims of S's
+// sum, which q's fragments follow, and gives O's rows 2 a and 2 a + 1 to one
+// lane.  2^ek multiplies the scores and 2^ev the weights, in fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -27,6 +41,9 @@ struct Params {
   const int* block_table;
   int S, T, max_pages, num_pages, n_q, n_kv, grp, max_kv_len;
   float scale_log2;
+  float* partials;  // split records [sequence][split][kv head]
+  int max_splits;   // of a sequence of max_kv_len keys
+  int no_chunks;    // the plan has as many rows as sequences: none may have several
   int* status;
 };
 
@@ -57,6 +74,7 @@ __global__ void __launch_bounds__(128) attention_e4m3_kernel(Params p) {
   }
   const int s = lo, q1 = ld_s32(p.q_start + s + 1), kvl = ld_s32(p.kv_len + s);
   const int last = kvl - (q1 - row);
+  if (row >= ld_s32(p.q_start + s) && q1 - ld_s32(p.q_start + s) == 1) return;  // a decode row
   if (row < ld_s32(p.q_start + s) || row >= q1 || last < 0 || kvl > p.max_kv_len || (kvl + 15) / 16 > p.max_pages) {
     flag_error(p.status, kStatusIndex);
     return;
@@ -95,9 +113,417 @@ __global__ void __launch_bounds__(128) attention_e4m3_kernel(Params p) {
     p.out[(static_cast<size_t>(row) * p.n_q + h) * D + lane * E + i] = __float2bfloat16(o[i] / l);
 }
 
+// ---------------------------------------------------------------- decode rows
+constexpr int kSplit = 256;     // keys of a unit
+constexpr int kDecWarps = 16;
+constexpr float kRescale = 8.0f;  // log2 growth of a head's maximum that rescales its sums
+
+// a split record: O [heads][D], the maximum and the sum of each head, fp32 (a multiple of 16 bytes)
+__host__ __device__ constexpr int rec_floats(int grp, int d) { return grp * (d + 4); }
+
+template <int D>
+struct DC {
+  static constexpr int PAGE = 16 * D;         // one page of one kv head, K or V
+  static constexpr int STAGE = 2 * PAGE;
+  static constexpr int DR = D == 128 ? 3 : 6;  // ring depth per warp
+  static constexpr int OFF_SCALE = kDecWarps * DR * STAGE;  // K and V scales, 16 + 16 bytes a stage
+  static constexpr int OFF_BAR = OFF_SCALE + kDecWarps * DR * 32;
+  static constexpr int OFF_PRE = OFF_BAR + kDecWarps * DR * 8;
+  static constexpr int SMEM = OFF_PRE + (kMaxSeqs + 1) * 4 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 8 x 8 matrix of 16-bit elements, transposed across the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Two E4M3 codes as bf16, exactly: sign, and the exponent and mantissa fields
+// moved to bf16's places make the value times 2^-120 (the exponents' biases
+// differ by 120, and a subnormal code becomes a subnormal number), so one
+// product with 2^120 ends it.  even: bytes 0 and 2 of w, odd: bytes 1 and 3.
+__device__ __forceinline__ uint32_t times_2_120(uint32_t v) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7b807b80u));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
+  return times_2_120(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u));
+}
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) { return codes_odd(w << 8); }
+
+// 2^e of a scale byte of the format: 27 .. 247, or 255 (NaN)
+__device__ __forceinline__ float scale_of(uint32_t b) {
+  return b == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(b << 23);
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Byte offset of 16-byte piece c of key r in a swizzled page.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+template <int D, int NT>
+struct Heads {  // a warp's state of NT x 8 q heads
+  uint32_t q[NT][D / 16][2];
+  float o[NT][D / 16][4];
+  float m[NT][2], l[NT][2];
+};
+
+// One 16-key page: S, the softmax step (a maximum that is raised only when it
+// grows by more than 2^8, so that most pages need no reduction), O.  Lane (a =
+// lane / 4, t = lane % 4) has keys a and a + 8 of heads 2 t and 2 t + 1.  `live`
+// keys of the page count.
+template <int D, int NT>
+__device__ __forceinline__ void page_step(uint32_t kp, uint32_t vp, uint32_t sp, Heads<D, NT>& w, int live,
+                                          float scale_log2, int lane) {
+  const int mat = lane >> 3, key = ((mat & 1) << 3) + (lane & 7), a = lane >> 2;
+  float s[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 16; c += 2) {
+    uint32_t r[4];
+    ldsm_x4(kp + piece_at<D>(key, c + (mat >> 1)), r);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a0 = codes_even(r[2 * i]), a1 = codes_even(r[2 * i + 1]);
+      const uint32_t a2 = codes_odd(r[2 * i]), a3 = codes_odd(r[2 * i + 1]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816(s[n], a0, a1, a2, a3, w.q[n][c + i][0], w.q[n][c + i][1]);
+    }
+  }
+  const float k0 = scale_of(lds_u8(sp + a)) * scale_log2, k1 = scale_of(lds_u8(sp + a + 8)) * scale_log2;
+  const float v0 = scale_of(lds_u8(sp + 16 + a)), v1 = scale_of(lds_u8(sp + 16 + a + 8));
+  const bool in0 = a < live, in1 = a + 8 < live;
+  bool grew = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s[n][h] = in0 ? s[n][h] * k0 : -INFINITY;
+      s[n][2 + h] = in1 ? s[n][2 + h] * k1 : -INFINITY;
+      grew |= fmaxf(s[n][h], s[n][2 + h]) > w.m[n][h] + kRescale;
+    }
+  if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float mx = fmaxf(s[n][h], s[n][2 + h]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        // per head: another head's growth must not move this one's maximum
+        const float mn = mx > w.m[n][h] + kRescale ? mx : w.m[n][h];
+        const float alpha = mn == w.m[n][h] ? 1.f : ex2_approx(w.m[n][h] - mn);
+        w.m[n][h] = mn;
+        w.l[n][h] *= alpha;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          w.o[n][i][h] *= alpha;
+          w.o[n][i][2 + h] *= alpha;
+        }
+      }
+  }
+  uint32_t b[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float p[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float m = w.m[n][h] == -INFINITY ? 0.f : w.m[n][h];
+      const float p0 = ex2_approx(s[n][h] - m), p1 = ex2_approx(s[n][2 + h] - m);
+      w.l[n][h] += p0 + p1;
+      p[h] = in0 ? p0 * v0 : 0.f;
+      p[2 + h] = in1 ? p1 * v1 : 0.f;
+    }
+    b[n][0] = transpose8(pack_bf16x2(p[0], p[1]));
+    b[n][1] = transpose8(pack_bf16x2(p[2], p[3]));
+  }
+#pragma unroll
+  for (int c = 0; c < D / 16; c += 2) {
+    uint32_t r[4];
+    ldsm_x4_t(vp + piece_at<D>(key, c + (mat >> 1)), r);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t a0 = codes_even(r[2 * i]), a1 = codes_odd(r[2 * i]);
+      const uint32_t a2 = codes_even(r[2 * i + 1]), a3 = codes_odd(r[2 * i + 1]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816(w.o[n][c + i], a0, a1, a2, a3, b[n][0], b[n][1]);
+    }
+  }
+}
+
+// Units of every sequence before each one, into pre[0 .. S]: one-row sequences
+// have n_kv per kSplit keys.  Lengths out of range are reported and have none.
+__device__ __forceinline__ void count_units(const Params& p, int* pre) {
+  for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
+    const int q0 = ld_s32(p.q_start + s), q1 = ld_s32(p.q_start + s + 1), kvl = ld_s32(p.kv_len + s);
+    int n = 0;
+    if (q0 < 0 || q1 > p.T || q1 <= q0 || kvl < q1 - q0 || kvl > p.max_kv_len || (kvl + 15) / 16 > p.max_pages ||
+        (p.no_chunks && q1 - q0 != 1))
+      flag_error(p.status, kStatusIndex);
+    else if (q1 - q0 == 1)
+      n = p.n_kv * ((kvl + kSplit - 1) / kSplit);
+    pre[s + 1] = n;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    if (threadIdx.x == 0) pre[0] = 0;
+    int carry = 0;
+    for (int s0 = 0; s0 < p.S; s0 += 32) {
+      const int s = s0 + static_cast<int>(threadIdx.x);
+      int v = s < p.S ? pre[s + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (static_cast<int>(threadIdx.x) >= o) v += u;
+      }
+      if (s < p.S) pre[s + 1] = v + carry;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int upper_index(const int* pre, int n, int u) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kDecWarps * 32, 1)
+    decode_e4m3_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Params p) {
+  using C = DC<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int* pre = reinterpret_cast<int*>(smem + C::OFF_PRE);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::DR;
+  uint8_t* ring = smem + warp * C::DR * C::STAGE;
+  uint8_t* scales = smem + C::OFF_SCALE + warp * C::DR * 32;
+  if (lane == 0) {
+    for (int i = 0; i < C::DR; ++i) mbar_init(&full[i], 1);
+    fence_barrier_init();
+  }
+  if (tid == 0) {
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  count_units(p, pre);
+  const int total = pre[p.S];
+  const int a = lane >> 2, t = lane & 3;
+  uint32_t phases = 0;  // bit s: parity to wait for on slot s
+  // neighbouring units on different SMs
+  for (int u = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); u < total;
+       u += kDecWarps * static_cast<int>(gridDim.x)) {
+    const int s = upper_index(pre, p.S, u), local = u - pre[s];
+    const int g = local % p.n_kv, split = local / p.n_kv;
+    const int kvl = ld_s32(p.kv_len + s), row = ld_s32(p.q_start + s);
+    const int key_begin = split * kSplit, keys = min(kvl - key_begin, kSplit);
+    const int npages = (keys + 15) / 16;
+    // lane b has the id of the unit's page b (kSplit / 16 of them at most)
+    int id = 0;
+    if (lane < npages) {
+      id = ld_s32(p.block_table + static_cast<size_t>(s) * p.max_pages + key_begin / 16 + lane);
+      if (id < 0 || id >= p.num_pages) {
+        flag_error(p.status, kStatusIndex);
+        id = 0;
+      }
+    }
+    auto issue = [&](int b) {
+      const int slot = b % C::DR;
+      const int at = (__shfl_sync(0xffffffffu, id, b) * p.n_kv + g) * 16;
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::STAGE + 32);
+      __syncwarp();
+      // each byte is read once: first out of L2
+      if (lane < 2)
+        tma_load_2d_hint(ring + slot * C::STAGE + lane * C::PAGE, lane ? &tmV : &tmK, &full[slot], 0, at,
+                         policy_evict_first());
+      else if (lane < 4)
+        bulk_load(scales + slot * 32 + (lane - 2) * 16, (lane == 2 ? p.ks : p.vs) + at, 16, &full[slot]);
+    };
+    for (int b = 0; b < min(C::DR, npages); ++b) issue(b);
+
+    Heads<D, NT> w;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = 8 * n + a;
+      const __nv_bfloat16* q = p.q + (static_cast<size_t>(row) * p.n_q + g * p.grp + (h < p.grp ? h : 0)) * D + 4 * t;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t lo = 0, hi = 0;
+        if (h < p.grp) {
+          lo = static_cast<uint32_t>(ld_s32(reinterpret_cast<const int*>(q + 16 * c)));
+          hi = static_cast<uint32_t>(ld_s32(reinterpret_cast<const int*>(q + 16 * c) + 1));
+        }
+        w.q[n][c][0] = __byte_perm(lo, hi, 0x5410);
+        w.q[n][c][1] = __byte_perm(lo, hi, 0x7632);
+        w.o[n][c][0] = w.o[n][c][1] = w.o[n][c][2] = w.o[n][c][3] = 0.f;
+      }
+      w.m[n][0] = w.m[n][1] = -INFINITY;
+      w.l[n][0] = w.l[n][1] = 0.f;
+    }
+
+    bool ok = true;
+    for (int b = 0; b < npages; ++b) {
+      const int slot = b % C::DR;
+      const bool landed = mbar_wait(&full[slot], (phases >> slot) & 1u, nullptr, p.status);
+      phases ^= 1u << slot;
+      if (!__all_sync(0xffffffffu, landed)) {
+        ok = false;
+        break;
+      }
+      const uint32_t kp = smem_u32(ring + slot * C::STAGE);
+      page_step<D, NT>(kp, kp + C::PAGE, smem_u32(scales + slot * 32), w, keys - 16 * b, p.scale_log2, lane);
+      __syncwarp();
+      if (b + C::DR < npages) issue(b + C::DR);
+    }
+    if (!ok) {
+      // let this warp's copies in flight land (bounded) before it leaves
+      if (lane == 0)
+        for (int i = 0; i < C::DR; ++i) mbar_drain(&full[i], (phases >> i) & 1u);
+      break;
+    }
+
+    const bool whole = kvl <= kSplit;
+    float* rec = p.partials + (static_cast<size_t>(s) * p.max_splits + split) * p.n_kv * rec_floats(p.grp, D) +
+                 static_cast<size_t>(g) * rec_floats(p.grp, D);
+    __nv_bfloat16* out = p.out + (static_cast<size_t>(row) * p.n_q + g * p.grp) * D;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float l = w.l[n][h];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int head = 8 * n + 2 * t + h;
+        if (head >= p.grp) continue;
+        if (whole) {
+          const float inv = 1.f / l;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            *reinterpret_cast<uint32_t*>(out + head * D + 16 * c + 2 * a) =
+                pack_bf16x2(w.o[n][c][h] * inv, w.o[n][c][2 + h] * inv);
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            *reinterpret_cast<float2*>(rec + head * D + 16 * c + 2 * a) = make_float2(w.o[n][c][h], w.o[n][c][2 + h]);
+          if (a == 0) {
+            rec[p.grp * D + head] = w.m[n][h];
+            rec[p.grp * (D + 1) + head] = l;
+          }
+        }
+      }
+  }
+}
+
+// The splits of one decode row and q head (a CTA), in an order of their number
+// alone: warp w takes splits w, w + 8, ..., the warps' sums are added in order.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_splits_kernel(Params p) {
+  constexpr int E = D / 32;
+  __shared__ float sum[kJoinWarps][D];
+  __shared__ float norm[kJoinWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int s = blockIdx.x, h = blockIdx.y, g = h / p.grp, r = h % p.grp;
+  const int q0 = ld_s32(p.q_start + s), q1 = ld_s32(p.q_start + s + 1), kvl = ld_s32(p.kv_len + s);
+  // as count_units: others were not computed, or were whole
+  if (q0 < 0 || q1 > p.T || q1 - q0 != 1 || kvl <= kSplit || kvl > p.max_kv_len || (kvl + 15) / 16 > p.max_pages) return;
+  const int n = (kvl + kSplit - 1) / kSplit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t step = static_cast<size_t>(p.n_kv) * rec_floats(p.grp, D);
+  const float* rec = p.partials + static_cast<size_t>(s) * p.max_splits * step +
+                     static_cast<size_t>(g) * rec_floats(p.grp, D);
+  const float* ms = rec + p.grp * D + r;
+  const float* ls = ms + p.grp;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, ld_f32(ms + i * step));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float mu = m == -INFINITY ? 0.f : m;
+  float acc[E] = {}, l = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += kJoinWarps) {
+    const float wgt = ex2_approx(ld_f32(ms + i * step) - mu);
+    l += wgt * ld_f32(ls + i * step);
+    const float* o = rec + i * step + r * D + lane * E;
+    if (E == 4) {
+      const float4 v = ld_f4(o);
+      acc[0] += wgt * v.x, acc[1] += wgt * v.y, acc[2 % E] += wgt * v.z, acc[3 % E] += wgt * v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += wgt * ld_f32(o + e);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[warp][lane * E + e] = acc[e];
+  if (lane == 0) norm[warp] = l;
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    float x = 0.f, y = 0.f, z = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      x += sum[w][2 * threadIdx.x];
+      y += sum[w][2 * threadIdx.x + 1];
+      z += norm[w];
+    }
+    *reinterpret_cast<uint32_t*>(p.out + (static_cast<size_t>(q0) * p.n_q + h) * D + 2 * threadIdx.x) =
+        pack_bf16x2(x / z, y / z);
+  }
+}
+
+template <int D, int NT>
+hb_status decode_launch(const DeviceCtx& ctx, const CUtensorMap& tmK, const CUtensorMap& tmV, const Params& p, int grid,
+                        cudaStream_t stream) {
+  static std::atomic<bool> attr_set[kMaxDevices];
+  const hb_status st = smem_limit_once(attr_set, ctx.device, decode_e4m3_kernel<D, NT>, DC<D>::SMEM,
+                                       "cudaFuncSetAttribute(decode_e4m3)");
+  if (st != HB_OK) return st;
+  return launch_pdl(decode_e4m3_kernel<D, NT>, grid, kDecWarps * 32, DC<D>::SMEM, stream, "decode_e4m3_kernel launch",
+                    tmK, tmV, p);
+}
+
 size_t workspace_bytes(const hb_layer_dims& dm, int max_seqs, int max_kv_len) {
-  (void)dm, (void)max_seqs, (void)max_kv_len;
-  return 256;
+  const size_t splits = (static_cast<size_t>(max_kv_len) + kSplit - 1) / kSplit;
+  const size_t recs = splits > 1 ? static_cast<size_t>(max_seqs) * splits * dm.n_kv : 0;
+  return 256 + recs * rec_floats(dm.n_q / dm.n_kv, dm.d_head) * 4;
 }
 
 }  // namespace
@@ -158,7 +584,29 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   p.max_kv_len = max_kv_len;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(dims->d_head)));
   p.status = ctx.status;
-  return launch_pdl(dims->d_head == 128 ? attention_e4m3_kernel<128> : attention_e4m3_kernel<64>,
-                    dim3(plan->n_rows, (dims->n_q + 3) / 4), 128, 0, static_cast<cudaStream_t>(stream),
-                    "attention_e4m3_kernel launch", p);
+  p.partials = static_cast<float*>(workspace);
+  p.max_splits = (max_kv_len + kSplit - 1) / kSplit;
+  p.no_chunks = plan->n_rows == plan->n_seqs;
+  const uint64_t rows = static_cast<uint64_t>(num_pages) * dims->n_kv * 16;
+  HB_REQUIRE(rows <= INT32_MAX, "hb_attention_e4m3: num_pages * n_kv * 16 must be below 2^31");
+  CUtensorMap tmK, tmV;
+  st = encode_tmap_code_pages(&tmK, k_cache, rows, dims->d_head);
+  if (st != HB_OK) return st;
+  st = encode_tmap_code_pages(&tmV, v_cache, rows, dims->d_head);
+  if (st != HB_OK) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!p.no_chunks) {
+    st = launch_pdl(dims->d_head == 128 ? attention_e4m3_kernel<128> : attention_e4m3_kernel<64>,
+                    dim3(plan->n_rows, (dims->n_q + 3) / 4), 128, 0, s, "attention_e4m3_kernel launch", p);
+    if (st != HB_OK) return st;
+  }
+  if (dims->d_head == 128)
+    st = p.grp <= 8 ? decode_launch<128, 1>(ctx, tmK, tmV, p, ctx.num_sms, s)
+                    : decode_launch<128, 2>(ctx, tmK, tmV, p, ctx.num_sms, s);
+  else
+    st = p.grp <= 8 ? decode_launch<64, 1>(ctx, tmK, tmV, p, ctx.num_sms, s)
+                    : decode_launch<64, 2>(ctx, tmK, tmV, p, ctx.num_sms, s);
+  if (st != HB_OK || p.max_splits == 1) return st;
+  return launch_pdl(dims->d_head == 128 ? join_splits_kernel<128> : join_splits_kernel<64>, dim3(p.S, p.n_q),
+                    kJoinWarps * 32, 0, s, "join_splits_kernel launch", p);
 }

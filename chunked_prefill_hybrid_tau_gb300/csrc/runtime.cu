@@ -150,6 +150,24 @@ hb_status encode_tmap_kv_pages(CUtensorMap* map, const void* pool, uint64_t rows
   return HB_OK;
 }
 
+hb_status encode_tmap_code_pages(CUtensorMap* map, const void* pool, uint64_t rows, int d_head) {
+  hb_status st = resolve_encode();
+  if (st != HB_OK) return st;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(d_head), rows};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(d_head)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(d_head), 16};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult res = g_encode.load(std::memory_order_acquire)(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          d_head == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (res != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled (code pages) failed (%d)", static_cast<int>(res));
+    return HB_ERR_INVALID_ARG;
+  }
+  return HB_OK;
+}
+
 // Kernels launched by this library in this process (all devices and host
 // threads).
 static std::atomic<uint64_t> g_launches{0};

@@ -93,6 +93,10 @@ hb_status encode_tmap_q3d(CUtensorMap* map, const void* q, int T, int n_q, int d
 // [half][key][128 bytes] with the 128-byte swizzle, the layout of two
 // separate 64-dim boxes placed 2 KB apart.
 hb_status encode_tmap_kv_pages(CUtensorMap* map, const void* pool, uint64_t rows, int d_head);
+// 2-D map over a pool of E4M3 codes [page][n_kv][16][d_head] seen as rows of
+// d_head bytes: one box is a whole 16-key page of one kv head, rows of 128 (64)
+// bytes with the 128-byte (64-byte) swizzle.
+hb_status encode_tmap_code_pages(CUtensorMap* map, const void* pool, uint64_t rows, int d_head);
 hb_status chunk_tc_launch(const DeviceCtx& ctx, const void* q, const CUtensorMap& tmK, const CUtensorMap& tmV,
                           const hb_device_plan& plan, const hb_layer_dims& dims, int num_pages, int max_kv_len,
                           void* out, int* work_counter, int grid, cudaStream_t stream);
