@@ -19,99 +19,15 @@
 // taking bytes (0, 2) and (1, 3) of them as the pairs permutes the dims of S's
 // sum, which q's fragments follow, and gives O's rows 2 a and 2 a + 1 to one
 // lane.  2^ek multiplies the scores and 2^ev the weights, in fp32.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
-#include "device.cuh"
-#include "runtime.h"
+#include "attention_e4m3.cuh"
 
 namespace hb {
 namespace {
 
 using namespace dev;
+using namespace kv8;
 
-constexpr int kMaxSeqs = 1024;
 
-struct Params {
-  const __nv_bfloat16* q;
-  __nv_bfloat16* out;
-  const uint8_t *k, *ks, *v, *vs;
-  const int* q_start;
-  const int* kv_len;
-  const int* block_table;
-  int S, T, max_pages, num_pages, n_q, n_kv, grp, max_kv_len;
-  float scale_log2;
-  float* partials;  // split records [sequence][split][kv head]
-  int max_splits;   // of a sequence of max_kv_len keys
-  int no_chunks;    // the plan has as many rows as sequences: none may have several
-  int* status;
-};
-
-__device__ __forceinline__ float code_value(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(__half(h));
-}
-
-__device__ __forceinline__ float scale_value(uint8_t b) {
-  return __uint_as_float(b == 255 ? 0x7fc00000u : b == 0 ? 0x00400000u : static_cast<uint32_t>(b) << 23);
-}
-
-template <int D>
-__global__ void __launch_bounds__(128) attention_e4m3_kernel(Params p) {
-  constexpr int E = D / 32;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31, row = blockIdx.x;
-  const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (row == 0 && blockIdx.y == 0)
-    for (int i = threadIdx.x; i < p.S; i += blockDim.x)
-      if (ld_s32(p.q_start + i + 1) <= ld_s32(p.q_start + i)) flag_error(p.status, kStatusIndex);
-  if (h >= p.n_q) return;
-  int lo = 0, hi = p.S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (ld_s32(p.q_start + mid) <= row) lo = mid; else hi = mid - 1;
-  }
-  const int s = lo, q1 = ld_s32(p.q_start + s + 1), kvl = ld_s32(p.kv_len + s);
-  const int last = kvl - (q1 - row);
-  if (row >= ld_s32(p.q_start + s) && q1 - ld_s32(p.q_start + s) == 1) return;  // a decode row
-  if (row < ld_s32(p.q_start + s) || row >= q1 || last < 0 || kvl > p.max_kv_len || (kvl + 15) / 16 > p.max_pages) {
-    flag_error(p.status, kStatusIndex);
-    return;
-  }
-  const int g = h / p.grp;
-  const int* bt = p.block_table + static_cast<size_t>(s) * p.max_pages;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = __bfloat162float(p.q[(static_cast<size_t>(row) * p.n_q + h) * D + lane * E + i]);
-    o[i] = 0.f;
-  }
-  for (int j = 0; j <= last; ++j) {
-    int page = ld_s32(bt + j / 16);
-    if (page < 0 || page >= p.num_pages) {
-      flag_error(p.status, kStatusIndex);
-      page = 0;
-    }
-    const size_t at = (static_cast<size_t>(page) * p.n_kv + g) * 16 + j % 16;
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) x += q[i] * code_value(p.k[at * D + lane * E + i]);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-    x *= scale_value(p.ks[at]) * p.scale_log2;
-    const float mn = fmaxf(m, x);
-    const float alpha = exp2f(m - mn), e = exp2f(x - mn);
-    m = mn;
-    l = l * alpha + e;
-    const float w = e * scale_value(p.vs[at]);
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * alpha + w * code_value(p.v[at * D + lane * E + i]);
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i)
-    p.out[(static_cast<size_t>(row) * p.n_q + h) * D + lane * E + i] = __float2bfloat16(o[i] / l);
-}
 
 // ---------------------------------------------------------------- decode rows
 constexpr int kSplit = 256;     // keys of a unit
@@ -160,18 +76,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-// Two E4M3 codes as bf16, exactly: sign, and the exponent and mantissa fields
-// moved to bf16's places make the value times 2^-120 (the exponents' biases
-// differ by 120, and a subnormal code becomes a subnormal number), so one
-// product with 2^120 ends it.  even: bytes 0 and 2 of w, odd: bytes 1 and 3.
-__device__ __forceinline__ uint32_t times_2_120(uint32_t v) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7b807b80u));
-  return r;
-}
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) {
-  return times_2_120(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u));
-}
+// Two codes of w as bf16: bytes 1 and 3, bytes 0 and 2.
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return mul_bf16x2(codes_moved(w), 0x7b807b80u); }
 __device__ __forceinline__ uint32_t codes_even(uint32_t w) { return codes_odd(w << 8); }
 
 // 2^e of a scale byte of the format: 27 .. 247, or 255 (NaN)
@@ -342,8 +248,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  griddep_wait();
   griddep_launch_dependents();
+  if (!p.wait_at_end) griddep_wait();
   count_units(p, pre);
   const int total = pre[p.S];
   const int a = lane >> 2, t = lane & 3;
@@ -451,6 +357,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
         }
       }
   }
+  if (p.wait_at_end) griddep_wait();
 }
 
 // The splits of one decode row and q head (a CTA), in an order of their number
@@ -520,6 +427,42 @@ hb_status decode_launch(const DeviceCtx& ctx, const CUtensorMap& tmK, const CUte
                     tmK, tmV, p);
 }
 
+// SMs for the chunk kernel when both kinds of rows run side by side on
+// disjoint SMs (each kernel's CTAs fill an SM's shared memory), from the plan's
+// hints; 0: one after the other on all SMs.  It only moves work: no row's
+// result depends on it.
+//   chunk : units of two 128-row tiles of a kv head, kUnitUs and kBlockUs per
+//           128 keys each, taken in order: about W / n + half a unit on n SMs,
+//           and at least the largest unit;
+//   decode: bytes at min(kDecodeBw, n kDecodeBwPerSm).
+constexpr double kUnitUs = 6.0;
+constexpr double kBlockUs = 2.0;             // d_head 128
+constexpr double kDecodeBwPerSm = 50000.0;   // bytes per us
+constexpr double kDecodeBw = 6.0e6;
+
+int chunk_sms(const DeviceCtx& ctx, const hb_device_plan& plan, const hb_layer_dims& dm) {
+  const int S = ctx.num_sms;
+  if (plan.chunk_pairs <= 0 || plan.decode_pairs <= 0 || plan.chunk_rows <= 0 || S < 4) return 0;
+  const double dscale = dm.d_head / 128.0;
+  const double tiles = ceil(static_cast<double>(plan.chunk_rows) / 128.0);
+  const double units = ceil(tiles * dm.n_q / 2.0);
+  const double blocks = static_cast<double>(plan.chunk_pairs) / 16384.0 + plan.chunk_rows / 128.0;
+  const double t_unit = kUnitUs + blocks / tiles * kBlockUs * (0.5 + 0.5 * dscale);
+  const double bytes = 2.0 * static_cast<double>(plan.decode_pairs) * dm.n_kv * (dm.d_head + 1);
+  auto t_chunk = [&](int n) { return units <= n ? t_unit : units * t_unit / n + 0.5 * t_unit; };
+  auto t_decode = [&](int n) { return bytes / (n * kDecodeBwPerSm < kDecodeBw ? n * kDecodeBwPerSm : kDecodeBw); };
+  int best = 0;
+  double t_best = t_chunk(S) + t_decode(S);
+  for (int n = 1; n < S; ++n) {
+    const double t = t_chunk(n) > t_decode(S - n) ? t_chunk(n) : t_decode(S - n);
+    if (t < t_best) {
+      t_best = t;
+      best = n;
+    }
+  }
+  return best;
+}
+
 size_t workspace_bytes(const hb_layer_dims& dm, int max_seqs, int max_kv_len) {
   const size_t splits = (static_cast<size_t>(max_kv_len) + kSplit - 1) / kSplit;
   const size_t recs = splits > 1 ? static_cast<size_t>(max_seqs) * splits * dm.n_kv : 0;
@@ -587,6 +530,8 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   p.partials = static_cast<float*>(workspace);
   p.max_splits = (max_kv_len + kSplit - 1) / kSplit;
   p.no_chunks = plan->n_rows == plan->n_seqs;
+  p.no_decodes = plan->n_seqs == 1 && plan->n_rows > 1;
+  p.wait_at_end = 0;
   const uint64_t rows = static_cast<uint64_t>(num_pages) * dims->n_kv * 16;
   HB_REQUIRE(rows <= INT32_MAX, "hb_attention_e4m3: num_pages * n_kv * 16 must be below 2^31");
   CUtensorMap tmK, tmV;
@@ -595,17 +540,20 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   st = encode_tmap_code_pages(&tmV, v_cache, rows, dims->d_head);
   if (st != HB_OK) return st;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int sms = ctx.num_sms;  // of the decode kernel
   if (!p.no_chunks) {
-    st = launch_pdl(dims->d_head == 128 ? attention_e4m3_kernel<128> : attention_e4m3_kernel<64>,
-                    dim3(plan->n_rows, (dims->n_q + 3) / 4), 128, 0, s, "attention_e4m3_kernel launch", p);
-    if (st != HB_OK) return st;
+    const int nc = p.no_decodes ? 0 : chunk_sms(ctx, *plan, *dims);
+    st = chunk_e4m3_launch(ctx, q, k_cache, v_cache, p, dims->d_head, nc > 0 ? nc : ctx.num_sms, s);
+    if (st != HB_OK || p.no_decodes) return st;
+    sms -= nc;
+    p.wait_at_end = 1;
   }
   if (dims->d_head == 128)
-    st = p.grp <= 8 ? decode_launch<128, 1>(ctx, tmK, tmV, p, ctx.num_sms, s)
-                    : decode_launch<128, 2>(ctx, tmK, tmV, p, ctx.num_sms, s);
+    st = p.grp <= 8 ? decode_launch<128, 1>(ctx, tmK, tmV, p, sms, s)
+                    : decode_launch<128, 2>(ctx, tmK, tmV, p, sms, s);
   else
-    st = p.grp <= 8 ? decode_launch<64, 1>(ctx, tmK, tmV, p, ctx.num_sms, s)
-                    : decode_launch<64, 2>(ctx, tmK, tmV, p, ctx.num_sms, s);
+    st = p.grp <= 8 ? decode_launch<64, 1>(ctx, tmK, tmV, p, sms, s)
+                    : decode_launch<64, 2>(ctx, tmK, tmV, p, sms, s);
   if (st != HB_OK || p.max_splits == 1) return st;
   return launch_pdl(dims->d_head == 128 ? join_splits_kernel<128> : join_splits_kernel<64>, dim3(p.S, p.n_q),
                     kJoinWarps * 32, 0, s, "join_splits_kernel launch", p);

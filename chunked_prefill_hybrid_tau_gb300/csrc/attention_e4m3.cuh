@@ -1,0 +1,53 @@
+// Pieces shared by the attention kernels over an E4M3 cache (attention_e4m3.cu:
+// decode rows; attention_e4m3_chunk.cu: prompt chunks).
+#pragma once
+#include <cuda_bf16.h>
+
+#include "device.cuh"
+#include "runtime.h"
+
+namespace hb {
+namespace kv8 {
+
+constexpr int kMaxSeqs = 1024;
+
+struct Params {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  const uint8_t *k, *ks, *v, *vs;
+  const int* q_start;
+  const int* kv_len;
+  const int* block_table;
+  int S, T, max_pages, num_pages, n_q, n_kv, grp, max_kv_len;
+  float scale_log2;
+  float* partials;  // split records [sequence][split][kv head]
+  int max_splits;   // of a sequence of max_kv_len keys
+  int no_chunks;    // the plan has as many rows as sequences: none may have several
+  int no_decodes;   // the plan has one sequence of several rows
+  // 1 when the chunk kernel precedes the decode kernel on the stream: it waited
+  // for the inputs before it let this one start, so the decode kernel's wait is
+  // deferred to its end (whose completion then implies the chunk kernel's)
+  int wait_at_end;
+  int* status;
+};
+
+// E4M3 to bf16, exactly, two codes at a time, a code in the upper byte of each
+// half: sign, and the exponent and mantissa fields moved to bf16's places make
+// the value times 2^-120 (the exponents' biases differ by 120, and a subnormal
+// code becomes a subnormal number); a product with 2^120 ends it.
+__device__ __forceinline__ uint32_t codes_moved(uint32_t w) {
+  return ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+}  // namespace kv8
+
+// Sequences of several rows; `grid` CTAs.
+hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const void* k_cache, const void* v_cache,
+                            const kv8::Params& p, int d_head, int grid, cudaStream_t stream);
+
+}  // namespace hb
