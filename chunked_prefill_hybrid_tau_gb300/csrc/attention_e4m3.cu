@@ -463,10 +463,29 @@ int chunk_sms(const DeviceCtx& ctx, const hb_device_plan& plan, const hb_layer_d
   return best;
 }
 
-size_t workspace_bytes(const hb_layer_dims& dm, int max_seqs, int max_kv_len) {
+// Keys of several-row sequences that are widened once, ahead of the chunk
+// kernel: all that the sizes allow, but no more than this and at least one
+// sequence (256 MB with 8 kv heads of 128).
+constexpr long long kScratchKeys = 65536;
+
+long long chunk_keys(int rows, int seqs, int max_kv_len) {
+  const long long n = seqs < rows / 2 ? seqs : rows / 2;
+  return n * ((max_kv_len + 127ll) / 128 * 128);
+}
+long long scratch_keys(int rows, int seqs, int max_kv_len) {
+  const long long all = chunk_keys(rows, seqs, max_kv_len), one = (max_kv_len + 127ll) / 128 * 128;
+  const long long most = one > kScratchKeys ? one : kScratchKeys;
+  return all < most ? all : most;
+}
+
+size_t partial_bytes(const hb_layer_dims& dm, int seqs, int max_kv_len) {
   const size_t splits = (static_cast<size_t>(max_kv_len) + kSplit - 1) / kSplit;
-  const size_t recs = splits > 1 ? static_cast<size_t>(max_seqs) * splits * dm.n_kv : 0;
-  return 256 + recs * rec_floats(dm.n_q / dm.n_kv, dm.d_head) * 4;
+  const size_t recs = splits > 1 ? static_cast<size_t>(seqs) * splits * dm.n_kv : 0;
+  return (recs * rec_floats(dm.n_q / dm.n_kv, dm.d_head) * 4 + 255) / 256 * 256;
+}
+size_t workspace_bytes(const hb_layer_dims& dm, int rows, int seqs, int max_kv_len) {
+  const size_t scratch = static_cast<size_t>(scratch_keys(rows, seqs, max_kv_len)) * dm.n_kv * dm.d_head * 2;
+  return 256 + partial_bytes(dm, seqs, max_kv_len) + 2 * scratch;
 }
 
 }  // namespace
@@ -474,9 +493,8 @@ size_t workspace_bytes(const hb_layer_dims& dm, int max_seqs, int max_kv_len) {
 
 extern "C" size_t hb_attention_e4m3_workspace_bytes(const hb_layer_dims* dims, int32_t max_rows, int32_t max_seqs,
                                                     int32_t max_kv_len) {
-  (void)max_rows;
-  if (!dims || max_seqs < 0 || max_kv_len < 0) return 0;
-  return hb::workspace_bytes(*dims, max_seqs, max_kv_len);
+  if (!dims || max_rows < 0 || max_seqs < 0 || max_kv_len < 0 || dims->n_kv < 1) return 0;
+  return hb::workspace_bytes(*dims, max_rows, max_seqs, max_kv_len);
 }
 
 extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const void* k_scale, const void* v_cache,
@@ -490,7 +508,8 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   HB_REQUIRE(plan != nullptr, "hb_attention_e4m3: null plan");
   HB_REQUIRE(plan->n_seqs >= 0 && plan->n_rows >= 0 && plan->max_pages >= 1, "hb_attention_e4m3: bad plan sizes");
   HB_REQUIRE(plan->n_seqs <= kMaxSeqs, "hb_attention_e4m3: at most %d sequences per iteration", kMaxSeqs);
-  HB_REQUIRE(max_kv_len >= 1 && num_pages > 0, "hb_attention_e4m3: max_kv_len and num_pages must be positive");
+  HB_REQUIRE(max_kv_len >= 1 && max_kv_len <= (1 << 28) && num_pages > 0,
+             "hb_attention_e4m3: max_kv_len (at most 2^28) and num_pages must be positive");
   if (plan->n_seqs == 0 || plan->n_rows == 0) return HB_OK;
   HB_REQUIRE(q && k_cache && k_scale && v_cache && v_scale && out, "hb_attention_e4m3: null pointer");
   HB_REQUIRE(plan->seq_q_start && plan->seq_kv_len && plan->block_table, "hb_attention_e4m3: null plan array");
@@ -499,7 +518,8 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   HB_REQUIRE(aligned16(q) && aligned16(out) && aligned16(k_cache) && aligned16(v_cache) && aligned16(k_scale) &&
                  aligned16(v_scale),
              "hb_attention_e4m3: 16-byte alignment");
-  const size_t need = workspace_bytes(*dims, plan->n_seqs, max_kv_len);
+  const bool no_chunks = plan->n_rows == plan->n_seqs;
+  const size_t need = workspace_bytes(*dims, no_chunks ? 0 : plan->n_rows, plan->n_seqs, max_kv_len);
   HB_REQUIRE(workspace != nullptr && ws_bytes >= need, "hb_attention_e4m3: workspace of %zu bytes needed, %zu given",
              need, ws_bytes);
   HB_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
@@ -528,12 +548,18 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   p.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(dims->d_head)));
   p.status = ctx.status;
   p.partials = static_cast<float*>(workspace);
+  p.scratch_keys = no_chunks ? 0 : static_cast<int>(scratch_keys(plan->n_rows, plan->n_seqs, max_kv_len));
+  p.scratch_k = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) +
+                                                 partial_bytes(*dims, plan->n_seqs, max_kv_len));
+  p.scratch_v = p.scratch_k + static_cast<size_t>(p.scratch_keys) * dims->n_kv * dims->d_head;
   p.max_splits = (max_kv_len + kSplit - 1) / kSplit;
-  p.no_chunks = plan->n_rows == plan->n_seqs;
+  p.no_chunks = no_chunks;
   p.no_decodes = plan->n_seqs == 1 && plan->n_rows > 1;
   p.wait_at_end = 0;
   const uint64_t rows = static_cast<uint64_t>(num_pages) * dims->n_kv * 16;
   HB_REQUIRE(rows <= INT32_MAX, "hb_attention_e4m3: num_pages * n_kv * 16 must be below 2^31");
+  HB_REQUIRE(static_cast<int64_t>(p.scratch_keys) * dims->n_kv <= INT32_MAX,
+             "hb_attention_e4m3: max_kv_len * n_kv must be below 2^31");
   CUtensorMap tmK, tmV;
   st = encode_tmap_code_pages(&tmK, k_cache, rows, dims->d_head);
   if (st != HB_OK) return st;
@@ -543,7 +569,8 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   int sms = ctx.num_sms;  // of the decode kernel
   if (!p.no_chunks) {
     const int nc = p.no_decodes ? 0 : chunk_sms(ctx, *plan, *dims);
-    st = chunk_e4m3_launch(ctx, q, k_cache, v_cache, p, dims->d_head, nc > 0 ? nc : ctx.num_sms, s);
+    st = chunk_e4m3_launch(ctx, q, p, dims->d_head, chunk_keys(p.T, p.S, max_kv_len) > p.scratch_keys,
+                           nc > 0 ? nc : ctx.num_sms, s);
     if (st != HB_OK || p.no_decodes) return st;
     sms -= nc;
     p.wait_at_end = 1;

@@ -20,6 +20,8 @@ struct Params {
   const int* block_table;
   int S, T, max_pages, num_pages, n_q, n_kv, grp, max_kv_len;
   float scale_log2;
+  __nv_bfloat16 *scratch_k, *scratch_v;  // widened sequences of several rows, [padded keys][d_head] a kv head
+  int scratch_keys;                      // that it holds
   float* partials;  // split records [sequence][split][kv head]
   int max_splits;   // of a sequence of max_kv_len keys
   int no_chunks;    // the plan has as many rows as sequences: none may have several
@@ -46,8 +48,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 
 }  // namespace kv8
 
-// Sequences of several rows; `grid` CTAs.
-hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const void* k_cache, const void* v_cache,
-                            const kv8::Params& p, int d_head, int grid, cudaStream_t stream);
+// Sequences of several rows: widened into the scratch, then attended by `grid`
+// CTAs; overflow: some may lie behind the scratch's end.
+hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const kv8::Params& p, int d_head, bool overflow,
+                            int grid, cudaStream_t stream);
 
 }  // namespace hb

@@ -7,19 +7,19 @@
 // K = 2^ek codes and V = 2^ev codes widened to bf16, which is exact (powers of
 // two), so the products are those of hb_attention with such a cache in bf16.
 //
+// Every 128 rows and q head go over the same K and V again, so the codes are
+// widened once, by a kernel ahead (widen_kernel), into scratch of the workspace
+// laid out for whole-block copies.  That scratch is bounded (kScratchKeys);
+// sequences behind its end are widened block by block beside the MMAs instead
+// (WIDEN: the same kernel with eight more warps), which takes 2.4 times as long.
+//
 // Unit: two 128-row tiles of one kv head -- (row tile, q head) pairs in that
 // order, so with an even number of q heads per kv head two heads of the same
-// rows -- and keys 0 .. last in blocks of 128.  Both tiles use every widened
-// block, which halves the widening a tile pays for; codes are half the bytes
-// that bf16 pages would bring in.
+// rows -- and keys 0 .. last in blocks of 128 that both tiles use.
 //
-// Warp roles (448 threads, one CTA per SM):
+// Warp roles (one CTA per SM):
 //   warp 0      finds the unit (its lanes scan the sequences), publishes it in
-//               shared memory, loads both Q tiles and, 64 keys a slot, the
-//               block's K and V codes with their scale bytes into a ring;
-//   warps 10-13 widen: a warp takes one 16-key page of a slot, 16 codes a lane
-//               at a time, into the 128-byte swizzled K or V block; keys behind
-//               the unit's last become zeros;
+//               shared memory, loads both Q tiles and the K and V blocks;
 //   warp 1      MMA issuer (one thread): S_x = Q_x K_j^T (M = N = 128) into
 //               tile x's tensor-memory columns, O_x += P_x V_j with P_x read
 //               from the same columns (bf16, written over S_x), whichever has
@@ -28,9 +28,16 @@
 //               for the maximum and once more for the exponentials, 32 columns
 //               at a time; O is rescaled only where a row's maximum grew by
 //               more than 2^8; at the end O / l to global memory.
-// A value whose scale is NaN must reach the rows that see its key and no other:
-// 0 * NaN would spread it, so the widening puts the NaN into the key's K row
-// (S is masked by selection) and zeros into V.
+// WIDEN: warp 0 loads K codes, 64 keys a slot, into a ring, warp 18 does so with
+// V's; scale bytes, 16 a page, go through their registers a block ahead (a copy
+// costs the issuing warp some 150 clocks).  Warps 10-17 widen: a warp takes one
+// 16-key page of every second slot, 16 codes a lane at a time, into the 128-byte
+// swizzled K or V block.
+//
+// Keys behind a sequence's last become zeros.  A value whose scale is NaN must
+// reach the rows that see its key and no other: 0 * NaN would spread it, so the
+// widening puts the NaN into the key's K row (S is masked by selection) and
+// zeros into V.
 // Every wait is bounded; an expired wait sets the status word and unwinds.
 #include "attention_e4m3.cuh"
 #include "attention_tc.cuh"
@@ -48,9 +55,9 @@ using tc::tmem_st_wait;
 
 constexpr int TQ = 128, TK = 128;
 constexpr int HK = 64;  // keys of a ring slot
-constexpr int kStages = 2;
-constexpr int kSoft0 = 2, kConv0 = 10, kConvWarps = 4;
-constexpr int kThreads = 32 * (kConv0 + kConvWarps);
+constexpr int kSoft0 = 2, kConv0 = 10, kConvWarps = 8, kVWarp = 18;
+template <bool WIDEN>
+constexpr int kThreads = 32 * (WIDEN ? kVWarp + 1 : kConv0);
 constexpr float kRescale = 8.0f;
 
 struct Tile {
@@ -58,22 +65,24 @@ struct Tile {
 };
 struct Unit {
   int valid, seq, g, nblk;
+  int row;  // of the scratch: key 0 of this sequence and kv head
   Tile t[2];
 };
 
-template <int D>
+template <int D, bool WIDEN>
 struct TC {
   static constexpr int HALVES = D / 64;
   static constexpr int HALF_TILE = 128 * 128;        // 128 rows x 128 bytes (64 dims)
   static constexpr int TILE = HALVES * HALF_TILE;    // a Q tile, a K or V block
-  static constexpr int SLOTS = D == 128 ? 4 : 8;
+  static constexpr int KST = WIDEN ? 2 : 3, VST = 2;      // blocks in flight
+  static constexpr int SLOTS = WIDEN ? (D == 128 ? 2 : 4) : 0;  // of the K and of the V code ring
   static constexpr int SLOT = HK * D;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 2 * TILE;
-  static constexpr int OFF_V = OFF_K + kStages * TILE;
-  static constexpr int OFF_C = OFF_V + kStages * TILE;
-  static constexpr int OFF_S = OFF_C + SLOTS * SLOT;  // scales: K's (or V's) 64 bytes, V's 64 bytes beside K
-  static constexpr int OFF_U = OFF_S + SLOTS * 2 * HK;
+  static constexpr int OFF_V = OFF_K + KST * TILE;
+  static constexpr int OFF_C = OFF_V + VST * TILE;
+  static constexpr int OFF_S = OFF_C + 2 * SLOTS * SLOT;  // scales: K's (or V's) 64 bytes, V's 64 bytes beside K
+  static constexpr int OFF_U = OFF_S + 2 * SLOTS * 2 * HK;
   static constexpr int OFF_BAR = OFF_U + 2 * 64;
   static constexpr int SMEM = OFF_BAR + 400 + 1024;
   static_assert(sizeof(Unit) <= 64 && SMEM <= 232448, "shared memory");
@@ -91,6 +100,61 @@ __device__ __forceinline__ Factor factor_of(uint32_t b) {
   return {f * 0x10001u, s * 0x10001u};
 }
 
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u8(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void sts_u4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 16 codes as bf16 in their order, times 2^120 * factor.  The fields are moved
+// by two multiply-adds where shifts and masks would do it in three (codes_moved):
+// with x = two codes in the lower byte of each half, x * 16 has exponent and
+// mantissa in place and the sign at bit 11, and sign * (256 - 16) takes that to
+// bit 15.  The widening shares its SM with the softmax, and the multiplier is
+// the less busy pipe.
+__device__ __forceinline__ uint32_t codes_moved_low(uint32_t x) { return (x & 0x00800080u) * 240u + x * 16u; }
+__device__ __forceinline__ void widen16(const uint4& raw, uint32_t factor, uint32_t (&o)[8]) {
+  const uint32_t word[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o[2 * e] = mul_bf16x2(codes_moved_low(__byte_perm(word[e], 0, 0x4140)), factor);
+    o[2 * e + 1] = mul_bf16x2(codes_moved_low(__byte_perm(word[e], 0, 0x4342)), factor);
+  }
+}
+
+// tcgen05.wait::ld that the loaded registers depend on
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // The tile that is the i-th of its kv head, heaviest rows first.
 __device__ __forceinline__ Tile tile_of(const Params& p, int i, int ntiles, int g, int q0, int qlen, int kvl) {
   Tile t = {0, 0, 0, 0};
@@ -104,11 +168,135 @@ __device__ __forceinline__ Tile tile_of(const Params& p, int i, int ntiles, int 
   return t;
 }
 
+// keys of a sequence in the scratch: whole blocks
+__device__ __forceinline__ int padded(int kvl) { return (kvl + TK - 1) / TK * TK; }
+
+// Which several-row sequence an item falls into, sequence by sequence in order,
+// by a whole warp; items ascend from call to call.  count(qlen, kvl, base): items
+// of a sequence whose scratch starts at key `base`.  Sequences out of range are
+// reported and have no items (and no scratch).
+struct SeqScan {
+  int s0 = 0, items = 0, keys = 0;  // of the sequences ahead of s0
+  int seq, q0, qlen, kvl;           // the one found
+  template <typename Count>
+  __device__ __forceinline__ bool find(const Params& p, int v, int lane, Count count, int* local, int* base) {
+    while (s0 < p.S) {
+      const int s = s0 + lane;
+      int c = 0, k = 0, a = 0, ql = 0, kl = 0;
+      if (s < p.S) {
+        a = ld_s32(p.q_start + s);
+        const int q1 = ld_s32(p.q_start + s + 1);
+        ql = q1 - a;
+        kl = ld_s32(p.kv_len + s);
+        if (a < 0 || q1 > p.T || ql < 1 || kl < ql || kl > p.max_kv_len || (kl + 15) / 16 > p.max_pages ||
+            (p.no_decodes && ql < 2))
+          flag_error(p.status, kStatusIndex);
+        else if (ql > 1)
+          k = padded(kl);
+      }
+      int kend = k;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, kend, o);
+        if (lane >= o) kend = min(kend + u, 1 << 29);  // (far behind any scratch: no overflow)
+      }
+      kend = min(kend + keys, 1 << 29);
+      if (k > 0) c = count(ql, kl, kend - k);
+      int end = c;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int u = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += u;
+      }
+      end += items;
+      const unsigned at = __ballot_sync(0xffffffffu, v < end);
+      if (at != 0) {
+        const int l = __ffs(static_cast<int>(at)) - 1;
+        seq = s0 + l;
+        *local = v - __shfl_sync(0xffffffffu, end - c, l);
+        *base = __shfl_sync(0xffffffffu, kend - k, l);
+        q0 = __shfl_sync(0xffffffffu, a, l);
+        qlen = __shfl_sync(0xffffffffu, ql, l);
+        kvl = __shfl_sync(0xffffffffu, kl, l);
+        return true;
+      }
+      items = __shfl_sync(0xffffffffu, end, 31);
+      keys = __shfl_sync(0xffffffffu, kend, 31);
+      s0 += 32;
+    }
+    return false;
+  }
+};
+
+// The codes of several-row sequences as bf16, key after key of each kv head, to
+// whole 128-key blocks; a warp takes one page of one kv head.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(256) widen_kernel(Params p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  constexpr int PIECES = D / 16, KEYS = 32 / PIECES, STEPS = 16 / KEYS;
+  const int lane = threadIdx.x & 31, c = lane % PIECES;
+  SeqScan scan;
+  // neighbouring items on different SMs
+  for (int v = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;; v += 8 * gridDim.x) {
+    int local, base;
+    if (!scan.find(p, v, lane, [&](int, int kvl, int at) {
+          return at + padded(kvl) <= p.scratch_keys ? padded(kvl) / 16 * p.n_kv : 0;
+        }, &local, &base))
+      return;
+    const int g = local % p.n_kv, pg = local / p.n_kv, live = scan.kvl - pg * 16;
+    uint4 k[STEPS], w[STEPS];
+    uint32_t kb[STEPS], vb[STEPS];
+    size_t at = 0;
+    if (live > 0) {
+      int id = ld_s32(p.block_table + static_cast<size_t>(scan.seq) * p.max_pages + pg);
+      if (id < 0 || id >= p.num_pages) {
+        flag_error(p.status, kStatusIndex);
+        id = 0;
+      }
+      at = (static_cast<size_t>(id) * p.n_kv + g) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int r = i * KEYS + lane / PIECES;
+      k[i] = w[i] = make_uint4(0, 0, 0, 0);
+      kb[i] = vb[i] = 127;
+      if (r < live) {
+        k[i] = ld_u4(p.k + (at + r) * D + c * 16);
+        w[i] = ld_u4(p.v + (at + r) * D + c * 16);
+        kb[i] = ld_u8(p.ks + at + r);
+        vb[i] = ld_u8(p.vs + at + r);
+      }
+    }
+    const size_t row = static_cast<size_t>(base) * p.n_kv + static_cast<size_t>(g) * padded(scan.kvl) + pg * 16;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const size_t to = (row + i * KEYS + lane / PIECES) * D + c * 16;
+      const Factor fk = factor_of(vb[i] == 255 ? 255 : kb[i]);
+      Factor fv = factor_of(vb[i]);
+      if (vb[i] == 255) fv = {0u, 0x3f803f80u};
+      uint32_t o[8];
+      widen16(k[i], fk.first, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], fk.second);
+      uint4* dst = reinterpret_cast<uint4*>(p.scratch_k + to);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      widen16(w[i], fv.first, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], fv.second);
+      dst = reinterpret_cast<uint4*>(p.scratch_v + to);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+template <int D, bool WIDEN>
+__global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     chunk_e4m3_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, Params p) {
-  using C = TC<D>;
+  using C = TC<D, WIDEN>;
   // the decode kernel behind this one starts beside it once its inputs are there
   griddep_wait();
   griddep_launch_dependents();
@@ -121,21 +309,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sS = smem + C::OFF_S;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* u_full = bar;            // [2] unit published
-  uint64_t* u_empty = bar + 2;       // [2] MMA warp, softmax warps, widening warps have read it
+  uint64_t* u_empty = bar + 2;       // [2] V's producer, the MMA, softmax and widening warps have read it
   uint64_t* q_full = bar + 4;
   uint64_t* q_empty = bar + 5;
-  uint64_t* c_full = bar + 6;        // [SLOTS] codes and scales landed
-  uint64_t* c_empty = bar + 14;      // [SLOTS] widening warps
-  uint64_t* k_full = bar + 22;       // [2] widening warps
-  uint64_t* k_empty = bar + 24;      // [2]
-  uint64_t* v_full = bar + 26;
-  uint64_t* v_empty = bar + 28;
-  uint64_t* s_full = bar + 30;       // [2] by tile
-  uint64_t* p_full = bar + 32;       // [2] four softmax warps
-  uint64_t* pv_done = bar + 34;      // [2]
-  uint64_t* o_empty = bar + 36;      // [2] four softmax warps
-  uint64_t* drain = bar + 38;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 39);
+  uint64_t* c_full = bar + 6;        // [2 SLOTS] codes landed, scales stored: K's ring, then V's
+  uint64_t* c_empty = bar + 14;      // [2 SLOTS] widening warps
+  uint64_t* k_full = bar + 22;       // [KST] block landed, or widening warps
+  uint64_t* k_empty = bar + 25;      // [KST]
+  uint64_t* v_full = bar + 28;       // [VST]
+  uint64_t* v_empty = bar + 30;
+  uint64_t* s_full = bar + 32;       // [2] by tile
+  uint64_t* p_full = bar + 34;       // [2] four softmax warps
+  uint64_t* pv_done = bar + 36;      // [2]
+  uint64_t* o_empty = bar + 38;      // [2] four softmax warps
+  uint64_t* drain = bar + 40;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 41);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Unit* units = reinterpret_cast<Unit*>(smem + C::OFF_U);  // [2], 64 bytes apart
 
@@ -143,19 +331,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&u_full[i], 1);
-      mbar_init(&u_empty[i], 1 + 8 + kConvWarps);
-      mbar_init(&k_full[i], kConvWarps);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], kConvWarps);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&u_empty[i], 1 + 8 + (WIDEN ? kConvWarps + 1 : 0));
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_empty[i], 4);
     }
-    for (int i = 0; i < C::SLOTS; ++i) {
+    for (int i = 0; i < C::KST; ++i) {
+      mbar_init(&k_full[i], WIDEN ? kConvWarps : 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::VST; ++i) {
+      mbar_init(&v_full[i], WIDEN ? kConvWarps : 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2 * C::SLOTS; ++i) {
       mbar_init(&c_full[i], 1);
-      mbar_init(&c_empty[i], kConvWarps);
+      mbar_init(&c_empty[i], kConvWarps / 2);
     }
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -182,60 +374,115 @@ __global__ void __launch_bounds__(kThreads, 1)
     return w.valid != 0;
   };
 
+  // the K or V codes of a unit's blocks into their ring, by a whole warp
+  constexpr int kSlots = WIDEN ? C::SLOTS : 1;
+  int half = 0;  // 64-key halves loaded so far
+  auto load_codes = [&](const Unit& w, bool is_v) {
+    const int* bt = p.block_table + static_cast<size_t>(w.seq) * p.max_pages;
+    const int npages = (w.t[0].pos0 + w.t[0].nrows + 15) / 16;
+    uint64_t* full = c_full + (is_v ? C::SLOTS : 0);
+    uint64_t* empty = c_empty + (is_v ? C::SLOTS : 0);
+    uint8_t* codes = sC + (is_v ? C::SLOTS * C::SLOT : 0);
+    uint8_t* scales = sS + (is_v ? C::SLOTS * 2 * HK : 0);
+    // lane l < 8 has row, of 16 in the pool, of page l of a block: the id loaded
+    // three blocks ahead, the scales one ahead
+    auto load_id = [&](int j) { return lane < 8 && j * 8 + lane < npages ? ld_s32(bt + j * 8 + lane) : 0; };
+    auto row_of = [&](int id) {
+      if (id < 0 || id >= p.num_pages) {
+        flag_error(p.status, kStatusIndex);
+        id = 0;
+      }
+      return (id * p.n_kv + w.g) * 16;
+    };
+    auto load_scale = [&](const uint8_t* base, int j, int row) {
+      return lane < 8 && j * 8 + lane < npages ? ld_u4(base + row) : make_uint4(0, 0, 0, 0);
+    };
+    int row = row_of(load_id(0)), id1 = load_id(1), id2 = load_id(2);
+    uint4 s0 = load_scale(is_v ? p.vs : p.ks, 0, row), s1 = make_uint4(0, 0, 0, 0);
+    if (!is_v) s1 = load_scale(p.vs, 0, row);
+    for (int j = 0; j < w.nblk; ++j) {
+      const int row1 = row_of(id1), id3 = load_id(j + 3);
+      const uint4 n0 = load_scale(is_v ? p.vs : p.ks, j + 1, row1);
+      const uint4 n1 = is_v ? n0 : load_scale(p.vs, j + 1, row1);
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i, ++half) {
+        const int slot = half % kSlots;
+        const bool free = mbar_wait(&empty[slot], ((half / kSlots) & 1) ^ 1u, abort_flag, p.status);
+        if (!__all_sync(0xffffffffu, free)) return false;
+        const int here = max(0, min(4, npages - j * 8 - i * 4)), l4 = lane & 3;
+        const bool mine = lane < 8 && (lane >> 2) == i && l4 < here;
+        if (mine) {
+          *reinterpret_cast<uint4*>(scales + slot * 2 * HK + l4 * 16) = s0;
+          if (!is_v) *reinterpret_cast<uint4*>(scales + slot * 2 * HK + HK + l4 * 16) = s1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], here * 16 * D);
+        __syncwarp();
+        if (mine) tma_load_2d(codes + slot * C::SLOT + l4 * 16 * D, is_v ? &tmV : &tmK, &full[slot], 0, row);
+      }
+      row = row1;
+      id1 = id2;
+      id2 = id3;
+      s0 = n0;
+      s1 = n1;
+    }
+    return true;
+  };
+  // the widened K and V blocks of a unit, by one thread
+  int blocks = 0;  // loaded so far: V's, and K's or one less
+  auto load_blocks = [&](const Unit& w) {
+    for (int j = 0; j < w.nblk; ++j, ++blocks) {
+      const int ks = blocks % C::KST, vs = blocks % C::VST, row = w.row + j * TK;
+      if (!mbar_wait(&k_empty[ks], ((blocks / C::KST) & 1) ^ 1u, abort_flag, p.status)) return false;
+      mbar_arrive_expect_tx(&k_full[ks], C::TILE);
+#pragma unroll
+      for (int hf = 0; hf < C::HALVES; ++hf)
+        tma_load_2d(sK + ks * C::TILE + hf * C::HALF_TILE, &tmK, &k_full[ks], hf * 64, row);
+      if (!mbar_wait(&v_empty[vs], ((blocks / C::VST) & 1) ^ 1u, abort_flag, p.status)) return false;
+      mbar_arrive_expect_tx(&v_full[vs], C::TILE);
+#pragma unroll
+      for (int hf = 0; hf < C::HALVES; ++hf)
+        tma_load_2d(sV + vs * C::TILE + hf * C::HALF_TILE, &tmV, &v_full[vs], hf * 64, row);
+    }
+    return true;
+  };
+  // after a wait that expired: this warp's copies in flight land (bounded) before it leaves
+  auto drain_slots = [&](bool ok) {
+    if (ok || lane != 0) return;
+    if (!WIDEN) {
+      for (int b = max(0, blocks - C::KST + 1); b <= blocks; ++b) mbar_drain(&k_full[b % C::KST], (b / C::KST) & 1);
+      for (int b = max(0, blocks - C::VST); b < blocks; ++b) mbar_drain(&v_full[b % C::VST], (b / C::VST) & 1);
+      return;
+    }
+    uint64_t* full = c_full + (warp == kVWarp ? kSlots : 0);
+    for (int h = max(0, half - kSlots); h < half; ++h) mbar_drain(&full[h % kSlots], (h / kSlots) & 1);
+  };
+
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
+    // ------------------------------------------------------------ producers
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
     }
-    int s0 = 0, before = 0;  // units of the sequences ahead of s0
-    int slot = 0;
-    uint32_t cph = 0, pending = 0, armed = 0;
+    SeqScan scan;
     bool ok = true;
     for (int n = 0, v = blockIdx.x; ok; ++n, v += gridDim.x) {
-      // the sequence that unit v falls into, 32 at a time
+      // the sequence that unit v falls into
       Unit w;
-      w.valid = 0;
-      while (s0 < p.S && !w.valid) {
-        const int s = s0 + lane;
-        int count = 0, q0 = 0, qlen = 0, kvl = 0;
-        if (s < p.S) {
-          q0 = ld_s32(p.q_start + s);
-          const int q1 = ld_s32(p.q_start + s + 1);
-          qlen = q1 - q0;
-          kvl = ld_s32(p.kv_len + s);
-          if (q0 < 0 || q1 > p.T || qlen < 1 || kvl < qlen || kvl > p.max_kv_len || (kvl + 15) / 16 > p.max_pages ||
-              (p.no_decodes && qlen < 2))
-            flag_error(p.status, kStatusIndex);
-          else if (qlen > 1)
-            count = p.n_kv * (((qlen + TQ - 1) / TQ * p.grp + 1) / 2);
-        }
-        int upto = count;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const int u = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += u;
-        }
-        upto += before;
-        const unsigned mine = __ballot_sync(0xffffffffu, v < upto);
-        if (mine == 0) {
-          before = __shfl_sync(0xffffffffu, upto, 31);
-          s0 += 32;
-          continue;
-        }
-        const int at = __ffs(static_cast<int>(mine)) - 1;
-        const int local = v - __shfl_sync(0xffffffffu, upto - count, at);
-        q0 = __shfl_sync(0xffffffffu, q0, at);
-        qlen = __shfl_sync(0xffffffffu, qlen, at);
-        kvl = __shfl_sync(0xffffffffu, kvl, at);
-        const int ntiles = (qlen + TQ - 1) / TQ;
-        w.valid = 1;
-        w.seq = s0 + at;
+      int local, base;
+      w.valid = scan.find(p, v, lane, [&](int qlen, int kvl, int at) {
+        const bool fits = at + padded(kvl) <= p.scratch_keys;
+        return fits != WIDEN ? p.n_kv * (((qlen + TQ - 1) / TQ * p.grp + 1) / 2) : 0;
+      }, &local, &base);
+      if (w.valid) {
+        const int ntiles = (scan.qlen + TQ - 1) / TQ;
+        w.seq = scan.seq;
         w.g = local % p.n_kv;
+        w.row = base * p.n_kv + w.g * padded(scan.kvl);
         const int i = local / p.n_kv * 2;
-        w.t[0] = tile_of(p, i, ntiles, w.g, q0, qlen, kvl);
-        w.t[1] = tile_of(p, i + 1, ntiles, w.g, q0, qlen, kvl);
+        w.t[0] = tile_of(p, i, ntiles, w.g, scan.q0, scan.qlen, scan.kvl);
+        w.t[1] = tile_of(p, i + 1, ntiles, w.g, scan.q0, scan.qlen, scan.kvl);
         // the second tile's rows are the same or earlier ones
         w.nblk = (w.t[0].pos0 + w.t[0].nrows + TK - 1) / TK;
       }
@@ -263,55 +510,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = false;
         break;
       }
-      const int* bt = p.block_table + static_cast<size_t>(w.seq) * p.max_pages;
-      const int key_end = w.t[0].pos0 + w.t[0].nrows;
-      const int npages = (key_end + 15) / 16;
-      // lane l < 8 has the id of page l of a block, loaded two blocks ahead
-      auto load_page = [&](int j) { return lane < 8 && j * 8 + lane < npages ? ld_s32(bt + j * 8 + lane) : 0; };
-      int pf0 = load_page(0), pf1 = load_page(1);
-      for (int j = 0; j < w.nblk && ok; ++j) {
-        int cur = pf0;
-        pf0 = pf1;
-        pf1 = load_page(j + 2);
-        if (cur < 0 || cur >= p.num_pages) {
-          flag_error(p.status, kStatusIndex);
-          cur = 0;
-        }
-#pragma unroll 1
-        for (int i = 0; i < 4 && ok; ++i) {  // K keys 0..63, 64..127, V the same
-          const bool is_v = i >= 2;
-          const int pg = (i & 1) * 4;
-          const int here = max(0, min(4, npages - j * 8 - pg));
-          if (lane == 0) {
-            ok = mbar_wait(&c_empty[slot], cph ^ 1u, abort_flag, p.status);
-            if (ok) {
-              pending |= 1u << slot;
-              armed = (armed & ~(1u << slot)) | (cph << slot);
-              mbar_arrive_expect_tx(&c_full[slot], here * (16 * D + (is_v ? 16 : 32)));
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          // lanes 0..3 a page of codes each, 4..7 its scales, 8..11 V's beside K's
-          const int l4 = lane & 3;
-          const int at = (__shfl_sync(0xffffffffu, cur, pg + l4) * p.n_kv + w.g) * 16;
-          if (ok && lane < 12 && l4 < here) {
-            if (lane < 4)
-              tma_load_2d(sC + slot * C::SLOT + l4 * 16 * D, is_v ? &tmV : &tmK, &c_full[slot], 0, at);
-            else if (lane < 8)
-              bulk_load(sS + slot * 2 * HK + l4 * 16, (is_v ? p.vs : p.ks) + at, 16, &c_full[slot]);
-            else if (!is_v)
-              bulk_load(sS + slot * 2 * HK + HK + l4 * 16, p.vs + at, 16, &c_full[slot]);
-          }
-          if (++slot == C::SLOTS) {
-            slot = 0;
-            cph ^= 1u;
-          }
-        }
+      if (WIDEN) {
+        ok = load_codes(w, false);
+      } else {
+        if (lane == 0) ok = load_blocks(w);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
     }
-    if (!ok && lane == 0)
-      for (int s = 0; s < C::SLOTS; ++s)
-        if (pending & (1u << s)) mbar_drain(&c_full[s], (armed >> s) & 1u);
+    drain_slots(ok);
+  } else if (WIDEN && warp == kVWarp) {
+    bool ok = true;
+    Unit w;
+    for (int n = 0; ok && next_unit(n, w); ++n) ok = load_codes(w, true);
+    drain_slots(ok);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     const bool leader = lane == 0;
@@ -335,9 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (jp[x] < js[x]) {
-              const int gv = J + jp[x], st = gv % kStages, use = nS[x] + jp[x];
+              const int gv = J + jp[x], st = gv % C::VST, use = nS[x] + jp[x];
               if (!o_free[x]) o_free[x] = mbar_test(&o_empty[x], (nU[x] & 1) ^ 1u);
-              if (o_free[x] && mbar_test(&p_full[x], use & 1) && mbar_test(&v_full[st], (gv / kStages) & 1)) {
+              if (o_free[x] && mbar_test(&p_full[x], use & 1) && mbar_test(&v_full[st], (gv / C::VST) & 1)) {
                 tc_fence_after();
                 const uint32_t v_addr = smem_u32(sV + st * C::TILE);
 #pragma unroll
@@ -353,8 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // S_x is written over P_x: its PV has to be complete
             if (js[x] < w.nblk && js[x] == jp[x]) {
-              const int gk = J + js[x], st = gk % kStages, use = nS[x] + js[x];
-              if (mbar_test(&pv_done[x], (use & 1) ^ 1u) && mbar_test(&k_full[st], (gk / kStages) & 1)) {
+              const int gk = J + js[x], st = gk % C::KST, use = nS[x] + js[x];
+              if (mbar_test(&pv_done[x], (use & 1) ^ 1u) && mbar_test(&k_full[st], (gk / C::KST) & 1)) {
                 tc_fence_after();
                 const uint32_t q_addr = smem_u32(sQ + x * C::TILE), k_addr = smem_u32(sK + st * C::TILE);
 #pragma unroll
@@ -396,88 +607,87 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(drain);
       mbar_drain(drain, 0);
     }
-  } else if (warp >= kConv0) {
+  } else if (WIDEN && warp >= kConv0) {
     // ------------------------------------------------------------ widening
-    const int cw = warp - kConv0;  // page of a slot
-    constexpr int PIECES = D / 16;  // 16-code pieces of a key
-    const int c = lane % PIECES;
-    int slot = 0, J = 0;
-    uint32_t cph = 0;
+    const int hf = (warp - kConv0) >> 2;  // 64-key half of a block
+    const int pg = (warp - kConv0) & 3;   // page of the half
+    constexpr int PIECES = D / 16;             // 16-code pieces of a key
+    constexpr int STEPS = 16 * PIECES / 32;    // pieces of a lane
+    constexpr int KEYS = 32 / PIECES;          // keys of a warp's step
+    const int c = lane % PIECES, key0 = pg * 16 + lane / PIECES;  // this lane's first key of the half
+    // 16 dims are two 16-byte chunks of the key's row in their 64-dim half.
+    // Lanes of the upper half store theirs in the other order: the eight lanes
+    // that a store takes at a time then meet eight different bank groups.
+    const int flip = c >> 2;
+    const uint32_t col = (c >> 2) * C::HALF_TILE;
+    const int j0 = 2 * (c & 3) + flip, j1 = 2 * (c & 3) + (flip ^ 1);
+    int J = 0;
     bool ok = true;
     Unit w;
     for (int n = 0; ok && next_unit(n, w); ++n) {
       const int key_end = w.t[0].pos0 + w.t[0].nrows;
-      for (int j = 0; j < w.nblk && ok; ++j) {
-        const int st = (J + j) % kStages, use = (J + j) / kStages;
+      for (int j = 0; j < w.nblk && ok; ++j, ++J) {
+        const int st = J % 2, use = J / 2;
 #pragma unroll 1
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          uint8_t* dst = (kv ? sV : sK) + st * C::TILE;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int at = J * 2 + hf, slot = at % kSlots + kv * kSlots;
+          bool landed = mbar_wait(&c_full[slot], (at / kSlots) & 1, abort_flag, p.status);
+          if (!__all_sync(0xffffffffu, landed)) {
+            ok = false;
+            break;
+          }
+          const uint32_t codes = smem_u32(sC + slot * C::SLOT) + key0 * D + c * 16;
+          const uint32_t scales = smem_u32(sS + slot * 2 * HK) + key0;
+          uint4 raw[STEPS];
+          uint32_t sb[STEPS];
+          bool plain = j * TK + (hf + 1) * HK <= key_end;
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) {
+            raw[i] = lds_u4(codes + i * KEYS * D);
+            sb[i] = lds_u8(scales + i * KEYS);
+            // a value's NaN goes into its key
+            if (kv == 0 && lds_u8(scales + HK + i * KEYS) == 255) sb[i] = 255;
+            plain &= sb[i] <= 134;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c_empty[slot]);
           bool free = mbar_wait(kv ? &v_empty[st] : &k_empty[st], (use & 1) ^ 1u, abort_flag, p.status);
           if (!__all_sync(0xffffffffu, free)) {
             ok = false;
             break;
           }
-#pragma unroll 1
-          for (int hf = 0; hf < 2; ++hf) {
-            bool landed = mbar_wait(&c_full[slot], cph, abort_flag, p.status);
-            if (!__all_sync(0xffffffffu, landed)) {
-              ok = false;
-              break;
-            }
-            const uint8_t* codes = sC + slot * C::SLOT + cw * 16 * D;
-            const uint8_t* scales = sS + slot * 2 * HK + cw * 16;
-            constexpr int STEPS = 16 * PIECES / 32;  // 16-code pieces of a lane
-            uint4 raw[STEPS];
-            uint32_t sb[STEPS];
+          const uint32_t dst = smem_u32((kv ? sV : sK) + st * C::TILE) + col;
+          auto put = [&](int i, const uint32_t (&o)[8]) {
+            const int r = hf * HK + key0 + i * KEYS;  // key of the block
+            const uint32_t row = dst + r * 128;
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            sts_u4(row + ((j0 ^ (r & 7)) << 4), flip ? hi : lo);
+            sts_u4(row + ((j1 ^ (r & 7)) << 4), flip ? lo : hi);
+          };
+          if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) {
-              const int r = i * (32 / PIECES) + lane / PIECES;
-              raw[i] = *reinterpret_cast<const uint4*>(codes + r * D + c * 16);
-              sb[i] = scales[r];
-              // a NaN value goes into its key
-              if (kv == 0 && scales[HK + r] == 255) sb[i] = 255;
-              if (kv == 1 && sb[i] == 255) sb[i] = 256;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c_empty[slot]);
-#pragma unroll
-            for (int i = 0; i < STEPS; ++i) {
-              const int r = hf * HK + cw * 16 + i * (32 / PIECES) + lane / PIECES;  // key of the block
-              Factor f = factor_of(sb[i]);
-              if (j * TK + r >= key_end || sb[i] == 256) f.first = 0, f.second = 0x3f803f80u;
-              const uint32_t word[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
               uint32_t o[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[2 * e] = mul_bf16x2(kv8::codes_moved(__byte_perm(word[e], 0, 0x1404)), f.first);
-                o[2 * e + 1] = mul_bf16x2(kv8::codes_moved(__byte_perm(word[e], 0, 0x3424)), f.first);
-              }
-              if (__any_sync(0xffffffffu, f.second != 0x3f803f80u)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f.second);
-              }
-              // 16 dims: two 16-byte chunks of row r in their 64-dim half.  Lanes of
-              // the upper half store theirs in the other order: the eight lanes of
-              // a key then meet eight different banks
-              const int flip = c >> 2;
-              uint8_t* row = dst + (c >> 2) * C::HALF_TILE + r * 128;
-              const int j0 = 2 * (c & 3);
-              const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-              *reinterpret_cast<uint4*>(row + (((j0 + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
-              *reinterpret_cast<uint4*>(row + (((j0 + (flip ^ 1)) ^ (r & 7)) << 4)) = flip ? lo : hi;
+              widen16(raw[i], ((sb[i] + 120) << 7) * 0x10001u, o);
+              put(i, o);
             }
-            if (++slot == C::SLOTS) {
-              slot = 0;
-              cph ^= 1u;
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < STEPS; ++i) {
+              Factor f = factor_of(sb[i]);
+              if (j * TK + hf * HK + key0 + i * KEYS >= key_end || (kv == 1 && sb[i] == 255)) f = {0u, 0x3f803f80u};
+              uint32_t o[8];
+              widen16(raw[i], f.first, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = mul_bf16x2(o[e], f.second);
+              put(i, o);
             }
           }
-          if (!ok) break;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(kv ? &v_full[st] : &k_full[st]);
         }
       }
-      J += w.nblk;
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
@@ -502,21 +712,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const int seen = lim - j * TK;  // columns 0 .. seen of the block
-        float mx = -INFINITY;
+        const bool full = __all_sync(0xffffffffu, seen >= TK - 1);
+        // 32 columns at a time, the next ones on their way
+        uint32_t sv[2][32];
+        float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tmem_ld_32x32b_x32(tS, sv[0]);
 #pragma unroll
-        for (int c = 0; c < TK; c += 64) {
-          uint32_t sv[64];
-          tmem_ld_32x32b_x32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-          tmem_ld_32x32b_x32(tS + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-          tmem_ld_wait();
-          if (seen >= c + 63) {
+        for (int c = 0; c < TK / 32; ++c) {
+          uint32_t(&v)[32] = sv[c & 1];
+          tmem_ld_wait32(v);
+          // behind the last come the first ones again, for the exponentials
+          tmem_ld_32x32b_x32(tS + (c + 1) % (TK / 32) * 32, sv[(c + 1) & 1]);
+          if (!full) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) mx = fmaxf(mx, __uint_as_float(sv[e]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 64; ++e) mx = fmaxf(mx, c + e <= seen ? __uint_as_float(sv[e]) : -INFINITY);
+            for (int e = 0; e < 32; ++e) v[e] = c * 32 + e <= seen ? v[e] : 0xff800000u;
           }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mp[(e / 2) & 3] = fmaxf(mp[(e / 2) & 3], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
         }
+        float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
         mx *= p.scale_log2;
         const bool raise = mx > m_used + kRescale;
         const float m_new = raise ? mx : m_used;
@@ -527,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < D; c += 32) {
             uint32_t ov[32];
             tmem_ld_32x32b_x32(tO + c, ov);
-            tmem_ld_wait();
+            tmem_ld_wait32(ov);
 #pragma unroll
             for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
             tmem_st_32x32b_x32(tO + c, ov);
@@ -536,28 +751,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_used = m_new;
         l *= alpha;
         const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-        float rs = 0.f;
+        float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < TK; c += 64) {
-          uint32_t sv[64], pk[32];
-          tmem_ld_32x32b_x32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-          tmem_ld_32x32b_x32(tS + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-          tmem_ld_wait();
-          if (seen < c + 63) {
+        for (int c = 0; c < TK / 32; ++c) {
+          uint32_t(&v)[32] = sv[c & 1];
+          tmem_ld_wait32(v);
+          if (c + 1 < TK / 32) tmem_ld_32x32b_x32(tS + (c + 1) * 32, sv[(c + 1) & 1]);
+          if (!full) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) sv[e] = c + e <= seen ? sv[e] : 0xff800000u;
+            for (int e = 0; e < 32; ++e) v[e] = c * 32 + e <= seen ? v[e] : 0xff800000u;
           }
+          uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float a0 = ex2_approx(fmaf(__uint_as_float(sv[2 * e]), p.scale_log2, neg_m));
-            const float a1 = ex2_approx(fmaf(__uint_as_float(sv[2 * e + 1]), p.scale_log2, neg_m));
-            rs += a0 + a1;
+          for (int e = 0; e < 16; ++e) {
+            const float a0 = ex2_approx(fmaf(__uint_as_float(v[2 * e]), p.scale_log2, neg_m));
+            const float a1 = ex2_approx(fmaf(__uint_as_float(v[2 * e + 1]), p.scale_log2, neg_m));
+            rs[e & 3] += a0 + a1;
             pk[e] = pack_bf16x2(a0, a1);
           }
           // over columns of S that are in registers already
-          tmem_st_32x32b_x32(tS + c / 2, pk);
+          tmem_st_32x32b_x16(tS + c * 16, pk);
         }
-        l += rs;
+        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -573,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < D; c += 32) {
         uint32_t ov[32];
         tmem_ld_32x32b_x32(tO + c, ov);
-        tmem_ld_wait();
+        tmem_ld_wait32(ov);
         if (r < t.nrows) {
           uint4* dst = reinterpret_cast<uint4*>(orow + c);
 #pragma unroll
@@ -600,32 +815,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
+template <int D, bool WIDEN>
 hb_status launch_chunk(const DeviceCtx& ctx, const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
                        const Params& p, int grid, cudaStream_t stream) {
   static std::atomic<bool> attr_set[kMaxDevices];
-  const hb_status st =
-      smem_limit_once(attr_set, ctx.device, chunk_e4m3_kernel<D>, TC<D>::SMEM, "cudaFuncSetAttribute(chunk_e4m3)");
+  const hb_status st = smem_limit_once(attr_set, ctx.device, chunk_e4m3_kernel<D, WIDEN>, TC<D, WIDEN>::SMEM,
+                                       "cudaFuncSetAttribute(chunk_e4m3)");
   if (st != HB_OK) return st;
-  return launch_pdl(chunk_e4m3_kernel<D>, grid, kThreads, TC<D>::SMEM, stream, "chunk_e4m3_kernel launch", tmQ, tmK, tmV,
-                    p);
+  return launch_pdl(chunk_e4m3_kernel<D, WIDEN>, grid, kThreads<WIDEN>, TC<D, WIDEN>::SMEM, stream,
+                    "chunk_e4m3_kernel launch", tmQ, tmK, tmV, p);
+}
+
+template <int D>
+hb_status launch_all(const DeviceCtx& ctx, const void* q, const Params& p, bool overflow, int grid,
+                     cudaStream_t stream) {
+  CUtensorMap tmQ, tmK, tmV;
+  hb_status st = encode_tmap_q3d(&tmQ, q, p.T, p.n_q, D);
+  if (st != HB_OK) return st;
+  const uint64_t rows = static_cast<uint64_t>(p.scratch_keys) * p.n_kv;
+  st = encode_tmap_2d(&tmK, p.scratch_k, D, rows, D * 2, 64, TK, true);
+  if (st != HB_OK) return st;
+  st = encode_tmap_2d(&tmV, p.scratch_v, D, rows, D * 2, 64, TK, true);
+  if (st != HB_OK) return st;
+  st = launch_pdl(widen_kernel<D>, ctx.num_sms * 2, 256, 0, stream, "widen_kernel launch", p);
+  if (st != HB_OK) return st;
+  st = launch_chunk<D, false>(ctx, tmQ, tmK, tmV, p, grid, stream);
+  if (st != HB_OK || !overflow) return st;
+  // whole pages of codes, unswizzled: 16 rows of D bytes
+  const uint64_t pool = static_cast<uint64_t>(p.num_pages) * p.n_kv * 16;
+  st = encode_tmap_2d(&tmK, p.k, D, pool, D, D, 16, false, 1);
+  if (st != HB_OK) return st;
+  st = encode_tmap_2d(&tmV, p.v, D, pool, D, D, 16, false, 1);
+  if (st != HB_OK) return st;
+  return launch_chunk<D, true>(ctx, tmQ, tmK, tmV, p, grid, stream);
 }
 
 }  // namespace
 
-hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const void* k_cache, const void* v_cache,
-                            const kv8::Params& p, int d_head, int grid, cudaStream_t stream) {
-  CUtensorMap tmQ, tmK, tmV;
-  const uint64_t rows = static_cast<uint64_t>(p.num_pages) * p.n_kv * 16;
-  hb_status st = encode_tmap_q3d(&tmQ, q, p.T, p.n_q, d_head);
-  if (st != HB_OK) return st;
-  // whole pages of codes, unswizzled: 16 rows of d_head bytes
-  st = encode_tmap_2d(&tmK, k_cache, d_head, rows, d_head, d_head, 16, false, 1);
-  if (st != HB_OK) return st;
-  st = encode_tmap_2d(&tmV, v_cache, d_head, rows, d_head, d_head, 16, false, 1);
-  if (st != HB_OK) return st;
-  return d_head == 128 ? launch_chunk<128>(ctx, tmQ, tmK, tmV, p, grid, stream)
-                       : launch_chunk<64>(ctx, tmQ, tmK, tmV, p, grid, stream);
+hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const Params& p, int d_head, bool overflow, int grid,
+                            cudaStream_t stream) {
+  return d_head == 128 ? launch_all<128>(ctx, q, p, overflow, grid, stream)
+                       : launch_all<64>(ctx, q, p, overflow, grid, stream);
 }
 
 }  // namespace hb
