@@ -463,10 +463,10 @@ int chunk_sms(const DeviceCtx& ctx, const hb_device_plan& plan, const hb_layer_d
   return best;
 }
 
-// Keys of several-row sequences that are widened once, ahead of the chunk
-// kernel: all that the sizes allow, but no more than this and at least one
-// sequence (256 MB with 8 kv heads of 128).
-constexpr long long kScratchKeys = 65536;
+// Keys of several-row sequences that are widened ahead of the chunk kernel:
+// what the sizes allow to come, but no more than this, and at least one
+// sequence (537 MB with 8 kv heads of 128).
+constexpr long long kScratchKeys = 131072;
 
 long long chunk_keys(int rows, int seqs, int max_kv_len) {
   const long long n = seqs < rows / 2 ? seqs : rows / 2;
@@ -569,18 +569,22 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   int sms = ctx.num_sms;  // of the decode kernel
   if (!p.no_chunks) {
     const int nc = p.no_decodes ? 0 : chunk_sms(ctx, *plan, *dims);
-    st = chunk_e4m3_launch(ctx, q, p, dims->d_head, chunk_keys(p.T, p.S, max_kv_len) > p.scratch_keys,
-                           nc > 0 ? nc : ctx.num_sms, s);
-    if (st != HB_OK || p.no_decodes) return st;
+    st = chunk_e4m3_launch(ctx, q, p, dims->d_head, nc > 0 ? nc : ctx.num_sms, s);
+    if (st != HB_OK) return st;
     sms -= nc;
     p.wait_at_end = 1;
   }
-  if (dims->d_head == 128)
-    st = p.grp <= 8 ? decode_launch<128, 1>(ctx, tmK, tmV, p, sms, s)
-                    : decode_launch<128, 2>(ctx, tmK, tmV, p, sms, s);
+  if (p.no_decodes)
+    st = HB_OK;
+  else if (dims->d_head == 128)
+    st = p.grp <= 8 ? decode_launch<128, 1>(ctx, tmK, tmV, p, sms, s) : decode_launch<128, 2>(ctx, tmK, tmV, p, sms, s);
   else
-    st = p.grp <= 8 ? decode_launch<64, 1>(ctx, tmK, tmV, p, sms, s)
-                    : decode_launch<64, 2>(ctx, tmK, tmV, p, sms, s);
+    st = p.grp <= 8 ? decode_launch<64, 1>(ctx, tmK, tmV, p, sms, s) : decode_launch<64, 2>(ctx, tmK, tmV, p, sms, s);
+  // behind the decode kernel, which runs beside the first: most calls that may
+  // have such sequences have none
+  if (st == HB_OK && !p.no_chunks && chunk_keys(p.T, p.S, max_kv_len) > p.scratch_keys)
+    st = chunk_e4m3_overflow_launch(ctx, q, p, dims->d_head, s);
+  if (p.no_decodes) return st;
   if (st != HB_OK || p.max_splits == 1) return st;
   return launch_pdl(dims->d_head == 128 ? join_splits_kernel<128> : join_splits_kernel<64>, dim3(p.S, p.n_q),
                     kJoinWarps * 32, 0, s, "join_splits_kernel launch", p);

@@ -48,9 +48,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 
 }  // namespace kv8
 
-// Sequences of several rows: widened into the scratch, then attended by `grid`
-// CTAs; overflow: some may lie behind the scratch's end.
-hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const kv8::Params& p, int d_head, bool overflow,
-                            int grid, cudaStream_t stream);
+// Sequences of several rows: those that the scratch holds, widened into it and
+// attended by `grid` CTAs; and those behind its end.
+hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const kv8::Params& p, int d_head, int grid,
+                            cudaStream_t stream);
+hb_status chunk_e4m3_overflow_launch(const DeviceCtx& ctx, const void* q, const kv8::Params& p, int d_head,
+                                     cudaStream_t stream);
 
 }  // namespace hb

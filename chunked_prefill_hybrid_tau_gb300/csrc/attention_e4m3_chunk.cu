@@ -20,19 +20,19 @@
 // Warp roles (one CTA per SM):
 //   warp 0      finds the unit (its lanes scan the sequences), publishes it in
 //               shared memory, loads both Q tiles and the K and V blocks;
-//   warp 1      MMA issuer (one thread): S_x = Q_x K_j^T (M = N = 128) into
-//               tile x's tensor-memory columns, O_x += P_x V_j with P_x read
-//               from the same columns (bf16, written over S_x), whichever has
-//               its inputs; while one tile's softmax runs, the other's MMAs do;
-//   warps 2-5, 6-9  softmax of tile 0 and 1: a thread has one row, reads S once
-//               for the maximum and once more for the exponentials, 32 columns
-//               at a time; O is rescaled only where a row's maximum grew by
-//               more than 2^8; at the end O / l to global memory.
-// WIDEN: warp 0 loads K codes, 64 keys a slot, into a ring, warp 18 does so with
+//   warps 1, 10 MMA issuers of tile 0 and 1: S = Q K_j^T (M = N = 128) into the
+//               tile's tensor-memory columns, O += P V_j with P read from the same
+//               columns (bf16, written over S).  One warp a tile, because a wait
+//               costs the issuer some 100 clocks even where it ends at once, and
+//               the tensor pipe runs dry meanwhile unless another warp issues;
+//   warps 2-5, 6-9  softmax of tile 0 and 1: a thread has one row and takes its
+//               128 scores into registers; O is rescaled only where a row's
+//               maximum grew by more than 2^8; at the end O / l to global memory.
+// WIDEN: warp 0 loads K codes, 64 keys a slot, into a ring, warp 15 does so with
 // V's; scale bytes, 16 a page, go through their registers a block ahead (a copy
-// costs the issuing warp some 150 clocks).  Warps 10-17 widen: a warp takes one
-// 16-key page of every second slot, 16 codes a lane at a time, into the 128-byte
-// swizzled K or V block.
+// costs the issuing warp some 150 clocks).  Warps 11-14 widen: a warp takes one
+// 16-key page of a slot, 16 codes a lane at a time, into the 128-byte swizzled K
+// or V block.
 //
 // Keys behind a sequence's last become zeros.  A value whose scale is NaN must
 // reach the rows that see its key and no other: 0 * NaN would spread it, so the
@@ -50,12 +50,11 @@ using kv8::mul_bf16x2;
 using kv8::Params;
 using tc::mma_bf16_ts;
 using tc::smem_desc_sw128_mn;
-using tc::tmem_st_32x32b_x32;
 using tc::tmem_st_wait;
 
 constexpr int TQ = 128, TK = 128;
 constexpr int HK = 64;  // keys of a ring slot
-constexpr int kSoft0 = 2, kConv0 = 10, kConvWarps = 8, kVWarp = 18;
+constexpr int kSoft0 = 2, kMma1 = 10, kConv0 = 11, kConvWarps = 4, kVWarp = 15;
 template <bool WIDEN>
 constexpr int kThreads = 32 * (WIDEN ? kVWarp + 1 : kConv0);
 constexpr float kRescale = 8.0f;
@@ -142,6 +141,14 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
                  "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
                  "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }
@@ -318,40 +325,41 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
   uint64_t* k_empty = bar + 25;      // [KST]
   uint64_t* v_full = bar + 28;       // [VST]
   uint64_t* v_empty = bar + 30;
-  uint64_t* s_full = bar + 32;       // [2] by tile
-  uint64_t* p_full = bar + 34;       // [2] four softmax warps
-  uint64_t* pv_done = bar + 36;      // [2]
-  uint64_t* o_empty = bar + 38;      // [2] four softmax warps
-  uint64_t* drain = bar + 40;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 41);
+  uint64_t* s_full = bar + 32;       // [tile]
+  uint64_t* p_full = bar + 34;       // [tile] four softmax warps
+  uint64_t* pv_done = bar + 36;      // [tile]
+  uint64_t* o_empty = bar + 38;      // [tile] four softmax warps
+  uint64_t* drain = bar + 40;        // [tile]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 42);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Unit* units = reinterpret_cast<Unit*>(smem + C::OFF_U);  // [2], 64 bytes apart
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&u_full[i], 1);
-      mbar_init(&u_empty[i], 1 + 8 + (WIDEN ? kConvWarps + 1 : 0));
+      mbar_init(&u_empty[i], 2 + 8 + (WIDEN ? kConvWarps + 1 : 0));
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
       mbar_init(&o_empty[i], 4);
+      mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < C::KST; ++i) {
       mbar_init(&k_full[i], WIDEN ? kConvWarps : 1);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], 2);  // both tiles (where there is one, its issuer twice)
     }
     for (int i = 0; i < C::VST; ++i) {
       mbar_init(&v_full[i], WIDEN ? kConvWarps : 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 2);
     }
     for (int i = 0; i < 2 * C::SLOTS; ++i) {
       mbar_init(&c_full[i], 1);
-      mbar_init(&c_empty[i], kConvWarps / 2);
+      mbar_init(&c_empty[i], kConvWarps);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(drain, 1);
+    mbar_init(q_empty, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -523,94 +531,84 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     Unit w;
     for (int n = 0; ok && next_unit(n, w); ++n) ok = load_codes(w, true);
     drain_slots(ok);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    const bool leader = lane == 0;
+  } else if (warp == 1 || warp == kMma1) {
+    // ------------------------------------------------------------ MMA issuers
+    // The whole warp walks the loop and one elected lane issues: in a single-lane
+    // branch every descriptor would be moved to a uniform register anew.
+    const int x = warp == kMma1 ? 1 : 0;  // tile
     constexpr uint32_t idS = idesc_bf16_f32(TQ, TK);
     constexpr uint32_t idPV = idesc_bf16_f32(TQ, D) | (1u << 16);  // B (V) is MN-major
-    int J = 0;                // blocks of the units before
-    int nS[2] = {0, 0};       // S and PV blocks of each tile in the units before
-    int nU[2] = {0, 0};       // units of each tile
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ + x * C::TILE)), k_desc = smem_desc_sw128(smem_u32(sK));
+    const uint64_t v_desc = smem_desc_sw128_mn(smem_u32(sV), C::HALF_TILE, 1024);
+    const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
+    int J = 0;        // blocks of the units before
+    int u = 0;        // blocks of this tile so far
+    int mine = 0;     // units of this tile
     bool ok = true;
     Unit w;
-    for (int n = 0; ok && next_unit(n, w); ++n) {
-      if (leader) {
-        const int tiles = w.t[1].nrows ? 2 : 1;
-        ok = mbar_wait(q_full, n & 1, abort_flag, p.status);
-        int js[2] = {0, 0}, jp[2] = {0, 0};
-        if (tiles == 1) js[1] = jp[1] = w.nblk;
-        bool o_free[2] = {false, false};
-        uint64_t t0 = globaltimer();
-        while (ok && (jp[0] < w.nblk || jp[1] < w.nblk)) {
-          bool progressed = false;
+    auto wait = [&](uint64_t* bar, int parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_at(smem_u32(bar), parity, abort_flag, p.status));
+    };
+    for (int n = 0; ok && next_unit(n, w); ++n, J += w.nblk) {
+      const bool alone = w.t[1].nrows == 0;
+      if (x == 1 && alone) continue;
+      // S is written over the last P: its PV has to be complete
+      auto score = [&](int j) {
+        const int st = (J + j) % C::KST;
+        wait(&k_full[st], ((J + j) / C::KST) & 1);
+        wait(&pv_done[x], (u & 1) ^ 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t kd = k_desc + ((st * C::TILE) >> 4);
+        if (elect_one()) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (jp[x] < js[x]) {
-              const int gv = J + jp[x], st = gv % C::VST, use = nS[x] + jp[x];
-              if (!o_free[x]) o_free[x] = mbar_test(&o_empty[x], (nU[x] & 1) ^ 1u);
-              if (o_free[x] && mbar_test(&p_full[x], use & 1) && mbar_test(&v_full[st], (gv / C::VST) & 1)) {
-                tc_fence_after();
-                const uint32_t v_addr = smem_u32(sV + st * C::TILE);
-#pragma unroll
-                for (int kk = 0; kk < TK / 16; ++kk)
-                  mma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8,
-                              smem_desc_sw128_mn(v_addr + kk * 2048, C::HALF_TILE, 1024), idPV,
-                              (jp[x] > 0 || kk > 0) ? 1u : 0u);
-                ++jp[x];
-                if (jp[x ^ 1] >= jp[x]) mma_commit(&v_empty[st]);  // both tiles have used the block
-                mma_commit(&pv_done[x]);
-                progressed = true;
-              }
-            }
-            // S_x is written over P_x: its PV has to be complete
-            if (js[x] < w.nblk && js[x] == jp[x]) {
-              const int gk = J + js[x], st = gk % C::KST, use = nS[x] + js[x];
-              if (mbar_test(&pv_done[x], (use & 1) ^ 1u) && mbar_test(&k_full[st], (gk / C::KST) & 1)) {
-                tc_fence_after();
-                const uint32_t q_addr = smem_u32(sQ + x * C::TILE), k_addr = smem_u32(sK + st * C::TILE);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t off = (kk >> 2) * C::HALF_TILE + (kk & 3) * 32;
-                  mma_bf16(tmem + x * 128, smem_desc_sw128(q_addr + off), smem_desc_sw128(k_addr + off), idS,
-                           kk > 0 ? 1u : 0u);
-                }
-                ++js[x];
-                if (js[x ^ 1] >= js[x]) {
-                  mma_commit(&k_empty[st]);
-                  if (js[x] == w.nblk) mma_commit(q_empty);
-                }
-                mma_commit(&s_full[x]);
-                progressed = true;
-              }
-            }
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::HALF_TILE + (kk & 3) * 32) >> 4;
+            mma_bf16(tS, q_desc + off, kd + off, idS, kk > 0 ? 1u : 0u);
           }
-          if (progressed) {
-            t0 = globaltimer();
-          } else if (*abort_flag) {
-            ok = false;
-          } else if (globaltimer() - t0 > kWaitTimeoutNs) {
-            flag_error(p.status, kStatusTimeout);
-            *abort_flag = 1;
-            ok = false;
+          mma_commit(&s_full[x]);
+          mma_commit(&k_empty[st]);
+          if (alone) mma_commit(&k_empty[st]);
+          if (j == w.nblk - 1) {
+            mma_commit(q_empty);
+            if (alone) mma_commit(q_empty);
           }
         }
-        J += w.nblk;
-        for (int x = 0; x < tiles; ++x) {
-          nS[x] += w.nblk;
-          ++nU[x];
+        __syncwarp();
+      };
+      wait(q_full, n & 1);
+      score(0);
+#pragma unroll 1
+      for (int j = 0; j < w.nblk && ok; ++j) {
+        const int st = (J + j) % C::VST;
+        if (j == 0) wait(&o_empty[x], (mine & 1) ^ 1);
+        wait(&v_full[st], ((J + j) / C::VST) & 1);
+        wait(&p_full[x], u & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = v_desc + ((st * C::TILE) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < TK / 16; ++kk)
+            mma_bf16_ts(tO, tS + kk * 8, vd + ((kk * 2048) >> 4), idPV, (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&pv_done[x]);
+          mma_commit(&v_empty[st]);
+          if (alone) mma_commit(&v_empty[st]);
         }
+        __syncwarp();
+        ++u;
+        if (j + 1 < w.nblk) score(j + 1);
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      ++mine;
     }
-    if (leader && !ok) {
+    if (!ok && elect_one()) {
       // nothing may still read shared memory or write tensor memory at the end
-      mma_commit(drain);
-      mbar_drain(drain, 0);
+      mma_commit(&drain[x]);
+      mbar_drain(&drain[x], 0);
     }
   } else if (WIDEN && warp >= kConv0) {
     // ------------------------------------------------------------ widening
-    const int hf = (warp - kConv0) >> 2;  // 64-key half of a block
-    const int pg = (warp - kConv0) & 3;   // page of the half
+    const int pg = warp - kConv0;  // page of a slot
     constexpr int PIECES = D / 16;             // 16-code pieces of a key
     constexpr int STEPS = 16 * PIECES / 32;    // pieces of a lane
     constexpr int KEYS = 32 / PIECES;          // keys of a warp's step
@@ -629,7 +627,8 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       for (int j = 0; j < w.nblk && ok; ++j, ++J) {
         const int st = J % 2, use = J / 2;
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
+        for (int i4 = 0; i4 < 4; ++i4) {  // K keys 0..63, 64..127, V the same
+          const int kv = i4 >> 1, hf = i4 & 1;
           const int at = J * 2 + hf, slot = at % kSlots + kv * kSlots;
           bool landed = mbar_wait(&c_full[slot], (at / kSlots) & 1, abort_flag, p.status);
           if (!__all_sync(0xffffffffu, landed)) {
@@ -683,6 +682,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
               put(i, o);
             }
           }
+          if (hf == 0) continue;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(kv ? &v_full[st] : &k_full[st]);
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     const int r = quarter * 32 + lane;
     const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + x * 128;
     const uint32_t tO = tS + 256;
-    int use = 0;
+    int u = 0;  // blocks so far
     Unit w;
     for (int n = 0; next_unit(n, w); ++n) {
       const Tile t = w.t[x];
@@ -704,73 +704,68 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       const int lim = r < t.nrows ? t.pos0 + r : t.pos0 + t.nrows - 1;  // last key this row sees
       float m_used = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < w.nblk; ++j, ++use) {
-        bool sok = mbar_wait(&s_full[x], use & 1, abort_flag, p.status);
+#pragma unroll 1
+      for (int j = 0; j < w.nblk; ++j, ++u) {
+        bool sok = mbar_wait(&s_full[x], u & 1, abort_flag, p.status);
         if (!__all_sync(0xffffffffu, sok)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, v[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait32(v[c]);
         const int seen = lim - j * TK;  // columns 0 .. seen of the block
-        const bool full = __all_sync(0xffffffffu, seen >= TK - 1);
-        // 32 columns at a time, the next ones on their way
-        uint32_t sv[2][32];
-        float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld_32x32b_x32(tS, sv[0]);
+        if (__any_sync(0xffffffffu, seen < TK - 1)) {
 #pragma unroll
-        for (int c = 0; c < TK / 32; ++c) {
-          uint32_t(&v)[32] = sv[c & 1];
-          tmem_ld_wait32(v);
-          // behind the last come the first ones again, for the exponentials
-          tmem_ld_32x32b_x32(tS + (c + 1) % (TK / 32) * 32, sv[(c + 1) & 1]);
-          if (!full) {
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = c * 32 + e <= seen ? v[e] : 0xff800000u;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            mp[(e / 2) & 3] = fmaxf(mp[(e / 2) & 3], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+            for (int e = 0; e < 32; ++e) v[c][e] = c * 32 + e <= seen ? v[c][e] : 0xff800000u;
         }
-        float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
-        mx *= p.scale_log2;
+        float mp[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mp[c] = __uint_as_float(v[c][0]);
+#pragma unroll
+          for (int e = 1; e < 31; e += 2)
+            mp[c] = fmaxf(mp[c], fmaxf(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])));
+          mp[c] = fmaxf(mp[c], __uint_as_float(v[c][31]));
+        }
+        const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
         const bool raise = mx > m_used + kRescale;
-        const float m_new = raise ? mx : m_used;
-        const float alpha = raise ? ex2_approx(m_used - m_new) : 1.f;
-        // S of this block was issued behind the PV of the last one: O is complete
-        if (j > 0 && __any_sync(0xffffffffu, raise)) {
+        if (__any_sync(0xffffffffu, raise)) {
+          const float m_new = raise ? mx : m_used;
+          const float alpha = raise ? ex2_approx(m_used - m_new) : 1.f;
+          // S of this block was issued behind the PV of the last one: O is complete
+          if (j > 0) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t ov[32];
-            tmem_ld_32x32b_x32(tO + c, ov);
-            tmem_ld_wait32(ov);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t ov[16];
+              tmem_ld_32x32b_x16(tO + c, ov);
+              tmem_ld_wait16(ov);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st_32x32b_x32(tO + c, ov);
+              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st_32x32b_x16(tO + c, ov);
+            }
           }
+          m_used = m_new;
+          l *= alpha;
         }
-        m_used = m_new;
-        l *= alpha;
         const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
         float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < TK / 32; ++c) {
-          uint32_t(&v)[32] = sv[c & 1];
-          tmem_ld_wait32(v);
-          if (c + 1 < TK / 32) tmem_ld_32x32b_x32(tS + (c + 1) * 32, sv[(c + 1) & 1]);
-          if (!full) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = c * 32 + e <= seen ? v[e] : 0xff800000u;
-          }
+        for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float a0 = ex2_approx(fmaf(__uint_as_float(v[2 * e]), p.scale_log2, neg_m));
-            const float a1 = ex2_approx(fmaf(__uint_as_float(v[2 * e + 1]), p.scale_log2, neg_m));
+            const float a0 = ex2_approx(fmaf(__uint_as_float(v[c][2 * e]), p.scale_log2, neg_m));
+            const float a1 = ex2_approx(fmaf(__uint_as_float(v[c][2 * e + 1]), p.scale_log2, neg_m));
             rs[e & 3] += a0 + a1;
             pk[e] = pack_bf16x2(a0, a1);
           }
-          // over columns of S that are in registers already
-          tmem_st_32x32b_x16(tS + c * 16, pk);
+          tmem_st_32x32b_x16(tS + c * 16, pk);  // over S, which is in registers
         }
         l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
         tmem_st_wait();
@@ -779,7 +774,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
         if (lane == 0) mbar_arrive(&p_full[x]);
       }
       if (!ok) break;
-      bool pok = mbar_wait(&pv_done[x], (use - 1) & 1, abort_flag, p.status);
+      bool pok = mbar_wait(&pv_done[x], (u - 1) & 1, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, pok)) break;
       tc_fence_after();
       const float inv = 1.f / l;
@@ -827,8 +822,7 @@ hb_status launch_chunk(const DeviceCtx& ctx, const CUtensorMap& tmQ, const CUten
 }
 
 template <int D>
-hb_status launch_all(const DeviceCtx& ctx, const void* q, const Params& p, bool overflow, int grid,
-                     cudaStream_t stream) {
+hb_status launch_all(const DeviceCtx& ctx, const void* q, const Params& p, int grid, cudaStream_t stream) {
   CUtensorMap tmQ, tmK, tmV;
   hb_status st = encode_tmap_q3d(&tmQ, q, p.T, p.n_q, D);
   if (st != HB_OK) return st;
@@ -839,23 +833,33 @@ hb_status launch_all(const DeviceCtx& ctx, const void* q, const Params& p, bool 
   if (st != HB_OK) return st;
   st = launch_pdl(widen_kernel<D>, ctx.num_sms * 2, 256, 0, stream, "widen_kernel launch", p);
   if (st != HB_OK) return st;
-  st = launch_chunk<D, false>(ctx, tmQ, tmK, tmV, p, grid, stream);
-  if (st != HB_OK || !overflow) return st;
+  return launch_chunk<D, false>(ctx, tmQ, tmK, tmV, p, grid, stream);
+}
+
+template <int D>
+hb_status launch_overflow(const DeviceCtx& ctx, const void* q, const Params& p, cudaStream_t stream) {
+  CUtensorMap tmQ, tmK, tmV;
+  hb_status st = encode_tmap_q3d(&tmQ, q, p.T, p.n_q, D);
+  if (st != HB_OK) return st;
   // whole pages of codes, unswizzled: 16 rows of D bytes
   const uint64_t pool = static_cast<uint64_t>(p.num_pages) * p.n_kv * 16;
   st = encode_tmap_2d(&tmK, p.k, D, pool, D, D, 16, false, 1);
   if (st != HB_OK) return st;
   st = encode_tmap_2d(&tmV, p.v, D, pool, D, D, 16, false, 1);
   if (st != HB_OK) return st;
-  return launch_chunk<D, true>(ctx, tmQ, tmK, tmV, p, grid, stream);
+  return launch_chunk<D, true>(ctx, tmQ, tmK, tmV, p, ctx.num_sms, stream);
 }
 
 }  // namespace
 
-hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const Params& p, int d_head, bool overflow, int grid,
+hb_status chunk_e4m3_launch(const DeviceCtx& ctx, const void* q, const Params& p, int d_head, int grid,
                             cudaStream_t stream) {
-  return d_head == 128 ? launch_all<128>(ctx, q, p, overflow, grid, stream)
-                       : launch_all<64>(ctx, q, p, overflow, grid, stream);
+  return d_head == 128 ? launch_all<128>(ctx, q, p, grid, stream) : launch_all<64>(ctx, q, p, grid, stream);
+}
+
+hb_status chunk_e4m3_overflow_launch(const DeviceCtx& ctx, const void* q, const Params& p, int d_head,
+                                     cudaStream_t stream) {
+  return d_head == 128 ? launch_overflow<128>(ctx, q, p, stream) : launch_overflow<64>(ctx, q, p, stream);
 }
 
 }  // namespace hb
