@@ -145,6 +145,28 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
@@ -712,21 +734,19 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
           break;
         }
         tc_fence_after();
-        uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, v[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait32(v[c]);
         const int seen = lim - j * TK;  // columns 0 .. seen of the block
-        if (__any_sync(0xffffffffu, seen < TK - 1)) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[c][e] = c * 32 + e <= seen ? v[c][e] : 0xff800000u;
-        }
+        const bool cut = __any_sync(0xffffffffu, seen < TK - 1);
+        uint32_t v[4][32];
         float mp[4];
+        tmem_ld_32x32b_x32(tS, v[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait32(v[c]);
+          if (c < 3) tmem_ld_32x32b_x32(tS + (c + 1) * 32, v[(c + 1) & 3]);
+          if (cut) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[c][e] = c * 32 + e <= seen ? v[c][e] : 0xff800000u;
+          }
           mp[c] = __uint_as_float(v[c][0]);
 #pragma unroll
           for (int e = 1; e < 31; e += 2)
@@ -754,20 +774,23 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
           l *= alpha;
         }
         const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), neg2 = pack_f32x2(neg_m, neg_m);
+        uint64_t rs[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float a0 = ex2_approx(fmaf(__uint_as_float(v[c][2 * e]), p.scale_log2, neg_m));
-            const float a1 = ex2_approx(fmaf(__uint_as_float(v[c][2 * e + 1]), p.scale_log2, neg_m));
-            rs[e & 3] += a0 + a1;
+            const float2 y = unpack_f32x2(
+                fma_f32x2(pack_f32x2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), scale2, neg2));
+            const float a0 = ex2_approx(y.x), a1 = ex2_approx(y.y);
+            rs[e & 1] = add_f32x2(rs[e & 1], pack_f32x2(a0, a1));
             pk[e] = pack_bf16x2(a0, a1);
           }
           tmem_st_32x32b_x16(tS + c * 16, pk);  // over S, which is in registers
         }
-        l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+        const float2 r2 = unpack_f32x2(add_f32x2(rs[0], rs[1]));
+        l += r2.x + r2.y;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
