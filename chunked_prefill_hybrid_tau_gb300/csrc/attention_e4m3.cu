@@ -6,19 +6,25 @@
 // Decode rows (sequences of one row): HBM bounds them, 2 n_kv (d + 1) bytes a
 // key.  A unit is one row x one kv head x one range of kSplit keys at fixed
 // positions, so a row's result does not depend on its batch; a warp owns whole
-// units and streams their 16-token pages through a ring of its own.
+// units and streams their 16-token pages through a ring of its own, the next
+// unit's pages behind the last ones without a pause.
 //
 // Both products run on m16n8k16 MMAs with the keys (S) or the head dimension
 // (O) as rows and the kv head's q heads as the 8 columns:
 //   S^T = K Q^T  : 16 keys x 8 heads, one MMA per 16 dims,
 //   O^T += V^T P^T : 16 dims x 8 heads, one MMA per 16 dims of the output,
 // half the MMAs and half the accumulators of the other way round.  More than 8
-// q heads a kv head take a second column tile.  The codes are widened to bf16
-// in registers, exactly; a 16-bit ldmatrix of 8-bit codes hands a lane four
-// neighbouring dims of a key (K), or two dims of two keys (V, transposed), and
-// taking bytes (0, 2) and (1, 3) of them as the pairs permutes the dims of S's
-// sum, which q's fragments follow, and gives O's rows 2 a and 2 a + 1 to one
-// lane.  2^ek multiplies the scores and 2^ev the weights, in fp32.
+// q heads a kv head take a second column tile.  A 16-bit ldmatrix of 8-bit codes
+// hands a lane four neighbouring dims of a key (K), or two dims of two keys (V,
+// transposed); q's fragments follow the order that this gives the dims of S's
+// sum, and O's rows 2 a and 2 a + 1 come to one lane.
+//
+// The codes are widened in registers, exactly.  K goes to fp16, for which there
+// is an instruction (4 clocks a word of four codes; to bf16 it takes 10), and q
+// with it: a q head is first multiplied by the power of two that takes its
+// largest magnitude to 2^13, so that each of its values keeps its 8 bits unless
+// it is below 2^-30 of the largest.  V stays bf16: its weights P 2^ev need
+// the range.  2^ek multiplies the scores and 2^ev the weights, in fp32.
 #include "attention_e4m3.cuh"
 
 namespace hb {
@@ -49,13 +55,21 @@ struct DC {
   static_assert(SMEM <= 232448, "shared memory");
 };
 
+template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -76,6 +90,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
+// Four codes as fp16, in their order.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 // Two codes of w as bf16: bytes 1 and 3, bytes 0 and 2.
 __device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return mul_bf16x2(codes_moved(w), 0x7b807b80u); }
 __device__ __forceinline__ uint32_t codes_even(uint32_t w) { return codes_odd(w << 8); }
@@ -83,6 +106,11 @@ __device__ __forceinline__ uint32_t codes_even(uint32_t w) { return codes_odd(w 
 // 2^e of a scale byte of the format: 27 .. 247, or 255 (NaN)
 __device__ __forceinline__ float scale_of(uint32_t b) {
   return b == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(b << 23);
+}
+__device__ __forceinline__ uint2 ld_u2(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
 }
 __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
   uint32_t v;
@@ -98,9 +126,9 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
 
 template <int D, int NT>
 struct Heads {  // a warp's state of NT x 8 q heads
-  uint32_t q[NT][D / 16][2];
+  uint32_t q[NT][D / 16][2];  // fp16, times a power of two
   float o[NT][D / 16][4];
-  float m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2], f[NT][2];  // f: takes the sums of S to log2 units
 };
 
 // One 16-key page: S, the softmax step (a maximum that is raised only when it
@@ -109,24 +137,28 @@ struct Heads {  // a warp's state of NT x 8 q heads
 // keys of the page count.
 template <int D, int NT>
 __device__ __forceinline__ void page_step(uint32_t kp, uint32_t vp, uint32_t sp, Heads<D, NT>& w, int live,
-                                          float scale_log2, int lane) {
+                                          int lane) {
   const int mat = lane >> 3, key = ((mat & 1) << 3) + (lane & 7), a = lane >> 2;
-  float s[NT][4];
+  float s[NT][4], s2[NT][4];  // two chains of dependent MMAs, not one
 #pragma unroll
-  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
 #pragma unroll
   for (int c = 0; c < D / 16; c += 2) {
     uint32_t r[4];
     ldsm_x4(kp + piece_at<D>(key, c + (mat >> 1)), r);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t a0 = codes_even(r[2 * i]), a1 = codes_even(r[2 * i + 1]);
-      const uint32_t a2 = codes_odd(r[2 * i]), a3 = codes_odd(r[2 * i + 1]);
+      uint32_t a0, a1, a2, a3;
+      codes_f16(r[2 * i], a0, a2);
+      codes_f16(r[2 * i + 1], a1, a3);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma16816(s[n], a0, a1, a2, a3, w.q[n][c + i][0], w.q[n][c + i][1]);
+      for (int n = 0; n < NT; ++n)
+        mma16816<true>(i ? s2[n] : s[n], a0, a1, a2, a3, w.q[n][c + i][0], w.q[n][c + i][1]);
     }
   }
-  const float k0 = scale_of(lds_u8(sp + a)) * scale_log2, k1 = scale_of(lds_u8(sp + a + 8)) * scale_log2;
+  const float k0 = scale_of(lds_u8(sp + a)), k1 = scale_of(lds_u8(sp + a + 8));
   const float v0 = scale_of(lds_u8(sp + 16 + a)), v1 = scale_of(lds_u8(sp + 16 + a + 8));
   const bool in0 = a < live, in1 = a + 8 < live;
   bool grew = false;
@@ -134,8 +166,8 @@ __device__ __forceinline__ void page_step(uint32_t kp, uint32_t vp, uint32_t sp,
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      s[n][h] = in0 ? s[n][h] * k0 : -INFINITY;
-      s[n][2 + h] = in1 ? s[n][2 + h] * k1 : -INFINITY;
+      s[n][h] = in0 ? (s[n][h] + s2[n][h]) * w.f[n][h] * k0 : -INFINITY;
+      s[n][2 + h] = in1 ? (s[n][2 + h] + s2[n][2 + h]) * w.f[n][h] * k1 : -INFINITY;
       grew |= fmaxf(s[n][h], s[n][2 + h]) > w.m[n][h] + kRescale;
     }
   if (__any_sync(0xffffffffu, grew)) {
@@ -183,8 +215,51 @@ __device__ __forceinline__ void page_step(uint32_t kp, uint32_t vp, uint32_t sp,
       const uint32_t a0 = codes_even(r[2 * i]), a1 = codes_odd(r[2 * i]);
       const uint32_t a2 = codes_even(r[2 * i + 1]), a3 = codes_odd(r[2 * i + 1]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma16816(w.o[n][c + i], a0, a1, a2, a3, b[n][0], b[n][1]);
+      for (int n = 0; n < NT; ++n) mma16816<false>(w.o[n][c + i], a0, a1, a2, a3, b[n][0], b[n][1]);
     }
+  }
+}
+
+// The q heads of one row and kv head: fragments, empty sums.
+template <int D, int NT>
+__device__ __forceinline__ void take_heads(const Params& p, Heads<D, NT>& w, int row, int g, int lane) {
+  const int a = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int h = 8 * n + a;
+    const __nv_bfloat16* q = p.q + (static_cast<size_t>(row) * p.n_q + g * p.grp + (h < p.grp ? h : 0)) * D + 4 * t;
+    uint32_t big = 0;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      const uint2 v = ld_u2(q + 16 * c);
+      w.q[n][c][0] = h < p.grp ? v.x : 0u;
+      w.q[n][c][1] = h < p.grp ? v.y : 0u;
+      big = max(big, max(v.x & 0x7fffu, (v.x >> 16) & 0x7fffu));
+      big = max(big, max(v.y & 0x7fffu, (v.y >> 16) & 0x7fffu));
+    }
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    // 2^s takes the largest magnitude to 2^13; s at most 100, so that it and its
+    // inverse are normal numbers
+    const int s = min(13 + 127 - static_cast<int>(big >> 7), 100);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - s) << 23) * p.scale_log2;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 f = unpack_bf16x2(w.q[n][c][i]);
+        const __half2 x = __floats2half2_rn(f.x * up, f.y * up);
+        w.q[n][c][i] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+#pragma unroll
+    for (int h2 = 0; h2 < 2; ++h2) {
+      w.f[n][h2] = __shfl_sync(0xffffffffu, down, (2 * t + h2) * 4);
+      w.m[n][h2] = -INFINITY;
+      w.l[n][h2] = 0.f;
+    }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) w.o[n][c][0] = w.o[n][c][1] = w.o[n][c][2] = w.o[n][c][3] = 0.f;
   }
 }
 
@@ -248,88 +323,91 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  griddep_launch_dependents();
   if (!p.wait_at_end) griddep_wait();
+  griddep_launch_dependents();
   count_units(p, pre);
   const int total = pre[p.S];
   const int a = lane >> 2, t = lane & 3;
-  uint32_t phases = 0;  // bit s: parity to wait for on slot s
-  // neighbouring units on different SMs
-  for (int u = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x); u < total;
-       u += kDecWarps * static_cast<int>(gridDim.x)) {
-    const int s = upper_index(pre, p.S, u), local = u - pre[s];
-    const int g = local % p.n_kv, split = local / p.n_kv;
-    const int kvl = ld_s32(p.kv_len + s), row = ld_s32(p.q_start + s);
-    const int key_begin = split * kSplit, keys = min(kvl - key_begin, kSplit);
-    const int npages = (keys + 15) / 16;
-    // lane b has the id of the unit's page b (kSplit / 16 of them at most)
-    int id = 0;
-    if (lane < npages) {
-      id = ld_s32(p.block_table + static_cast<size_t>(s) * p.max_pages + key_begin / 16 + lane);
-      if (id < 0 || id >= p.num_pages) {
-        flag_error(p.status, kStatusIndex);
-        id = 0;
-      }
-    }
-    auto issue = [&](int b) {
-      const int slot = b % C::DR;
-      const int at = (__shfl_sync(0xffffffffu, id, b) * p.n_kv + g) * 16;
-      if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::STAGE + 32);
-      __syncwarp();
-      // each byte is read once: first out of L2
-      if (lane < 2)
-        tma_load_2d_hint(ring + slot * C::STAGE + lane * C::PAGE, lane ? &tmV : &tmK, &full[slot], 0, at,
-                         policy_evict_first());
-      else if (lane < 4)
-        bulk_load(scales + slot * 32 + (lane - 2) * 16, (lane == 2 ? p.ks : p.vs) + at, 16, &full[slot]);
-    };
-    for (int b = 0; b < min(C::DR, npages); ++b) issue(b);
-
-    Heads<D, NT> w;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int h = 8 * n + a;
-      const __nv_bfloat16* q = p.q + (static_cast<size_t>(row) * p.n_q + g * p.grp + (h < p.grp ? h : 0)) * D + 4 * t;
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t lo = 0, hi = 0;
-        if (h < p.grp) {
-          lo = static_cast<uint32_t>(ld_s32(reinterpret_cast<const int*>(q + 16 * c)));
-          hi = static_cast<uint32_t>(ld_s32(reinterpret_cast<const int*>(q + 16 * c) + 1));
+  // a unit: its sequence, kv head and split, its keys, and the ids of its pages
+  // (lane b has that of page b)
+  struct Work {
+    int s, g, split, keys, whole, id;
+  };
+  auto look_up = [&](int u) {
+    Work w = {0, 0, 0, 0, 0, 0};
+    if (u < total) {
+      w.s = upper_index(pre, p.S, u);
+      const int local = u - pre[w.s];
+      w.g = local % p.n_kv;
+      w.split = local / p.n_kv;
+      const int kvl = ld_s32(p.kv_len + w.s);
+      w.keys = min(kvl - w.split * kSplit, kSplit);
+      w.whole = kvl <= kSplit;
+      if (lane * 16 < w.keys) {
+        w.id = ld_s32(p.block_table + static_cast<size_t>(w.s) * p.max_pages + w.split * (kSplit / 16) + lane);
+        if (w.id < 0 || w.id >= p.num_pages) {
+          flag_error(p.status, kStatusIndex);
+          w.id = 0;
         }
-        w.q[n][c][0] = __byte_perm(lo, hi, 0x5410);
-        w.q[n][c][1] = __byte_perm(lo, hi, 0x7632);
-        w.o[n][c][0] = w.o[n][c][1] = w.o[n][c][2] = w.o[n][c][3] = 0.f;
       }
-      w.m[n][0] = w.m[n][1] = -INFINITY;
-      w.l[n][0] = w.l[n][1] = 0.f;
     }
-
-    bool ok = true;
-    for (int b = 0; b < npages; ++b) {
-      const int slot = b % C::DR;
-      const bool landed = mbar_wait(&full[slot], (phases >> slot) & 1u, nullptr, p.status);
-      phases ^= 1u << slot;
+    return w;
+  };
+  int slot_in = 0, slot_out = 0;  // ring slots of the next copy and of the next page
+  uint32_t phases = 0;            // bit s: parity to wait for on slot s
+  auto issue = [&](const Work& w, int b) {
+    const int at = (__shfl_sync(0xffffffffu, w.id, b) * p.n_kv + w.g) * 16;
+    if (lane == 0) mbar_arrive_expect_tx(&full[slot_in], C::STAGE + 32);
+    __syncwarp();
+    // each byte is read once: first out of L2
+    if (lane < 2)
+      tma_load_2d_hint(ring + slot_in * C::STAGE + lane * C::PAGE, lane ? &tmV : &tmK, &full[slot_in], 0, at,
+                       policy_evict_first());
+    else if (lane < 4)
+      bulk_load(scales + slot_in * 32 + (lane - 2) * 16, (lane == 2 ? p.ks : p.vs) + at, 16, &full[slot_in]);
+    if (++slot_in == C::DR) slot_in = 0;
+  };
+  // neighbouring units on different SMs
+  const int stride = kDecWarps * static_cast<int>(gridDim.x);
+  int u = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  Work cur = look_up(u);
+  int ahead = 0, flying = 0;  // pages of cur issued; pages of both on their way
+  auto fill = [&](const Work& w, int& issued) {
+    while (flying < C::DR && issued * 16 < w.keys) {
+      issue(w, issued++);
+      ++flying;
+    }
+  };
+  fill(cur, ahead);
+  bool ok = true;
+  while (u < total && ok) {
+    u += stride;
+    const Work next = look_up(u);
+    int early = 0;  // pages of next issued
+    fill(next, early);
+    const int row = ld_s32(p.q_start + cur.s);
+    Heads<D, NT> w;
+    take_heads<D, NT>(p, w, row, cur.g, lane);
+    for (int b = 0; b * 16 < cur.keys; ++b) {
+      const bool landed = mbar_wait(&full[slot_out], (phases >> slot_out) & 1u, nullptr, p.status);
+      phases ^= 1u << slot_out;
       if (!__all_sync(0xffffffffu, landed)) {
         ok = false;
         break;
       }
-      const uint32_t kp = smem_u32(ring + slot * C::STAGE);
-      page_step<D, NT>(kp, kp + C::PAGE, smem_u32(scales + slot * 32), w, keys - 16 * b, p.scale_log2, lane);
+      const uint32_t kp = smem_u32(ring + slot_out * C::STAGE);
+      page_step<D, NT>(kp, kp + C::PAGE, smem_u32(scales + slot_out * 32), w, cur.keys - 16 * b, lane);
       __syncwarp();
-      if (b + C::DR < npages) issue(b + C::DR);
+      if (++slot_out == C::DR) slot_out = 0;
+      --flying;
+      fill(cur, ahead);
+      fill(next, early);
     }
-    if (!ok) {
-      // let this warp's copies in flight land (bounded) before it leaves
-      if (lane == 0)
-        for (int i = 0; i < C::DR; ++i) mbar_drain(&full[i], (phases >> i) & 1u);
-      break;
-    }
+    if (!ok) break;
 
-    const bool whole = kvl <= kSplit;
-    float* rec = p.partials + (static_cast<size_t>(s) * p.max_splits + split) * p.n_kv * rec_floats(p.grp, D) +
-                 static_cast<size_t>(g) * rec_floats(p.grp, D);
-    __nv_bfloat16* out = p.out + (static_cast<size_t>(row) * p.n_q + g * p.grp) * D;
+    float* rec = p.partials +
+                 ((static_cast<size_t>(cur.s) * p.max_splits + cur.split) * p.n_kv + cur.g) * rec_floats(p.grp, D);
+    __nv_bfloat16* out = p.out + (static_cast<size_t>(row) * p.n_q + cur.g * p.grp) * D;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -340,7 +418,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         const int head = 8 * n + 2 * t + h;
         if (head >= p.grp) continue;
-        if (whole) {
+        if (cur.whole) {
           const float inv = 1.f / l;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c)
@@ -356,60 +434,92 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
           }
         }
       }
+    cur = next;
+    ahead = early;
   }
+  // after a wait that expired: the copies in flight land (bounded) before the warp leaves
+  if (!ok && lane == 0)
+    for (int i = 0; i < C::DR; ++i) mbar_drain(&full[i], (phases >> i) & 1u);
   if (p.wait_at_end) griddep_wait();
 }
 
 // The splits of one decode row and q head (a CTA), in an order of their number
-// alone: warp w takes splits w, w + 8, ..., the warps' sums are added in order.
-constexpr int kJoinWarps = 8;
+// alone: warp w takes splits w, w + 8, ..., kJoin of them in flight with their
+// maxima and sums; the warps' results are joined in order.  The plan is read
+// ahead of the wait: the decode kernel lets this one start only once everything
+// ahead of itself is complete.
+constexpr int kJoinWarps = 8, kJoin = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_splits_kernel(Params p) {
   constexpr int E = D / 32;
   __shared__ float sum[kJoinWarps][D];
-  __shared__ float norm[kJoinWarps];
+  __shared__ float2 state[kJoinWarps];
   griddep_launch_dependents();
-  griddep_wait();
   const int s = blockIdx.x, h = blockIdx.y, g = h / p.grp, r = h % p.grp;
   const int q0 = ld_s32(p.q_start + s), q1 = ld_s32(p.q_start + s + 1), kvl = ld_s32(p.kv_len + s);
+  griddep_wait();
   // as count_units: others were not computed, or were whole
   if (q0 < 0 || q1 > p.T || q1 - q0 != 1 || kvl <= kSplit || kvl > p.max_kv_len || (kvl + 15) / 16 > p.max_pages) return;
   const int n = (kvl + kSplit - 1) / kSplit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t step = static_cast<size_t>(p.n_kv) * rec_floats(p.grp, D);
   const float* rec = p.partials + static_cast<size_t>(s) * p.max_splits * step +
                      static_cast<size_t>(g) * rec_floats(p.grp, D);
-  const float* ms = rec + p.grp * D + r;
-  const float* ls = ms + p.grp;
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, ld_f32(ms + i * step));
+  float acc[E] = {}, l = 0.f, m = -INFINITY;
+  for (int i0 = warp; i0 < n; i0 += kJoinWarps * kJoin) {
+    float mi[kJoin], li[kJoin], o[kJoin][E];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float mu = m == -INFINITY ? 0.f : m;
-  float acc[E] = {}, l = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += kJoinWarps) {
-    const float wgt = ex2_approx(ld_f32(ms + i * step) - mu);
-    l += wgt * ld_f32(ls + i * step);
-    const float* o = rec + i * step + r * D + lane * E;
-    if (E == 4) {
-      const float4 v = ld_f4(o);
-      acc[0] += wgt * v.x, acc[1] += wgt * v.y, acc[2 % E] += wgt * v.z, acc[3 % E] += wgt * v.w;
-    } else {
+    for (int k = 0; k < kJoin; ++k) {
+      // behind the last: the last again, with weight 0
+      const int i = i0 + k * kJoinWarps;
+      const float* at = rec + min(i, n - 1) * step;
+      mi[k] = ld_f32(at + p.grp * D + r);
+      li[k] = ld_f32(at + p.grp * (D + 1) + r);
+      if (E == 4) {
+        const float4 v = ld_f4(at + r * D + lane * E);
+        o[k][0] = v.x, o[k][1] = v.y, o[k][2 % E] = v.z, o[k][3 % E] = v.w;
+      } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += wgt * ld_f32(o + e);
+        for (int e = 0; e < E; ++e) o[k][e] = ld_f32(at + r * D + lane * E + e);
+      }
+      if (i >= n) {
+        mi[k] = -INFINITY;
+        li[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[k][e] = 0.f;
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) mn = fmaxf(mn, mi[k]);
+    const float mu = mn == -INFINITY ? 0.f : mn, alpha = ex2_approx(m - mu);
+    m = mn;
+    l *= alpha;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+      const float w = ex2_approx(mi[k] - mu);
+      l += w * li[k];
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w * o[k][e];
     }
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[warp][lane * E + e] = acc[e];
-  if (lane == 0) norm[warp] = l;
+  if (lane == 0) state[warp] = make_float2(m, l);
   __syncthreads();
   if (threadIdx.x < D / 2) {
+    float all = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) all = fmaxf(all, state[w].x);
+    if (all == -INFINITY) all = 0.f;
     float x = 0.f, y = 0.f, z = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-      x += sum[w][2 * threadIdx.x];
-      y += sum[w][2 * threadIdx.x + 1];
-      z += norm[w];
+      const float f = ex2_approx(state[w].x - all);
+      x += f * sum[w][2 * threadIdx.x];
+      y += f * sum[w][2 * threadIdx.x + 1];
+      z += f * state[w].y;
     }
     *reinterpret_cast<uint32_t*>(p.out + (static_cast<size_t>(q0) * p.n_q + h) * D + 2 * threadIdx.x) =
         pack_bf16x2(x / z, y / z);
@@ -465,8 +575,8 @@ int chunk_sms(const DeviceCtx& ctx, const hb_device_plan& plan, const hb_layer_d
 
 // Keys of several-row sequences that are widened ahead of the chunk kernel:
 // what the sizes allow to come, but no more than this, and at least one
-// sequence (537 MB with 8 kv heads of 128).
-constexpr long long kScratchKeys = 131072;
+// sequence (1.07 GB with 8 kv heads of 128).
+constexpr long long kScratchKeys = 262144;
 
 long long chunk_keys(int rows, int seqs, int max_kv_len) {
   const long long n = seqs < rows / 2 ? seqs : rows / 2;

@@ -255,7 +255,7 @@ def test_attention_rows_do_not_depend_on_the_batch():
 def test_attention_more_chunk_keys_than_are_widened_ahead(n_q, n_kv, d):
     """Sequences behind the end of the workspace's scratch: the same bits as alone."""
     dims = dims_of(n_q, n_kv, d)
-    hp, q, cache, table = batch(dims, [900], [(70000, 69990), (60000, 59870), (20000, 19800)],
+    hp, q, cache, table = batch(dims, [900], [(140000, 139990), (122000, 121870), (20000, 19800)],
                               1 + 10 + 130 + 200, 200, seed=19)
     assert sorted(np.diff(hp.seq_q_start).tolist()) == [1, 10, 130, 200]
     out = attend(hp, q, cache, dims)
@@ -266,8 +266,8 @@ def test_attention_more_chunk_keys_than_are_widened_ahead(n_q, n_kv, d):
         r0, r1 = hp.seq_q_start[s], hp.seq_q_start[s + 1]
         one = hb.DevicePlan(_alone(hp, s))
         o = torch.empty((r1 - r0, n_q * d), dtype=BF, device="cuda")
-        ws = wd.workspace(hb.hb_attention_e4m3_workspace_bytes(dims, r1 - r0, 1, 70000))
-        hb.hb_attention_e4m3(q[r0:r1].contiguous(), *[t.cuda() for t in cache], one, dims, 70000, o, ws)
+        ws = wd.workspace(hb.hb_attention_e4m3_workspace_bytes(dims, r1 - r0, 1, 140000))
+        hb.hb_attention_e4m3(q[r0:r1].contiguous(), *[t.cuda() for t in cache], one, dims, 140000, o, ws)
         assert torch.equal(o, out[r0:r1]), s
 
 
