@@ -9,11 +9,11 @@
 // an error of m * 2^-24 into every term.
 //
 // The k best: every thread keeps the largest of its elements.  Four lanes'
-// largest make a group; of the CTA's 128 groups the k-th largest is a bound
-// that at least k elements reach, and only the groups that reach it (k, and
-// ties) can hold one of the k best.  Their elements are read again (a 128th of
-// the row each, from L2), those at or above the bound are collected (a few
-// more than k) and ranked by counting.
+// largest make a group; of the CTA's 64 groups the k-th largest is a bound that
+// at least k elements reach, and only the groups that reach it (k, and ties)
+// can hold one of the k best.  Their elements are read again (a 64th of the row
+// each, from L2), those at or above the bound are collected (a few more than k)
+// and ranked by counting.
 //
 // A row has 8 fixed segments, and thread t of a segment fixed elements; states
 // join over segments first, in a fixed tree, then over threads.  1, 2, 4 or 8
@@ -31,7 +31,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegs = 8;
 constexpr int kElems = 16;            // elements a thread takes at a time
@@ -108,25 +108,34 @@ struct Row {
     asm volatile("ld.global.u16 %0, [%1];" : "=h"(b) : "l"(p));
     return __uint_as_float(static_cast<uint32_t>(b) << 16);
   }
-  // The elements of piece v; those outside the row are -inf.
-  __device__ __forceinline__ void load(int v, float (&f)[E]) const {
+  // Piece v as it lies in memory; elements outside the row are -inf.
+  __device__ __forceinline__ uint4 load(int v) const {
     const int i0 = v * E - shift;
-    if (i0 >= 0 && i0 + E <= vocab) {
+    if (i0 >= 0 && i0 + E <= vocab) return ld_u4(x + i0);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
       if (sizeof(T) == 4) {
-        const float4 w = ld_f4(x + i0);
-        f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
+        const int at = i0 + j;
+        w[j] = at >= 0 && at < vocab ? __float_as_uint(one(x + at)) : 0xff800000u;
       } else {
-        const uint4 w = ld_u4(x + i0);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f[(2 * j) % E] = __uint_as_float(u[j] << 16);
-          f[(2 * j + 1) % E] = __uint_as_float(u[j] & 0xffff0000u);
-        }
+        const int at = i0 + 2 * j;
+        const uint32_t lo = at >= 0 && at < vocab ? __float_as_uint(one(x + at)) >> 16 : 0xff80u;
+        w[j] = lo | (at + 1 >= 0 && at + 1 < vocab ? __float_as_uint(one(x + at + 1)) : 0xff800000u);
       }
-    } else {
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ static void values(const uint4& r, float (&f)[E]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int j = 0; j < E; ++j) f[j] = i0 + j >= 0 && i0 + j < vocab ? one(x + i0 + j) : -INFINITY;
+    for (int j = 0; j < 4; ++j) {
+      if (sizeof(T) == 4) {
+        f[j] = __uint_as_float(w[j]);
+      } else {
+        f[(2 * j) % E] = __uint_as_float(w[j] << 16);
+        f[(2 * j + 1) % E] = __uint_as_float(w[j] & 0xffff0000u);
+      }
     }
   }
 };
@@ -138,6 +147,12 @@ __device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
 }
 __device__ __forceinline__ float ld_dsmem_f32(const void* p, uint32_t rank) {
   return __uint_as_float(ld_dsmem_u32(p, rank));
+}
+
+// The logit that a candidate's key was made of (-0 comes back as +0).
+__device__ __forceinline__ float logit_of(unsigned long long key) {
+  const uint32_t o = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float(o == 0xffffffffu ? 0x7fc00000u : o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
 // Binary tree over a power of two of states, in place; the result is a[0].
@@ -173,57 +188,103 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
   const int row = blockIdx.x / CL;
   const Row<T> x(a.logits, a.stride, row, a.vocab);
 
-  // ---- one pass: (m, s, t) of each segment's elements of this thread, the
-  // segments joined as the leaves of a binary tree; and the largest element
-  State seg[SEGS];
-  float best = -INFINITY;
-#pragma unroll 1
-  for (int i = 0; i < SEGS; ++i) {
-    const int v0 = (rank * SEGS + i) * x.per_seg, v1 = min(v0 + x.per_seg, x.pieces);
-    State st = {-INFINITY, 0.f, 0.f};
-#pragma unroll 1
-    for (int v = v0 + tid; v < v1; v += kThreads * P) {
-      float f[P][E];
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        if (v + p * kThreads < v1) {
-          x.load(v + p * kThreads, f[p]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; ++j) f[p][j] = -INFINITY;
-        }
-      }
-      float mt = f[0][0];
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int j = 0; j < E; ++j) mt = fmaxf(mt, f[p][j]);
-      if (mt > st.m) {
-        if (st.m != -INFINITY) {
-          const float d = fmaxf(__fsub_rn(st.m, mt), kLeast), c = ex2_approx(__fmul_rn(d, kLog2e));
-          st.t = __fmul_rn(__fmaf_rn(st.s, d, st.t), c);
-          st.s = __fmul_rn(st.s, c);
-        }
-        st.m = mt;
-      }
-      const float m = st.m == -INFINITY ? 0.f : st.m;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const float d = __fsub_rn(f[p][j], m), e = ex2_approx(__fmul_rn(d, kLog2e));
-          st.s = __fadd_rn(st.s, e);
-          st.t = __fmaf_rn(e, fmaxf(d, kLeast), st.t);  // e = 0 at d = -inf: the product is 0
-        }
-    }
-    best = fmaxf(best, st.m);
-    // a NaN among the elements has made s a NaN: carry it on whatever m is
-#pragma unroll
-    for (int k = 0; k < SEGS; ++k)
-      if (k == i) seg[k] = st;
+  // the given tokens' logits, far ahead of their use
+  int id = -1;
+  float given = 0.f;
+  if (rank == 0 && tid < a.n_tokens) {
+    id = ld_s32(a.tokens + static_cast<size_t>(row) * a.n_tokens + tid);
+    if (id >= a.vocab) flag_error(a.status, kStatusIndex);
+    if (id >= 0 && id < a.vocab) given = Row<T>::one(x.x + id);
   }
-  join_tree(seg);
-  sh.state[tid] = seg[0];
+
+  // ---- one pass: (m, s, t) of each segment's elements of this thread, the
+  // segments joined as the leaves of a binary tree; and the largest element.
+  // The next pieces are on their way while these are worked on.
+  State st = {-INFINITY, 0.f, 0.f}, half, quarter, eighth;
+  float best = -INFINITY;
+  const int v_end = min((rank + 1) * SEGS * x.per_seg, x.pieces);
+  int i = 0, v = rank * SEGS * x.per_seg, stop = min(v + x.per_seg, x.pieces);
+  auto fetch = [&](int at, int end, uint4 (&raw)[P]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int w = at + tid + p * kThreads;
+      constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+      raw[p] = w < end ? x.load(w) : make_uint4(kNone, kNone, kNone, kNone);
+    }
+  };
+  uint4 raw[P];
+  fetch(v, stop, raw);
+#pragma unroll 1
+  while (true) {
+    uint4 now[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) now[p] = raw[p];
+    v += kThreads * P;
+    const bool ends = v >= stop;
+    if (ends) {
+      v = (rank * SEGS + i + 1) * x.per_seg;
+      stop = min(v + x.per_seg, x.pieces);
+    }
+    if (i + ends < SEGS && v < v_end) fetch(v, stop, raw);
+    float mt = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float f[E];
+      Row<T>::values(now[p], f);
+#pragma unroll
+      for (int j = 0; j < E; j += 2) mt = fmaxf(mt, fmaxf(f[j], f[j + 1]));
+    }
+    if (mt > st.m) {
+      if (st.m != -INFINITY) {
+        const float d = fmaxf(__fsub_rn(st.m, mt), kLeast), c = ex2_approx(__fmul_rn(d, kLog2e));
+        st.t = __fmul_rn(__fmaf_rn(st.s, d, st.t), c);
+        st.s = __fmul_rn(st.s, c);
+      }
+      st.m = mt;
+    }
+    const float m = st.m == -INFINITY ? 0.f : st.m;
+    float s2 = 0.f, t2 = 0.f;  // odd elements: two chains of dependent adds
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float f[E];
+      Row<T>::values(now[p], f);
+#pragma unroll
+      for (int j = 0; j < E; j += 2) {
+        const float d = __fsub_rn(f[j], m), e = ex2_approx(__fmul_rn(d, kLog2e));
+        st.s = __fadd_rn(st.s, e);
+        st.t = __fmaf_rn(e, fmaxf(d, kLeast), st.t);  // e = 0 at d = -inf: the product is 0
+        const float d2 = __fsub_rn(f[j + 1], m), e2 = ex2_approx(__fmul_rn(d2, kLog2e));
+        s2 = __fadd_rn(s2, e2);
+        t2 = __fmaf_rn(e2, fmaxf(d2, kLeast), t2);
+      }
+    }
+    st.s = __fadd_rn(st.s, s2);
+    st.t = __fadd_rn(st.t, t2);
+    if (!ends) continue;
+    // (where a NaN was among the elements s is one, whatever m is)
+    best = fmaxf(best, st.m);
+    if (i & 1) {
+      st = join(half, st);
+      if (i & 2) {
+        st = join(quarter, st);
+        if (i & 4) st = join(eighth, st);
+        else eighth = st;
+      } else {
+        quarter = st;
+      }
+    } else {
+      half = st;
+    }
+    if (++i == SEGS) break;
+    st = {-INFINITY, 0.f, 0.f};
+    if (v >= v_end) {  // segments without a piece (short rows) join as empty ones
+      constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+      for (int p = 0; p < P; ++p) raw[p] = make_uint4(kNone, kNone, kNone, kNone);
+    }
+  }
+  const State mine = st;
+  sh.state[tid] = mine;
 
   // ---- the k best of this CTA's segments, in falling order in sh.top
   const int k = a.top_k;
@@ -235,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
     if (tid < kMaxTop) sh.top[tid] = 0;
     if (tid == 0) sh.n_winners = sh.n_cand = 0;
     // fmaxf passes over a NaN: with one about, the bound goes by exact keys
-    bool by_key = __syncthreads_or(seg[0].s != seg[0].s) != 0;
+    bool by_key = __syncthreads_or(mine.s != mine.s) != 0;
     // rank of each group among the groups, equal ones by the lower group
     if (tid < kGroups) {
       const float mine = sh.best[tid];
@@ -250,26 +311,26 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
     while (true) {
       if (by_key && !keyed) {
         // the exact largest key of each group's elements, and the k-th of them
-        unsigned long long mine = 0;
+        unsigned long long top = 0;
         for (int v0 = rank * SEGS * x.per_seg, i = 0; i < SEGS; ++i, v0 += x.per_seg)
           for (int v = v0 + tid; v < min(v0 + x.per_seg, x.pieces); v += kThreads) {
             float f[E];
-            x.load(v, f);
+            Row<T>::values(x.load(v), f);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
               const int at = v * E - x.shift + j;
-              if (at >= 0 && at < x.vocab) mine = max(mine, key_of(f[j], at));
+              if (at >= 0 && at < x.vocab) top = max(top, key_of(f[j], at));
             }
           }
-        mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
-        mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 2));
-        if ((lane & 3) == 0) sh.best_key[tid >> 2] = mine;
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if ((lane & 3) == 0) sh.best_key[tid >> 2] = top;
         __syncthreads();
         if (tid < kGroups) {
-          mine = sh.best_key[tid];
+          top = sh.best_key[tid];
           int above = 0;
-          for (int i = 0; i < kGroups; ++i) above += sh.best_key[i] > mine || (sh.best_key[i] == mine && i < tid);
-          if (above == k - 1) sh.bound = max(sh.bound, mine);
+          for (int i = 0; i < kGroups; ++i) above += sh.best_key[i] > top || (sh.best_key[i] == top && i < tid);
+          if (above == k - 1) sh.bound = max(sh.bound, top);
         }
         keyed = true;
         __syncthreads();
@@ -288,7 +349,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
           const int v0 = (rank * SEGS + i) * x.per_seg, v1 = min(v0 + x.per_seg, x.pieces);
           for (int v = v0 + 4 * grp + (lane & 3) + (lane >> 2) * kThreads; v < v1; v += 8 * kThreads) {
             float f[E];
-            x.load(v, f);
+            Row<T>::values(x.load(v), f);
 #pragma unroll
             for (int j = 0; j < E; ++j) {
               const int at = v * E - x.shift + j;
@@ -368,17 +429,18 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
     join_tree(ws);
     const float m = ws[0].m, log_s = logf(ws[0].s);
     if (a.entropy && tid == 0) a.entropy[row] = __fsub_rn(log_s, __fdiv_rn(ws[0].t, ws[0].s));
-    for (int j = tid; j < a.n_tokens; j += kThreads) {
+    auto log_prob = [&](float logit) { return __fsub_rn(__fsub_rn(logit, m), log_s); };
+    if (id >= 0 && id < a.vocab) a.token_lp[static_cast<size_t>(row) * a.n_tokens + tid] = log_prob(given);
+    for (int j = tid + kThreads; j < a.n_tokens; j += kThreads) {
       const size_t at = static_cast<size_t>(row) * a.n_tokens + j;
-      const int id = ld_s32(a.tokens + at);
-      if (id >= a.vocab) flag_error(a.status, kStatusIndex);
-      if (id >= 0 && id < a.vocab) a.token_lp[at] = __fsub_rn(__fsub_rn(Row<T>::one(x.x + id), m), log_s);
+      const int more = ld_s32(a.tokens + at);
+      if (more >= a.vocab) flag_error(a.status, kStatusIndex);
+      if (more >= 0 && more < a.vocab) a.token_lp[at] = log_prob(Row<T>::one(x.x + more));
     }
     auto put = [&](int at, unsigned long long best_key) {
-      const int id = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best_key));
       const size_t to = static_cast<size_t>(row) * k + at;
-      a.top_ids[to] = id;
-      a.top_lp[to] = __fsub_rn(__fsub_rn(Row<T>::one(x.x + id), m), log_s);
+      a.top_ids[to] = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best_key));
+      a.top_lp[to] = log_prob(logit_of(best_key));
     };
     if (CL == 1) {
       if (tid < k) put(tid, sh.top[tid]);
@@ -412,8 +474,8 @@ hb_status logprobs_launch(const Args& a, int rows, cudaStream_t stream) {
 
 template <typename T>
 hb_status logprobs_rows(const Args& a, int rows, int num_sms, cudaStream_t stream) {
-  // as many CTAs a row as keep the grid within two a SM
-  const long long room = 2ll * num_sms;
+  // as many CTAs a row as keep the grid within four a SM
+  const long long room = 4ll * num_sms;
   if (rows * 8ll <= room) return logprobs_launch<T, 8>(a, rows, stream);
   if (rows * 4ll <= room) return logprobs_launch<T, 4>(a, rows, stream);
   if (rows * 2ll <= room) return logprobs_launch<T, 2>(a, rows, stream);
