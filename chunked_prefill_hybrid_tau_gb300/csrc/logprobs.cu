@@ -34,7 +34,7 @@ using namespace dev;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSegs = 8;
-constexpr int kElems = 16;            // elements a thread takes at a time
+constexpr int P = 4;                  // 16-byte pieces that a thread takes at a time
 constexpr int kGroups = kThreads / 4;
 constexpr int kMaxTop = 32;
 constexpr int kCap = 1024;            // collected candidates
@@ -88,12 +88,12 @@ __device__ __forceinline__ unsigned long long key_of(float x, int i) {
 template <typename T>
 struct Row {
   static constexpr int E = 16 / sizeof(T);  // elements of a 16-byte piece
-  static constexpr int P = kElems / E;      // pieces a thread takes at a time
   const T* x;
   int vocab;
   int shift;   // elements by which the row starts behind a 16-byte boundary
   int pieces;  // 16-byte pieces that the row touches; piece v holds elements v E - shift ...
   int per_seg;
+  int inner0, inner1;  // pieces that lie inside the row
 
   __device__ Row(const void* base, long long stride, int row, int n) {
     x = static_cast<const T*>(base) + static_cast<long long>(row) * stride;
@@ -101,6 +101,8 @@ struct Row {
     shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
     pieces = (shift + n + E - 1) / E;
     per_seg = (pieces + kSegs - 1) / kSegs;
+    inner0 = shift > 0 ? 1 : 0;
+    inner1 = (shift + n) / E;
   }
   __device__ static float one(const T* p) {
     if (sizeof(T) == 4) return ld_f32(reinterpret_cast<const float*>(p));
@@ -126,6 +128,16 @@ struct Row {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
+  // The largest of the elements of a piece (bf16: two at a time).
+  __device__ __forceinline__ static float largest(const uint4& r) {
+    if (sizeof(T) == 4)
+      return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+    uint32_t a, b;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(r.x), "r"(r.y));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(r.z), "r"(r.w));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
   __device__ __forceinline__ static void values(const uint4& r, float (&f)[E]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -139,6 +151,33 @@ struct Row {
     }
   }
 };
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 __device__ __forceinline__ uint32_t ld_dsmem_u32(const void* p, uint32_t rank) {
   uint32_t v;
@@ -172,14 +211,15 @@ struct Shared {
   unsigned long long cand[kCap];
   unsigned long long top[kMaxTop];
   unsigned long long all[8 * kMaxTop];
-  State warp_state[kWarps];
+  float warp_max[kWarps];
+  float2 warp_sum[kWarps];
   unsigned long long bound;
   int n_winners, n_cand;
 };
 
 template <typename T, int CL>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
-  constexpr int E = Row<T>::E, P = Row<T>::P, SEGS = kSegs / CL;
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
+  constexpr int E = Row<T>::E, SEGS = kSegs / CL;
   griddep_launch_dependents();
   griddep_wait();
   __shared__ Shared sh;
@@ -204,21 +244,31 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
   float best = -INFINITY;
   const int v_end = min((rank + 1) * SEGS * x.per_seg, x.pieces);
   int i = 0, v = rank * SEGS * x.per_seg, stop = min(v + x.per_seg, x.pieces);
+  constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf throughout
   auto fetch = [&](int at, int end, uint4 (&raw)[P]) {
+    if (at >= x.inner0 && min(at + kThreads * P, end) <= x.inner1) {
+      const T* first = x.x + (at + tid) * E - x.shift;
+      const int left = end - at - tid;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        raw[p] = p * kThreads < left ? ld_u4(first + p * kThreads * E) : make_uint4(kNone, kNone, kNone, kNone);
+      return;
+    }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int w = at + tid + p * kThreads;
-      constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
       raw[p] = w < end ? x.load(w) : make_uint4(kNone, kNone, kNone, kNone);
     }
   };
   uint4 raw[P];
   fetch(v, stop, raw);
+  int left = stop - v - tid;  // of this thread's pieces, kThreads apart, those below it are there
 #pragma unroll 1
   while (true) {
     uint4 now[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) now[p] = raw[p];
+    const int here = left;
     v += kThreads * P;
     const bool ends = v >= stop;
     if (ends) {
@@ -226,14 +276,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
       stop = min(v + x.per_seg, x.pieces);
     }
     if (i + ends < SEGS && v < v_end) fetch(v, stop, raw);
-    float mt = -INFINITY;
+    left = stop - v - tid;
+    float mt = Row<T>::largest(now[0]);
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float f[E];
-      Row<T>::values(now[p], f);
-#pragma unroll
-      for (int j = 0; j < E; j += 2) mt = fmaxf(mt, fmaxf(f[j], f[j + 1]));
-    }
+    for (int p = 1; p < P; ++p) mt = fmaxf(mt, Row<T>::largest(now[p]));
     if (mt > st.m) {
       if (st.m != -INFINITY) {
         const float d = fmaxf(__fsub_rn(st.m, mt), kLeast), c = ex2_approx(__fmul_rn(d, kLog2e));
@@ -243,23 +289,42 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
       st.m = mt;
     }
     const float m = st.m == -INFINITY ? 0.f : st.m;
-    float s2 = 0.f, t2 = 0.f;  // odd elements: two chains of dependent adds
+    const uint64_t neg = pack2(-m, -m), log2e = pack2(kLog2e, kLog2e);
+    uint64_t s2[2] = {0, 0}, t2[2] = {0, 0};
 #pragma unroll
     for (int p = 0; p < P; ++p) {
+      if (p * kThreads >= here) break;
       float f[E];
       Row<T>::values(now[p], f);
 #pragma unroll
       for (int j = 0; j < E; j += 2) {
-        const float d = __fsub_rn(f[j], m), e = ex2_approx(__fmul_rn(d, kLog2e));
-        st.s = __fadd_rn(st.s, e);
-        st.t = __fmaf_rn(e, fmaxf(d, kLeast), st.t);  // e = 0 at d = -inf: the product is 0
-        const float d2 = __fsub_rn(f[j + 1], m), e2 = ex2_approx(__fmul_rn(d2, kLog2e));
-        s2 = __fadd_rn(s2, e2);
-        t2 = __fmaf_rn(e2, fmaxf(d2, kLeast), t2);
+        const uint64_t d = add2(pack2(f[j], f[j + 1]), neg);
+        const float2 y = unpack2(mul2(d, log2e));
+        const uint64_t e = pack2(ex2_approx(y.x), ex2_approx(y.y));
+        s2[(j / 2) & 1] = add2(s2[(j / 2) & 1], e);
+        t2[(j / 2) & 1] = fma2(e, d, t2[(j / 2) & 1]);
       }
     }
-    st.s = __fadd_rn(st.s, s2);
-    st.t = __fadd_rn(st.t, t2);
+    const float2 sa = unpack2(add2(s2[0], s2[1])), ta = unpack2(add2(t2[0], t2[1]));
+    float tt = __fadd_rn(ta.x, ta.y);
+    if (tt != tt) {
+      // 0 * -inf of a masked token (or a NaN, which s has too): once more, with
+      // a large number for the infinity
+      tt = 0.f;
+#pragma unroll 1
+      for (int p = 0; p < P; ++p) {
+        float f[E];
+        Row<T>::values(now[0], f);
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const float d = __fsub_rn(f[j], m);
+          tt = __fmaf_rn(ex2_approx(__fmul_rn(d, kLog2e)), fmaxf(d, kLeast), tt);
+        }
+        now[0] = now[1], now[1] = now[2], now[2] = now[3];
+      }
+    }
+    st.s = __fadd_rn(st.s, __fadd_rn(sa.x, sa.y));
+    st.t = __fadd_rn(st.t, tt);
     if (!ends) continue;
     // (where a NaN was among the elements s is one, whatever m is)
     best = fmaxf(best, st.m);
@@ -278,7 +343,6 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
     if (++i == SEGS) break;
     st = {-INFINITY, 0.f, 0.f};
     if (v >= v_end) {  // segments without a piece (short rows) join as empty ones
-      constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
 #pragma unroll
       for (int p = 0; p < P; ++p) raw[p] = make_uint4(kNone, kNone, kNone, kNone);
     }
@@ -342,24 +406,27 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
         if (wins) sh.winners[atomicAdd(&sh.n_winners, 1)] = tid;
       }
       __syncthreads();
-      // the winners' elements at or above the bound: a warp takes a winner
-      for (int w = warp; w < sh.n_winners; w += kWarps) {
-        const int grp = sh.winners[w];
-        for (int i = 0; i < SEGS; ++i) {
-          const int v0 = (rank * SEGS + i) * x.per_seg, v1 = min(v0 + x.per_seg, x.pieces);
-          for (int v = v0 + 4 * grp + (lane & 3) + (lane >> 2) * kThreads; v < v1; v += 8 * kThreads) {
-            float f[E];
-            Row<T>::values(x.load(v), f);
+      // the winners' elements at or above the bound, a piece a thread; the
+      // comparison by value leaves few keys to be formed
+      const float least = logit_of(bound);
+      const int each = (x.per_seg + kThreads - 1) / kThreads * 4;  // pieces of a group in a segment
+      for (int n = tid; n < sh.n_winners * SEGS * each; n += kThreads) {
+        const int pair = n / each, q = n - pair * each;
+        const int v0 = (rank * SEGS + pair % SEGS) * x.per_seg;
+        const int v = v0 + (q >> 2) * kThreads + 4 * sh.winners[pair / SEGS] + (q & 3);
+        if (v >= min(v0 + x.per_seg, x.pieces)) continue;
+        const uint4 piece = x.load(v);
+        if (!by_key && Row<T>::largest(piece) < least) continue;
+        float f[E];
+        Row<T>::values(piece, f);
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-              const int at = v * E - x.shift + j;
-              if (at < 0 || at >= x.vocab) continue;
-              const unsigned long long key = key_of(f[j], at);
-              if (key >= bound) {
-                const int n = atomicAdd(&sh.n_cand, 1);
-                if (n < kCap) sh.cand[n] = key;
-              }
-            }
+        for (int j = 0; j < E; ++j) {
+          const int at = v * E - x.shift + j;
+          if (f[j] < least || at < 0 || at >= x.vocab) continue;
+          const unsigned long long key = key_of(f[j], at);
+          if (key >= bound) {
+            const int c = atomicAdd(&sh.n_cand, 1);
+            if (c < kCap) sh.cand[c] = key;
           }
         }
       }
@@ -412,23 +479,34 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(Args a) {
       sh.all[tid] = key;
     }
     join_tree(c);
+    // the row's largest logit, every thread's sums for it, and their sum
     State st = c[0];
+    float m = st.m;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      State other;
-      other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-      other.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-      other.t = __shfl_xor_sync(0xffffffffu, st.t, o);
-      st = (lane & o) ? join(other, st) : join(st, other);
-    }
-    if (lane == 0) sh.warp_state[warp] = st;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) sh.warp_max[warp] = m;
     __syncthreads();
-    State ws[kWarps];
+    m = sh.warp_max[0];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) ws[i] = sh.warp_state[i];
-    join_tree(ws);
-    const float m = ws[0].m, log_s = logf(ws[0].s);
-    if (a.entropy && tid == 0) a.entropy[row] = __fsub_rn(log_s, __fdiv_rn(ws[0].t, ws[0].s));
+    for (int i = 1; i < kWarps; ++i) m = fmaxf(m, sh.warp_max[i]);
+    const float d = st.m == -INFINITY ? 0.f : fmaxf(__fsub_rn(st.m, m), kLeast), f = ex2_approx(__fmul_rn(d, kLog2e));
+    st.t = __fmul_rn(__fmaf_rn(st.s, d, st.t), f);
+    st.s = __fmul_rn(st.s, f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      st.s = __fadd_rn(st.s, __shfl_xor_sync(0xffffffffu, st.s, o));
+      st.t = __fadd_rn(st.t, __shfl_xor_sync(0xffffffffu, st.t, o));
+    }
+    if (lane == 0) sh.warp_sum[warp] = make_float2(st.s, st.t);
+    __syncthreads();
+    float sum = sh.warp_sum[0].x, sum_t = sh.warp_sum[0].y;
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) {
+      sum = __fadd_rn(sum, sh.warp_sum[i].x);
+      sum_t = __fadd_rn(sum_t, sh.warp_sum[i].y);
+    }
+    const float log_s = logf(sum);
+    if (a.entropy && tid == 0) a.entropy[row] = __fsub_rn(log_s, __fdiv_rn(sum_t, sum));
     auto log_prob = [&](float logit) { return __fsub_rn(__fsub_rn(logit, m), log_s); };
     if (id >= 0 && id < a.vocab) a.token_lp[static_cast<size_t>(row) * a.n_tokens + tid] = log_prob(given);
     for (int j = tid + kThreads; j < a.n_tokens; j += kThreads) {
