@@ -10,10 +10,10 @@
 //
 // The k best: every thread keeps the largest of its elements.  Four lanes'
 // largest make a group; of the CTA's 64 groups the k-th largest is a bound that
-// at least k elements reach, and only the groups that reach it (k, and ties)
-// can hold one of the k best.  Their elements are read again (a 64th of the row
-// each, from L2), those at or above the bound are collected (a few more than k)
-// and ranked by counting.
+// at least k elements reach, and only threads whose largest reaches it (k, and
+// some more) can hold one of the k best.  Their elements are read again (a 256th
+// of the row each, from L2), those at or above the bound are collected (a few
+// more than k) and ranked by counting.
 //
 // A row has 8 fixed segments, and thread t of a segment fixed elements; states
 // join over segments first, in a fixed tree, then over threads.  1, 2, 4 or 8
@@ -205,9 +205,9 @@ __device__ __forceinline__ void join_tree(State (&a)[N]) {
 
 struct Shared {
   State state[kThreads];
-  float best[kGroups];
+  alignas(16) float best[kGroups];
   unsigned long long best_key[kGroups];
-  int winners[kGroups];
+  int winners[kThreads];
   unsigned long long cand[kCap];
   unsigned long long top[kMaxTop];
   unsigned long long all[8 * kMaxTop];
@@ -228,58 +228,33 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
   const int row = blockIdx.x / CL;
   const Row<T> x(a.logits, a.stride, row, a.vocab);
 
-  // the given tokens' logits, far ahead of their use
-  int id = -1;
-  float given = 0.f;
-  if (rank == 0 && tid < a.n_tokens) {
-    id = ld_s32(a.tokens + static_cast<size_t>(row) * a.n_tokens + tid);
-    if (id >= a.vocab) flag_error(a.status, kStatusIndex);
-    if (id >= 0 && id < a.vocab) given = Row<T>::one(x.x + id);
-  }
-
   // ---- one pass: (m, s, t) of each segment's elements of this thread, the
   // segments joined as the leaves of a binary tree; and the largest element.
-  // The next pieces are on their way while these are worked on.
+  // Once a piece has been worked on its registers take the next one.
   State st = {-INFINITY, 0.f, 0.f}, half, quarter, eighth;
   float best = -INFINITY;
-  const int v_end = min((rank + 1) * SEGS * x.per_seg, x.pieces);
-  int i = 0, v = rank * SEGS * x.per_seg, stop = min(v + x.per_seg, x.pieces);
   constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf throughout
-  auto fetch = [&](int at, int end, uint4 (&raw)[P]) {
-    if (at >= x.inner0 && min(at + kThreads * P, end) <= x.inner1) {
-      const T* first = x.x + (at + tid) * E - x.shift;
-      const int left = end - at - tid;
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-        raw[p] = p * kThreads < left ? ld_u4(first + p * kThreads * E) : make_uint4(kNone, kNone, kNone, kNone);
-      return;
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int w = at + tid + p * kThreads;
-      raw[p] = w < end ? x.load(w) : make_uint4(kNone, kNone, kNone, kNone);
-    }
-  };
   uint4 raw[P];
-  fetch(v, stop, raw);
-  int left = stop - v - tid;  // of this thread's pieces, kThreads apart, those below it are there
+  // the P pieces of this thread, kThreads apart from `at` on and below `end`
+  int at = rank * SEGS * x.per_seg, end = min(at + x.per_seg, x.pieces);
+  auto inside = [&] { return at >= x.inner0 && min(at + kThreads * P, end) <= x.inner1; };
+  auto fetch = [&](int p, bool in) {
+    const int w = at + tid + p * kThreads;
+    raw[p] = make_uint4(kNone, kNone, kNone, kNone);
+    if (w < end) raw[p] = in ? ld_u4(x.x + w * E - x.shift) : x.load(w);
+  };
+  {
+    const bool in = inside();
+#pragma unroll
+    for (int p = 0; p < P; ++p) fetch(p, in);
+  }
+  int id = -1;  // a given token, far ahead of its use
+  if (rank == 0 && tid < a.n_tokens) id = ld_s32(a.tokens + static_cast<size_t>(row) * a.n_tokens + tid);
 #pragma unroll 1
-  while (true) {
-    uint4 now[P];
+  for (int i = 0; i < SEGS;) {
+    float mt = Row<T>::largest(raw[0]);
 #pragma unroll
-    for (int p = 0; p < P; ++p) now[p] = raw[p];
-    const int here = left;
-    v += kThreads * P;
-    const bool ends = v >= stop;
-    if (ends) {
-      v = (rank * SEGS + i + 1) * x.per_seg;
-      stop = min(v + x.per_seg, x.pieces);
-    }
-    if (i + ends < SEGS && v < v_end) fetch(v, stop, raw);
-    left = stop - v - tid;
-    float mt = Row<T>::largest(now[0]);
-#pragma unroll
-    for (int p = 1; p < P; ++p) mt = fmaxf(mt, Row<T>::largest(now[p]));
+    for (int p = 1; p < P; ++p) mt = fmaxf(mt, Row<T>::largest(raw[p]));
     if (mt > st.m) {
       if (st.m != -INFINITY) {
         const float d = fmaxf(__fsub_rn(st.m, mt), kLeast), c = ex2_approx(__fmul_rn(d, kLog2e));
@@ -291,40 +266,33 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
     const float m = st.m == -INFINITY ? 0.f : st.m;
     const uint64_t neg = pack2(-m, -m), log2e = pack2(kLog2e, kLog2e);
     uint64_t s2[2] = {0, 0}, t2[2] = {0, 0};
+    const int here = end - at - tid;
+    at += kThreads * P;
+    const bool ends = at >= end;
+    if (ends) {
+      at = (rank * SEGS + i + 1) * x.per_seg;
+      end = i + 1 < SEGS ? min(at + x.per_seg, x.pieces) : at;
+    }
+    const bool in = inside();
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      if (p * kThreads >= here) break;
       float f[E];
-      Row<T>::values(now[p], f);
+      Row<T>::values(raw[p], f);
+      fetch(p, in);
+      if (p * kThreads >= here) continue;
 #pragma unroll
       for (int j = 0; j < E; j += 2) {
         const uint64_t d = add2(pack2(f[j], f[j + 1]), neg);
-        const float2 y = unpack2(mul2(d, log2e));
+        const float2 y = unpack2(mul2(d, log2e)), dd = unpack2(d);
         const uint64_t e = pack2(ex2_approx(y.x), ex2_approx(y.y));
         s2[(j / 2) & 1] = add2(s2[(j / 2) & 1], e);
-        t2[(j / 2) & 1] = fma2(e, d, t2[(j / 2) & 1]);
+        // e = 0 at d = -inf: the product is 0
+        t2[(j / 2) & 1] = fma2(e, pack2(fmaxf(dd.x, kLeast), fmaxf(dd.y, kLeast)), t2[(j / 2) & 1]);
       }
     }
     const float2 sa = unpack2(add2(s2[0], s2[1])), ta = unpack2(add2(t2[0], t2[1]));
-    float tt = __fadd_rn(ta.x, ta.y);
-    if (tt != tt) {
-      // 0 * -inf of a masked token (or a NaN, which s has too): once more, with
-      // a large number for the infinity
-      tt = 0.f;
-#pragma unroll 1
-      for (int p = 0; p < P; ++p) {
-        float f[E];
-        Row<T>::values(now[0], f);
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const float d = __fsub_rn(f[j], m);
-          tt = __fmaf_rn(ex2_approx(__fmul_rn(d, kLog2e)), fmaxf(d, kLeast), tt);
-        }
-        now[0] = now[1], now[1] = now[2], now[2] = now[3];
-      }
-    }
     st.s = __fadd_rn(st.s, __fadd_rn(sa.x, sa.y));
-    st.t = __fadd_rn(st.t, tt);
+    st.t = __fadd_rn(st.t, __fadd_rn(ta.x, ta.y));
     if (!ends) continue;
     // (where a NaN was among the elements s is one, whatever m is)
     best = fmaxf(best, st.m);
@@ -340,15 +308,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
     } else {
       half = st;
     }
-    if (++i == SEGS) break;
-    st = {-INFINITY, 0.f, 0.f};
-    if (v >= v_end) {  // segments without a piece (short rows) join as empty ones
-#pragma unroll
-      for (int p = 0; p < P; ++p) raw[p] = make_uint4(kNone, kNone, kNone, kNone);
-    }
+    if (++i < SEGS) st = {-INFINITY, 0.f, 0.f};
   }
   const State mine = st;
   sh.state[tid] = mine;
+  float given = 0.f;
+  if (id >= 0 && id < a.vocab) given = Row<T>::one(x.x + id);
 
   // ---- the k best of this CTA's segments, in falling order in sh.top
   const int k = a.top_k;
@@ -363,19 +328,23 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
     bool by_key = __syncthreads_or(mine.s != mine.s) != 0;
     // rank of each group among the groups, equal ones by the lower group
     if (tid < kGroups) {
-      const float mine = sh.best[tid];
+      const float own = sh.best[tid];
       int above = 0;
-#pragma unroll 8
-      for (int i = 0; i < kGroups; ++i) above += sh.best[i] > mine || (sh.best[i] == mine && i < tid);
-      if (above == k - 1) sh.bound = static_cast<unsigned long long>(order_of(mine)) << 32;
+#pragma unroll
+      for (int i = 0; i < kGroups; i += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(sh.best + i);
+        above += (o.x > own || (o.x == own && i < tid)) + (o.y > own || (o.y == own && i + 1 < tid)) +
+                 (o.z > own || (o.z == own && i + 2 < tid)) + (o.w > own || (o.w == own && i + 3 < tid));
+      }
+      if (above == k - 1) sh.bound = static_cast<unsigned long long>(order_of(own)) << 32;
     }
     __syncthreads();
     bool keyed = false;
+    unsigned long long top = 0;  // of this thread's keys, once they are looked at
 #pragma unroll 1
     while (true) {
       if (by_key && !keyed) {
         // the exact largest key of each group's elements, and the k-th of them
-        unsigned long long top = 0;
         for (int v0 = rank * SEGS * x.per_seg, i = 0; i < SEGS; ++i, v0 += x.per_seg)
           for (int v = v0 + tid; v < min(v0 + x.per_seg, x.pieces); v += kThreads) {
             float f[E];
@@ -386,34 +355,31 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
               if (at >= 0 && at < x.vocab) top = max(top, key_of(f[j], at));
             }
           }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        if ((lane & 3) == 0) sh.best_key[tid >> 2] = top;
+        unsigned long long most = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        if ((lane & 3) == 0) sh.best_key[tid >> 2] = most;
         __syncthreads();
         if (tid < kGroups) {
-          top = sh.best_key[tid];
+          most = sh.best_key[tid];
           int above = 0;
-          for (int i = 0; i < kGroups; ++i) above += sh.best_key[i] > top || (sh.best_key[i] == top && i < tid);
-          if (above == k - 1) sh.bound = max(sh.bound, top);
+          for (int i = 0; i < kGroups; ++i) above += sh.best_key[i] > most || (sh.best_key[i] == most && i < tid);
+          if (above == k - 1) sh.bound = max(sh.bound, most);
         }
         keyed = true;
         __syncthreads();
       }
       const unsigned long long bound = sh.bound;
-      if (tid < kGroups) {
-        const bool wins = by_key ? sh.best_key[tid] >= bound && sh.best_key[tid] != 0
-                                 : order_of(sh.best[tid]) >= static_cast<uint32_t>(bound >> 32);
-        if (wins) sh.winners[atomicAdd(&sh.n_winners, 1)] = tid;
-      }
+      if (by_key ? top >= bound && top != 0 : order_of(best) >= static_cast<uint32_t>(bound >> 32))
+        sh.winners[atomicAdd(&sh.n_winners, 1)] = tid;
       __syncthreads();
       // the winners' elements at or above the bound, a piece a thread; the
       // comparison by value leaves few keys to be formed
       const float least = logit_of(bound);
-      const int each = (x.per_seg + kThreads - 1) / kThreads * 4;  // pieces of a group in a segment
+      const int each = (x.per_seg + kThreads - 1) / kThreads;  // pieces of a thread in a segment
       for (int n = tid; n < sh.n_winners * SEGS * each; n += kThreads) {
         const int pair = n / each, q = n - pair * each;
         const int v0 = (rank * SEGS + pair % SEGS) * x.per_seg;
-        const int v = v0 + (q >> 2) * kThreads + 4 * sh.winners[pair / SEGS] + (q & 3);
+        const int v = v0 + q * kThreads + sh.winners[pair / SEGS];
         if (v >= min(v0 + x.per_seg, x.pieces)) continue;
         const uint4 piece = x.load(v);
         if (!by_key && Row<T>::largest(piece) < least) continue;
@@ -508,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
     const float log_s = logf(sum);
     if (a.entropy && tid == 0) a.entropy[row] = __fsub_rn(log_s, __fdiv_rn(sum_t, sum));
     auto log_prob = [&](float logit) { return __fsub_rn(__fsub_rn(logit, m), log_s); };
+    if (id >= a.vocab) flag_error(a.status, kStatusIndex);
     if (id >= 0 && id < a.vocab) a.token_lp[static_cast<size_t>(row) * a.n_tokens + tid] = log_prob(given);
     for (int j = tid + kThreads; j < a.n_tokens; j += kThreads) {
       const size_t at = static_cast<size_t>(row) * a.n_tokens + j;
