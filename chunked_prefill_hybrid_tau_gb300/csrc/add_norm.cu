@@ -10,7 +10,9 @@
 // code's.
 //
 // Reads 4 and writes 3 or 4 bytes an element, each once: HBM bounds it for
-// many rows, the chain load - sum - maximum - store for few.
+// many rows, the chain load - sum - maximum - store for few.  8192 x 7168 with a
+// scale per row: 68 us (floor 60.6 at the copy rate); one row of 4096 in blocks:
+// 2.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -240,7 +242,11 @@ extern "C" hb_status hb_add_rmsnorm(const void* x, const void* residual, const v
   a.inv_d = 1.0f / d;
   a.eps = eps;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // a warp a row up to 1024 columns (4 pieces a lane), the CTA above
+  // A warp a row up to 1024 columns (4 pieces a lane), the CTA above, whatever the
+  // rows, so that a row's sum has one order.  Measured, 57344 rows of 1024, bf16 /
+  // scale per row / per block: a warp 68 / 60 / 61 us, the CTA 78 / 101 / 90 (one
+  // row: 2.0 / 2.0 / 2.8 and 1.5 / 1.7 / 1.6); 28672 rows of 2048: a warp 69 / 60 /
+  // 71, the CTA 67 / 66 / 65, and one row 3.0 / 2.6 / 4.6 against 1.6 / 1.8 / 1.7.
   if (a.d8 <= 32) return add_rmsnorm_launch<1, 32>(a, format, s);
   if (a.d8 <= 64) return add_rmsnorm_launch<2, 32>(a, format, s);
   if (a.d8 <= 128) return add_rmsnorm_launch<4, 32>(a, format, s);

@@ -11,7 +11,7 @@
 // widened once, by a kernel ahead (widen_kernel), into scratch of the workspace
 // laid out for whole-block copies.  That scratch is bounded (kScratchKeys);
 // sequences behind its end are widened block by block beside the MMAs instead
-// (WIDEN: the same kernel with eight more warps), which takes 2.4 times as long.
+// (WIDEN: the same kernel with five more warps), which takes 2.4 times as long.
 //
 // Unit: two 128-row tiles of one kv head -- (row tile, q head) pairs in that
 // order, so with an even number of q heads per kv head two heads of the same

@@ -20,7 +20,12 @@
 // CTAs (a cluster) share a row's segments, more the fewer rows there are: the
 // arithmetic, and so every bit, is the same.
 //
-// Reads 4 or 2 bytes an element once: HBM bounds it for many rows.
+// Reads 4 or 2 bytes an element once: HBM bounds it for many rows, 2048 x 64000
+// bf16 in 67 us (floor 38.7 at the copy rate).  58 of these are the pass itself:
+// a CTA that starts, ends or joins has no loads in flight, and four CTAs of 64
+// registers cover that only in part (five spill); the 8 best cost 9 us, 32 cost 26.
+// One row takes 7 us, most of it in the cluster's barriers and the chain of the
+// selection.
 #include <cuda_bf16.h>
 
 #include "device.cuh"
@@ -519,7 +524,10 @@ hb_status logprobs_launch(const Args& a, int rows, cudaStream_t stream) {
 
 template <typename T>
 hb_status logprobs_rows(const Args& a, int rows, int num_sms, cudaStream_t stream) {
-  // as many CTAs a row as keep the grid within four a SM
+  // As many CTAs a row as keep the grid within four a SM, which is what is resident
+  // at a time.  Measured, fp32 rows of 32000 (L2 flushed, with the launch): 160 rows
+  // 19.4 us with 2 CTAs a row, 25.1 with 4, 32.6 with 8; 512 rows 27.9 with 1, 35.3
+  // with 2.
   const long long room = 4ll * num_sms;
   if (rows * 8ll <= room) return logprobs_launch<T, 8>(a, rows, stream);
   if (rows * 4ll <= room) return logprobs_launch<T, 4>(a, rows, stream);
