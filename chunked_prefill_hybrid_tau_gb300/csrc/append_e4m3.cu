@@ -30,7 +30,7 @@ using namespace dev;
 // thread owns 8 elements of a head's first half and the matching 8 of its
 // second half, so the rotation stays in the thread, and the norm's sum and the
 // maximum are shuffles among the head's d / 16 neighbouring lanes; two heads
-// in flight a thread.  8192 rows of 72 heads of 128 (floor 42.7 us at the copy
+// in flight a thread.  8192 rows of 72 heads of 128 (floor 43.3 us at the copy
 // rate): 46.5 us at 72 registers, as many CTAs as fit; 50.5 at 64, 56.7 at 56,
 // 53.8 at 80.
 constexpr int U = 2;

@@ -34,7 +34,7 @@ using namespace dev;
 using namespace kv8;
 
 // ---------------------------------------------------------------- decode rows
-// 64 rows of 513 to 8189 keys, 8 kv heads of 128 (floor 84.8 us at the copy rate):
+// 64 rows of 513 to 8189 keys, 8 kv heads of 128 (floor 86.1 us at the copy rate):
 // 101 us back to back.  16 warps with 3 stages of 16 keys each: 12 with 4 103, 8
 // with 6 128 (too few chains of conversions and MMAs in flight), 18 with 3 117 and
 // 24 with 2 134 (fewer registers a thread); 20 with 2 as fast here, but one row of

@@ -13,6 +13,15 @@
 // sequences behind its end are widened block by block beside the MMAs instead
 // (WIDEN: the same kernel with five more warps), which takes 2.4 times as long.
 //
+// The tensor pipe bounds it, 4 d_head FLOP a pair and q head: 2048 rows behind
+// 14336 keys, 56 q heads on 8 of 128, 700 us with the widening, floor 466 at
+// cuBLAS's bf16 rate; the pipe is 60% active.  What keeps it from more is the chain
+// S - softmax - P - PV of a tile: S and O of both tiles fill tensor memory, so a
+// tile's next S waits for its PV.  Shorter chains were slower, because each more
+// group of MMAs or exchange costs 200 to 400 clocks: steps of 64 keys, PV in two
+// halves (870 us), two warps to 32 rows that exchange their maxima (873); and so
+// was one issuing warp for both tiles (775).
+//
 // Unit: two 128-row tiles of one kv head -- (row tile, q head) pairs in that
 // order, so with an even number of q heads per kv head two heads of the same
 // rows -- and keys 0 .. last in blocks of 128 that both tiles use.

@@ -21,9 +21,10 @@
 // arithmetic, and so every bit, is the same.
 //
 // Reads 4 or 2 bytes an element once: HBM bounds it for many rows, 2048 x 64000
-// bf16 in 67 us (floor 38.7 at the copy rate).  58 of these are the pass itself:
-// a CTA that starts, ends or joins has no loads in flight, and four CTAs of 64
-// registers cover that only in part (five spill); the 8 best cost 9 us, 32 cost 26.
+// bf16 in 67 us (floor 39.2 at the copy rate).  58 of these are the pass itself:
+// the issue slots are 79% busy, 14 instructions an element, and a CTA that starts,
+// ends or joins has no loads in flight, which four CTAs of 64 registers cover only
+// in part (five spill); the 8 best cost 9 us, 32 cost 26.
 // One row takes 7 us, most of it in the cluster's barriers and the chain of the
 // selection.
 #include <cuda_bf16.h>
