@@ -21,10 +21,10 @@
 // arithmetic, and so every bit, is the same.
 //
 // Reads 4 or 2 bytes an element once: HBM bounds it for many rows, 2048 x 64000
-// bf16 in 67 us (floor 39.2 at the copy rate).  58 of these are the pass itself:
-// the issue slots are 79% busy, 14 instructions an element, and a CTA that starts,
+// bf16 in 59 us (floor 39.2 at the copy rate).  52 of these are the pass itself:
+// the issue slots are 79% busy, 13 instructions an element, and a CTA that starts,
 // ends or joins has no loads in flight, which four CTAs of 64 registers cover only
-// in part (five spill); the 8 best cost 9 us, 32 cost 26.
+// in part (five spill); the 8 best cost 7 us, 32 cost 22.
 // One row takes 7 us, most of it in the cluster's barriers and the chain of the
 // selection.
 #include <cuda_bf16.h>
@@ -63,6 +63,12 @@ struct Args {
 
 struct State {
   float m, s, t;
+};
+struct Yes {
+  static constexpr bool value = true;
+};
+struct No {
+  static constexpr bool value = false;
 };
 
 // The states of two parts of a row as one.
@@ -134,15 +140,23 @@ struct Row {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // The largest of the elements of a piece (bf16: two at a time).
-  __device__ __forceinline__ static float largest(const uint4& r) {
-    if (sizeof(T) == 4)
-      return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)), fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
-    uint32_t a, b;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(r.x), "r"(r.y));
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(r.z), "r"(r.w));
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
-    return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  __device__ __forceinline__ const uint4* first() const { return reinterpret_cast<const uint4*>(x - shift); }
+  // The largest of the elements of pieces (bf16: two at a time).
+  template <int N>
+  __device__ __forceinline__ static float largest(const uint4 (&r)[N]) {
+    auto more = [](uint32_t a, uint32_t b) {
+      if (sizeof(T) == 4) return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+      return a;
+    };
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t one = more(more(r[i].x, r[i].y), more(r[i].z, r[i].w));
+      m = i == 0 ? one : more(m, one);
+    }
+    if (sizeof(T) == 4) return __uint_as_float(m);
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
   __device__ __forceinline__ static void values(const uint4& r, float (&f)[E]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -211,6 +225,7 @@ __device__ __forceinline__ void join_tree(State (&a)[N]) {
 
 struct Shared {
   State state[kThreads];
+  State leaf[3][kThreads];  // of a thread alone: joined states of its first half, quarter, ... of segments
   alignas(16) float best[kGroups];
   unsigned long long best_key[kGroups];
   int winners[kThreads];
@@ -237,30 +252,31 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
   // ---- one pass: (m, s, t) of each segment's elements of this thread, the
   // segments joined as the leaves of a binary tree; and the largest element.
   // Once a piece has been worked on its registers take the next one.
-  State st = {-INFINITY, 0.f, 0.f}, half, quarter, eighth;
+  State st = {-INFINITY, 0.f, 0.f};
   float best = -INFINITY;
   constexpr uint32_t kNone = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf throughout
   uint4 raw[P];
   // the P pieces of this thread, kThreads apart from `at` on and below `end`
   int at = rank * SEGS * x.per_seg, end = min(at + x.per_seg, x.pieces);
   auto inside = [&] { return at >= x.inner0 && min(at + kThreads * P, end) <= x.inner1; };
-  auto fetch = [&](int p, bool in) {
+  const uint4* from;  // the first of them
+  auto fetch = [&](int p, auto in) {
     const int w = at + tid + p * kThreads;
     raw[p] = make_uint4(kNone, kNone, kNone, kNone);
-    if (w < end) raw[p] = in ? ld_u4(x.x + w * E - x.shift) : x.load(w);
+    if (w < end) raw[p] = decltype(in)::value ? ld_u4(from + p * kThreads) : x.load(w);
   };
-  {
-    const bool in = inside();
+  auto fetch_all = [&](auto in) {
+    from = x.first() + at + tid;
 #pragma unroll
     for (int p = 0; p < P; ++p) fetch(p, in);
-  }
+  };
+  if (inside()) fetch_all(Yes{});
+  else fetch_all(No{});
   int id = -1;  // a given token, far ahead of its use
   if (rank == 0 && tid < a.n_tokens) id = ld_s32(a.tokens + static_cast<size_t>(row) * a.n_tokens + tid);
 #pragma unroll 1
   for (int i = 0; i < SEGS;) {
-    float mt = Row<T>::largest(raw[0]);
-#pragma unroll
-    for (int p = 1; p < P; ++p) mt = fmaxf(mt, Row<T>::largest(raw[p]));
+    const float mt = Row<T>::largest(raw);
     if (mt > st.m) {
       if (st.m != -INFINITY) {
         const float d = fmaxf(__fsub_rn(st.m, mt), kLeast), c = ex2_approx(__fmul_rn(d, kLog2e));
@@ -272,47 +288,45 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
     const float m = st.m == -INFINITY ? 0.f : st.m;
     const uint64_t neg = pack2(-m, -m), log2e = pack2(kLog2e, kLog2e);
     uint64_t s2[2] = {0, 0}, t2[2] = {0, 0};
-    const int here = end - at - tid;
+    const int here = end - at;
     at += kThreads * P;
     const bool ends = at >= end;
     if (ends) {
       at = (rank * SEGS + i + 1) * x.per_seg;
       end = i + 1 < SEGS ? min(at + x.per_seg, x.pieces) : at;
     }
-    const bool in = inside();
+    auto work = [&](auto in) {
+      from = x.first() + at + tid;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float f[E];
-      Row<T>::values(raw[p], f);
-      fetch(p, in);
-      if (p * kThreads >= here) continue;
+      for (int p = 0; p < P; ++p) {
+        float f[E];
+        Row<T>::values(raw[p], f);
+        fetch(p, in);
+        // of no thread (those of some threads only are -inf elsewhere and add 0)
+        if (p * kThreads >= here) continue;
 #pragma unroll
-      for (int j = 0; j < E; j += 2) {
-        const uint64_t d = add2(pack2(f[j], f[j + 1]), neg);
-        const float2 y = unpack2(mul2(d, log2e)), dd = unpack2(d);
-        const uint64_t e = pack2(ex2_approx(y.x), ex2_approx(y.y));
-        s2[(j / 2) & 1] = add2(s2[(j / 2) & 1], e);
-        // e = 0 at d = -inf: the product is 0
-        t2[(j / 2) & 1] = fma2(e, pack2(fmaxf(dd.x, kLeast), fmaxf(dd.y, kLeast)), t2[(j / 2) & 1]);
+        for (int j = 0; j < E; j += 2) {
+          const uint64_t d = add2(pack2(f[j], f[j + 1]), neg);
+          const float2 y = unpack2(mul2(d, log2e)), dd = unpack2(d);
+          const uint64_t e = pack2(ex2_approx(y.x), ex2_approx(y.y));
+          s2[(j / 2) & 1] = add2(s2[(j / 2) & 1], e);
+          // e = 0 at d = -inf: the product is 0
+          t2[(j / 2) & 1] = fma2(e, pack2(fmaxf(dd.x, kLeast), fmaxf(dd.y, kLeast)), t2[(j / 2) & 1]);
+        }
       }
-    }
+    };
+    if (inside()) work(Yes{});
+    else work(No{});
     const float2 sa = unpack2(add2(s2[0], s2[1])), ta = unpack2(add2(t2[0], t2[1]));
     st.s = __fadd_rn(st.s, __fadd_rn(sa.x, sa.y));
     st.t = __fadd_rn(st.t, __fadd_rn(ta.x, ta.y));
     if (!ends) continue;
     // (where a NaN was among the elements s is one, whatever m is)
     best = fmaxf(best, st.m);
-    if (i & 1) {
-      st = join(half, st);
-      if (i & 2) {
-        st = join(quarter, st);
-        if (i & 4) st = join(eighth, st);
-        else eighth = st;
-      } else {
-        quarter = st;
-      }
-    } else {
-      half = st;
+    if (SEGS > 1) {
+      int level = 0;
+      for (; i >> level & 1; ++level) st = join(sh.leaf[level][tid], st);
+      if (level < 3) sh.leaf[level][tid] = st;
     }
     if (++i < SEGS) st = {-INFINITY, 0.f, 0.f};
   }
@@ -387,10 +401,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
         const int v0 = (rank * SEGS + pair % SEGS) * x.per_seg;
         const int v = v0 + q * kThreads + sh.winners[pair / SEGS];
         if (v >= min(v0 + x.per_seg, x.pieces)) continue;
-        const uint4 piece = x.load(v);
+        const uint4 piece[1] = {x.load(v)};
         if (!by_key && Row<T>::largest(piece) < least) continue;
         float f[E];
-        Row<T>::values(piece, f);
+        Row<T>::values(piece[0], f);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
           const int at = v * E - x.shift + j;
@@ -527,8 +541,7 @@ template <typename T>
 hb_status logprobs_rows(const Args& a, int rows, int num_sms, cudaStream_t stream) {
   // As many CTAs a row as keep the grid within four a SM, which is what is resident
   // at a time.  Measured, fp32 rows of 32000 (L2 flushed, with the launch): 160 rows
-  // 19.4 us with 2 CTAs a row, 25.1 with 4, 32.6 with 8; 512 rows 27.9 with 1, 35.3
-  // with 2.
+  // 19 us with 2 CTAs a row, 25 with 4, 33 with 8; 512 rows 28 with 1, 35 with 2.
   const long long room = 4ll * num_sms;
   if (rows * 8ll <= room) return logprobs_launch<T, 8>(a, rows, stream);
   if (rows * 4ll <= room) return logprobs_launch<T, 4>(a, rows, stream);
