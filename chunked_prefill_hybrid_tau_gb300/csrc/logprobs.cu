@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
       st.m = mt;
     }
     const float m = st.m == -INFINITY ? 0.f : st.m;
-    const uint64_t neg = pack2(-m, -m), log2e = pack2(kLog2e, kLog2e);
+    const uint64_t log2e = pack2(kLog2e, kLog2e);
     uint64_t s2[2] = {0, 0}, t2[2] = {0, 0};
     const int here = end - at;
     at += kThreads * P;
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(Args a) {
         if (p * kThreads >= here) continue;
 #pragma unroll
         for (int j = 0; j < E; j += 2) {
-          const uint64_t d = add2(pack2(f[j], f[j + 1]), neg);
+          const uint64_t d = pack2(__fsub_rn(f[j], m), __fsub_rn(f[j + 1], m));
           const float2 y = unpack2(mul2(d, log2e)), dd = unpack2(d);
           const uint64_t e = pack2(ex2_approx(y.x), ex2_approx(y.y));
           s2[(j / 2) & 1] = add2(s2[(j / 2) & 1], e);
