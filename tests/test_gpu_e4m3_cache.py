@@ -251,6 +251,20 @@ def test_attention_rows_do_not_depend_on_the_batch():
         hb.hb_check_status()
 
 
+@pytest.mark.parametrize("n_q,n_kv,d", [(8, 2, 128), (5, 1, 64)])
+def test_attention_hints_move_work_only(n_q, n_kv, d):
+    """Whatever the plan says of its work (SMs of either kind, tiles of a unit)."""
+    dims = dims_of(n_q, n_kv, d)
+    hp, q, cache, _ = batch(dims, [40, 700, 1300], [(900, 300)], 3 + 290, 290, seed=17)
+    dp = hb.DevicePlan(hp)
+    want = attend(hp, q, cache, dims, dp=dp)
+    seen = [dp.hints, (0, 0, 0), (1, 10 ** 9, 2 ** 20), (10 ** 9, 1, 1), (0, 290 * 600, 290), (10 ** 6, 290 * 600, 10 ** 5)]
+    for hints in seen[1:]:
+        dp.hints = hints
+        assert torch.equal(attend(hp, q, cache, dims, dp=dp), want), hints
+    hb.hb_check_status()
+
+
 @pytest.mark.parametrize("n_q,n_kv,d", [(4, 1, 128), (3, 1, 64)])
 def test_attention_more_chunk_keys_than_are_widened_ahead(n_q, n_kv, d):
     """Sequences behind the end of the workspace's scratch: the same bits as alone."""
