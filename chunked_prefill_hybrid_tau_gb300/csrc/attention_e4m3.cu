@@ -541,56 +541,45 @@ hb_status decode_launch(const DeviceCtx& ctx, const CUtensorMap& tmK, const CUte
                     tmK, tmV, p);
 }
 
-// How the SMs are shared when both kinds of rows run side by side on disjoint
-// ones (each kernel's CTAs fill an SM's shared memory), and the tiles of a chunk
-// unit, from the plan's hints.  sms 0: one kind after the other on all SMs.  It
-// only moves work: no row's result depends on it.
-//   chunk : units of one or two 128-row tiles of a kv head, kUnitUs and kBlockUs
-//           per 128 keys each, in rounds of n on n SMs: two tiles overlap on the
-//           tensor pipe, one is done sooner where SMs are left;
+// SMs for the chunk kernel when both kinds of rows run side by side on
+// disjoint SMs (each kernel's CTAs fill an SM's shared memory), from the plan's
+// hints; 0: one after the other on all SMs.  It only moves work: no row's
+// result depends on it.
+//   chunk : units of a 128-row tile of a q head, kUnitUs and kBlockUs per 128
+//           keys each, in rounds of n on n SMs;
 //   decode: bytes at min(kDecodeBw, n kDecodeBwPerSm);
 //   side by side: the longer, and kBeside of the shorter;
 //   one after the other: both, and kTurnUs.
-// Measured, 32 heads: 480 chunk rows behind 1024 keys beside 32 decodes 54.7 us
-// on 64 SMs (as chosen), 67 on 48, 70 on 80, 68.6 one after the other; 2016 rows
-// behind 4096 keys 209 us one after the other (as chosen), 220 on 128 SMs.  The
-// 480 rows alone: 28.9 us with one tile a unit (as chosen), 36.8 with two; 1024
-// rows without a prefix 30.3 and 29.4 (as chosen).
-constexpr double kUnitUs[2] = {3.0, 6.0};     // one tile, two
-constexpr double kBlockUs[2] = {1.65, 2.0};   // d_head 128
-constexpr double kDecodeBwPerSm = 50000.0;    // bytes per us
+// Measured, 32 heads: 480 chunk rows behind 1024 keys beside 32 decodes 51.8 us
+// on 43 SMs (as chosen) and one after the other, 55 on 64, 60 on 32; beside 8
+// decodes 35.4 on 64 (as chosen), 38 one after the other; 2016 rows behind 4096
+// keys beside 32 decodes 175 on 128 (as chosen), 181 one after the other.
+constexpr double kUnitUs = 3.5;
+constexpr double kBlockUs = 0.75;            // d_head 128
+constexpr double kDecodeBwPerSm = 44000.0;   // bytes per us
 constexpr double kDecodeBw = 6.0e6;
-constexpr double kBeside = 0.25;
-constexpr double kTurnUs = 5.0;
+constexpr double kBeside = 0.12;
+constexpr double kTurnUs = 7.0;
 
-struct Shares {
-  int sms;    // of the chunk kernel; 0: all
-  int tiles;  // of a unit
-};
-
-Shares shares(const DeviceCtx& ctx, const hb_device_plan& plan, const hb_layer_dims& dm) {
+int chunk_sms(const DeviceCtx& ctx, const hb_device_plan& plan, const hb_layer_dims& dm) {
   const int S = ctx.num_sms;
-  if (plan.chunk_pairs <= 0 || plan.decode_pairs < 0 || plan.chunk_rows <= 0 || S < 4) return {0, 2};
-  const double dscale = 0.5 + 0.5 * dm.d_head / 128.0;
+  if (plan.chunk_pairs <= 0 || plan.decode_pairs <= 0 || plan.chunk_rows <= 0 || S < 4) return 0;
+  const double dscale = dm.d_head / 128.0;
   const double tiles = ceil(static_cast<double>(plan.chunk_rows) / 128.0);
-  const double blocks = (static_cast<double>(plan.chunk_pairs) / 16384.0 + plan.chunk_rows / 128.0) / tiles;
+  const double units = tiles * dm.n_q;
+  const double blocks = static_cast<double>(plan.chunk_pairs) / 16384.0 + plan.chunk_rows / 128.0;
+  const double t_unit = kUnitUs + blocks / tiles * kBlockUs * (0.5 + 0.5 * dscale);
   const double bytes = 2.0 * static_cast<double>(plan.decode_pairs) * dm.n_kv * (dm.d_head + 1);
+  auto t_chunk = [&](int n) { return ceil(units / n) * t_unit; };
   auto t_decode = [&](int n) { return bytes / (n * kDecodeBwPerSm < kDecodeBw ? n * kDecodeBwPerSm : kDecodeBw); };
-  Shares best = {0, 2};
-  double t_best = INFINITY;
-  for (int k = 2; k >= 1; --k) {
-    const double units = ceil(tiles * dm.n_q / k), t_unit = kUnitUs[k - 1] + blocks * kBlockUs[k - 1] * dscale;
-    auto t_chunk = [&](int n) { return ceil(units / n) * t_unit; };
-    auto take = [&](int n, double t) {
-      if (t < t_best) {
-        t_best = t;
-        best = {n, k};
-      }
-    };
-    take(0, t_chunk(S) + (bytes > 0 ? t_decode(S) + kTurnUs : 0));
-    for (int n = 1; n < S && bytes > 0; ++n) {
-      const double tc = t_chunk(n), td = t_decode(S - n);
-      take(n, tc > td ? tc + kBeside * td : td + kBeside * tc);
+  int best = 0;
+  double t_best = t_chunk(S) + t_decode(S) + kTurnUs;
+  for (int n = 1; n < S; ++n) {
+    const double tc = t_chunk(n), td = t_decode(S - n);
+    const double t = tc > td ? tc + kBeside * td : td + kBeside * tc;
+    if (t < t_best) {
+      t_best = t;
+      best = n;
     }
   }
   return best;
@@ -688,7 +677,6 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   p.max_splits = (max_kv_len + kSplit - 1) / kSplit;
   p.no_chunks = no_chunks;
   p.no_decodes = plan->n_seqs == 1 && plan->n_rows > 1;
-  p.two_tiles = 1;
   p.wait_at_end = 0;
   const uint64_t rows = static_cast<uint64_t>(num_pages) * dims->n_kv * 16;
   HB_REQUIRE(rows <= INT32_MAX, "hb_attention_e4m3: num_pages * n_kv * 16 must be below 2^31");
@@ -702,9 +690,7 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   int sms = ctx.num_sms;  // of the decode kernel
   if (!p.no_chunks) {
-    const Shares share = shares(ctx, *plan, *dims);
-    const int nc = p.no_decodes ? 0 : share.sms;
-    p.two_tiles = share.tiles == 2;
+    const int nc = p.no_decodes ? 0 : chunk_sms(ctx, *plan, *dims);
     st = chunk_e4m3_launch(ctx, q, p, dims->d_head, nc > 0 ? nc : ctx.num_sms, s);
     if (st != HB_OK) return st;
     sms -= nc;

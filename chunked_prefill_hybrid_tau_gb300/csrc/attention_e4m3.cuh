@@ -26,7 +26,6 @@ struct Params {
   int max_splits;   // of a sequence of max_kv_len keys
   int no_chunks;    // the plan has as many rows as sequences: none may have several
   int no_decodes;   // the plan has one sequence of several rows
-  int two_tiles;    // 1: a chunk kernel's unit has two 128-row tiles, 0: one
   // 1 when the chunk kernel precedes the decode kernel on the stream: it waited
   // for the inputs before it let this one start, so the decode kernel's wait is
   // deferred to its end (whose completion then implies the chunk kernel's)

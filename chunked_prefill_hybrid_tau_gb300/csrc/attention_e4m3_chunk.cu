@@ -13,31 +13,24 @@
 // sequences behind its end are widened block by block beside the MMAs instead
 // (WIDEN: the same kernel with five more warps), which takes 2.4 times as long.
 //
-// The tensor pipe bounds it, 4 d_head FLOP a pair and q head: 2048 rows behind
-// 14336 keys, 56 q heads on 8 of 128, 700 us with the widening, floor 466 at
-// cuBLAS's bf16 rate; the pipe is 60% active.  What keeps it from more is the chain
-// S - softmax - P - PV of a tile: S and O of both tiles fill tensor memory, so a
-// tile's next S waits for its PV.  Shorter chains were slower, because each more
-// group of MMAs or exchange costs 200 to 400 clocks: steps of 64 keys, PV in two
-// halves (870 us), two warps to 32 rows that exchange their maxima (873); and so
-// was one issuing warp for both tiles (775).
-//
-// Unit: two 128-row tiles of one kv head -- (row tile, q head) pairs in that
-// order, so with an even number of q heads per kv head two heads of the same
-// rows -- and keys 0 .. last in blocks of 128 that both tiles use.  Where there
-// are SMs for all, one tile (two_tiles 0), whose blocks take 1.65 us and not 2.
+// Unit: a 128-row tile of one q head, and keys 0 .. last in blocks of 128.
+// Tensor memory holds O and three sets of S columns: block G of the CTA has set
+// G % 3, P is written over its S.  So the S of two blocks ahead is computed while
+// one block is in its softmax and another in its PV.
 //
 // Warp roles (one CTA per SM):
 //   warp 0      finds the unit (its lanes scan the sequences), publishes it in
-//               shared memory, loads both Q tiles and the K and V blocks;
-//   warps 1, 10 MMA issuers of tile 0 and 1: S = Q K_j^T (M = N = 128) into the
-//               tile's tensor-memory columns, O += P V_j with P read from the same
-//               columns (bf16, written over S).  One warp a tile, because a wait
-//               costs the issuer some 100 clocks even where it ends at once, and
-//               the tensor pipe runs dry meanwhile unless another warp issues;
-//   warps 2-5, 6-9  softmax of tile 0 and 1: a thread has one row and takes its
-//               128 scores into registers; O is rescaled only where a row's
-//               maximum grew by more than 2^8; at the end O / l to global memory.
+//               shared memory, loads its Q tile and the K and V blocks;
+//   warp 1      S = Q K_j^T (M = N = 128) into the set's columns;
+//   warp 10     O += P V_j with P read from the same columns (bf16, written over
+//               S).  Two issuing warps, because a wait costs an issuer some 100
+//               clocks even where it ends at once;
+//   warps 2-5, 6-9  softmax of every other block: a thread has one row and takes
+//               its 128 scores into registers.  A row's maximum goes from group to
+//               group through shared memory, block by block, ahead of the
+//               exponentials, which are most of the work; each group keeps the sum
+//               of its own blocks.  O is rescaled only where a row's maximum grew
+//               by more than 2^8.  The group of a unit's last block stores O / l.
 // WIDEN: warp 0 loads K codes, 64 keys a slot, into a ring, warp 15 does so with
 // V's; scale bytes, 16 a page, go through their registers a block ahead (a copy
 // costs the issuing warp some 150 clocks).  Warps 11-14 widen: a warp takes one
@@ -64,19 +57,17 @@ using tc::tmem_st_wait;
 
 constexpr int TQ = 128, TK = 128;
 constexpr int HK = 64;  // keys of a ring slot
-constexpr int kSoft0 = 2, kMma1 = 10, kConv0 = 11, kConvWarps = 4, kVWarp = 15;
+constexpr int kSoft0 = 2, kPv = 10, kConv0 = 11, kConvWarps = 4, kVWarp = 15;
 template <bool WIDEN>
 constexpr int kThreads = 32 * (WIDEN ? kVWarp + 1 : kConv0);
 constexpr float kRescale = 8.0f;
 
-struct Tile {
-  int row0, nrows, pos0, head;  // nrows 0: the unit has one tile
-};
 struct Unit {
   int valid, seq, g, nblk;
   int row;  // of the scratch: key 0 of this sequence and kv head
-  Tile t[2];
+  int row0, nrows, pos0, head;
 };
+constexpr int SETS = 3;  // of S and P columns: block G of the CTA has set G % 3
 
 template <int D, bool WIDEN>
 struct TC {
@@ -86,16 +77,19 @@ struct TC {
   static constexpr int KST = WIDEN ? 2 : 3, VST = 2;      // blocks in flight
   static constexpr int SLOTS = WIDEN ? (D == 128 ? 2 : 4) : 0;  // of the K and of the V code ring
   static constexpr int SLOT = HK * D;
+  static constexpr int QST = WIDEN ? 1 : 2;          // Q tiles
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_K = QST * TILE;
   static constexpr int OFF_V = OFF_K + KST * TILE;
   static constexpr int OFF_C = OFF_V + VST * TILE;
   static constexpr int OFF_S = OFF_C + 2 * SLOTS * SLOT;  // scales: K's (or V's) 64 bytes, V's 64 bytes beside K
   static constexpr int OFF_U = OFF_S + 2 * SLOTS * 2 * HK;
-  static constexpr int OFF_BAR = OFF_U + 2 * 64;
-  static constexpr int SMEM = OFF_BAR + 400 + 1024;
-  static_assert(sizeof(Unit) <= 64 && SMEM <= 232448, "shared memory");
-  static constexpr uint32_t TMEM_COLS = 512;  // S0 S1 (P over them) O0 O1
+  static constexpr int OFF_M = OFF_U + 80;           // a row's maximum, from block to block
+  static constexpr int OFF_L = OFF_M + TQ * 4;       // [2] a row's sum over the other group's blocks
+  static constexpr int OFF_BAR = OFF_L + 2 * TQ * 4;
+  static constexpr int SMEM = OFF_BAR + (42 + 4 * SLOTS) * 8 + 8 + 1024;
+  static_assert(2 * sizeof(Unit) <= 80 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
+  static constexpr uint32_t TMEM_COLS = 512;  // S0 S1 S2 (P over them) O
 };
 
 // bf16 factors of a scale byte b: code * 2^-120 times `first` times `second` is
@@ -195,16 +189,13 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
 }
 
 // The tile that is the i-th of its kv head, heaviest rows first.
-__device__ __forceinline__ Tile tile_of(const Params& p, int i, int ntiles, int g, int q0, int qlen, int kvl) {
-  Tile t = {0, 0, 0, 0};
-  if (i < ntiles * p.grp) {
-    const int rt = ntiles - 1 - i / p.grp;
-    t.head = g * p.grp + i % p.grp;
-    t.row0 = q0 + rt * TQ;
-    t.nrows = min(TQ, qlen - rt * TQ);
-    t.pos0 = kvl - qlen + rt * TQ;
-  }
-  return t;
+__device__ __forceinline__ void tile_of(const Params& p, int i, int ntiles, int q0, int qlen, int kvl, Unit& w) {
+  const int rt = ntiles - 1 - i / p.grp;
+  w.head = w.g * p.grp + i % p.grp;
+  w.row0 = q0 + rt * TQ;
+  w.nrows = min(TQ, qlen - rt * TQ);
+  w.pos0 = kvl - qlen + rt * TQ;
+  w.nblk = (w.pos0 + w.nrows + TK - 1) / TK;
 }
 
 // keys of a sequence in the scratch: whole blocks
@@ -349,22 +340,24 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* u_full = bar;            // [2] unit published
   uint64_t* u_empty = bar + 2;       // [2] V's producer, the MMA, softmax and widening warps have read it
-  uint64_t* q_full = bar + 4;
-  uint64_t* q_empty = bar + 5;
-  uint64_t* c_full = bar + 6;        // [2 SLOTS] codes landed, scales stored: K's ring, then V's
-  uint64_t* c_empty = bar + 14;      // [2 SLOTS] widening warps
-  uint64_t* k_full = bar + 22;       // [KST] block landed, or widening warps
-  uint64_t* k_empty = bar + 25;      // [KST]
-  uint64_t* v_full = bar + 28;       // [VST]
-  uint64_t* v_empty = bar + 30;
-  uint64_t* s_full = bar + 32;       // [tile]
-  uint64_t* p_full = bar + 34;       // [tile] four softmax warps
-  uint64_t* pv_done = bar + 36;      // [tile]
-  uint64_t* o_empty = bar + 38;      // [tile] four softmax warps
-  uint64_t* drain = bar + 40;        // [tile]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 42);
+  uint64_t* q_full = bar + 4;        // [QST]
+  uint64_t* q_empty = bar + 6;
+  uint64_t* k_full = bar + 8;        // [KST] block landed, or widening warps
+  uint64_t* k_empty = bar + 11;      // [KST]
+  uint64_t* v_full = bar + 14;       // [VST]
+  uint64_t* v_empty = bar + 16;
+  uint64_t* s_full = bar + 18;       // [SETS]
+  uint64_t* p_full = bar + 21;       // [SETS] four softmax warps
+  uint64_t* pv_done = bar + 24;      // [SETS]
+  uint64_t* o_empty = bar + 27;      // four softmax warps
+  uint64_t* drain = bar + 28;        // [issuer]
+  uint64_t* m_full = bar + 30;       // [quarter] a block's maximum is known
+  uint64_t* l_full = bar + 34;       // [2][quarter] the other group's sums are there
+  uint64_t* c_full = bar + 42;       // [2 SLOTS] codes landed, scales stored: K's ring, then V's
+  uint64_t* c_empty = c_full + 2 * C::SLOTS;  // [2 SLOTS] widening warps
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 42 + 4 * C::SLOTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Unit* units = reinterpret_cast<Unit*>(smem + C::OFF_U);  // [2], 64 bytes apart
+  Unit* units = reinterpret_cast<Unit*>(smem + C::OFF_U);  // [2]
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
@@ -372,26 +365,30 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&u_full[i], 1);
       mbar_init(&u_empty[i], 2 + 8 + (WIDEN ? kConvWarps + 1 : 0));
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&pv_done[i], 1);
-      mbar_init(&o_empty[i], 4);
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < C::KST; ++i) {
       mbar_init(&k_full[i], WIDEN ? kConvWarps : 1);
-      mbar_init(&k_empty[i], 2);  // both tiles (where there is one, its issuer twice)
+      mbar_init(&k_empty[i], 1);
     }
     for (int i = 0; i < C::VST; ++i) {
       mbar_init(&v_full[i], WIDEN ? kConvWarps : 1);
-      mbar_init(&v_empty[i], 2);
+      mbar_init(&v_empty[i], 1);
     }
+    for (int i = 0; i < SETS; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&m_full[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&l_full[i], 1);
     for (int i = 0; i < 2 * C::SLOTS; ++i) {
       mbar_init(&c_full[i], 1);
       mbar_init(&c_empty[i], kConvWarps);
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 2);
+    mbar_init(o_empty, 4);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -408,7 +405,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
   auto next_unit = [&](int n, Unit& w) {
     const bool got = mbar_wait(&u_full[n & 1], (n >> 1) & 1, abort_flag, p.status);
     if (!__all_sync(0xffffffffu, got)) return false;
-    w = *reinterpret_cast<const Unit*>(reinterpret_cast<const uint8_t*>(units) + (n & 1) * 64);
+    w = units[n & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&u_empty[n & 1]);
     return w.valid != 0;
@@ -419,7 +416,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
   int half = 0;  // 64-key halves loaded so far
   auto load_codes = [&](const Unit& w, bool is_v) {
     const int* bt = p.block_table + static_cast<size_t>(w.seq) * p.max_pages;
-    const int npages = (w.t[0].pos0 + w.t[0].nrows + 15) / 16;
+    const int npages = (w.pos0 + w.nrows + 15) / 16;
     uint64_t* full = c_full + (is_v ? C::SLOTS : 0);
     uint64_t* empty = c_empty + (is_v ? C::SLOTS : 0);
     uint8_t* codes = sC + (is_v ? C::SLOTS * C::SLOT : 0);
@@ -468,21 +465,28 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     }
     return true;
   };
-  // the widened K and V blocks of a unit, by one thread
-  int blocks = 0;  // loaded so far: V's, and K's or one less
+  // the widened K and V blocks of a unit, by one thread: K's two ahead, as S is
+  int k_blocks = 0, v_blocks = 0;  // loaded so far
   auto load_blocks = [&](const Unit& w) {
-    for (int j = 0; j < w.nblk; ++j, ++blocks) {
-      const int ks = blocks % C::KST, vs = blocks % C::VST, row = w.row + j * TK;
-      if (!mbar_wait(&k_empty[ks], ((blocks / C::KST) & 1) ^ 1u, abort_flag, p.status)) return false;
-      mbar_arrive_expect_tx(&k_full[ks], C::TILE);
+    for (int j = -2; j < w.nblk; ++j) {
+      if (j + 2 < w.nblk) {
+        const int st = k_blocks % C::KST, row = w.row + (j + 2) * TK;
+        if (!mbar_wait(&k_empty[st], ((k_blocks / C::KST) & 1) ^ 1u, abort_flag, p.status)) return false;
+        mbar_arrive_expect_tx(&k_full[st], C::TILE);
 #pragma unroll
-      for (int hf = 0; hf < C::HALVES; ++hf)
-        tma_load_2d(sK + ks * C::TILE + hf * C::HALF_TILE, &tmK, &k_full[ks], hf * 64, row);
-      if (!mbar_wait(&v_empty[vs], ((blocks / C::VST) & 1) ^ 1u, abort_flag, p.status)) return false;
-      mbar_arrive_expect_tx(&v_full[vs], C::TILE);
+        for (int hf = 0; hf < C::HALVES; ++hf)
+          tma_load_2d(sK + st * C::TILE + hf * C::HALF_TILE, &tmK, &k_full[st], hf * 64, row);
+        ++k_blocks;
+      }
+      if (j >= 0) {
+        const int st = v_blocks % C::VST, row = w.row + j * TK;
+        if (!mbar_wait(&v_empty[st], ((v_blocks / C::VST) & 1) ^ 1u, abort_flag, p.status)) return false;
+        mbar_arrive_expect_tx(&v_full[st], C::TILE);
 #pragma unroll
-      for (int hf = 0; hf < C::HALVES; ++hf)
-        tma_load_2d(sV + vs * C::TILE + hf * C::HALF_TILE, &tmV, &v_full[vs], hf * 64, row);
+        for (int hf = 0; hf < C::HALVES; ++hf)
+          tma_load_2d(sV + st * C::TILE + hf * C::HALF_TILE, &tmV, &v_full[st], hf * 64, row);
+        ++v_blocks;
+      }
     }
     return true;
   };
@@ -490,8 +494,8 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
   auto drain_slots = [&](bool ok) {
     if (ok || lane != 0) return;
     if (!WIDEN) {
-      for (int b = max(0, blocks - C::KST + 1); b <= blocks; ++b) mbar_drain(&k_full[b % C::KST], (b / C::KST) & 1);
-      for (int b = max(0, blocks - C::VST); b < blocks; ++b) mbar_drain(&v_full[b % C::VST], (b / C::VST) & 1);
+      for (int b = max(0, k_blocks - C::KST); b < k_blocks; ++b) mbar_drain(&k_full[b % C::KST], (b / C::KST) & 1);
+      for (int b = max(0, v_blocks - C::VST); b < v_blocks; ++b) mbar_drain(&v_full[b % C::VST], (b / C::VST) & 1);
       return;
     }
     uint64_t* full = c_full + (warp == kVWarp ? kSlots : 0);
@@ -513,37 +517,32 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       int local, base;
       w.valid = scan.find(p, v, lane, [&](int qlen, int kvl, int at) {
         const bool fits = at + padded(kvl) <= p.scratch_keys;
-        return fits != WIDEN ? p.n_kv * (((qlen + TQ - 1) / TQ * p.grp + p.two_tiles) >> p.two_tiles) : 0;
+        return fits != WIDEN ? p.n_q * ((qlen + TQ - 1) / TQ) : 0;
       }, &local, &base);
       if (w.valid) {
         const int ntiles = (scan.qlen + TQ - 1) / TQ;
         w.seq = scan.seq;
         w.g = local % p.n_kv;
         w.row = base * p.n_kv + w.g * padded(scan.kvl);
-        const int i = local / p.n_kv << p.two_tiles;
-        w.t[0] = tile_of(p, i, ntiles, w.g, scan.q0, scan.qlen, scan.kvl);
-        w.t[1] = tile_of(p, i + 1, p.two_tiles ? ntiles : 0, w.g, scan.q0, scan.qlen, scan.kvl);
-        // the second tile's rows are the same or earlier ones
-        w.nblk = (w.t[0].pos0 + w.t[0].nrows + TK - 1) / TK;
+        tile_of(p, local / p.n_kv, ntiles, scan.q0, scan.qlen, scan.kvl, w);
       }
       if (lane == 0) {
         ok = mbar_wait(&u_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag, p.status);
         if (ok) {
-          *reinterpret_cast<Unit*>(reinterpret_cast<uint8_t*>(units) + (n & 1) * 64) = w;
+          units[n & 1] = w;
           mbar_arrive(&u_full[n & 1]);
         }
       }
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) ok = false;
       if (!ok || !w.valid) break;
-      const int tiles = w.t[1].nrows ? 2 : 1;
       if (lane == 0) {
-        ok = mbar_wait(q_empty, (n & 1) ^ 1u, abort_flag, p.status);
+        const int st = n % C::QST;
+        ok = mbar_wait(&q_empty[st], ((n / C::QST) & 1) ^ 1u, abort_flag, p.status);
         if (ok) {
-          mbar_arrive_expect_tx(q_full, tiles * C::TILE);
-          for (int x = 0; x < tiles; ++x)
+          mbar_arrive_expect_tx(&q_full[st], C::TILE);
 #pragma unroll
-            for (int hf = 0; hf < C::HALVES; ++hf)
-              tma_load_3d(sQ + x * C::TILE + hf * C::HALF_TILE, &tmQ, q_full, hf * 64, w.t[x].head, w.t[x].row0);
+          for (int hf = 0; hf < C::HALVES; ++hf)
+            tma_load_3d(sQ + st * C::TILE + hf * C::HALF_TILE, &tmQ, &q_full[st], hf * 64, w.head, w.row0);
         }
       }
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
@@ -563,80 +562,73 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     Unit w;
     for (int n = 0; ok && next_unit(n, w); ++n) ok = load_codes(w, true);
     drain_slots(ok);
-  } else if (warp == 1 || warp == kMma1) {
+  } else if (warp == 1 || warp == kPv) {
     // ------------------------------------------------------------ MMA issuers
     // The whole warp walks the loop and one elected lane issues: in a single-lane
     // branch every descriptor would be moved to a uniform register anew.
-    const int x = warp == kMma1 ? 1 : 0;  // tile
-    constexpr uint32_t idS = idesc_bf16_f32(TQ, TK);
-    constexpr uint32_t idPV = idesc_bf16_f32(TQ, D) | (1u << 16);  // B (V) is MN-major
-    const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ + x * C::TILE)), k_desc = smem_desc_sw128(smem_u32(sK));
-    const uint64_t v_desc = smem_desc_sw128_mn(smem_u32(sV), C::HALF_TILE, 1024);
-    const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
-    int J = 0;        // blocks of the units before
-    int u = 0;        // blocks of this tile so far
-    int mine = 0;     // units of this tile
+    int G = 0;  // blocks so far
     bool ok = true;
     Unit w;
     auto wait = [&](uint64_t* bar, int parity) {
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_at(smem_u32(bar), parity, abort_flag, p.status));
     };
-    for (int n = 0; ok && next_unit(n, w); ++n, J += w.nblk) {
-      const bool alone = w.t[1].nrows == 0;
-      if (x == 1 && alone) continue;
-      // S is written over the last P: its PV has to be complete
-      auto score = [&](int j) {
-        const int st = (J + j) % C::KST;
-        wait(&k_full[st], ((J + j) / C::KST) & 1);
-        wait(&pv_done[x], (u & 1) ^ 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t kd = k_desc + ((st * C::TILE) >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * C::HALF_TILE + (kk & 3) * 32) >> 4;
-            mma_bf16(tS, q_desc + off, kd + off, idS, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&s_full[x]);
-          mma_commit(&k_empty[st]);
-          if (alone) mma_commit(&k_empty[st]);
-          if (j == w.nblk - 1) {
-            mma_commit(q_empty);
-            if (alone) mma_commit(q_empty);
-          }
-        }
-        __syncwarp();
-      };
-      wait(q_full, n & 1);
-      score(0);
+    if (warp == 1) {
+      constexpr uint32_t idS = idesc_bf16_f32(TQ, TK);
+      const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ)), k_desc = smem_desc_sw128(smem_u32(sK));
+      for (int n = 0; ok && next_unit(n, w); ++n) {
+        const uint64_t qd = q_desc + ((n % C::QST * C::TILE) >> 4);
+        wait(&q_full[n % C::QST], (n / C::QST) & 1);
 #pragma unroll 1
-      for (int j = 0; j < w.nblk && ok; ++j) {
-        const int st = (J + j) % C::VST;
-        if (j == 0) wait(&o_empty[x], (mine & 1) ^ 1);
-        wait(&v_full[st], ((J + j) / C::VST) & 1);
-        wait(&p_full[x], u & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t vd = v_desc + ((st * C::TILE) >> 4);
-        if (elect_one()) {
+        for (int j = 0; j < w.nblk && ok; ++j, ++G) {
+          const int st = G % C::KST, set = G % SETS;
+          wait(&k_full[st], (G / C::KST) & 1);
+          wait(&pv_done[set], ((G / SETS) & 1) ^ 1);  // S is written over the set's last P
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = k_desc + ((st * C::TILE) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < TK / 16; ++kk)
-            mma_bf16_ts(tO, tS + kk * 8, vd + ((kk * 2048) >> 4), idPV, (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&pv_done[x]);
-          mma_commit(&v_empty[st]);
-          if (alone) mma_commit(&v_empty[st]);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::HALF_TILE + (kk & 3) * 32) >> 4;
+              mma_bf16(tmem + set * 128, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(&s_full[set]);
+            mma_commit(&k_empty[st]);
+            if (j == w.nblk - 1) mma_commit(&q_empty[n % C::QST]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        ++u;
-        if (j + 1 < w.nblk) score(j + 1);
       }
-      ++mine;
+    } else {
+      constexpr uint32_t idPV = idesc_bf16_f32(TQ, D) | (1u << 16);  // B (V) is MN-major
+      const uint64_t v_desc = smem_desc_sw128_mn(smem_u32(sV), C::HALF_TILE, 1024);
+      const uint32_t tO = tmem + SETS * 128;
+      for (int n = 0; ok && next_unit(n, w); ++n) {
+        wait(o_empty, (n & 1) ^ 1);
+#pragma unroll 1
+        for (int j = 0; j < w.nblk && ok; ++j, ++G) {
+          const int st = G % C::VST, set = G % SETS;
+          wait(&v_full[st], (G / C::VST) & 1);
+          wait(&p_full[set], (G / SETS) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = v_desc + ((st * C::TILE) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < TK / 16; ++kk)
+              mma_bf16_ts(tO, tmem + set * 128 + kk * 8, vd + ((kk * 2048) >> 4), idPV, (j > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&pv_done[set]);
+            mma_commit(&v_empty[st]);
+          }
+          __syncwarp();
+        }
+      }
     }
     if (!ok && elect_one()) {
       // nothing may still read shared memory or write tensor memory at the end
-      mma_commit(&drain[x]);
-      mbar_drain(&drain[x], 0);
+      uint64_t* done = &drain[warp == 1 ? 0 : 1];
+      mma_commit(done);
+      mbar_drain(done, 0);
     }
   } else if (WIDEN && warp >= kConv0) {
     // ------------------------------------------------------------ widening
@@ -655,7 +647,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     bool ok = true;
     Unit w;
     for (int n = 0; ok && next_unit(n, w); ++n) {
-      const int key_end = w.t[0].pos0 + w.t[0].nrows;
+      const int key_end = w.pos0 + w.nrows;
       for (int j = 0; j < w.nblk && ok; ++j, ++J) {
         const int st = J % 2, use = J / 2;
 #pragma unroll 1
@@ -723,22 +715,25 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
-    const int x = (warp - kSoft0) >> 2;  // tile
+    const int group = (warp - kSoft0) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
-    const uint32_t tS = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + x * 128;
-    const uint32_t tO = tS + 256;
-    int u = 0;  // blocks so far
+    const uint32_t tT = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tO = tT + SETS * 128;
+    volatile float* m_row = reinterpret_cast<float*>(smem + C::OFF_M) + r;
+    volatile float* l_row = reinterpret_cast<float*>(smem + C::OFF_L) + r;
+    int J = 0;     // blocks of the units before
+    int both = 0;  // units before of both groups
     Unit w;
     for (int n = 0; next_unit(n, w); ++n) {
-      const Tile t = w.t[x];
-      if (t.nrows == 0) continue;
-      const int lim = r < t.nrows ? t.pos0 + r : t.pos0 + t.nrows - 1;  // last key this row sees
-      float m_used = -INFINITY, l = 0.f;
+      const int lim = r < w.nrows ? w.pos0 + r : w.pos0 + w.nrows - 1;  // last key this row sees
+      float m_used = -INFINITY, m_in = -INFINITY, l = 0.f;
       bool ok = true;
 #pragma unroll 1
-      for (int j = 0; j < w.nblk; ++j, ++u) {
-        bool sok = mbar_wait(&s_full[x], u & 1, abort_flag, p.status);
+      for (int j = (group ^ J) & 1; j < w.nblk; j += 2) {
+        const int G = J + j, set = G % SETS;
+        const uint32_t tS = tT + set * 128;
+        bool sok = mbar_wait(&s_full[set], (G / SETS) & 1, abort_flag, p.status);
         if (!__all_sync(0xffffffffu, sok)) {
           ok = false;
           break;
@@ -764,24 +759,42 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
           mp[c] = fmaxf(mp[c], __uint_as_float(v[c][31]));
         }
         const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * p.scale_log2;
-        const bool raise = mx > m_used + kRescale;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float m_new = raise ? mx : m_used;
-          const float alpha = raise ? ex2_approx(m_used - m_new) : 1.f;
-          // S of this block was issued behind the PV of the last one: O is complete
-          if (j > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t ov[16];
-              tmem_ld_32x32b_x16(tO + c, ov);
-              tmem_ld_wait16(ov);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-              tmem_st_32x32b_x16(tO + c, ov);
-            }
+        // the last block's maximum, from the other group; of the last unit it only
+        // keeps the groups in step
+        if (G > 0) {
+          bool mok = mbar_wait(&m_full[quarter], (G - 1) & 1, abort_flag, p.status);
+          if (!__all_sync(0xffffffffu, mok)) {
+            ok = false;
+            break;
           }
+          if (j > 0) m_in = *m_row;
+        }
+        const bool raise = mx > m_in + kRescale;
+        const float m_new = raise ? mx : m_in;
+        *m_row = m_new;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m_full[quarter]);
+        if (j > 0 && __any_sync(0xffffffffu, raise)) {
+          const float alpha = raise ? ex2_approx(m_in - m_new) : 1.f;
+          bool lok = mbar_wait(&pv_done[(G - 1) % SETS], ((G - 1) / SETS) & 1, abort_flag, p.status);
+          if (!__all_sync(0xffffffffu, lok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t ov[16];
+            tmem_ld_32x32b_x16(tO + c, ov);
+            tmem_ld_wait16(ov);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st_32x32b_x16(tO + c, ov);
+          }
+        }
+        if (m_new != m_used) {
+          l *= ex2_approx(m_used - m_new);
           m_used = m_new;
-          l *= alpha;
         }
         const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
         const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), neg2 = pack_f32x2(neg_m, neg_m);
@@ -804,20 +817,37 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[x]);
+        if (lane == 0) mbar_arrive(&p_full[set]);
       }
       if (!ok) break;
-      bool pok = mbar_wait(&pv_done[x], (u - 1) & 1, abort_flag, p.status);
+      // the group of the last block stores the rows, with the other's sums
+      const int last = J + w.nblk - 1, slot = both & 1;
+      J += w.nblk;
+      if (w.nblk > 1) {
+        if ((last & 1) != group) {
+          l_row[slot * TQ] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&l_full[slot * 4 + quarter]);
+        } else {
+          bool lok = mbar_wait(&l_full[slot * 4 + quarter], (both >> 1) & 1, abort_flag, p.status);
+          if (!__all_sync(0xffffffffu, lok)) break;
+          const float other = l_row[slot * TQ];
+          l += m_in == m_used ? other : other * ex2_approx(m_in - m_used);
+        }
+        ++both;
+      }
+      if ((last & 1) != group) continue;
+      bool pok = mbar_wait(&pv_done[last % SETS], (last / SETS) & 1, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, pok)) break;
       tc_fence_after();
       const float inv = 1.f / l;
-      __nv_bfloat16* orow = p.out + (static_cast<size_t>(t.row0 + r) * p.n_q + t.head) * D;
+      __nv_bfloat16* orow = p.out + (static_cast<size_t>(w.row0 + r) * p.n_q + w.head) * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t ov[32];
         tmem_ld_32x32b_x32(tO + c, ov);
         tmem_ld_wait32(ov);
-        if (r < t.nrows) {
+        if (r < w.nrows) {
           uint4* dst = reinterpret_cast<uint4*>(orow + c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -831,7 +861,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&o_empty[x]);  // O was read into registers
+      if (lane == 0) mbar_arrive(o_empty);  // O was read into registers
     }
   }
 
