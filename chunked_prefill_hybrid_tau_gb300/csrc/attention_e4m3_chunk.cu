@@ -74,12 +74,11 @@ struct TC {
   static constexpr int HALVES = D / 64;
   static constexpr int HALF_TILE = 128 * 128;        // 128 rows x 128 bytes (64 dims)
   static constexpr int TILE = HALVES * HALF_TILE;    // a Q tile, a K or V block
-  static constexpr int KST = WIDEN ? 2 : 3, VST = 2;      // blocks in flight
+  static constexpr int KST = WIDEN ? 2 : 3, VST = KST;    // blocks in flight
   static constexpr int SLOTS = WIDEN ? (D == 128 ? 2 : 4) : 0;  // of the K and of the V code ring
   static constexpr int SLOT = HK * D;
-  static constexpr int QST = WIDEN ? 1 : 2;          // Q tiles
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = QST * TILE;
+  static constexpr int OFF_K = TILE;
   static constexpr int OFF_V = OFF_K + KST * TILE;
   static constexpr int OFF_C = OFF_V + VST * TILE;
   static constexpr int OFF_S = OFF_C + 2 * SLOTS * SLOT;  // scales: K's (or V's) 64 bytes, V's 64 bytes beside K
@@ -87,7 +86,7 @@ struct TC {
   static constexpr int OFF_M = OFF_U + 80;           // a row's maximum, from block to block
   static constexpr int OFF_L = OFF_M + TQ * 4;       // [2] a row's sum over the other group's blocks
   static constexpr int OFF_BAR = OFF_L + 2 * TQ * 4;
-  static constexpr int SMEM = OFF_BAR + (42 + 4 * SLOTS) * 8 + 8 + 1024;
+  static constexpr int SMEM = OFF_BAR + (44 + 4 * SLOTS) * 8 + 8 + 1024;
   static_assert(2 * sizeof(Unit) <= 80 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;  // S0 S1 S2 (P over them) O
 };
@@ -340,22 +339,22 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* u_full = bar;            // [2] unit published
   uint64_t* u_empty = bar + 2;       // [2] V's producer, the MMA, softmax and widening warps have read it
-  uint64_t* q_full = bar + 4;        // [QST]
-  uint64_t* q_empty = bar + 6;
+  uint64_t* q_full = bar + 4;
+  uint64_t* q_empty = bar + 5;
   uint64_t* k_full = bar + 8;        // [KST] block landed, or widening warps
   uint64_t* k_empty = bar + 11;      // [KST]
   uint64_t* v_full = bar + 14;       // [VST]
-  uint64_t* v_empty = bar + 16;
-  uint64_t* s_full = bar + 18;       // [SETS]
-  uint64_t* p_full = bar + 21;       // [SETS] four softmax warps
-  uint64_t* pv_done = bar + 24;      // [SETS]
-  uint64_t* o_empty = bar + 27;      // four softmax warps
-  uint64_t* drain = bar + 28;        // [issuer]
-  uint64_t* m_full = bar + 30;       // [quarter] a block's maximum is known
-  uint64_t* l_full = bar + 34;       // [2][quarter] the other group's sums are there
-  uint64_t* c_full = bar + 42;       // [2 SLOTS] codes landed, scales stored: K's ring, then V's
+  uint64_t* v_empty = bar + 17;
+  uint64_t* s_full = bar + 20;       // [SETS]
+  uint64_t* p_full = bar + 23;       // [SETS] four softmax warps
+  uint64_t* pv_done = bar + 26;      // [SETS]
+  uint64_t* o_empty = bar + 29;      // four softmax warps
+  uint64_t* drain = bar + 30;        // [issuer]
+  uint64_t* m_full = bar + 32;       // [quarter] a block's maximum is known
+  uint64_t* l_full = bar + 36;       // [2][quarter] the other group's sums are there
+  uint64_t* c_full = bar + 44;       // [2 SLOTS] codes landed, scales stored: K's ring, then V's
   uint64_t* c_empty = c_full + 2 * C::SLOTS;  // [2 SLOTS] widening warps
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 42 + 4 * C::SLOTS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 44 + 4 * C::SLOTS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Unit* units = reinterpret_cast<Unit*>(smem + C::OFF_U);  // [2]
 
@@ -365,8 +364,6 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&u_full[i], 1);
       mbar_init(&u_empty[i], 2 + 8 + (WIDEN ? kConvWarps + 1 : 0));
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
       mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < C::KST; ++i) {
@@ -388,6 +385,8 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       mbar_init(&c_full[i], 1);
       mbar_init(&c_empty[i], kConvWarps);
     }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     mbar_init(o_empty, 4);
     *abort_flag = 0;
     fence_barrier_init();
@@ -536,13 +535,12 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) ok = false;
       if (!ok || !w.valid) break;
       if (lane == 0) {
-        const int st = n % C::QST;
-        ok = mbar_wait(&q_empty[st], ((n / C::QST) & 1) ^ 1u, abort_flag, p.status);
+        ok = mbar_wait(q_empty, (n & 1) ^ 1u, abort_flag, p.status);
         if (ok) {
-          mbar_arrive_expect_tx(&q_full[st], C::TILE);
+          mbar_arrive_expect_tx(q_full, C::TILE);
 #pragma unroll
           for (int hf = 0; hf < C::HALVES; ++hf)
-            tma_load_3d(sQ + st * C::TILE + hf * C::HALF_TILE, &tmQ, &q_full[st], hf * 64, w.head, w.row0);
+            tma_load_3d(sQ + hf * C::HALF_TILE, &tmQ, q_full, hf * 64, w.head, w.row0);
         }
       }
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
@@ -576,8 +574,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       constexpr uint32_t idS = idesc_bf16_f32(TQ, TK);
       const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ)), k_desc = smem_desc_sw128(smem_u32(sK));
       for (int n = 0; ok && next_unit(n, w); ++n) {
-        const uint64_t qd = q_desc + ((n % C::QST * C::TILE) >> 4);
-        wait(&q_full[n % C::QST], (n / C::QST) & 1);
+        wait(q_full, n & 1);
 #pragma unroll 1
         for (int j = 0; j < w.nblk && ok; ++j, ++G) {
           const int st = G % C::KST, set = G % SETS;
@@ -590,11 +587,11 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * C::HALF_TILE + (kk & 3) * 32) >> 4;
-              mma_bf16(tmem + set * 128, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
+              mma_bf16(tmem + set * 128, q_desc + off, kd + off, idS, kk > 0 ? 1u : 0u);
             }
             mma_commit(&s_full[set]);
             mma_commit(&k_empty[st]);
-            if (j == w.nblk - 1) mma_commit(&q_empty[n % C::QST]);
+            if (j == w.nblk - 1) mma_commit(q_empty);
           }
           __syncwarp();
         }
