@@ -326,9 +326,10 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     chunk_e4m3_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, Params p) {
   using C = TC<D, WIDEN>;
-  // the decode kernel behind this one starts beside it once its inputs are there
-  griddep_wait();
+  // The decode kernel behind this one runs beside it.  Its inputs are there: the
+  // widening's CTAs had waited for all that is ahead before this kernel could start.
   griddep_launch_dependents();
+  griddep_wait();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + C::OFF_Q;
