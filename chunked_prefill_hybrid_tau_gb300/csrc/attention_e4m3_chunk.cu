@@ -11,7 +11,13 @@
 // widened once, by a kernel ahead (widen_kernel), into scratch of the workspace
 // laid out for whole-block copies.  That scratch is bounded (kScratchKeys);
 // sequences behind its end are widened block by block beside the MMAs instead
-// (WIDEN: the same kernel with five more warps), which takes 2.4 times as long.
+// (WIDEN: the same kernel with five more warps), which takes 3.7 times as long.
+//
+// The tensor pipe bounds it, 4 d_head FLOP a pair and q head: 2048 rows behind
+// 14336 keys, 56 q heads on 8 of 128, 596 us back to back with the widening, under
+// the power limit (floor 466 at cuBLAS's burst rate, 520 at its sustained one);
+// alone the kernel takes 550, the pipe 73% active.  With two tiles a CTA and one
+// set of S columns each, so that a tile's next S waits for its PV, 701.
 //
 // Unit: a 128-row tile of one q head, and keys 0 .. last in blocks of 128.
 // Tensor memory holds O and three sets of S columns: block G of the CTA has set
@@ -491,8 +497,10 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     return true;
   };
   // after a wait that expired: this warp's copies in flight land (bounded) before it leaves
+  int q_tiles = 0;  // loaded so far
   auto drain_slots = [&](bool ok) {
     if (ok || lane != 0) return;
+    if (q_tiles > 0) mbar_drain(q_full, (q_tiles - 1) & 1);
     if (!WIDEN) {
       for (int b = max(0, k_blocks - C::KST); b < k_blocks; ++b) mbar_drain(&k_full[b % C::KST], (b / C::KST) & 1);
       for (int b = max(0, v_blocks - C::VST); b < v_blocks; ++b) mbar_drain(&v_full[b % C::VST], (b / C::VST) & 1);
@@ -542,6 +550,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
 #pragma unroll
           for (int hf = 0; hf < C::HALVES; ++hf)
             tma_load_3d(sQ + hf * C::HALF_TILE, &tmQ, q_full, hf * 64, w.head, w.row0);
+          ++q_tiles;
         }
       }
       if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {

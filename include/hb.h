@@ -367,7 +367,7 @@ hb_status hb_kv_append_e4m3(const void* qkv, int32_t T, const int32_t* row_pos, 
  *     may overlap (other streams, graphs replayed side by side) need one each.
  *     It holds the decode rows' split records and the keys and values of
  *     sequences of several rows as bf16, those of at most 262144 keys (or of
- *     one sequence, if that has more); further ones take 2.4 times as long
+ *     one sequence, if that has more); further ones take 3.7 times as long
  * Requires d_head == 64 or 128, page_size == 16, at most 1024 sequences.
  * A row's result does not depend on the other sequences of the batch.
  * ---------------------------------------------------------------------- */
