@@ -447,24 +447,86 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
   if (p.wait_at_end) griddep_wait();
 }
 
+constexpr int kJoinWarps = 8, kJoin = 4;
+
+// The parts of a chunk row whose keys are split (a CTA): a warp takes every
+// eighth q head, all its records in flight.  The row's sequence is found ahead
+// of the wait.
+template <int D>
+__device__ __forceinline__ void join_parts(const Params& p, int row, int warp, int lane) {
+  constexpr int E = D / 32;
+  int s = -1, q0 = 0, q1 = 0, kvl = 0;  // the last sequence that starts at or ahead of the row
+  for (int i0 = 0; i0 < p.S; i0 += 32) {
+    const bool ahead = i0 + lane < p.S && ld_s32(p.q_start + i0 + lane) <= row;
+    s += __popc(__ballot_sync(0xffffffffu, ahead));
+  }
+  if (s >= 0) {
+    q0 = ld_s32(p.q_start + s);
+    q1 = ld_s32(p.q_start + s + 1);
+    kvl = ld_s32(p.kv_len + s);
+  }
+  const int rows = q1 - q0;
+  griddep_wait();  // by all: the kernel's end has to imply its predecessor's
+  if (q0 < 0 || q1 > p.T || row < q0 || row >= q1 || rows < 2 || kvl < rows || kvl > p.max_kv_len ||
+      (kvl + 15) / 16 > p.max_pages)
+    return;
+  const int parts = part_count(p.n_q * ((rows + 127) / 128), first_tile_blocks(rows, kvl));
+  if (parts == 1) return;
+  for (int h = warp; h < p.n_q; h += kJoinWarps) {
+    const float* rec = p.chunk_partials +
+                       (static_cast<size_t>(part_row(p, row, q0)) * p.n_q + h) * p.max_parts * part_floats(D);
+    float m[kMaxParts], l[kMaxParts], o[kMaxParts][E];
+    float all = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) {
+      // behind the last: the last again, with weight 0
+      const float* at = rec + min(i, parts - 1) * part_floats(D);
+      m[i] = ld_f32(at + D);
+      l[i] = ld_f32(at + D + 1);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[i][e] = ld_f32(at + lane + 32 * e);
+      all = fmaxf(all, m[i]);
+    }
+    if (all == -INFINITY) all = 0.f;
+    float z = 0.f, x[E] = {};
+#pragma unroll
+    for (int i = 0; i < kMaxParts; ++i) {
+      if (i >= parts) break;
+      const float f = ex2_approx(m[i] - all);
+      z += f * l[i];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] += f * o[i][e];
+    }
+    __nv_bfloat16* out = p.out + (static_cast<size_t>(row) * p.n_q + h) * D + lane;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[32 * e] = __float2bfloat16_rn(x[e] / z);
+  }
+}
+
 // The splits of one decode row and q head (a CTA), in an order of their number
 // alone: warp w takes splits w, w + 8, ..., kJoin of them in flight with their
 // maxima and sums; the warps' results are joined in order.  The plan is read
 // ahead of the wait: the decode kernel lets this one start only once everything
 // ahead of itself is complete.
-constexpr int kJoinWarps = 8, kJoin = 4;
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_splits_kernel(Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_splits_kernel(Params p, int decode_items) {
   constexpr int E = D / 32;
   __shared__ float sum[kJoinWarps][D];
   __shared__ float2 state[kJoinWarps];
   griddep_launch_dependents();
-  const int s = blockIdx.x, h = blockIdx.y, g = h / p.grp, r = h % p.grp;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // CTAs of a decode row and q head, then of a chunk row
+  const int item = static_cast<int>(blockIdx.x) - decode_items;
+  if (item >= 0) {
+    join_parts<D>(p, item, warp, lane);
+    return;
+  }
+  const int s = blockIdx.x / p.n_q, h = blockIdx.x % p.n_q, g = h / p.grp, r = h % p.grp;
   const int q0 = ld_s32(p.q_start + s), q1 = ld_s32(p.q_start + s + 1), kvl = ld_s32(p.kv_len + s);
   griddep_wait();
   // as count_units: others were not computed, or were whole
   if (q0 < 0 || q1 > p.T || q1 - q0 != 1 || kvl <= kSplit || kvl > p.max_kv_len || (kvl + 15) / 16 > p.max_pages) return;
-  const int n = (kvl + kSplit - 1) / kSplit, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = (kvl + kSplit - 1) / kSplit;
   const size_t step = static_cast<size_t>(p.n_kv) * rec_floats(p.grp, D);
   const float* rec = p.partials + static_cast<size_t>(s) * p.max_splits * step +
                      static_cast<size_t>(g) * rec_floats(p.grp, D);
@@ -565,10 +627,16 @@ int chunk_sms(const DeviceCtx& ctx, const hb_device_plan& plan, const hb_layer_d
   const int S = ctx.num_sms;
   if (plan.chunk_pairs <= 0 || plan.decode_pairs <= 0 || plan.chunk_rows <= 0 || S < 4) return 0;
   const double dscale = dm.d_head / 128.0;
-  const double tiles = ceil(static_cast<double>(plan.chunk_rows) / 128.0);
-  const double units = tiles * dm.n_q;
-  const double blocks = static_cast<double>(plan.chunk_pairs) / 16384.0 + plan.chunk_rows / 128.0;
-  const double t_unit = kUnitUs + blocks / tiles * kBlockUs * (0.5 + 0.5 * dscale);
+  // sequences of several rows, alike for want of more: the others have one each
+  const double seqs = plan.n_seqs - (plan.n_rows - plan.chunk_rows) > 1
+                          ? static_cast<double>(plan.n_seqs - (plan.n_rows - plan.chunk_rows)) : 1.0;
+  double units = ceil(plan.chunk_rows / seqs / 128.0) * dm.n_q;
+  double blocks = static_cast<double>(plan.chunk_pairs) / plan.chunk_rows / 128.0 + 0.5;
+  const int parts = part_count(static_cast<int>(units < 1e6 ? units : 1e6),
+                               static_cast<int>(blocks < 1e6 ? blocks : 1e6));
+  units *= seqs * parts;
+  blocks /= parts;
+  const double t_unit = kUnitUs + blocks * kBlockUs * (0.5 + 0.5 * dscale);
   const double bytes = 2.0 * static_cast<double>(plan.decode_pairs) * dm.n_kv * (dm.d_head + 1);
   auto t_chunk = [&](int n) { return ceil(units / n) * t_unit; };
   auto t_decode = [&](int n) { return bytes / (n * kDecodeBwPerSm < kDecodeBw ? n * kDecodeBwPerSm : kDecodeBw); };
@@ -605,9 +673,16 @@ size_t partial_bytes(const hb_layer_dims& dm, int seqs, int max_kv_len) {
   const size_t recs = splits > 1 ? static_cast<size_t>(seqs) * splits * dm.n_kv : 0;
   return (recs * rec_floats(dm.n_q / dm.n_kv, dm.d_head) * 4 + 255) / 256 * 256;
 }
+// of chunk rows (part_row); one sequence alone is split only where it has few
+int max_parts(const hb_layer_dims& dm, int max_kv_len) { return part_count(dm.n_q, (max_kv_len + 127ll) / 128); }
+size_t chunk_partial_bytes(const hb_layer_dims& dm, int rows, int seqs, int max_kv_len) {
+  const int parts = max_parts(dm, max_kv_len), few = 128 * (kSplitUnits / 2 / dm.n_q);
+  const size_t n = parts == 1 || seqs < 1 || rows < 2 ? 0 : seqs == 1 && rows > few ? few : rows;
+  return (n * dm.n_q * parts * part_floats(dm.d_head) * 4 + 255) / 256 * 256;
+}
 size_t workspace_bytes(const hb_layer_dims& dm, int rows, int seqs, int max_kv_len) {
   const size_t scratch = static_cast<size_t>(scratch_keys(rows, seqs, max_kv_len)) * dm.n_kv * dm.d_head * 2;
-  return 256 + partial_bytes(dm, seqs, max_kv_len) + 2 * scratch;
+  return 256 + partial_bytes(dm, seqs, max_kv_len) + chunk_partial_bytes(dm, rows, seqs, max_kv_len) + 2 * scratch;
 }
 
 }  // namespace
@@ -615,7 +690,7 @@ size_t workspace_bytes(const hb_layer_dims& dm, int rows, int seqs, int max_kv_l
 
 extern "C" size_t hb_attention_e4m3_workspace_bytes(const hb_layer_dims* dims, int32_t max_rows, int32_t max_seqs,
                                                     int32_t max_kv_len) {
-  if (!dims || max_rows < 0 || max_seqs < 0 || max_kv_len < 0 || dims->n_kv < 1) return 0;
+  if (!dims || max_rows < 0 || max_seqs < 0 || max_kv_len < 0 || dims->n_kv < 1 || dims->n_q < 1) return 0;
   return hb::workspace_bytes(*dims, max_rows, max_seqs, max_kv_len);
 }
 
@@ -671,8 +746,11 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   p.status = ctx.status;
   p.partials = static_cast<float*>(workspace);
   p.scratch_keys = no_chunks ? 0 : static_cast<int>(scratch_keys(plan->n_rows, plan->n_seqs, max_kv_len));
-  p.scratch_k = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) +
-                                                 partial_bytes(*dims, plan->n_seqs, max_kv_len));
+  uint8_t* at = static_cast<uint8_t*>(workspace) + partial_bytes(*dims, plan->n_seqs, max_kv_len);
+  p.chunk_partials = reinterpret_cast<float*>(at);
+  p.max_parts = max_parts(*dims, max_kv_len);
+  at += chunk_partial_bytes(*dims, no_chunks ? 0 : plan->n_rows, plan->n_seqs, max_kv_len);
+  p.scratch_k = reinterpret_cast<__nv_bfloat16*>(at);
   p.scratch_v = p.scratch_k + static_cast<size_t>(p.scratch_keys) * dims->n_kv * dims->d_head;
   p.max_splits = (max_kv_len + kSplit - 1) / kSplit;
   p.no_chunks = no_chunks;
@@ -706,8 +784,9 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   // have such sequences have none
   if (st == HB_OK && !p.no_chunks && chunk_keys(p.T, p.S, max_kv_len) > p.scratch_keys)
     st = chunk_e4m3_overflow_launch(ctx, q, p, dims->d_head, s);
-  if (p.no_decodes) return st;
-  if (st != HB_OK || p.max_splits == 1) return st;
-  return launch_pdl(dims->d_head == 128 ? join_splits_kernel<128> : join_splits_kernel<64>, dim3(p.S, p.n_q),
-                    kJoinWarps * 32, 0, s, "join_splits_kernel launch", p);
+  const int decode_items = p.no_decodes || p.max_splits == 1 ? 0 : p.S * p.n_q;
+  const int items = decode_items + (p.no_chunks || p.max_parts == 1 ? 0 : p.T);
+  if (st != HB_OK || items == 0) return st;
+  return launch_pdl(dims->d_head == 128 ? join_splits_kernel<128> : join_splits_kernel<64>, items,
+                    kJoinWarps * 32, 0, s, "join_splits_kernel launch", p, decode_items);
 }

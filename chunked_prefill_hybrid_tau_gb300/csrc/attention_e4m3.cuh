@@ -24,6 +24,8 @@ struct Params {
   int scratch_keys;                      // that it holds
   float* partials;  // split records [sequence][split][kv head]
   int max_splits;   // of a sequence of max_kv_len keys
+  float* chunk_partials;  // records of chunk rows whose keys are split, [part_row][q head][part]
+  int max_parts;          // of a sequence of max_kv_len keys
   int no_chunks;    // the plan has as many rows as sequences: none may have several
   int no_decodes;   // the plan has one sequence of several rows
   // 1 when the chunk kernel precedes the decode kernel on the stream: it waited
@@ -32,6 +34,25 @@ struct Params {
   int wait_at_end;
   int* status;
 };
+
+// A chunk of few rows has few units for the SMs, which take its keys block by
+// block: they are split into as many parts as give kSplitUnits (an SM each), at
+// most kMaxParts and of at least kPartBlocks blocks, joined afterwards.  By the
+// sequence and the dims alone, so that a row's result does not depend on its
+// batch; `blocks`: 128-key blocks that the first tile sees.
+constexpr int kSplitUnits = 152, kMaxParts = 8, kPartBlocks = 8;
+__host__ __device__ inline int part_count(int units, int blocks) {
+  int n = blocks / kPartBlocks < kSplitUnits / units ? blocks / kPartBlocks : kSplitUnits / units;
+  n = n < kMaxParts ? n : kMaxParts;
+  return n < 1 ? 1 : n;
+}
+__host__ __device__ inline int first_tile_blocks(int qlen, int kvl) {
+  return (kvl - qlen + (qlen < 128 ? qlen : 128) + 127) / 128;
+}
+// which record row a row of the sequence that starts at q0 has
+__device__ __forceinline__ int part_row(const Params& p, int row, int q0) { return p.S == 1 ? row - q0 : row; }
+// a record: O [D], its maximum and sum, fp32 (a multiple of 16 bytes)
+__host__ __device__ constexpr int part_floats(int d) { return d + 4; }
 
 // E4M3 to bf16, exactly, two codes at a time, a code in the upper byte of each
 // half: sign, and the exponent and mantissa fields moved to bf16's places make

@@ -24,6 +24,10 @@
 // G % 3, P is written over its S.  So the S of two blocks ahead is computed while
 // one block is in its softmax and another in its PV.
 //
+// The keys of a short chunk behind a long prefix are split (part_count), a unit a
+// part: 6 rows behind 10610 keys, 12 q heads on 4 of 64, 61 us
+// whole and 28 in 8 parts, with the widening and the join.
+//
 // Warp roles (one CTA per SM):
 //   warp 0      finds the unit (its lanes scan the sequences), publishes it in
 //               shared memory, loads its Q tile and the K and V blocks;
@@ -55,8 +59,12 @@ namespace hb {
 namespace {
 
 using namespace dev;
+using kv8::first_tile_blocks;
 using kv8::mul_bf16x2;
 using kv8::Params;
+using kv8::part_count;
+using kv8::part_floats;
+using kv8::part_row;
 using tc::mma_bf16_ts;
 using tc::smem_desc_sw128_mn;
 using tc::tmem_st_wait;
@@ -72,6 +80,9 @@ struct Unit {
   int valid, seq, g, nblk;
   int row;  // of the scratch: key 0 of this sequence and kv head
   int row0, nrows, pos0, head;
+  int part_row;
+  int page0, part;  // a part of the keys: row and pos0 count from its first key, in page page0 of the
+                    // sequence; part -1: all keys
 };
 constexpr int SETS = 3;  // of S and P columns: block G of the CTA has set G % 3
 
@@ -89,11 +100,11 @@ struct TC {
   static constexpr int OFF_C = OFF_V + VST * TILE;
   static constexpr int OFF_S = OFF_C + 2 * SLOTS * SLOT;  // scales: K's (or V's) 64 bytes, V's 64 bytes beside K
   static constexpr int OFF_U = OFF_S + 2 * SLOTS * 2 * HK;
-  static constexpr int OFF_M = OFF_U + 80;           // a row's maximum, from block to block
+  static constexpr int OFF_M = OFF_U + 96;           // a row's maximum, from block to block
   static constexpr int OFF_L = OFF_M + TQ * 4;       // [2] a row's sum over the other group's blocks
   static constexpr int OFF_BAR = OFF_L + 2 * TQ * 4;
   static constexpr int SMEM = OFF_BAR + (44 + 4 * SLOTS) * 8 + 8 + 1024;
-  static_assert(2 * sizeof(Unit) <= 80 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
+  static_assert(2 * sizeof(Unit) <= 96 && OFF_BAR % 8 == 0 && SMEM <= 232448, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;  // S0 S1 S2 (P over them) O
 };
 
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
   constexpr int kSlots = WIDEN ? C::SLOTS : 1;
   int half = 0;  // 64-key halves loaded so far
   auto load_codes = [&](const Unit& w, bool is_v) {
-    const int* bt = p.block_table + static_cast<size_t>(w.seq) * p.max_pages;
+    const int* bt = p.block_table + static_cast<size_t>(w.seq) * p.max_pages + w.page0;
     const int npages = (w.pos0 + w.nrows + 15) / 16;
     uint64_t* full = c_full + (is_v ? C::SLOTS : 0);
     uint64_t* empty = c_empty + (is_v ? C::SLOTS : 0);
@@ -525,14 +536,28 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       int local, base;
       w.valid = scan.find(p, v, lane, [&](int qlen, int kvl, int at) {
         const bool fits = at + padded(kvl) <= p.scratch_keys;
-        return fits != WIDEN ? p.n_q * ((qlen + TQ - 1) / TQ) : 0;
+        const int units = p.n_q * ((qlen + TQ - 1) / TQ);
+        return fits != WIDEN ? units * part_count(units, first_tile_blocks(qlen, kvl)) : 0;
       }, &local, &base);
       if (w.valid) {
         const int ntiles = (scan.qlen + TQ - 1) / TQ;
         w.seq = scan.seq;
         w.g = local % p.n_kv;
         w.row = base * p.n_kv + w.g * padded(scan.kvl);
-        tile_of(p, local / p.n_kv, ntiles, scan.q0, scan.qlen, scan.kvl, w);
+        const int blocks = first_tile_blocks(scan.qlen, scan.kvl), parts = part_count(p.n_q * ntiles, blocks);
+        const int i = local / p.n_kv;
+        tile_of(p, i / parts, ntiles, scan.q0, scan.qlen, scan.kvl, w);
+        w.part = -1;
+        w.page0 = 0;
+        if (parts > 1) {
+          w.part = i % parts;
+          w.part_row = part_row(p, w.row0, scan.q0);
+          const int per = blocks / parts, first = w.part * per;
+          w.nblk = w.part == parts - 1 ? w.nblk - first : per;
+          w.row += first * TK;
+          w.pos0 -= first * TK;
+          w.page0 = first * (TK / 16);
+        }
       }
       if (lane == 0) {
         ok = mbar_wait(&u_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag, p.status);
@@ -847,6 +872,25 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
       bool pok = mbar_wait(&pv_done[last % SETS], (last / SETS) & 1, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, pok)) break;
       tc_fence_after();
+      if (w.part >= 0) {
+        float* rec = p.chunk_partials +
+                     ((static_cast<size_t>(w.part_row + r) * p.n_q + w.head) * p.max_parts + w.part) * part_floats(D);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t ov[32];
+          tmem_ld_32x32b_x32(tO + c, ov);
+          tmem_ld_wait32(ov);
+          if (r < w.nrows)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(rec + c + 4 * i) = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+        }
+        if (r < w.nrows) *reinterpret_cast<float2*>(rec + D) = make_float2(m_used, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty);  // O was read into registers
+        continue;
+      }
       const float inv = 1.f / l;
       __nv_bfloat16* orow = p.out + (static_cast<size_t>(w.row0 + r) * p.n_q + w.head) * D;
 #pragma unroll 1

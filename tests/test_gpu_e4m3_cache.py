@@ -265,6 +265,25 @@ def test_attention_hints_move_work_only(n_q, n_kv, d):
     hb.hb_check_status()
 
 
+@pytest.mark.parametrize("n_q,n_kv,d", [(4, 2, 128), (12, 4, 64), (40, 8, 128)])
+@pytest.mark.parametrize("prefills,chunk", [([(1025, 1020)], 5), ([(2048, 2041)], 7), ([(5000, 4990)], 130),
+                                            ([(1030, 1000), (9216, 9215 - 126), (2300, 2100)], 200),
+                                            ([(9000, 8000)], 300)])
+def test_attention_short_chunks_behind_long_prefixes(n_q, n_kv, d, prefills, chunk):
+    """Their keys are taken in parts: each row's result is that of its sequence alone."""
+    dims = dims_of(n_q, n_kv, d)
+    rows = sum(min(chunk, n - done) for n, done in prefills)
+    hp = check(dims, [3, 600], prefills, 2 + rows, chunk, seed=rows + n_q)
+    assert hp.n_rows == 2 + rows
+    hp, q, cache, _ = batch(dims, [3, 600], prefills, 2 + rows, chunk, rows + n_q)
+    out = attend(hp, q, cache, dims)
+    for s in range(2, hp.n_seqs):
+        r0, r1 = hp.seq_q_start[s], hp.seq_q_start[s + 1]
+        one = attend(_alone(hp, s), q[r0:r1].contiguous(), cache, dims, max_kv=12000)
+        assert torch.equal(one, out[r0:r1]), s
+    hb.hb_check_status()
+
+
 @pytest.mark.parametrize("n_q,n_kv,d", [(4, 1, 128), (3, 1, 64)])
 def test_attention_more_chunk_keys_than_are_widened_ahead(n_q, n_kv, d):
     """Sequences behind the end of the workspace's scratch: the same bits as alone."""

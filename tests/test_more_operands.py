@@ -210,3 +210,20 @@ def test_logprobs_refusals(lib):
     refused(lib, call(vocab=4, k=5), b"top_k")
     assert call(rows=0, x=None) == L.HB_OK
     assert call(n=0, k=0, e=None, t=None, lp=None, ids=None, tlp=None) == L.HB_OK
+
+
+def test_attention_e4m3_workspace_of_bad_sizes():
+    """0, whatever else is given; and never less for more."""
+    dims = lambda n_q, n_kv: wl.Dims(d_model=64, n_q=n_q, n_kv=n_kv, d_head=64, d_ff=64)  # noqa: E731
+    size = B.hb_attention_e4m3_workspace_bytes
+    assert size(dims(0, 1), 10, 2, 100) == 0 and size(dims(4, 0), 10, 2, 100) == 0
+    assert size(dims(4, 2), -1, 2, 100) == 0 and size(dims(4, 2), 10, -1, 100) == 0 and size(dims(4, 2), 10, 2, -1) == 0
+    for n_q in (1, 4, 75, 77, 160):
+        for a in range(3):
+            last = 0
+            for v in (0, 1, 2, 100, 1000, 5000, 20000, 300000):
+                args = [600, 3, 9000]
+                args[a] = v
+                got = size(dims(n_q, 1), *args)
+                assert got >= last, (n_q, args)
+                last = got
