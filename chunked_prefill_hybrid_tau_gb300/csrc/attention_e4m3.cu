@@ -506,8 +506,8 @@ __device__ __forceinline__ void join_parts(const Params& p, int row, int warp, i
 // The splits of one decode row and q head (a CTA), in an order of their number
 // alone: warp w takes splits w, w + 8, ..., kJoin of them in flight with their
 // maxima and sums; the warps' results are joined in order.  The plan is read
-// ahead of the wait: the decode kernel lets this one start only once everything
-// ahead of itself is complete.
+// ahead of the wait: the first kernel of the call (the widening, or the decode
+// kernel) lets the next ones start only once everything ahead of it is complete.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_splits_kernel(Params p, int decode_items) {
   constexpr int E = D / 32;

@@ -14,7 +14,7 @@
 // (WIDEN: the same kernel with five more warps), which takes 3.7 times as long.
 //
 // The tensor pipe bounds it, 4 d_head FLOP a pair and q head: 2048 rows behind
-// 14336 keys, 56 q heads on 8 of 128, 596 us back to back with the widening, under
+// 14336 keys, 56 q heads on 8 of 128, 578 us back to back with the widening, under
 // the power limit (floor 466 at cuBLAS's burst rate, 520 at its sustained one);
 // alone the kernel takes 550, the pipe 73% active.  With two tiles a CTA and one
 // set of S columns each, so that a tile's next S waits for its PV, 701.
