@@ -315,11 +315,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     for (int b = 0; b < npages; ++b) {
       const int slot = b % DR;
       bool fok = mbar_wait(&full[slot], (phases >> slot) & 1u, nullptr, p.status);
-      phases ^= 1u << slot;
       if (!__all_sync(0xffffffffu, fok)) {
         ok = false;
         break;
       }
+      phases ^= 1u << slot;  // only now: the drain below waits for the phase that is still open
       uint8_t* st = ring + slot * STAGE_BYTES;
       const int key0 = key_begin + 16 * b;
       const bool tail = key0 + 16 > key_end;

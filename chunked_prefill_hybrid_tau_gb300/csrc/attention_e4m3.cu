@@ -394,11 +394,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 1)
     take_heads<D, NT>(p, w, row, cur.g, lane);
     for (int b = 0; b * 16 < cur.keys; ++b) {
       const bool landed = mbar_wait(&full[slot_out], (phases >> slot_out) & 1u, nullptr, p.status);
-      phases ^= 1u << slot_out;
       if (!__all_sync(0xffffffffu, landed)) {
         ok = false;
         break;
       }
+      phases ^= 1u << slot_out;  // only now: the drain below waits for the phase that is still open
       const uint32_t kp = smem_u32(ring + slot_out * C::STAGE);
       page_step<D, NT>(kp, kp + C::PAGE, smem_u32(scales + slot_out * 32), w, cur.keys - 16 * b, lane);
       __syncwarp();

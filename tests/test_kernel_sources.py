@@ -82,3 +82,16 @@ def test_no_warp_leaves_the_others_at_a_named_barrier():
         # leaving the sums of a group past the last K block, and a lambda's value
         outer = body.replace("if (kb0 + g0 + g >= kblocks) break;", "").replace("{ return chunk_col(", "{ chunk_col(")
         assert not re.search(r"\bbreak\b|\breturn\b", outer)
+
+
+@pytest.mark.parametrize("name,wait", [("attention.cu", "mbar_wait(&full[slot],"),
+                                       ("attention_e4m3.cu", "mbar_wait(&full[slot_out],")])
+def test_a_ring_slot_turns_over_only_once_its_copy_has_landed(name, wait):
+    """The drain of an expired wait goes by the parities that are open, the
+    expired one's among them: a parity turned ahead of the test would make it
+    look at the phase before, which is over."""
+    text = source(name)
+    at = text.index(wait)
+    turn, left = text.index("phases ^=", at), text.index("if (!__all_sync(", at)
+    assert text.count("phases ^=") == 1 and turn > text.index(block_from(text, left), at)
+    assert "break;" in block_from(text, left) and re.search(r"mbar_drain\(&full\[(\w+)\], \(phases >> \1\) & 1u\)", text)
