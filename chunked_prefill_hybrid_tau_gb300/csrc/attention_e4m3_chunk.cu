@@ -507,18 +507,24 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
     }
     return true;
   };
-  // after a wait that expired: this warp's copies in flight land (bounded) before it leaves
+  // A copying warp leaves once its copies have landed, whichever warp's wait expires
+  // meanwhile: it waits for the last ones as their readers do, and after an expired
+  // wait for a while more (bounded).
   int q_tiles = 0;  // loaded so far
-  auto drain_slots = [&](bool ok) {
-    if (ok || lane != 0) return;
-    if (q_tiles > 0) mbar_drain(q_full, (q_tiles - 1) & 1);
+  auto land_copies = [&](bool ok) {
+    if (lane != 0) return;
+    auto land = [&](uint64_t* full, int use) {
+      ok = ok && mbar_wait(full, use & 1, abort_flag, p.status);
+      if (!ok) mbar_drain(full, use & 1);
+    };
+    if (q_tiles > 0) land(q_full, q_tiles - 1);
     if (!WIDEN) {
-      for (int b = max(0, k_blocks - C::KST); b < k_blocks; ++b) mbar_drain(&k_full[b % C::KST], (b / C::KST) & 1);
-      for (int b = max(0, v_blocks - C::VST); b < v_blocks; ++b) mbar_drain(&v_full[b % C::VST], (b / C::VST) & 1);
+      for (int b = max(0, k_blocks - C::KST); b < k_blocks; ++b) land(&k_full[b % C::KST], b / C::KST);
+      for (int b = max(0, v_blocks - C::VST); b < v_blocks; ++b) land(&v_full[b % C::VST], b / C::VST);
       return;
     }
     uint64_t* full = c_full + (warp == kVWarp ? kSlots : 0);
-    for (int h = max(0, half - kSlots); h < half; ++h) mbar_drain(&full[h % kSlots], (h / kSlots) & 1);
+    for (int h = max(0, half - kSlots); h < half; ++h) land(&full[h % kSlots], h / kSlots);
   };
 
   if (warp == 0) {
@@ -589,12 +595,12 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
     }
-    drain_slots(ok);
+    land_copies(ok);
   } else if (WIDEN && warp == kVWarp) {
     bool ok = true;
     Unit w;
     for (int n = 0; ok && next_unit(n, w); ++n) ok = load_codes(w, true);
-    drain_slots(ok);
+    land_copies(ok);
   } else if (warp == 1 || warp == kPv) {
     // ------------------------------------------------------------ MMA issuers
     // The whole warp walks the loop and one elected lane issues: in a single-lane
@@ -656,8 +662,9 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
         }
       }
     }
-    if (!ok && elect_one()) {
-      // nothing may still read shared memory or write tensor memory at the end
+    if (elect_one()) {
+      // nothing may still read shared memory or write tensor memory at the end, where
+      // another warp's wait has expired too
       uint64_t* done = &drain[warp == 1 ? 0 : 1];
       mma_commit(done);
       mbar_drain(done, 0);

@@ -95,3 +95,19 @@ def test_a_ring_slot_turns_over_only_once_its_copy_has_landed(name, wait):
     turn, left = text.index("phases ^=", at), text.index("if (!__all_sync(", at)
     assert text.count("phases ^=") == 1 and turn > text.index(block_from(text, left), at)
     assert "break;" in block_from(text, left) and re.search(r"mbar_drain\(&full\[(\w+)\], \(phases >> \1\) & 1u\)", text)
+
+
+def test_no_warp_of_the_chunk_kernel_leaves_its_copies_or_products_in_flight():
+    """Its own waits may all have held while another warp's expires: what it
+    started lands before it leaves, not only after a wait of its own."""
+    text = source("attention_e4m3_chunk.cu")
+    assert re.search(r"if \(elect_one\(\)\) \{\s+uint64_t\* done = &drain\[[^;]+;\s+mma_commit\(done\);\s+mbar_drain\(done, 0\);",
+                     text)
+    leave = re.findall(r"(\w+)\(ok\);\n  \} else if", text)
+    assert leave == ["land_copies"] * 2
+    body = block_from(text, text.index("auto land_copies"))
+    assert re.findall(r"if \([^)]*\) return;", body) == ["if (lane != 0) return;"]
+    land = block_from(body, body.index("auto land ="))
+    assert re.search(r"ok = ok && mbar_wait\((\w+), (\w+) & 1, abort_flag, p\.status\);\s+if \(!ok\) mbar_drain\(\1, \2 & 1\);", land)
+    # the Q tile, K blocks, V blocks, codes
+    assert body.count("land(") == 4
