@@ -474,7 +474,7 @@ __device__ __forceinline__ void join_parts(const Params& p, int row, int warp, i
   if (parts == 1) return;
   for (int h = warp; h < p.n_q; h += kJoinWarps) {
     const float* rec = p.chunk_partials +
-                       (static_cast<size_t>(part_row(p, row, q0)) * p.n_q + h) * p.max_parts * part_floats(D);
+                       (static_cast<size_t>(part_row(p, row, s, q0)) * p.n_q + h) * p.max_parts * part_floats(D);
     float m[kMaxParts], l[kMaxParts], o[kMaxParts][E];
     float all = -INFINITY;
 #pragma unroll
@@ -673,11 +673,15 @@ size_t partial_bytes(const hb_layer_dims& dm, int seqs, int max_kv_len) {
   const size_t recs = splits > 1 ? static_cast<size_t>(seqs) * splits * dm.n_kv : 0;
   return (recs * rec_floats(dm.n_q / dm.n_kv, dm.d_head) * 4 + 255) / 256 * 256;
 }
-// of chunk rows (part_row); one sequence alone is split only where it has few
+// of chunk rows
 int max_parts(const hb_layer_dims& dm, int max_kv_len) { return part_count(dm.n_q, (max_kv_len + 127ll) / 128); }
+int part_stride(const hb_layer_dims& dm, int rows, int seqs) {
+  return static_cast<long long>(seqs) * split_rows(dm.n_q) < rows ? split_rows(dm.n_q) : 0;
+}
 size_t chunk_partial_bytes(const hb_layer_dims& dm, int rows, int seqs, int max_kv_len) {
-  const int parts = max_parts(dm, max_kv_len), few = 128 * (kSplitUnits / 2 / dm.n_q);
-  const size_t n = parts == 1 || seqs < 1 || rows < 2 ? 0 : seqs == 1 && rows > few ? few : rows;
+  const int parts = max_parts(dm, max_kv_len);
+  const long long most = static_cast<long long>(seqs) * split_rows(dm.n_q);
+  const size_t n = parts == 1 || rows < 2 ? 0 : most < rows ? most : rows;
   return (n * dm.n_q * parts * part_floats(dm.d_head) * 4 + 255) / 256 * 256;
 }
 size_t workspace_bytes(const hb_layer_dims& dm, int rows, int seqs, int max_kv_len) {
@@ -748,6 +752,7 @@ extern "C" hb_status hb_attention_e4m3(const void* q, const void* k_cache, const
   p.scratch_keys = no_chunks ? 0 : static_cast<int>(scratch_keys(plan->n_rows, plan->n_seqs, max_kv_len));
   uint8_t* at = static_cast<uint8_t*>(workspace) + partial_bytes(*dims, plan->n_seqs, max_kv_len);
   p.chunk_partials = reinterpret_cast<float*>(at);
+  p.part_stride = part_stride(*dims, plan->n_rows, plan->n_seqs);
   p.max_parts = max_parts(*dims, max_kv_len);
   at += chunk_partial_bytes(*dims, no_chunks ? 0 : plan->n_rows, plan->n_seqs, max_kv_len);
   p.scratch_k = reinterpret_cast<__nv_bfloat16*>(at);

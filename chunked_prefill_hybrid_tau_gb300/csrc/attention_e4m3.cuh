@@ -25,6 +25,7 @@ struct Params {
   float* partials;  // split records [sequence][split][kv head]
   int max_splits;   // of a sequence of max_kv_len keys
   float* chunk_partials;  // records of chunk rows whose keys are split, [part_row][q head][part]
+  int part_stride;        // rows of a sequence there; 0: by the plan's rows (part_row)
   int max_parts;          // of a sequence of max_kv_len keys
   int no_chunks;    // the plan has as many rows as sequences: none may have several
   int no_decodes;   // the plan has one sequence of several rows
@@ -49,8 +50,14 @@ __host__ __device__ inline int part_count(int units, int blocks) {
 __host__ __device__ inline int first_tile_blocks(int qlen, int kvl) {
   return (kvl - qlen + (qlen < 128 ? qlen : 128) + 127) / 128;
 }
-// which record row a row of the sequence that starts at q0 has
-__device__ __forceinline__ int part_row(const Params& p, int row, int q0) { return p.S == 1 ? row - q0 : row; }
+// Most rows of a sequence whose keys are split: more have too many units.
+inline int split_rows(int n_q) { return 128 * (kSplitUnits / 2 / n_q); }
+// Which record row a row of sequence seq, which starts at q0, has: its place among
+// the split_rows of its sequence, or its own number where the plan has fewer rows
+// than that takes.
+__device__ __forceinline__ int part_row(const Params& p, int row, int seq, int q0) {
+  return p.part_stride > 0 ? seq * p.part_stride + row - q0 : row;
+}
 // a record: O [D], its maximum and sum, fp32 (a multiple of 16 bytes)
 __host__ __device__ constexpr int part_floats(int d) { return d + 4; }
 

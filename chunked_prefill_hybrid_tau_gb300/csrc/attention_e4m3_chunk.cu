@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads<WIDEN>, 1)
         w.page0 = 0;
         if (parts > 1) {
           w.part = i % parts;
-          w.part_row = part_row(p, w.row0, scan.q0);
+          w.part_row = part_row(p, w.row0, scan.seq, scan.q0);
           const int per = blocks / parts, first = w.part * per;
           w.nblk = w.part == parts - 1 ? w.nblk - first : per;
           w.row += first * TK;

@@ -365,9 +365,13 @@ hb_status hb_kv_append_e4m3(const void* qkv, int32_t T, const int32_t* row_pos, 
  *   workspace: device scratch of hb_attention_e4m3_workspace_bytes(...)
  *     bytes, 256-byte aligned, contents need not be initialised; calls that
  *     may overlap (other streams, graphs replayed side by side) need one each.
- *     It holds split records, of decode rows and of chunks of few rows behind
- *     long prefixes, and the keys and values of sequences of several rows as bf16, those of at most 262144 keys (or of
- *     one sequence, if that has more); further ones take 3.7 times as long
+ *     It holds fp32 split records of d_head + 4 numbers: of decode rows, one a
+ *     q head and 256 keys (where max_kv_len is above 256); of chunks of few
+ *     rows behind long prefixes, up to min(8, 152 / n_q, max_kv_len / 1024) a
+ *     row and q head, for min(max_rows, max_seqs * 128 * (76 / n_q)) rows.
+ *     And the keys and values of sequences of several rows as bf16, those of
+ *     at most 262144 keys (or of one sequence, if that has more); further
+ *     ones take 3.7 times as long.
  * Requires d_head == 64 or 128, page_size == 16, at most 1024 sequences.
  * A row's result does not depend on the other sequences of the batch.
  * ---------------------------------------------------------------------- */

@@ -400,3 +400,18 @@ def test_attention_large_pool_offsets():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("n_q,n_kv,d", [(40, 8, 128), (12, 4, 64)])
+@pytest.mark.parametrize("prefills,chunk", [([(10000, 9994), (2000, 0)], 2000), ([(2000, 0), (9300, 9300 - 128)], 2000)])
+def test_attention_records_of_a_short_chunk_beside_a_long_one(n_q, n_kv, d, prefills, chunk):
+    """More rows than sequences of split keys can have: the records go by the
+    place in the sequence and not in the plan."""
+    dims = dims_of(n_q, n_kv, d)
+    rows = sum(min(chunk, n - done) for n, done in prefills)
+    hp = check(dims, [], prefills, rows, chunk, seed=n_q)
+    assert hp.n_rows == rows
+    hp, q, cache, _ = batch(dims, [], prefills, rows, chunk, n_q)
+    out = attend(hp, q, cache, dims)
+    for s in range(hp.n_seqs):
+        r0, r1 = hp.seq_q_start[s], hp.seq_q_start[s + 1]
+        assert torch.equal(attend(_alone(hp, s), q[r0:r1].contiguous(), cache, dims, max_kv=12000), out[r0:r1]), s
+    hb.hb_check_status()

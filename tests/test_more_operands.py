@@ -227,3 +227,21 @@ def test_attention_e4m3_workspace_of_bad_sizes():
                 got = size(dims(n_q, 1), *args)
                 assert got >= last, (n_q, args)
                 last = got
+
+
+def test_attention_e4m3_workspace_counts_only_rows_whose_keys_can_be_split():
+    """What the sizes ask for, part by part: the keys of decode rows in splits of
+    256, the keys of short chunks in parts of up to 128 * (76 / n_q) rows a
+    sequence (152 units of a tile and head at least twice), and widened keys."""
+    up = lambda n, m: -(-n // m) * m  # noqa: E731
+    for n_q, n_kv, d in ((4, 2, 64), (32, 8, 128), (56, 8, 128), (76, 4, 64), (80, 8, 128)):
+        dims = wl.Dims(d_model=64, n_q=n_q, n_kv=n_kv, d_head=d, d_ff=64)
+        for rows, seqs, kv in ((8192, 2, 32768), (8192, 1, 32768), (2048, 33, 4097), (64, 3, 9000), (130, 130, 9000)):
+            splits = -(-kv // 256)
+            decode = up(seqs * splits * n_kv * (n_q // n_kv) * (d + 4) * 4, 256)
+            parts = max(1, min(8, 152 // n_q, -(-kv // 128) // 8))
+            records = min(rows, seqs * 128 * (76 // n_q)) if parts > 1 else 0
+            chunk = up(records * n_q * parts * (d + 4) * 4, 256)
+            keys = min(min(seqs, rows // 2) * up(kv, 128), max(262144, up(kv, 128)))
+            want = 256 + decode + chunk + 2 * keys * n_kv * d * 2
+            assert B.hb_attention_e4m3_workspace_bytes(dims, rows, seqs, kv) == want, (n_q, rows, seqs, kv)
