@@ -467,8 +467,8 @@ __device__ __forceinline__ void join_parts(const Params& p, int row, int warp, i
   }
   const int rows = q1 - q0;
   griddep_wait();  // by all: the kernel's end has to imply its predecessor's
-  if (q0 < 0 || q1 > p.T || row < q0 || row >= q1 || rows < 2 || kvl < rows || kvl > p.max_kv_len ||
-      (kvl + 15) / 16 > p.max_pages)
+  if (q0 < 0 || q1 > p.T || row < q0 || row >= q1 || (rows < 2 && !p.no_decodes) || kvl < rows ||
+      kvl > p.max_kv_len || (kvl + 15) / 16 > p.max_pages)
     return;
   const int parts = part_count(p.n_q * ((rows + 127) / 128), first_tile_blocks(rows, kvl));
   if (parts == 1) return;

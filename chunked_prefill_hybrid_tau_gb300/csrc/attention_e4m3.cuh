@@ -28,7 +28,9 @@ struct Params {
   int part_stride;        // rows of a sequence there; 0: by the plan's rows (part_row)
   int max_parts;          // of a sequence of max_kv_len keys
   int no_chunks;    // the plan has as many rows as sequences: none may have several
-  int no_decodes;   // the plan has one sequence of several rows
+  // the plan has one sequence and more rows than that: the chunk kernel takes the
+  // sequence even if it has one row (and the others of the plan are padding)
+  int no_decodes;
   // 1 when the chunk kernel precedes the decode kernel on the stream: it waited
   // for the inputs before it let this one start, so the decode kernel's wait is
   // deferred to its end (whose completion then implies the chunk kernel's)

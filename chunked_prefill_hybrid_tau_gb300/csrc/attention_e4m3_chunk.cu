@@ -217,10 +217,10 @@ __device__ __forceinline__ void tile_of(const Params& p, int i, int ntiles, int 
 // keys of a sequence in the scratch: whole blocks
 __device__ __forceinline__ int padded(int kvl) { return (kvl + TK - 1) / TK * TK; }
 
-// Which several-row sequence an item falls into, sequence by sequence in order,
-// by a whole warp; items ascend from call to call.  count(qlen, kvl, base): items
-// of a sequence whose scratch starts at key `base`.  Sequences out of range are
-// reported and have no items (and no scratch).
+// Which of this kernel's sequences (those of several rows) an item falls into,
+// sequence by sequence in order, by a whole warp; items ascend from call to call.
+// count(qlen, kvl, base): items of a sequence whose scratch starts at key `base`.
+// Sequences out of range are reported and have no items (and no scratch).
 struct SeqScan {
   int s0 = 0, items = 0, keys = 0;  // of the sequences ahead of s0
   int seq, q0, qlen, kvl;           // the one found
@@ -234,10 +234,9 @@ struct SeqScan {
         const int q1 = ld_s32(p.q_start + s + 1);
         ql = q1 - a;
         kl = ld_s32(p.kv_len + s);
-        if (a < 0 || q1 > p.T || ql < 1 || kl < ql || kl > p.max_kv_len || (kl + 15) / 16 > p.max_pages ||
-            (p.no_decodes && ql < 2))
+        if (a < 0 || q1 > p.T || ql < 1 || kl < ql || kl > p.max_kv_len || (kl + 15) / 16 > p.max_pages)
           flag_error(p.status, kStatusIndex);
-        else if (ql > 1)
+        else if (ql > 1 || p.no_decodes)
           k = padded(kl);
       }
       int kend = k;

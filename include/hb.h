@@ -362,6 +362,7 @@ hb_status hb_kv_append_e4m3(const void* qkv, int32_t T, const int32_t* row_pos, 
  *   q, plan, out, max_kv_len : as hb_attention.  Every sequence of the plan
  *     has at least one row; a plan with another count is reported as
  *     HB_ERR_DEVICE by hb_check_status, and rows may be left unwritten.
+ *     Rows behind the last sequence's are padding: their out stays as it was.
  *   workspace: device scratch of hb_attention_e4m3_workspace_bytes(...)
  *     bytes, 256-byte aligned, contents need not be initialised; calls that
  *     may overlap (other streams, graphs replayed side by side) need one each.
@@ -373,7 +374,9 @@ hb_status hb_kv_append_e4m3(const void* qkv, int32_t T, const int32_t* row_pos, 
  *     at most 262144 keys (or of one sequence, if that has more); further
  *     ones take 3.7 times as long.
  * Requires d_head == 64 or 128, page_size == 16, at most 1024 sequences.
- * A row's result does not depend on the other sequences of the batch.
+ * A row's result does not depend on the other sequences of the batch.  (One
+ * row of the only sequence of a plan with padding goes the way of chunk rows:
+ * its sums are formed in another order than without the padding.)
  * ---------------------------------------------------------------------- */
 size_t hb_attention_e4m3_workspace_bytes(const hb_layer_dims* dims, int32_t max_rows, int32_t max_seqs,
                                          int32_t max_kv_len);

@@ -415,3 +415,28 @@ def test_attention_records_of_a_short_chunk_beside_a_long_one(n_q, n_kv, d, pref
         r0, r1 = hp.seq_q_start[s], hp.seq_q_start[s + 1]
         assert torch.equal(attend(_alone(hp, s), q[r0:r1].contiguous(), cache, dims, max_kv=12000), out[r0:r1]), s
     hb.hb_check_status()
+
+
+@pytest.mark.parametrize("n_q,n_kv,d", [(8, 2, 128), (12, 4, 64)])
+@pytest.mark.parametrize("dec_ctx,prefills,tau,chunk,pad", [([0], [], 1, 1, 7), ([700], [], 1, 1, 1),
+                                                            ([9000], [], 1, 1, 300), ([], [(900, 300)], 130, 130, 62),
+                                                            ([], [(9000, 8990)], 10, 10, 6), ([5, 700], [], 2, 1, 6),
+                                                            ([40], [(900, 300)], 131, 130, 5)])
+def test_attention_rows_behind_the_last_sequence(n_q, n_kv, d, dec_ctx, prefills, tau, chunk, pad):
+    """A plan with more rows than its sequences have, one row of one sequence
+    among them: the sequences' rows as ever, the others as they were."""
+    dims = dims_of(n_q, n_kv, d)
+    hp, q, cache, table = batch(dims, dec_ctx, prefills, tau, chunk, seed=pad + n_q)
+    n = hp.n_rows
+    dp = hb.DevicePlan(hp)
+    dp.n_rows = n + pad
+    q = torch.cat([q, torch.full((pad, n_q, d), math.nan, dtype=BF, device="cuda")])
+    out = torch.full((n + pad, n_q * d), 7.0, dtype=BF, device="cuda")
+    ws = wd.workspace(hb.hb_attention_e4m3_workspace_bytes(dims, n + pad, hp.n_seqs, 9500))
+    hb.hb_attention_e4m3(q, *[t.cuda() for t in cache], dp, dims, 9500, out, ws)
+    hb.hb_check_status()
+    want, bound = ec.attention(q[:n].cpu(), *cache, table, hp.seq_q_start.tolist(), hp.seq_kv_len.tolist())
+    assert ((out[:n].cpu().double() - want).abs() <= bound).all()
+    assert (out[n:] == 7).all()
+    if hp.n_seqs > 1 or n > 1:
+        assert torch.equal(out[:n], attend(hp, q[:n].contiguous(), cache, dims, max_kv=9500))
