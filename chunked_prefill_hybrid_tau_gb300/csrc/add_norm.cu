@@ -3,15 +3,17 @@
 //   h = bf16(x + residual)                  (h = x without a residual)
 //   y = h / sqrt(mean(h^2) + eps) * gamma   (fp32, from the rounded h)
 // with y stored as bf16, or as E4M3 codes with an fp32 scale per row or per
-// 128 columns: top = max(amax |y|, 2^-112), inv = 448 / top, scale =
-// top / 448 (correctly rounded), code = E4M3(fp32(y * inv)); a group of zeros
-// gets scale 0 and zero codes.  y goes into its codes from fp32: the only
+// 128 columns: inv = 448 / top, scale = top / 448 (correctly rounded), code =
+// E4M3(fp32(y * inv)); a group of zeros gets scale 0 and zero codes.  top is
+// amax |y|; of 128 columns 2^-112 at least, as in the block quantization.  A row's
+// is taken as it is: where 448 / amax might not be finite, y and amax are first
+// multiplied by 2^40.  y goes into its codes from fp32: the only
 // roundings are h's to bf16, which is what the next residual reads, and the
 // code's.
 //
 // Reads 4 and writes 3 or 4 bytes an element, each once: HBM bounds it for
 // many rows, the chain load - sum - maximum - store for few.  8192 x 7168 with a
-// scale per row: 68 us (floor 61.5 at the copy rate); one row of 4096 in blocks:
+// scale per row: 61 us (floor 61.5 at the copy rate); one row of 4096 in blocks:
 // 2.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -25,6 +27,7 @@ namespace {
 using namespace dev;
 
 constexpr float kAmaxMin = 0x1p-112f;
+constexpr float kLift = 0x1p40f;
 constexpr int kMaxD = 32768;
 
 struct NormArgs {
@@ -39,11 +42,13 @@ struct NormArgs {
 struct Scale {
   float inv, scale;
 };
-// of a maximum given as the bits of its magnitude (a NaN's are above all)
-__device__ __forceinline__ Scale scale_of(uint32_t amax) {
+// of a maximum given as the bits of its magnitude (a NaN's are above all); of a row,
+// inv is that of y and amax times `lift`
+template <bool ROW>
+__device__ __forceinline__ Scale scale_of(uint32_t amax, float lift) {
   if (amax == 0) return {0.f, 0.f};
-  const float top = amax < __float_as_uint(kAmaxMin) ? kAmaxMin : __uint_as_float(amax);
-  return {__fdiv_rn(448.0f, top), __fdiv_rn(top, 448.0f)};
+  const float top = !ROW && amax < __float_as_uint(kAmaxMin) ? kAmaxMin : __uint_as_float(amax);
+  return {__fdiv_rn(448.0f, ROW ? __fmul_rn(top, lift) : top), __fdiv_rn(top, 448.0f)};
 }
 
 __device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(256) add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (i < a.d8) {
-        const Scale s = scale_of(m);
+        const Scale s = scale_of<false>(m, 1.f);
         y[i] = codes8(f, s.inv);
         if ((t & 15) == 0) a.scale[static_cast<size_t>(row) * a.kb + i / 16] = s.scale;
       }
@@ -184,7 +189,8 @@ __global__ void __launch_bounds__(256) add_rmsnorm_kernel(NormArgs a) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = max(m, red_max[w]);
     }
-    const Scale s = scale_of(m);
+    const bool tiny = m < __float_as_uint(kAmaxMin);  // of the row: all its threads agree
+    const Scale s = scale_of<true>(m, tiny ? kLift : 1.f);
     if (t == 0) a.scale[row] = s.scale;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -192,6 +198,10 @@ __global__ void __launch_bounds__(256) add_rmsnorm_kernel(NormArgs a) {
       if (i >= a.d8) break;
       float f[8];
       normed(v[k], g[k], inv, f);
+      if (tiny) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], kLift);
+      }
       y[i] = codes8(f, s.inv);
     }
   }

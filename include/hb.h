@@ -492,11 +492,13 @@ hb_status hb_gemm_e4m3_block(const void* A, const float* s_a, const void* B, con
  *                        hb_quantize_e4m3_block's rule (block_rows 1) on y
  * Where weights carry no folded gain (block codes cannot take one afterwards)
  * this is the operand preparation with the gain on the tokens' side.  The
- * fp32 y is quantized directly, without a rounding to bf16 between; maxima
- * below 2^-112 count as 2^-112 in both coded forms.  NaN and infinities
- * follow the formulas: a NaN in h makes the whole row's y NaN, an infinity its
- * own y NaN and the row's others 0; a NaN among a scale's y makes that scale
- * and its codes NaN.  Other rows do not notice.
+ * fp32 y is quantized directly, without a rounding to bf16 between.  Maxima
+ * below 2^-112 count as 2^-112 in the block form, as there; in the row form
+ * they are taken as they are, down to the smallest subnormal one (448 / amax
+ * is kept finite; the scale may be subnormal or round to 0).  NaN and
+ * infinities follow the formulas: a NaN in h makes the whole row's y NaN, an
+ * infinity its own y NaN and the row's others 0; a NaN among a scale's y makes
+ * that scale and its codes NaN.  Other rows do not notice.
  * x, residual, h_out: device bf16 [rows][d]; h_out may be NULL (h is not
  * stored), or be x or residual; gamma: device bf16 [d]; y aliases nothing.
  * d % 8 == 0 (codes: d % 16 == 0), d <= 32768; 16-byte aligned (y_scale: 4).

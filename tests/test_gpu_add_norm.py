@@ -167,3 +167,34 @@ def test_another_stream_and_a_graph():
         torch.cuda.synchronize()
         # as values: x + r = 0 is +0 for either sign of the two
         assert torch.equal(ec.values(y) * sign, ec.values(want)) and torch.equal(sc, ws)
+
+
+@pytest.mark.parametrize("d", [256, 1024, 4096])
+@pytest.mark.parametrize("fmt", ["e4m3", "e4m3_block"])
+def test_maxima_around_the_smallest_of_a_block(fmt, d):
+    """Gains that take a row's largest y to 2^-100 ... 2^-132.  The block form
+    counts maxima below 2^-112 as 2^-112, the row form has no smallest one.
+    Beside the bounds above, y (its product with the gain) and the scale may be
+    subnormal in fp32: off by half a step of those, 2^-150."""
+    x, r, gamma = inputs(5, d)
+    for e in (100, 110, 111, 112, 113, 114, 118, 119, 120, 126, 130, 132):
+        g = (gamma.float() * 2.0 ** -e).to(BF)  # subnormal bf16 gains from 2^-126 on
+        y, scale = hb.hb_add_rmsnorm(x, r, g, EPS, fmt=fmt)
+        hb.hb_check_status()
+        h = (x.float() + r.float()).to(BF).cpu().double()
+        want = h / torch.sqrt(h.square().mean(1, keepdim=True) + EPS) * g.cpu().double()
+        rel, sub = (d / 2 + 8) * 2.0 ** -24, 2.0 ** -150
+        width = d if fmt == "e4m3" else 128
+        part = want.view(5, -1, width)
+        amax = part.abs().amax(2)
+        top = amax if fmt == "e4m3" else torch.where(amax > 0, amax.clamp(min=2.0 ** -112), amax)
+        s = scale.cpu().double().view(5, -1)
+        assert ((s - top / 448).abs() <= (rel + 2.0 ** -23) * top / 448 + (1 + 1 / 448) * sub).all(), e
+        # the codes themselves: a maximum's is 448 (or what 2^-112 leaves of it), the others' by the quotient.  amax is off
+        # by rel and half a step, twice the factor's own roundings; a code is within half a step
+        q = part * 448 / top[..., None]
+        off = (2 * rel + 2.0 ** -21) * q.abs() + (q.abs() + 448) * sub / top[..., None] * 2
+        got = ec.values(y.cpu()).view(5, -1, width)
+        assert ((got - q).abs() <= ec.HALF_E4M3 * (q.abs() + off) + ec.HALF_SUB + off).all(), e
+        if fmt == "e4m3":
+            assert (got.abs().amax(2) == 448).all()
