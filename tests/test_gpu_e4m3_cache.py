@@ -440,3 +440,33 @@ def test_attention_rows_behind_the_last_sequence(n_q, n_kv, d, dec_ctx, prefills
     assert (out[n:] == 7).all()
     if hp.n_seqs > 1 or n > 1:
         assert torch.equal(out[:n], attend(hp, q[:n].contiguous(), cache, dims, max_kv=9500))
+
+
+@pytest.mark.parametrize("normed", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_keys_that_are_not_finite(d, normed):
+    """A NaN, an infinity, or a rotation that passes fp32's range: byte 255 and
+    NaN codes throughout that head's key; its row's other heads and the other
+    rows as without it."""
+    dims, rows = dims_of(2, 2, d), 6
+    g = wd.device_generator(d)
+    clean = wd.randn_bf16((rows, 6, d), g)
+    qkv = clean.clone()
+    qkv[1, 2, 3] = math.nan
+    qkv[2, 3, d - 1] = math.inf
+    qkv[3, 2, 0] = -math.inf
+    if not normed:
+        qkv[4, 3] = 3.38e38  # 3.38e38 (|cos| + |sin|) is past 3.40e38 at any angle off the axes
+    pos = torch.tensor([7, 0, 5, 31, 11, 2], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([3, 17, 0, 9, 30, 5], dtype=torch.int32, device="cuda")
+    gains = [(1 + 0.3 * torch.randn(d, generator=g, device="cuda")).to(BF) for _ in range(2)] if normed else (None, None)
+    rope = wd.rope_table_device(32, dims)
+    q, cache = append(qkv.view(rows, -1), pos, slots, dims, 2, rope, 32, gains)
+    want_q, want = append(clean.view(rows, -1), pos, slots, dims, 2, rope, 32, gains)
+    hb.hb_check_status()
+    assert torch.equal(q, want_q) and torch.equal(cache[2], want[2]) and torch.equal(cache[3], want[3])
+    for r, h in ((1, 0), (2, 1), (3, 0)) + (() if normed else ((4, 1),)):
+        page, off = int(slots[r]) // 16, int(slots[r]) % 16
+        assert cache[1][page, h, off] == 255 and (cache[0][page, h, off] == 0x7f).all(), (r, h)
+        want[1][page, h, off], want[0][page, h, off] = 255, 0x7f
+    assert torch.equal(cache[0], want[0]) and torch.equal(cache[1], want[1])
