@@ -329,8 +329,11 @@ hb_status hb_attention_noalloc(const void* q, const void* k_cache, const void* v
  *   code = E4M3(y * 2^-e), nearest-even (OCP E4M3), scale byte = e + 127.
  * The scale is a power of two (an exponent byte with bias 127, OCP E8M0), so
  * code * 2^e is exact in bf16 and in fp32: reading the cache rounds nothing.
- * A vector with a NaN or an infinity gets scale byte 255 (NaN) and NaN codes
- * (0x7f) throughout.
+ * (The one exception is the top of the range: a magnitude from 1.9375 * 2^127
+ * on has the code of 256 * 2^120 = 2^128, which reads as an infinity.)
+ * A vector with a NaN or an infinity, a key that its rotation takes past
+ * fp32's range among them, gets scale byte 255 (NaN) and NaN codes (0x7f)
+ * throughout.
  *   g_q, g_k : bf16 [d_head] gains: every q and k head is RMS-normed before
  *              its rotation as hb_kv_append_norm does; both NULL: not normed
  *   k_cache, v_cache : device bytes [num_pages][n_kv][page_size][d_head]
@@ -352,7 +355,9 @@ hb_status hb_kv_append_e4m3(const void* qkv, int32_t T, const int32_t* row_pos, 
  *   P_j = exp(2^ek_j (q . K_j) / sqrt(d_head) - m),
  * with codes K, V, scales 2^ek, 2^ev of key j and the q row in bf16; products
  * are summed and the softmax is kept in fp32, P is rounded to bf16 for its
- * product with V.  What lies behind a sequence's last key, in its last page
+ * product with V (for decode rows P 2^ev).  Decode rows take q to fp16, each
+ * head times a power of two of its own: exact but for values below 2^-30 of
+ * the head's largest, which lose bits.  What lies behind a sequence's last key, in its last page
  * or in pages of the block table behind it, is never used, whatever it holds.
  * A key or value of scale byte 255 reads as NaN.  The append writes scale
  * bytes 27 to 247 and 255, and codes 0x7f or 0xff under byte 255 only; a cache
@@ -373,7 +378,9 @@ hb_status hb_kv_append_e4m3(const void* qkv, int32_t T, const int32_t* row_pos, 
  *     And the keys and values of sequences of several rows as bf16, those of
  *     at most 262144 keys (or of one sequence, if that has more); further
  *     ones take 3.7 times as long.
- * Requires d_head == 64 or 128, page_size == 16, at most 1024 sequences.
+ * Requires d_head == 64 or 128, page_size == 16, at most 1024 sequences,
+ * max_kv_len <= 2^28, num_pages * n_kv * 16 below 2^31, and with sequences of
+ * several rows n_kv times the widened keys below 2^31 too.
  * A row's result does not depend on the other sequences of the batch.  (One
  * row of the only sequence of a plan with padding goes the way of chunk rows:
  * its sums are formed in another order than without the padding.)
@@ -656,7 +663,7 @@ hb_status hb_final_logits(const void* x, int32_t T, const int32_t* rows, int32_t
  * in fp32, from the logits as they are (no temperature).
  *   logits : device fp32 (HB_LOGITS_F32) or bf16 (HB_LOGITS_BF16)
  *            [n_rows][vocab], rows `row_stride` elements apart (>= vocab);
- *            aligned to an element
+ *            aligned to an element; vocab <= 2^30, n_rows <= 2^28
  *   tokens : device int32 [n_rows][n_tokens]; a negative id is padding, its
  *            entry is left as it was; an id >= vocab sets HB_ERR_DEVICE and
  *            is skipped.  n_tokens 0: tokens and token_logprobs may be NULL

@@ -228,3 +228,20 @@ def test_final_logits_then_logprobs():
     out = call(logits)
     hb.hb_check_status()
     check(logits, *out)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,vocab", [(1, 152001), (64, 32000), (160, 12345), (700, 5003)])
+@pytest.mark.parametrize("allowed", [1, 12, 100])
+def test_rows_of_a_few_allowed_tokens(rows, vocab, allowed, dtype):
+    """A hard mask: fewer finite logits than best alternatives asked for, or a few more; the rest of
+    the alternatives are the first masked tokens."""
+    x = logits_of(rows, vocab, dtype)
+    g = wd.device_generator(allowed)
+    at = torch.stack([torch.randperm(vocab, generator=g, device="cuda")[:allowed] for _ in range(rows)])
+    kept = x.gather(1, at)
+    x.fill_(-math.inf)
+    x.scatter_(1, at, kept)
+    check(x, *call(x, tokens=at[:, :1].to(torch.int32), k=20))
+    check(x, *call(x, tokens=at[:, -1:].to(torch.int32), k=1))
+    hb.hb_check_status()
