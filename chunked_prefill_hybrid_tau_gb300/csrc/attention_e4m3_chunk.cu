@@ -11,7 +11,8 @@
 // widened once, by a kernel ahead (widen_kernel), into scratch of the workspace
 // laid out for whole-block copies.  That scratch is bounded (kScratchKeys);
 // sequences behind its end are widened block by block beside the MMAs instead
-// (WIDEN: the same kernel with five more warps), which takes 3.7 times as long.
+// (WIDEN: the same kernel with five more warps, whose 16 at 128 registers spill 544
+// bytes), which takes 3.7 times as long.
 //
 // The tensor pipe bounds it, 4 d_head FLOP a pair and q head: 2048 rows behind
 // 14336 keys, 56 q heads on 8 of 128, 578 us back to back with the widening, under

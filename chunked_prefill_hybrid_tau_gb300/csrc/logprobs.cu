@@ -25,6 +25,10 @@
 // the issue slots are 79% busy, 13 instructions an element, and a CTA that starts,
 // ends or joins has no loads in flight, which four CTAs of 64 registers cover only
 // in part (five spill); the 8 best cost 7 us, 32 cost 22.
+// 2048 x 32000 fp32: 54 us, 700 rows 19 (floor 13.4).  Where fewer than k groups hold
+// a finite logit (a mask that leaves a few tokens; vocabularies of a few thousand) the
+// bound is -inf and the row is read again for exact keys: 64 x 32000 fp32 with 12
+// tokens left 144 us, unmasked 12.7.
 // One row takes 7 us, most of it in the cluster's barriers and the chain of the
 // selection.
 #include <cuda_bf16.h>
