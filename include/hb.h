@@ -355,13 +355,13 @@ hb_status hb_kv_append_e4m3(const void* qkv, int32_t T, const int32_t* row_pos, 
  *   P_j = exp(2^ek_j (q . K_j) / sqrt(d_head) - m),
  * with codes K, V, scales 2^ek, 2^ev of key j and the q row in bf16; products
  * are summed and the softmax is kept in fp32, P is rounded to bf16 for its
- * product with V (for decode rows P 2^ev).  Decode rows take q to fp16, each
+ * product with V (for decode rows P 2^ev). Decode rows take q to fp16, each
  * head times a power of two of its own: exact but for values below 2^-30 of
- * the head's largest, which lose bits.  What lies behind a sequence's last key, in its last page
- * or in pages of the block table behind it, is never used, whatever it holds.
- * A key or value of scale byte 255 reads as NaN.  The append writes scale
- * bytes 27 to 247 and 255, and codes 0x7f or 0xff under byte 255 only; a cache
- * with others at keys that a row sees gives unspecified values.
+ * the head's largest, which lose bits. What lies behind a sequence's last key,
+ * in its last page or in pages of the block table behind it, is never used,
+ * whatever it holds. A key or value of scale byte 255 reads as NaN. The append
+ * writes scale bytes 27 to 247 and 255, and codes 0x7f or 0xff under byte 255
+ * only; a cache with others at keys that a row sees gives unspecified values.
  *   k_cache, v_cache, k_scale, v_scale : as in hb_kv_append_e4m3 (after this
  *     iteration's append), each 16-byte aligned
  *   q, plan, out, max_kv_len : as hb_attention.  Every sequence of the plan
